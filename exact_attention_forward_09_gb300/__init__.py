@@ -17,14 +17,16 @@ import torch
 
 from .build import LIB as _LIB_PATH
 
-__all__ = ["fwd_host", "fwd_host_workspace_bytes", "bwd", "bwd_workspace_bytes", "fwd_splitkv", "splitkv_workspace_bytes", "fwd", "fwd_gqa", "fwd_fp8", "fwd_fp8_gqa", "quant_fp8", "quant_fp8_per_tensor_noalloc", "check_device_error", "lib",
+__all__ = ["fwd_host", "fwd_host_workspace_bytes", "bwd", "bwd_workspace_bytes", "fwd_splitkv", "splitkv_workspace_bytes", "fwd", "fwd_gqa", "fwd_window",
+           "fwd_paged", "paged_workspace_bytes", "cache_append", "fwd_fp8", "fwd_fp8_gqa", "quant_fp8", "quant_fp8_per_tensor_noalloc", "check_device_error", "lib",
            "FaError", "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
-           "FA_ERR_SCRATCH_LIMIT", "FA_DTYPE_BF16", "FA_DTYPE_FP16", "FP8_BLOCK_ROWS",
+           "FA_ERR_SCRATCH_LIMIT", "FA_ERR_INDEX", "FA_DTYPE_BF16", "FA_DTYPE_FP16", "FP8_BLOCK_ROWS",
            "FA_ROPE_INTERLEAVED", "FA_ROPE_HALF",
            "QUANT_NOALLOC_MAX_BLOCKS"]
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = 0, 1, 2, 3, 4
 FA_ERR_SCRATCH_LIMIT = 5
+FA_ERR_INDEX = 6
 QUANT_NOALLOC_MAX_BLOCKS = 65536
 FA_DTYPE_BF16, FA_DTYPE_FP16 = 0, 1
 FA_ROPE_INTERLEAVED, FA_ROPE_HALF = 1, 2
@@ -35,6 +37,14 @@ class FaError(RuntimeError):
     def __init__(self, status: int, where: str):
         self.status = status
         super().__init__(f"{where}: {_lib().fa_status_string(status).decode()}")
+
+
+class _KvCache(ctypes.Structure):
+    """``fa_kv_cache``."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
+                ("page_size", ctypes.c_int64), ("heads", ctypes.c_int64), ("d", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+                ("dtype", ctypes.c_int)]
 
 
 _LIB = None
@@ -80,6 +90,16 @@ def _lib():
         lib.fa_bwd.restype = i32
         lib.fa_bwd_workspace_bytes.argtypes = [i64, i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)]
         lib.fa_bwd_workspace_bytes.restype = i32
+        cache = ctypes.POINTER(_KvCache)
+        lib.fa_fwd_window.argtypes = [vp, vp, vp, vp, vp] + [i64] * 8 + [f32, i32, vp]
+        lib.fa_fwd_window.restype = i32
+        lib.fa_paged_workspace_bytes.argtypes = [i64, ctypes.POINTER(ctypes.c_size_t)]
+        lib.fa_paged_workspace_bytes.restype = i32
+        lib.fa_fwd_paged.argtypes = [vp, cache, vp, vp, vp, i64, i64, vp, vp] + [i64] * 7 + [f32, vp, ctypes.c_size_t, vp]
+        lib.fa_fwd_paged.restype = i32
+        lib.fa_cache_append.argtypes = [cache, vp, vp, vp, vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, i64, i64, vp,
+                                        vp, i64, i32, vp]
+        lib.fa_cache_append.restype = i32
         lib.fa_status_string.argtypes = [i32]
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_check_device_error.argtypes = [vp]
@@ -299,6 +319,177 @@ def fwd_gqa(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = Fa
                                B, Hq, Hkv, Nq, Nk, d, int(bool(causal)), float(scale), dt, _stream(q))
     _check(st, "fa_fwd_gqa")
     return out, lse
+
+
+def _scale(scale, d):
+    return 1.0 / math.sqrt(d) if scale is None else float(scale)
+
+
+def _check_out(name, t, shape, dtype, device):
+    if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != dtype \
+            or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
+
+
+def fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0,
+               scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None):
+    """Attention under a sliding window with sinks (``fa_fwd_window``): q [B,
+    Hq, Nq, d], k/v [B, Hkv, Nk, d]; query i at position p = i + Nk - Nq sees
+    key j iff j <= p and (j > p - window or j < sinks).  Returns
+    (O [B, Hq, Nq, d], LSE [B, Hq, Nq])."""
+    _check_gqa(q, k, v, (torch.bfloat16, torch.float16))
+    B, Hq, Nq, d = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _check_out("out", out, q.shape, q.dtype, q.device)
+    if lse is None:
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
+    else:
+        _check_out("lse", lse, (B, Hq, Nq), torch.float32, q.device)
+    dt = FA_DTYPE_BF16 if q.dtype == torch.bfloat16 else FA_DTYPE_FP16
+    with torch.cuda.device(q.device):
+        st = _lib().fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                  B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks), _scale(scale, d), dt, _stream(q))
+    _check(st, "fa_fwd_window")
+    return out, lse
+
+
+def _cache(k_pages, v_pages):
+    """The ``fa_kv_cache`` of two [num_pages, heads, page_size, d] tensors (or
+    views of that shape with other strides)."""
+    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
+            raise ValueError(f"{name} must be a [num_pages, heads, page_size, d] CUDA tensor")
+        if t.dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"{name} has dtype {t.dtype}; expected bf16 or fp16")
+        if t.stride(3) != 1:
+            raise ValueError(f"{name} must have its last dimension contiguous")
+    if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() or k_pages.dtype != v_pages.dtype \
+            or k_pages.device != v_pages.device:
+        raise ValueError("k_pages and v_pages must share shape, strides, dtype and device")
+    n, h, ps, d = k_pages.shape
+    sp, sh, st, _ = k_pages.stride()
+    dt = FA_DTYPE_BF16 if k_pages.dtype == torch.bfloat16 else FA_DTYPE_FP16
+    return _KvCache(k_pages.data_ptr(), v_pages.data_ptr(), n, ps, h, d, sp, sh, st, dt)
+
+
+def _check_batch(block_table, cu_q, seq_k, device):
+    """(B, table stride, table width) of a ragged batch's index tensors."""
+    for name, t, dim in (("block_table", block_table, 2), ("cu_q", cu_q, 1), ("seq_k", seq_k, 1)):
+        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dim or t.device != device \
+                or (t.numel() > 0 and t.stride(-1) != 1):
+            raise ValueError(f"{name} must be a {dim}-D int32 tensor on {device} with its last dimension contiguous")
+    B = seq_k.shape[0]
+    if block_table.shape[0] != B or cu_q.shape[0] != B + 1:
+        raise ValueError("block_table must be [B, max_pages], cu_q [B + 1] and seq_k [B]")
+    return B, block_table.stride(0), block_table.shape[1]
+
+
+def _check_tokens(name, t, T, heads, d, dtype, device):
+    """The token stride of a packed [T, heads, d] tensor."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype != dtype or t.device != device \
+            or t.shape[0] != T or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be a {dtype} [T, heads, d] tensor on {device}")
+    if t.numel() > 0 and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
+        raise ValueError(f"{name} must have each token's heads contiguous")
+    return t.stride(0)
+
+
+def paged_workspace_bytes(d: int) -> int:
+    """Bytes of device workspace ``fwd_paged`` needs on the current device."""
+    n = ctypes.c_size_t(0)
+    _check(_lib().fa_paged_workspace_bytes(d, ctypes.byref(n)), "fa_paged_workspace_bytes")
+    return int(n.value)
+
+
+def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+              cu_q: torch.Tensor, seq_k: torch.Tensor, window: int | None = None, sinks: int = 0,
+              scale: float | None = None, max_q: int = 0, out: torch.Tensor | None = None,
+              lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """Attention of the new tokens of a ragged batch over a paged cache
+    (``fa_fwd_paged``): q [T, Hq, d] (sequence b has rows cu_q[b] to
+    cu_q[b+1]), pages [num_pages, Hkv, page_size, d], block_table [B,
+    max_pages], seq_k [B] keys per sequence with the new tokens' last.
+    ``window`` None: every key up to a query's own.  ``max_q``: the most new
+    tokens of any sequence, if known.  Returns (O [T, Hq, d], LSE [T, Hq]);
+    rows outside every sequence are left as they were."""
+    cache = _cache(k_pages, v_pages)
+    dev = k_pages.device
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [T, Hq, d] CUDA tensor")
+    T, Hq, d = q.shape
+    q_stride = _check_tokens("q", q, T, None, cache.d, k_pages.dtype, dev)
+    B, table_stride, max_pages = _check_batch(block_table, cu_q, seq_k, dev)
+    if cache.heads == 0 or Hq % cache.heads != 0:
+        raise ValueError("the number of query heads must be a multiple of the number of key/value heads")
+    if out is None:
+        out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+    else:
+        _check_out("out", out, (T, Hq, d), q.dtype, dev)
+    if lse is None:
+        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+    else:
+        _check_out("lse", lse, (T, Hq), torch.float32, dev)
+    with torch.cuda.device(dev):
+        if workspace is None:
+            workspace = torch.empty((paged_workspace_bytes(d),), dtype=torch.uint8, device=dev)
+        st = _lib().fa_fwd_paged(q.data_ptr(), ctypes.byref(cache), out.data_ptr(), lse.data_ptr(),
+                                 block_table.data_ptr(), table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(),
+                                 B, T, Hq, q_stride, int(max_q), 1 << 30 if window is None else int(window),
+                                 int(sinks), _scale(scale, d), workspace.data_ptr(),
+                                 workspace.numel() * workspace.element_size(), _stream(k_pages))
+    _check(st, "fa_fwd_paged")
+    return out, lse
+
+
+def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                 block_table: torch.Tensor, cu_q: torch.Tensor, seq_k: torch.Tensor, q: torch.Tensor | None = None,
+                 rope=None, q_out: torch.Tensor | None = None):
+    """Writes the new tokens' keys and values, [T, heads, d], into their pages
+    (``fa_cache_append``; the batch as in ``fwd_paged``).  ``rope``: None, or
+    (cos, sin, layout) with cos / sin contiguous fp32 [positions, d/2] and
+    layout FA_ROPE_INTERLEAVED or FA_ROPE_HALF: keys, and the queries q [T,
+    Hq, d] if given, are rotated by their positions first.  k, v and q may be
+    slices of one projection.  Returns the rotated queries (``q_out``), or
+    None without q."""
+    cache = _cache(k_pages, v_pages)
+    dev, dt = k_pages.device, k_pages.dtype
+    if not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("k must be a [T, heads, d] CUDA tensor")
+    T = k.shape[0]
+    ks = _check_tokens("k", k, T, cache.heads, cache.d, dt, dev)
+    vs = _check_tokens("v", v, T, cache.heads, cache.d, dt, dev)
+    B, table_stride, max_pages = _check_batch(block_table, cu_q, seq_k, dev)
+    Hq, qs, qp, op = 0, 0, None, None
+    if q is not None:
+        qs = _check_tokens("q", q, T, None, cache.d, dt, dev)
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((T, Hq, cache.d), dtype=dt, device=dev)
+        else:
+            _check_out("q_out", q_out, (T, Hq, cache.d), dt, dev)
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out needs q")
+    cp, sp, n, layout = None, None, 0, 0
+    if rope is not None:
+        cos, sin, layout = rope
+        n = cos.shape[0]
+        for nm, t in (("cos", cos), ("sin", sin)):
+            if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_contiguous() \
+                    or tuple(t.shape) != (n, cache.d // 2) or t.device != dev:
+                raise ValueError(f"rope {nm} must be a contiguous fp32 [positions, d/2] tensor on {dev}")
+        if layout not in (FA_ROPE_INTERLEAVED, FA_ROPE_HALF):
+            raise ValueError("rope layout must be FA_ROPE_INTERLEAVED or FA_ROPE_HALF")
+        cp, sp = cos.data_ptr(), sin.data_ptr()
+    with torch.cuda.device(dev):
+        st = _lib().fa_cache_append(ctypes.byref(cache), qp, k.data_ptr(), v.data_ptr(), op, qs, ks, vs,
+                                    block_table.data_ptr(), table_stride, max_pages, cu_q.data_ptr(),
+                                    seq_k.data_ptr(), B, T, Hq, cp, sp, n, int(layout), _stream(k_pages))
+    _check(st, "fa_cache_append")
+    return q_out
 
 
 def fwd_fp8_gqa(q8, k8, v8, q_descale, k_descale, v_descale, causal: bool = False,

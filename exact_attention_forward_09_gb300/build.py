@@ -21,9 +21,11 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libfa.so")
 LIB_ABLATE = os.path.join(HERE, "libfa_ablate.so")
 UNITS = ["api.cu", "attn_bf16.cu", "attn_fp16.cu", "attn_fp8.cu", "quant_fp8.cu", "quant_fp8_noalloc.cu",
-         "splitkv.cu", "attn_split_bf16.cu", "attn_split_fp16.cu", "attn_bwd.cu"]
+         "splitkv.cu", "attn_split_bf16.cu", "attn_split_fp16.cu", "attn_bwd.cu", "window_api.cu", "attn_window_bf16.cu",
+         "attn_window_fp16.cu", "attn_paged_bf16.cu", "attn_paged_fp16.cu", "paged.cu"]
 ABLATE_UNITS = ["ablate_api.cu", "ablate_bf16.cu", "ablate_bf16_causal.cu", "ablate_fp8.cu", "ablate_d64.cu"]
-HEADERS = ["ptx.cuh", "attn_fwd.cuh", "quant_fp8.h", "attn_bwd.h", "splitkv.h", "ablate_inst.h"]
+HEADERS = ["ptx.cuh", "attn_fwd.cuh", "quant_fp8.h", "attn_bwd.h", "splitkv.h", "ablate_inst.h", "api_internal.h",
+           "attn_window.cuh", "paged.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

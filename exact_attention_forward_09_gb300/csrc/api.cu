@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "fa.h"
+#include "api_internal.h"
 #include "attn_fwd.cuh"
 #include "splitkv.h"
 #include "quant_fp8.h"
@@ -646,6 +647,35 @@ fa_status quant_impl(const float* x, void* x8, float* descale, int64_t B, int64_
 
 namespace fa {
 fa_status internal_device_setup(int* dev, int** err) { return device_setup(dev, err); }
+int internal_sm_count(int dev) { return device_sm_count(dev); }
+bool internal_take_inject() { return (g_inject.exchange(0) & 1) != 0; }
+
+fa_status internal_check_common(const void* q, const void* k, const void* v, const void* o, const float* lse, int64_t B,
+                                int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d, float scale, bool* empty) {
+  return check_common(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, empty);
+}
+
+fa_status internal_encode_map(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int elem_bytes, int64_t BH,
+                              int64_t N, int64_t d, uint32_t box_rows) {
+  return encode_map(map, base, dt, elem_bytes, BH, N, d, box_rows);
+}
+
+fa_status internal_encode_map_nd(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int rank,
+                                 const uint64_t* dims, const uint64_t* strides, const uint32_t* box) {
+  cuuint64_t dm[5], sd[4];
+  cuuint32_t bx[5], es[5];
+  if (rank < 2 || rank > 5) return FA_ERR_INVALID_ARG;
+  for (int i = 0; i < rank; ++i) {
+    dm[i] = dims[i];
+    bx[i] = box[i];
+    es[i] = 1;
+    if (i + 1 < rank) sd[i] = strides[i];
+  }
+  const CUresult r = g_encode(map, dt, (cuuint32_t)rank, const_cast<void*>(base), dm, sd, bx, es,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? FA_OK : FA_ERR_CUDA;
+}
 
 fa_status internal_encode_quant_map(CUtensorMap* map, const float* x, int64_t BH, int64_t N, int64_t d) {
   // 32-float (128-byte) x 64-row boxes, 128-byte swizzle, rows past N read as 0
@@ -858,6 +888,8 @@ const char* fa_status_string(fa_status status) {
     case FA_ERR_TIMEOUT: return "FA_ERR_TIMEOUT: a kernel pipeline wait ran out of time";
     case FA_ERR_SCRATCH_LIMIT:
       return "FA_ERR_SCRATCH_LIMIT: B*H*ceil(N/128) exceeds FA_QUANT_NOALLOC_MAX_BLOCKS (static scratch)";
+    case FA_ERR_INDEX:
+      return "FA_ERR_INDEX: a length, position or page number read from device memory was out of range";
   }
   return "FA_ERR_UNKNOWN";
 }
@@ -873,7 +905,7 @@ fa_status fa_check_device_error(cudaStream_t stream) {
   if (h != 0) {
     const int zero = 0;
     if (cudaMemcpyToSymbol(g_fa_device_error, &zero, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
-    return FA_ERR_TIMEOUT;
+    return h == fa::FA_DEVERR_INDEX ? FA_ERR_INDEX : FA_ERR_TIMEOUT;
   }
   return FA_OK;
 }

@@ -1,0 +1,8 @@
+// Instances of the windowed attention forward kernel, paged key/value cache, bf16 operands.
+#include "attn_window.cuh"
+
+namespace fa {
+template cudaError_t launch_attn_window<kBF16, 64, true>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 128, true>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 256, true>(const WinLaunch&);
+}  // namespace fa

@@ -1,0 +1,1190 @@
+// attn_window.cuh -- attention forward under a sliding window with sinks, on
+// dense tensors and over a paged key/value cache, for sm_103a (tcgen05 + TMEM
+// + TMA).
+//
+// What it computes, for a query at position p of its sequence:
+//   O = sum_j softmax_j(scale q . k_j) v_j,   LSE = ln sum_j exp(scale q . k_j)
+// over the visible keys: j <= p and (j > p - window or j < sinks).  A window
+// of at least the sequence length makes it plain causal attention.
+//
+// Key tiles.  A query tile visits the 128-key tiles that hold a sink (first
+// `ns` tiles) and those from its first row's window start to its last row's
+// position; the tiles between the two are skipped (never loaded nor
+// multiplied).  The visited tiles are numbered 0 .. L-1 without the gap
+// ("list index"); with two query tiles per CTA the list is the union of both
+// tiles' ranges and each tile takes part in its own list indices only.
+//
+// The CTA is organised as the full-mask kernel of attn_fwd.cuh: a load warp
+// (TMA through an NS-slot ring), an MMA warp that issues S = Q K^T and
+// O += P V with P in TMEM, and one softmax warpgroup per query tile with one
+// thread per row and a lazily rescaled O.  What differs is described where it
+// happens: visibility as four 32-bit words per row and tile, and, for PAGED:
+//   * rows: the g query heads of a key/value head are packed, row = token * g
+//     + head, so that each key/value byte is read once per group;
+//   * pages: a key tile is gathered by one TMA box per page (4-D map: column,
+//     row in page, head, page); pages without a visible key are not read;
+//   * work: the (sequence, query group, head) units of the ragged batch are
+//     laid end to end in units of key tiles and every CTA takes an equal run
+//     of that line, so that one long sequence, or a few, fill the GPU as well
+//     as many; a unit that is cut leaves fp32 partial results (O normalised
+//     over its run and the run's LSE), which a second kernel joins by LSE
+//     weights.  Every CTA derives the line from cu_q and seq_k itself, so a
+//     captured graph follows lengths that change on the device;
+//   * what no query may see but a key tile holds all the same (rows behind
+//     the sequence's end in its last page, pages that left the window) may be
+//     anything, NaN included: its scores are replaced, and its V rows are
+//     zeroed in shared memory before P V.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attn_fwd.cuh"
+#include "ptx.cuh"
+
+namespace fa {
+
+template <int ELEM, int D, bool PAGED>
+struct WinCfg {
+  static_assert(ELEM == kBF16 || ELEM == kFP16, "16-bit operands");
+  static constexpr int ROW_BYTES = D * 2;
+  static constexpr int CH_ELEMS = 64;                      // elements per 128-byte chunk
+  static constexpr int NCH = D / CH_ELEMS;
+  static constexpr int CHUNK_BYTES = 128 * 128;            // 128 rows x 128 bytes
+  static constexpr int NQT = D <= 128 ? 2 : 1;             // query tiles per CTA
+  static constexpr int TILE_BYTES = kBN * ROW_BYTES;
+  static constexpr int SLOT_BYTES = TILE_BYTES < 32768 ? TILE_BYTES : 32768;
+  static constexpr int SPT = TILE_BYTES / SLOT_BYTES;      // ring slots per tile
+  static constexpr int SLOT_CH = SLOT_BYTES / CHUNK_BYTES;
+  static constexpr int SLOT_D = SLOT_CH * CH_ELEMS;
+  static constexpr int Q_BYTES = NQT * kBM * ROW_BYTES;
+  // dense d <= 128: O goes out through per-warp staging boxes and bulk tensor
+  // copies (as attn_fwd.cuh); a paged row tile ends inside its neighbours'
+  // rows, so there every thread stores its own row
+  static constexpr bool EPI_TMA = !PAGED && D <= 128;
+  static constexpr int EPI_WARP_BYTES = 32 * 64 * 2;
+  static constexpr int EPI_BYTES = EPI_TMA ? 4 * NQT * EPI_WARP_BYTES : 0;
+  static constexpr int NS_MAX = (kSmemLimit - 2048 - EPI_BYTES - Q_BYTES) / SLOT_BYTES;
+  static constexpr int NS = NS_MAX > 8 ? 8 : NS_MAX;
+  static_assert(NS >= 2 * SPT, "ring too shallow");
+  static constexpr int P_COLS = kBN / 2;
+  static constexpr uint32_t TMEM_COLS = 512;
+  static constexpr uint32_t O_COL0 = 256;                  // S / P buffers at 0 and 128
+  static_assert(O_COL0 + NQT * D <= TMEM_COLS, "TMEM budget");
+  static constexpr int SOFTMAX_WARPS = 4 * NQT;
+  static constexpr int MMA_WARP = SOFTMAX_WARPS;
+  static constexpr int LOAD_WARP = SOFTMAX_WARPS + 1;
+  // two query tiles: a third, control warpgroup gives registers to the
+  // softmax warpgroups (the split of attn_fwd.cuh)
+  static constexpr bool REALLOC = NQT == 2;
+  static constexpr int THREADS = REALLOC ? 32 * (SOFTMAX_WARPS + 4) : 32 * (SOFTMAX_WARPS + 2);
+  static constexpr int CTRL_REGS = 104;
+  static constexpr int SOFTMAX_REGS = 200;
+  static constexpr float TAU = 8.0f;                       // lazy-rescale threshold, log2 units
+  static constexpr uint32_t FMT = ELEM == kBF16 ? 1u : 0u;
+  static constexpr uint32_t IDESC_QK = instr_desc(FMT, FMT, 0, 0, 128, kBN);
+  static constexpr uint32_t IDESC_PV = instr_desc(FMT, FMT, 0, 1, 128, SLOT_D);
+  static constexpr int OFF_Q = 0;
+  static constexpr int OFF_RING = Q_BYTES;
+  static constexpr int OFF_EPI = OFF_RING + NS * SLOT_BYTES;
+  static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
+  static_assert(OFF_EPI % 1024 == 0 && OFF_BAR % 1024 == 0, "1024-byte swizzle atoms");
+  static constexpr int SMEM_BYTES = OFF_BAR + 1024 + 1024;  // + barriers + alignment slack
+  static_assert(SMEM_BYTES <= kSmemLimit, "shared memory budget");
+};
+
+struct WinParams {
+  void* o;            // dense [BH, N, D]; paged [T, Hq, D]
+  float* lse;         // dense [BH, N]; paged [T, Hq]
+  int* err;           // device error word
+  int window, sinks;  // both at most 2^30
+  float scale_log2;   // scale * log2(e), never zero
+  int Hq, Hkv;
+  int o_vec32;        // o is 32-byte aligned
+  int drop_pos;       // test hook: ring position CTA 0 never fills (-1: none)
+  // dense
+  int N, Nk;          // query rows / keys per head
+  int BH;             // batch x query heads
+  int head_chunk;     // heads taken together, heaviest units first (see attn_fwd.cuh)
+  // paged
+  const int* cu_q;    // [B + 1] first token of each sequence in q
+  const int* seq_k;   // [B] keys per sequence, the new tokens' included
+  const int* table;   // [B, table_stride] page of each run of page_size keys
+  int B, T;
+  int max_pages;      // table entries per sequence
+  long long table_stride;
+  int num_pages, page_shift;
+  int g;              // query heads per key/value head
+  int tpt;            // tokens per query tile (tpt * g <= 128)
+  int min_tiles;      // a CTA's run of the line is at least this long
+  float* o_part;      // [2 * grid][NQT * 128][D] partial results of cut units
+  float* lse_part;    // [2 * grid][NQT * 128]
+  int4* desc;         // [grid] cut units: {parts, first token, kv head, rows}
+};
+
+// The key tiles that a unit of up to two query tiles visits.
+struct WinTiles {
+  int ns, skip;       // list index l is tile l (l < ns) or l + skip
+  int len;            // list length
+  int sa[2], la[2], lb[2];  // query tile t takes part in l < sa[t] and in la[t] <= l < lb[t]
+};
+
+// Visited tiles of a query tile whose valid rows sit at positions first ..
+// last (last <= nk - 1): window tiles [w0, w1), sink tiles [0, sk).
+__host__ __device__ __forceinline__ void win_range(int first, int last, int window, int sinks, int& w0, int& w1,
+                                                   int& sk) {
+  w1 = last < 0 ? 0 : last / kBN + 1;
+  const int lo = first - window + 1;
+  w0 = lo > 0 ? lo / kBN : 0;
+  if (w0 > w1) w0 = w1;
+  sk = (sinks + kBN - 1) / kBN;
+  if (sk > w1) sk = w1;
+}
+
+// p0: position of the unit's first token; ntok: its valid tokens, tpt to a query tile.
+__host__ __device__ __forceinline__ WinTiles win_tiles(int p0, int ntok, int tpt, int nqt, int window, int sinks) {
+  WinTiles u;
+  int w0[2] = {0, 0}, w1[2] = {0, 0}, sk[2] = {0, 0};
+  const int n0 = ntok < tpt ? ntok : tpt;
+  win_range(p0, p0 + n0 - 1, window, sinks, w0[0], w1[0], sk[0]);
+  const bool two = nqt == 2 && ntok > tpt;
+  if (two) win_range(p0 + tpt, p0 + ntok - 1, window, sinks, w0[1], w1[1], sk[1]);
+  const int top = two ? w1[1] : w1[0];
+  u.ns = two ? sk[1] : sk[0];
+  u.skip = w0[0] > u.ns ? w0[0] - u.ns : 0;
+  u.len = top - u.skip;
+  for (int t = 0; t < 2; ++t) {
+    auto index = [&](int x) { return x <= u.ns ? x : (x - u.skip > u.ns ? x - u.skip : u.ns); };
+    u.sa[t] = sk[t];
+    u.la[t] = index(w0[t]) > sk[t] ? index(w0[t]) : sk[t];
+    u.lb[t] = index(w1[t]) > u.la[t] ? index(w1[t]) : u.la[t];
+  }
+  return u;
+}
+
+// One unit as the load warp hands it to the other roles.
+struct alignas(16) WinUnit {
+  int kz;       // key/value coordinate (dense: batch * Hkv + head; paged: head); -1: no more units
+  int qz;       // query coordinate (dense: batch * Hq + head; paged: first token in q)
+  int q_row;    // dense: first row
+  int p0;       // position of the first token
+  int ntok;     // valid tokens (dense: rows) of the unit
+  int nk;       // keys of the sequence
+  int ns, skip;
+  int r0, r1;   // the run of list indices to do
+  int sa[2], la[2], lb[2];
+  int part;     // -1: whole unit, written to o; else the partial slot
+  int lo;       // keys in [sinks, lo) are visible to no query of the unit
+  int pad[2];
+};
+static_assert(sizeof(WinUnit) == 80, "WinUnit is copied in 16-byte pieces");
+
+// The list indices of one query tile.  (Selected rather than indexed: t is a
+// run-time value in the softmax warps, and the unit stays in registers.)
+struct WinPart {
+  int sa, la, lb;
+  __device__ __forceinline__ WinPart(const WinUnit& w, int t)
+      : sa(t ? w.sa[1] : w.sa[0]), la(t ? w.la[1] : w.la[0]), lb(t ? w.lb[1] : w.lb[0]) {}
+  __device__ __forceinline__ bool has(int l) const { return l < sa || (l >= la && l < lb); }
+  __device__ __forceinline__ int count(int r0, int r1) const {  // of [r0, r1)
+    return max(0, min(r1, sa) - r0) + max(0, min(r1, lb) - max(r0, la));
+  }
+};
+__device__ __forceinline__ bool win_active(const WinUnit& w, int t, int l) { return WinPart(w, t).has(l); }
+__device__ __forceinline__ int win_count(const WinUnit& w, int t) { return WinPart(w, t).count(w.r0, w.r1); }
+
+template <int NS>
+struct WinBars {
+  uint64_t q_full, q_empty;
+  uint64_t full[NS], empty[NS];
+  uint64_t s_full[2];
+  uint64_t p_full[2][2];   // [S/P buffer][half of the key tile]
+  uint64_t o_ready[2];
+  uint64_t o_full[2];
+  uint64_t drain, clc_bar;
+  uint64_t unit_full[2], unit_empty[2];
+  alignas(16) uint32_t clc_resp[4];
+  WinUnit unit[2];
+  // the line of work (paged): per-warp sums, then where this CTA's run starts
+  long long warp_sum[12];
+  long long start_off;
+  int start_b;
+  uint32_t tmem_base;
+  int abort_flag;
+};
+
+// One sequence of the ragged batch.  Values that would lead out of range
+// (they are device data, so the host cannot refuse them) are cut to what
+// exists; *bad is then set.
+struct WinSeq {
+  int tok0, nq, nk;
+};
+__device__ __forceinline__ WinSeq win_seq(const WinParams& prm, int b, bool* bad) {
+  WinSeq s;
+  const int a = prm.cu_q[b], e = prm.cu_q[b + 1], n = prm.seq_k[b];
+  s.tok0 = min(max(a, 0), prm.T);
+  const int end = min(max(e, s.tok0), prm.T);
+  s.nq = end - s.tok0;
+  const long long cap = (long long)prm.max_pages << prm.page_shift;
+  s.nk = (long long)n > cap ? (int)cap : (n < 0 ? 0 : n);
+  if (s.nk > (1 << 30)) s.nk = 1 << 30;
+  if (s.tok0 != a || end != e || s.nk != n) *bad = true;
+  return s;
+}
+// Key tiles of query group i (at least 1, so that a group without visible
+// keys still has its place on the line and gets its zero rows written).
+__device__ __forceinline__ int win_group_len(const WinParams& prm, const WinSeq& s, int tpg, int i) {
+  const int first = s.nk - s.nq + i * tpg;
+  const int last = min(first + tpg, s.nk) - 1;
+  int w0, w1, sk;
+  win_range(first, last, prm.window, prm.sinks, w0, w1, sk);
+  const int len = w1 - max(0, w0 - sk);
+  return len > 0 ? len : 1;
+}
+
+// bits [0, n) of a 32-bit word, n clamped to 0..32
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : (0xffffffffu >> (32 - (n < 32 ? n : 32)));
+}
+
+template <int ELEM, int D, bool PAGED>
+__global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
+    attn_window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                       const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
+                       const WinParams prm) {
+  using C = WinCfg<ELEM, D, PAGED>;
+  using Bars = WinBars<C::NS>;
+  static_assert(sizeof(Bars) <= 1024, "barrier area");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
+  volatile int* abort_flag = &bars->abort_flag;
+
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  const int g = PAGED ? prm.g : 1;
+  const int tpt = PAGED ? prm.tpt : kBM;   // tokens per query tile
+  const int rpt = tpt * g;                 // rows per query tile
+  const int tpg = C::NQT * tpt;            // tokens per unit
+
+  if (threadIdx.x == 0) {
+    mbar_init(&bars->q_full, 1);
+    mbar_init(&bars->q_empty, 1);
+    for (int s = 0; s < C::NS; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&bars->s_full[t], 1);
+      mbar_init(&bars->p_full[t][0], 128);
+      mbar_init(&bars->p_full[t][1], 128);
+      mbar_init(&bars->o_ready[t], 1);
+      mbar_init(&bars->o_full[t], 1);
+      mbar_init(&bars->unit_full[t], 1);
+      mbar_init(&bars->unit_empty[t], 1 + C::SOFTMAX_WARPS);
+    }
+    mbar_init(&bars->drain, 1);
+    mbar_init(&bars->clc_bar, 1);
+    bars->abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == C::MMA_WARP) {
+    tmem_alloc(&bars->tmem_base, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+
+  // paged: this CTA's run [line0, line0 + line_n) of the line of key tiles
+  long long line_per = 0, line0 = 0, line_n = 0;
+  if constexpr (PAGED) {
+    // rows of a query tile that no TMA box covers (128 % g != 0) are zeros
+    if (rpt < kBM) {
+      for (int i = threadIdx.x; i < C::NQT * C::NCH * (kBM - rpt) * 8; i += C::THREADS) {
+        const int c = i / ((kBM - rpt) * 8), x = i % ((kBM - rpt) * 8);
+        *reinterpret_cast<uint4*>(smem + C::OFF_Q + c * C::CHUNK_BYTES + rpt * 128 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      fence_proxy_async_smem();
+    }
+    if (threadIdx.x == 0) prm.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    // each thread sums the key tiles of a contiguous share of the sequences
+    bool bad = false;
+    const int share = (prm.B + C::THREADS - 1) / C::THREADS;
+    const int b0 = min(prm.B, (int)threadIdx.x * share), b1 = min(prm.B, b0 + share);
+    auto seq_len = [&](int b) -> long long {
+      const WinSeq s = win_seq(prm, b, &bad);
+      long long n = 0;
+      for (int i = 0; i * tpg < s.nq; ++i) n += win_group_len(prm, s, tpg, i);
+      return n * prm.Hkv;
+    };
+    long long mine = 0;
+    for (int b = b0; b < b1; ++b) mine += seq_len(b);
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += x;
+    }
+    if (lane == 31) bars->warp_sum[warp] = incl;
+    __syncthreads();
+    long long before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < C::THREADS / 32; ++w) {
+      const long long x = bars->warp_sum[w];
+      if (w < warp) before += x;
+      total += x;
+    }
+    line_per = (total + gridDim.x - 1) / gridDim.x;
+    if (line_per < prm.min_tiles) line_per = prm.min_tiles;
+    line0 = line_per * blockIdx.x;
+    line_n = total - line0 < line_per ? total - line0 : line_per;
+    long long at = before + incl - mine;
+    if (line0 >= at && line0 < at + mine) {
+      int b = b0;
+      for (; b < b1; ++b) {
+        const long long n = seq_len(b);
+        if (line0 < at + n) break;
+        at += n;
+      }
+      bars->start_b = b;
+      bars->start_off = line0 - at;
+    }
+    if (bad && blockIdx.x == 0) atomicOr(prm.err, FA_DEVERR_INDEX);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+
+  // Unit number r of this CTA from the queue; the slot is released by one
+  // lane per consuming warp.
+  auto fetch_unit = [&](int r, bool arrive, bool& okr) -> WinUnit {
+    const int slot = r & 1;
+    okr = mbar_wait(&bars->unit_full[slot], (uint32_t)((r >> 1) & 1), abort_flag, prm.err);
+    WinUnit w = bars->unit[slot];
+    if (!okr) w.kz = -1;
+    __syncwarp();  // every lane has read the slot before one of them releases it
+    if (arrive) mbar_arrive(&bars->unit_empty[slot]);
+    return w;
+  };
+
+  if (warp >= C::SOFTMAX_WARPS) {
+    if constexpr (C::REALLOC) regs_dec<C::CTRL_REGS>();
+    if (warp == C::LOAD_WARP) {
+      // ---------------------------------------------------------- load --
+      // The whole warp runs the loop; lane 0 waits, arms barriers and
+      // publishes units; paged boxes are issued one per lane.
+      if (lane == 0) {
+        tma_prefetch_desc(&tm_q);
+        tma_prefetch_desc(&tm_k);
+        tma_prefetch_desc(&tm_v);
+      }
+      const uint64_t pol_kv = policy_evict_last();
+      const uint64_t pol_q = policy_evict_first();
+      int pos = 0;    // ring position (continues across units)
+      int k = 0;      // units with keys loaded by this CTA
+      bool ok = true;
+      // publish unit r (w.kz < 0: no more units)
+      auto publish = [&](int r, const WinUnit& w) -> bool {
+        bool good = true;
+        if (lane == 0) {
+          const int slot = r & 1;
+          if (r >= 2) good = mbar_wait(&bars->unit_empty[slot], (uint32_t)(((r - 2) >> 1) & 1), abort_flag, prm.err);
+          if (good) {
+            bars->unit[slot] = w;
+            mbar_arrive(&bars->unit_full[slot]);
+          }
+        }
+        return __shfl_sync(0xffffffffu, (int)good, 0) != 0;
+      };
+      // page numbers of list index l: lane i holds that of box i (-1: read as zeros)
+      const int page_rows = PAGED ? 1 << prm.page_shift : 0;
+      const int box_rows = page_rows < kBN ? page_rows : kBN;
+      const int nbox = PAGED ? kBN / box_rows : 1;
+      auto pages_of = [&](const WinUnit& w, const int* table, int l) -> int {
+        int id = -1;
+        if (PAGED && lane < nbox && l < w.r1) {
+          const int tile = l < w.ns ? l : l + w.skip;
+          const int key = tile * kBN + lane * box_rows;
+          if (key < w.nk && (key < prm.sinks || key + box_rows > w.lo)) {
+            id = table[key >> prm.page_shift];
+            if ((unsigned)id >= (unsigned)prm.num_pages) {
+              atomicOr(prm.err, FA_DEVERR_INDEX);
+              id = -1;
+            }
+          }
+        }
+        return id;
+      };
+      // one K or V tile (SPT ring slots) into the ring
+      auto load_tile = [&](const WinUnit& w, bool is_v, int l, int ids) {
+        const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+        const int key0 = (l < w.ns ? l : l + w.skip) * kBN;
+        for (int sp = 0; sp < C::SPT && ok; ++sp, ++pos) {
+          const int slot = pos % C::NS;
+          const uint32_t ph = (uint32_t)((pos / C::NS) & 1);
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[slot], ph ^ 1u, abort_flag, prm.err));
+          if (!ok) break;
+          // failure-injection hook (tests only): this slot is never filled,
+          // so the MMA warp's wait on it runs out and the kernel aborts
+          if (pos == prm.drop_pos && blockIdx.x == 0) continue;
+          uint8_t* dst = smem + C::OFF_RING + slot * C::SLOT_BYTES;
+          if (lane == 0) mbar_arrive_expect_tx(&bars->full[slot], C::SLOT_BYTES);
+          __syncwarp();
+          if constexpr (PAGED) {
+            const int box = lane % nbox, ch = lane / nbox;
+            const int id = __shfl_sync(0xffffffffu, ids, box);
+            if (ch < C::SLOT_CH)
+              tma_load_4d_hint(dst + ch * C::CHUNK_BYTES + box * box_rows * 128, map, &bars->full[slot],
+                               (sp * C::SLOT_CH + ch) * C::CH_ELEMS, (key0 + box * box_rows) & (page_rows - 1), w.kz, id,
+                               pol_kv);
+          } else if (lane < C::SLOT_CH) {
+            tma_load_3d_hint(dst + lane * C::CHUNK_BYTES, map, &bars->full[slot],
+                             (sp * C::SLOT_CH + lane) * C::CH_ELEMS, key0, w.kz, pol_kv);
+          }
+        }
+      };
+      // Q tiles and every key/value tile of a unit
+      auto load_unit = [&](const WinUnit& w, const int* table) {
+        if (w.r1 <= w.r0) return;  // no visible key: nothing to load
+        int ids = pages_of(w, table, w.r0), ids1 = pages_of(w, table, w.r0 + 1), ids2 = -1;
+        const int n0 = win_count(w, 0), n1 = C::NQT == 2 ? win_count(w, 1) : 0;
+        // the Q buffer is free once the previous unit's last Q K^T finished
+        if (k > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (uint32_t)((k - 1) & 1), abort_flag, prm.err));
+        if (!ok) return;
+        if (lane == 0) {
+          const uint32_t tile = (uint32_t)(rpt * C::ROW_BYTES);
+          mbar_arrive_expect_tx(&bars->q_full, (n0 > 0 ? tile : 0u) + (n1 > 0 ? tile : 0u));
+          for (int t = 0; t < C::NQT; ++t) {
+            if ((t == 0 ? n0 : n1) == 0) continue;
+            for (int ch = 0; ch < C::NCH; ++ch) {
+              uint8_t* dst = smem + C::OFF_Q + (t * C::NCH + ch) * C::CHUNK_BYTES;
+              if constexpr (PAGED)
+                tma_load_3d_hint(dst, &tm_q, &bars->q_full, ch * C::CH_ELEMS, w.kz * g, w.qz + t * tpt, pol_q);
+              else
+                tma_load_3d_hint(dst, &tm_q, &bars->q_full, ch * C::CH_ELEMS, w.q_row + t * kBM, w.qz, pol_q);
+            }
+          }
+        }
+        __syncwarp();
+        if constexpr (C::NQT == 2) {
+          // K0 V0 K1 V1 ...
+          for (int l = w.r0; l < w.r1 && ok; ++l) {
+            ids2 = pages_of(w, table, l + 2);  // two tiles ahead: its latency hides behind the loads
+            load_tile(w, false, l, ids);
+            load_tile(w, true, l, ids);
+            ids = ids1;
+            ids1 = ids2;
+          }
+        } else {
+          // K0 K1 V0 K2 V1 K3 V2 ...
+          load_tile(w, false, w.r0, ids);
+          if (w.r0 + 1 < w.r1) load_tile(w, false, w.r0 + 1, ids1);
+          for (int l = w.r0; l < w.r1 && ok; ++l) {
+            ids2 = pages_of(w, table, l + 2);
+            load_tile(w, true, l, ids);
+            if (l + 2 < w.r1) load_tile(w, false, l + 2, ids2);
+            ids = ids1;
+            ids1 = ids2;
+          }
+        }
+        ++k;
+      };
+      WinUnit w;
+      auto take_tiles = [&](const WinTiles& u) {
+        w.ns = u.ns;
+        w.skip = u.skip;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          w.sa[t] = u.sa[t];
+          w.la[t] = u.la[t];
+          w.lb[t] = u.lb[t];
+        }
+      };
+      w.pad[0] = w.pad[1] = 0;
+      if constexpr (PAGED) {
+        int r = 0;
+        if (line_n > 0) {
+          long long rem = line_n, at = line0;
+          int b = bars->start_b, i = 0;
+          long long off = bars->start_off;
+          bool bad = false;
+          WinSeq s = win_seq(prm, b, &bad);
+          int len = win_group_len(prm, s, tpg, 0);
+          while (off >= (long long)len * prm.Hkv) {
+            off -= (long long)len * prm.Hkv;
+            len = win_group_len(prm, s, tpg, ++i);
+          }
+          int head = (int)(off / len), r0 = (int)(off % len);
+          while (ok && rem > 0) {
+            const int run = (int)(rem < len - r0 ? rem : len - r0);
+            w.kz = head;
+            w.q_row = i * tpg;
+            w.qz = s.tok0 + w.q_row;
+            w.p0 = s.nk - s.nq + w.q_row;
+            w.ntok = min(tpg, s.nq - w.q_row);
+            w.nk = s.nk;
+            w.lo = max(0, w.p0 - prm.window + 1);
+            const WinTiles u = win_tiles(w.p0, w.ntok, tpt, C::NQT, prm.window, prm.sinks);
+            take_tiles(u);
+            w.r0 = r0;
+            w.r1 = min(u.len, r0 + run);  // (len counts a unit without keys as one tile)
+            w.part = (r0 == 0 && run == len) ? -1 : 2 * (int)blockIdx.x + (r0 > 0 ? 0 : 1);
+            if (r0 == 0 && run < len && lane == 0) {
+              const long long last = (at + len - 1) / line_per;  // CTA that holds the unit's last tile
+              prm.desc[blockIdx.x] = make_int4((int)(last - blockIdx.x) + 1, w.qz, head, w.ntok * g);
+            }
+            ok = publish(r++, w);
+            if (ok) load_unit(w, prm.table + (long long)b * prm.table_stride);
+            rem -= run;
+            at += run;
+            if (rem == 0) break;
+            r0 = 0;
+            if (++head == prm.Hkv) {
+              head = 0;
+              if (++i * tpg >= s.nq) {
+                i = 0;
+                do {
+                  s = win_seq(prm, ++b, &bad);
+                } while (s.nq == 0 && b + 1 < prm.B);
+              }
+              len = win_group_len(prm, s, tpg, i);
+            }
+          }
+        }
+        w.kz = -1;
+        if (ok) publish(r, w);
+      } else {
+        // dense: one unit per launched CTA, heaviest first within chunks of
+        // heads; a CTA about to finish takes over the next CTA that has not
+        // started (cluster launch control), so its loads overlap the tail
+        const int n_groups = (prm.N + tpg - 1) / tpg;
+        const int units = prm.BH * n_groups;
+        const int qgroup = prm.Hq / prm.Hkv;
+        int n_req = 0;
+        bool more = true;
+        auto decode = [&](int v) {
+          const int per_chunk = prm.head_chunk * n_groups;
+          const int c = v / per_chunk;
+          const int idx = v - c * per_chunk;
+          const int heads_here = min(prm.head_chunk, prm.BH - c * prm.head_chunk);
+          const int bh = c * prm.head_chunk + idx % heads_here;
+          w.q_row = (n_groups - 1 - idx / heads_here) * tpg;
+          w.qz = bh;
+          w.kz = (bh / prm.Hq) * prm.Hkv + (bh % prm.Hq) / qgroup;
+          w.p0 = w.q_row + prm.Nk - prm.N;
+          w.ntok = min(tpg, prm.N - w.q_row);
+          w.nk = prm.Nk;
+          w.lo = max(0, w.p0 - prm.window + 1);
+          const WinTiles u = win_tiles(w.p0, w.ntok, tpt, C::NQT, prm.window, prm.sinks);
+          take_tiles(u);
+          w.r0 = 0;
+          w.r1 = u.len;
+          w.part = -1;
+        };
+        int u = (int)blockIdx.x;
+        decode(u);
+        ok = publish(0, w);
+        for (int r = 0; ok; ++r) {
+          load_unit(w, nullptr);
+          if (!ok) break;
+          int nu = -1;
+          if (more) {
+            if (lane == 0) {
+              mbar_arrive_expect_tx(&bars->clc_bar, 16);
+              clc_try_cancel(bars->clc_resp, &bars->clc_bar);
+            }
+            __syncwarp();
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->clc_bar, (uint32_t)(n_req & 1), abort_flag, prm.err));
+            if (!ok) break;
+            ++n_req;
+            nu = clc_query_x(bars->clc_resp);
+            if (nu < 0 || nu >= units) {
+              nu = -1;
+              more = false;
+            }
+            __syncwarp();  // the response is read by every lane before it is asked for again
+          }
+          if (nu >= 0) decode(nu);
+          else w.kz = -1;
+          if (!publish(r + 1, w)) ok = false;
+          if (nu < 0) break;
+        }
+      }
+      // never leave with copies in flight: the last fill of every used slot
+      // and the last Q tiles
+      const int used = pos < C::NS ? pos : C::NS;
+      for (int i = 0; i < used; ++i) {
+        const int p_last = pos - 1 - i;
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(&bars->full[p_last % C::NS], (uint32_t)((p_last / C::NS) & 1)) &&
+               globaltimer() - t0 < FA_WAIT_LIMIT_NS) {
+        }
+      }
+      if (k > 0) {
+        const uint64_t t0 = globaltimer();
+        while (!mbar_try_wait(&bars->q_full, (uint32_t)((k - 1) & 1)) && globaltimer() - t0 < FA_WAIT_LIMIT_NS) {
+        }
+      }
+      __syncwarp();
+    } else if (warp == C::MMA_WARP) {
+      // ----------------------------------------------------------- MMA --
+      // warp-converged issue; elect.sync picks the issuing lane
+      const uint32_t q_s = smem_u32(smem + C::OFF_Q);
+      const uint32_t ring_s = smem_u32(smem + C::OFF_RING);
+      int pos = 0;          // ring position of the next tile to consume
+      int k = 0;            // units with keys processed
+      int pc[2] = {0, 0};   // two query tiles: P handshakes consumed per tile
+      int it = 0;           // one query tile: S/P iterations so far (buffer = it & 1)
+      bool ok = true;
+      auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, prm.err));
+      };
+      auto wait_tile = [&](int p) -> bool {
+        for (int sp = 0; sp < C::SPT; ++sp)
+          if (!warp_wait(&bars->full[(p + sp) % C::NS], (uint32_t)(((p + sp) / C::NS) & 1))) return false;
+        tc_fence_after();
+        return true;
+      };
+      auto release_tile = [&](int p) {
+        for (int sp = 0; sp < C::SPT; ++sp) mma_commit_elect(&bars->empty[(p + sp) % C::NS]);
+      };
+      const uint64_t q_desc0 = smem_desc(q_s, 16, 1024, 2);                      // Q tiles, K-major
+      const uint64_t ring_k_desc0 = smem_desc(ring_s, 16, 1024, 2);              // K slots, K-major
+      const uint64_t ring_v_desc0 = smem_desc(ring_s, C::CHUNK_BYTES, 1024, 2);  // V slots, MN-major
+      auto slot_off = [&](int p) -> uint32_t { return (uint32_t)(p % C::NS) * C::SLOT_BYTES; };
+      // S_buf = Q_t K^T for the K tile at ring position p
+      auto issue_qk = [&](int t, int buf, int p) {
+        const uint64_t a0 = q_desc0 + (uint64_t)((t * C::NCH * C::CHUNK_BYTES) >> 4);
+        uint64_t b0[C::SPT];
+#pragma unroll
+        for (int sp = 0; sp < C::SPT; ++sp) b0[sp] = ring_k_desc0 + (uint64_t)(slot_off(p + sp) >> 4);
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const int ch = ks / 4, in_ch = (ks % 4) * 32;
+          const uint64_t a = a0 + (uint64_t)((ch * C::CHUNK_BYTES + in_ch) >> 4);
+          const uint64_t b = b0[ch / C::SLOT_CH] + (uint64_t)(((ch % C::SLOT_CH) * C::CHUNK_BYTES + in_ch) >> 4);
+          mma_ss_elect<0>(tmem + buf * kBN, a, b, C::IDESC_QK, ks > 0 ? 1u : 0u);
+        }
+      };
+      // O_t (+)= P_buf V for half h of the keys of the V tile at ring position p
+      auto issue_pv = [&](int t, int buf, int p, bool acc, int h) {
+#pragma unroll
+        for (int sp = 0; sp < C::SPT; ++sp) {
+          const uint32_t d_tmem = tmem + C::O_COL0 + t * D + sp * C::SLOT_D;
+          const uint64_t v0 = ring_v_desc0 + (uint64_t)(slot_off(p + sp) >> 4);
+#pragma unroll
+          for (int ks = h * 4; ks < h * 4 + 4; ++ks)
+            mma_ts_elect<0>(d_tmem, tmem + buf * kBN + ks * 8, v0 + (uint64_t)((ks * 2048) >> 4), C::IDESC_PV,
+                            (acc || ks > 0) ? 1u : 0u);
+        }
+      };
+      for (int r = 0; ok; ++r) {
+        const WinUnit w = fetch_unit(r, lane == 0, ok);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok || w.kz < 0) break;
+        if (w.r1 <= w.r0) continue;
+        ok = warp_wait(&bars->q_full, (uint32_t)(k & 1));
+        if (!ok) break;
+        tc_fence_after();
+        const int n0 = win_count(w, 0), n1 = C::NQT == 2 ? win_count(w, 1) : 0;
+        int qk_left = n0 + n1;
+        auto qk_issued = [&]() {
+          if (--qk_left == 0) mma_commit_elect(&bars->q_empty);  // the unit's Q has been read
+        };
+        if constexpr (C::NQT == 2) {
+          int left[2] = {n0, n1};
+          bool begun[2] = {false, false};
+          ok = wait_tile(pos);
+          if (!ok) break;
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+            if (win_active(w, t, w.r0)) {
+              issue_qk(t, t, pos);
+              mma_commit_elect(&bars->s_full[t]);
+              qk_issued();
+            }
+          release_tile(pos);
+          pos += C::SPT;
+          for (int l = w.r0; l < w.r1 && ok; ++l) {
+            const int pv_pos = pos, k_pos = pos + C::SPT;  // V_l, K_{l+1}
+            const bool more = l + 1 < w.r1;
+            bool v_ready = false, k_ready = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (!ok) break;
+              if (win_active(w, t, l)) {
+                if (!v_ready) {
+                  ok = wait_tile(pv_pos);
+                  v_ready = true;
+                  if (!ok) break;
+                }
+#pragma unroll
+                for (int h = 0; h < 2 && ok; ++h) {
+                  ok = warp_wait(&bars->p_full[t][h], (uint32_t)(pc[t] & 1));
+                  if (!ok) break;
+                  tc_fence_after();
+                  issue_pv(t, t, pv_pos, begun[t], h);
+                }
+                if (!ok) break;
+                ++pc[t];
+                begun[t] = true;
+                if (--left[t] == 0) mma_commit_elect(&bars->o_full[t]);
+              }
+              if (more && win_active(w, t, l + 1)) {
+                if (!k_ready) {
+                  ok = wait_tile(k_pos);
+                  k_ready = true;
+                  if (!ok) break;
+                }
+                issue_qk(t, t, k_pos);
+                mma_commit_elect(&bars->s_full[t]);
+                qk_issued();
+              }
+            }
+            if (!ok) break;
+            // (every list index has a query tile that takes part in it)
+            release_tile(pv_pos);
+            pos += C::SPT;
+            if (more) {
+              release_tile(k_pos);
+              pos += C::SPT;
+            }
+          }
+        } else {
+          // one query tile, S double-buffered: S(0), S(1), then PV(j), S(j+2)
+          const int n = w.r1 - w.r0;
+          for (int j = 0; j < 2 && j < n && ok; ++j) {
+            ok = wait_tile(pos);
+            if (!ok) break;
+            issue_qk(0, (it + j) & 1, pos);
+            mma_commit_elect(&bars->s_full[(it + j) & 1]);
+            qk_issued();
+            release_tile(pos);
+            pos += C::SPT;
+          }
+          for (int j = 0; j < n && ok; ++j) {
+            const int x = it + j, b = x & 1;
+            ok = wait_tile(pos);  // V_j
+            if (!ok) break;
+#pragma unroll
+            for (int h = 0; h < 2 && ok; ++h) {
+              ok = warp_wait(&bars->p_full[b][h], (uint32_t)((x >> 1) & 1));
+              if (!ok) break;
+              tc_fence_after();
+              issue_pv(0, b, pos, j > 0, h);
+            }
+            if (!ok) break;
+            mma_commit_elect(&bars->o_ready[b]);
+            release_tile(pos);
+            pos += C::SPT;
+            if (j + 2 < n) {
+              ok = wait_tile(pos);  // K_{j+2}
+              if (!ok) break;
+              issue_qk(0, b, pos);
+              mma_commit_elect(&bars->s_full[b]);
+              qk_issued();
+              release_tile(pos);
+              pos += C::SPT;
+            }
+          }
+          if (ok) mma_commit_elect(&bars->o_full[0]);
+          it += n;
+        }
+        ++k;
+      }
+      // every MMA issued here has completed before TMEM is freed
+      mma_commit_elect(&bars->drain);
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(&bars->drain, 0) && globaltimer() - t0 < FA_WAIT_LIMIT_NS) {
+      }
+      __syncwarp();
+    }
+  } else {
+    // ------------------------------------------------------- softmax --
+    if constexpr (C::REALLOC) regs_inc<C::SOFTMAX_REGS>();
+    const int t = warp / 4;                  // query tile of this warp
+    const int wq = warp % 4;                 // TMEM lane quarter
+    const int r_in = wq * 32 + lane;         // row within the tile, and key row of a V tile
+    const uint32_t lane_addr = (uint32_t)(wq * 32) << 16;
+    const bool neg = prm.scale_log2 < 0.0f;
+    const float mask_val = neg ? INFINITY : -INFINITY;
+    const float cj = prm.scale_log2;
+    int sc = 0;        // two query tiles: S handshakes consumed (this tile)
+    int it = 0;        // one query tile: iterations so far
+    int oc = 0;        // o_full phases consumed
+    int pv_seen = 0;   // one query tile: P V completions consumed
+    int ring = 0;      // ring position of the unit's first tile
+    bool ok = true;
+
+    for (int rr = 0; ok; ++rr) {
+      bool okr = true;
+      const WinUnit w = fetch_unit(rr, lane == 0, okr);
+      ok = __all_sync(0xffffffffu, okr);
+      if (!ok || w.kz < 0) break;
+      const int nrun = w.r1 > w.r0 ? w.r1 - w.r0 : 0;
+      const int ring0 = ring;
+      ring += 2 * nrun * C::SPT;
+      do {  // one unit (skipped when this tile has no valid row)
+        const int rows = min(rpt, (w.ntok - t * tpt) * g);  // valid rows of this tile
+        if (rows <= 0) break;
+        const bool valid = r_in < rows;
+        const int tok = t * tpt + (PAGED ? r_in / g : r_in);   // token within the unit
+        // where this row's results go
+        size_t out_row = 0;
+        if (valid) {
+          if (w.part >= 0) out_row = (size_t)w.part * (C::NQT * kBM) + t * rpt + r_in;
+          else if (PAGED) out_row = (size_t)(w.qz + tok) * prm.Hq + w.kz * g + r_in % g;
+          else out_row = (size_t)w.qz * prm.N + w.q_row + tok;
+        }
+        const WinPart mine(w, t);
+        const int n = C::NQT == 2 ? mine.count(w.r0, w.r1) : nrun;
+        if (n == 0) {
+          // no row of this tile sees a key of this run: O = 0, LSE = -inf
+          if (valid) {
+            if (w.part >= 0) {
+              float4* dst = reinterpret_cast<float4*>(prm.o_part + out_row * D);
+#pragma unroll 1
+              for (int i = 0; i < D / 4; ++i) dst[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              prm.lse_part[out_row] = -INFINITY;
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(prm.o) + out_row * D * 2);
+#pragma unroll 1
+              for (int i = 0; i < D / 8; ++i) dst[i] = make_uint4(0u, 0u, 0u, 0u);
+              prm.lse[out_row] = -INFINITY;
+            }
+          }
+          break;
+        }
+        // this row's last and first (window) visible key; the tile's strictest ones
+        const int last = min(w.p0 + tok, w.nk - 1);
+        const int lo = w.p0 + tok - prm.window + 1;
+        const int tile_last = w.p0 + t * tpt;                              // of its first row
+        const int tile_lo = w.p0 + t * tpt + (rows - 1) / g - prm.window + 1;  // of its last row
+        float m_run = -INFINITY;  // reference maximum, log2 units
+        float l_run = 0.0f;
+        // one query tile: consume o_ready completions up to the P V of
+        // iteration x (they complete in order)
+        auto consume_o = [&](int x) -> bool {
+          while (pv_seen <= x) {
+            if (!__all_sync(0xffffffffu, mbar_wait(&bars->o_ready[pv_seen & 1], (uint32_t)((pv_seen >> 1) & 1),
+                                                   abort_flag, prm.err)))
+              return false;
+            ++pv_seen;
+          }
+          return true;
+        };
+        int j = 0;  // tiles done by this query tile
+        for (int l = w.r0; l < w.r1 && ok; ++l) {
+          if (C::NQT == 2 && !mine.has(l)) continue;
+          const int x = it + j;
+          const int buf = C::NQT == 2 ? t : (x & 1);
+          const uint32_t ph = C::NQT == 2 ? (uint32_t)(sc & 1) : (uint32_t)((x >> 1) & 1);
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], ph, abort_flag, prm.err));
+          ++sc;
+          if (!ok) break;
+          tc_fence_after();
+          if constexpr (C::NQT == 1) {
+            // P V(x-2) was issued before S(x): consume its o_ready phase to
+            // keep at most one pending per buffer
+            if (x >= 2 && !consume_o(x - 2)) {
+              ok = false;
+              break;
+            }
+          }
+          const uint32_t s_addr = tmem + lane_addr + buf * kBN;
+          const int col0 = (l < w.ns ? l : l + w.skip) * kBN;
+          const bool need_mask = col0 + kBN - 1 > tile_last || (col0 < tile_lo && col0 + kBN > prm.sinks);
+          float s[kBN];
+          {
+            uint32_t u[32];
+#pragma unroll
+            for (int c4 = 0; c4 < 4; ++c4) {
+              tmem_ld32(s_addr + c4 * 32, u);
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[c4 * 32 + i] = __uint_as_float(u[i]);
+            }
+            tmem_wait_ld();
+          }
+          if (need_mask) {
+            // visible columns of this row as four words: up to `last`, and
+            // from `lo` on or below `sinks`
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int c0 = col0 + 32 * q;
+              const uint32_t see = low_bits(last + 1 - c0) & (~low_bits(lo - c0) | low_bits(prm.sinks - c0));
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[32 * q + i] = (see & (1u << i)) ? s[32 * q + i] : mask_val;
+            }
+          }
+          // row maximum (minimum for a negative scale): eight chains of 3-input max
+          float mx, r8[8];
+          if (!neg) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r8[i] = fmaxf(s[i], s[8 + i]);
+#pragma unroll
+            for (int c = 16; c < kBN; c += 16)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) r8[i] = max3f(r8[i], s[c + i], s[c + 8 + i]);
+            mx = max3f(max3f(r8[0], r8[1], r8[2]), max3f(r8[3], r8[4], r8[5]), fmaxf(r8[6], r8[7]));
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r8[i] = fminf(s[i], s[8 + i]);
+#pragma unroll
+            for (int c = 16; c < kBN; c += 16)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) r8[i] = min3f(r8[i], s[c + i], s[c + 8 + i]);
+            mx = min3f(min3f(r8[0], r8[1], r8[2]), min3f(r8[3], r8[4], r8[5]), fminf(r8[6], r8[7]));
+          }
+          const float mx2 = mx * cj;  // (a row that sees no key of this tile: -inf)
+          float alpha = 1.0f;
+          const bool move = (mx2 > m_run + C::TAU) || (m_run == -INFINITY && mx2 != -INFINITY);
+          if (move) {
+            alpha = ex2(m_run - mx2);  // 0 on the row's first visible tile
+            m_run = mx2;
+          }
+          l_run *= alpha;
+          if (j > 0 && __any_sync(0xffffffffu, move)) {
+            if constexpr (C::NQT == 1) {
+              // O holds P V(x-1): wait for it
+              if (!consume_o(x - 1)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+            }
+            rescale_o_cols<D>(tmem + lane_addr + C::O_COL0 + t * D, alpha);
+          }
+          if constexpr (PAGED) {
+            // Rows of the V tile that no query of the unit may see can hold
+            // anything; P = 0 there would still give NaN from a NaN, so they
+            // become zeros before P is handed over.  Thread r clears key r;
+            // both query tiles do so (the writes are the same), each before
+            // its own P V.
+            const bool gap = w.lo > prm.sinks && col0 < w.lo && col0 + kBN > prm.sinks;
+            if (col0 + kBN > w.nk || gap) {
+              // (one query tile: the slot's previous fill may still be the V tile
+              // before, so that one's P V is waited for first; with two, K of
+              // this tile lies between)
+              if (C::NQT == 1 && j > 0 && !consume_o(x - 1)) {
+                ok = false;
+                break;
+              }
+              const int v_at = C::NQT == 2 ? 2 * (l - w.r0) + 1 : j + min(j + 2, n);
+              const int pv = ring0 + v_at * C::SPT;
+#pragma unroll
+              for (int sp = 0; sp < C::SPT; ++sp)
+                ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->full[(pv + sp) % C::NS],
+                                                             (uint32_t)(((pv + sp) / C::NS) & 1), abort_flag, prm.err));
+              if (!ok) break;
+              const int key = col0 + r_in;
+              if (key >= w.nk || (key < w.lo && key >= prm.sinks)) {
+#pragma unroll 1
+                for (int ch = 0; ch < C::NCH; ++ch) {
+                  const uint32_t row = smem_u32(smem + C::OFF_RING) + ((pv + ch / C::SLOT_CH) % C::NS) * C::SLOT_BYTES +
+                                       (ch % C::SLOT_CH) * C::CHUNK_BYTES + r_in * 128;
+#pragma unroll
+                  for (int i = 0; i < 8; ++i) st_shared_v4(row + 16 * i, 0u, 0u, 0u, 0u);
+                }
+              }
+              fence_proxy_async_smem();
+            }
+          }
+          // P = 2^(s*cj - m); a masked score gives 2^-inf = 0 (a row without
+          // a visible key yet takes 0 in place of -m)
+          const float2 cj2 = make_float2(cj, cj);
+          const float nm = m_run == -INFINITY ? 0.0f : -m_run;
+          const float2 nm2 = make_float2(nm, nm);
+          float2 acc[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[i] = make_float2(0.0f, 0.0f);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (q == 2) {
+              // keys 0..63 of P are in TMEM: let their MMAs start
+              tmem_wait_st();
+              tc_fence_before();
+              mbar_arrive(&bars->p_full[buf][0]);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t u[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const int c = q * 32 + h * 16 + 2 * i;
+                const float2 e = fma2(make_float2(s[c], s[c + 1]), cj2, nm2);
+                const float2 p = make_float2(ex2(e.x), ex2(e.y));
+                acc[i & 3] = add2(acc[i & 3], p);
+                u[i] = (ELEM == kBF16) ? pack_bf16x2(p.x, p.y) : pack_f16x2(p.x, p.y);
+              }
+              tmem_st8(s_addr + q * 16 + h * 8, u);
+            }
+          }
+          const float2 tt = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+          l_run += tt.x + tt.y;
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(&bars->p_full[buf][1]);
+          ++j;
+        }
+
+        // -------------------------------------------------------- epilogue --
+        if (!ok) break;
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[t], (uint32_t)(oc & 1), abort_flag, prm.err));
+        ++oc;
+        if (!ok) break;
+        tc_fence_after();
+        const float f = (l_run > 0.0f) ? (1.0f / l_run) : 0.0f;
+        const float lse_row = (m_run + lg2(l_run)) * 0.69314718055994530942f;
+        const uint32_t o_addr = tmem + lane_addr + C::O_COL0 + t * D;
+        if (w.part >= 0) {
+          // fp32 partial: O normalised over this run's keys and the run's LSE
+          float* prow = prm.o_part + out_row * D;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t u[32];
+            tmem_ld32(o_addr + c0, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] = __float_as_uint(__uint_as_float(u[i]) * f);
+            if (valid) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) st_global_v8(prow + c0 + 8 * i, u + 8 * i);
+            }
+          }
+          if (valid) prm.lse_part[out_row] = lse_row;
+        } else if constexpr (C::EPI_TMA) {
+          // this warp's 32 rows through its staging box, 64 columns at a time
+          // (128-byte swizzle: 16-byte chunk c of row `lane` at c ^ (lane % 8))
+          uint8_t* stg = smem + C::OFF_EPI + (t * 4 + wq) * C::EPI_WARP_BYTES;
+          const uint32_t my_row = smem_u32(stg) + (uint32_t)lane * 128u;
+          const int row0 = w.q_row + t * kBM + wq * 32;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 64) {
+            uint32_t u[32], u2[32], pk[32];
+            tmem_ld32(o_addr + c0, u);
+            tmem_ld32(o_addr + c0 + 32, u2);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float a = __uint_as_float(u[2 * i]) * f, b = __uint_as_float(u[2 * i + 1]) * f;
+              const float a2 = __uint_as_float(u2[2 * i]) * f, b2 = __uint_as_float(u2[2 * i + 1]) * f;
+              pk[i] = (ELEM == kFP16) ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+              pk[16 + i] = (ELEM == kFP16) ? pack_f16x2(a2, b2) : pack_bf16x2(a2, b2);
+            }
+            if (lane == 0) bulk_wait_read_all();  // the previous box has been read out of the buffer
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+              st_shared_v4(my_row + ((uint32_t)(c ^ (lane & 7)) << 4), pk[4 * c], pk[4 * c + 1], pk[4 * c + 2],
+                           pk[4 * c + 3]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0 && row0 < prm.N) {  // rows at or past N are outside the map and not written
+              tma_store_3d(&tm_o, stg, c0, row0, w.qz);
+              bulk_commit_group();
+            }
+          }
+          if (valid) prm.lse[out_row] = lse_row;
+        } else {
+          uint8_t* orow = reinterpret_cast<uint8_t*>(prm.o) + out_row * D * 2;
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t u[32], pk[16];
+            tmem_ld32(o_addr + c0, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const float a = __uint_as_float(u[2 * i]) * f, b = __uint_as_float(u[2 * i + 1]) * f;
+              pk[i] = (ELEM == kFP16) ? pack_f16x2(a, b) : pack_bf16x2(a, b);
+            }
+            if (valid) {
+              if (prm.o_vec32) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) st_global_v8(orow + c0 * 2 + 32 * i, pk + 8 * i);
+              } else {
+                uint4* dst = reinterpret_cast<uint4*>(orow + c0 * 2);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dst[i] = make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+              }
+            }
+          }
+          if (valid) prm.lse[out_row] = lse_row;
+        }
+        // this warp's reads of O are ordered before the next unit's S, which
+        // the MMA warp issues after this tile's next P arrives
+        tc_fence_before();
+      } while (0);
+      if constexpr (C::NQT == 1) it += nrun;
+    }
+  }
+  // the epilogue's bulk stores have completed before the CTA ends
+  if (C::EPI_TMA && warp < C::SOFTMAX_WARPS && lane == 0) bulk_wait_all();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == C::MMA_WARP) {
+    tc_fence_after();
+    tmem_dealloc(tmem, C::TMEM_COLS);
+  }
+}
+
+struct WinLaunch {
+  CUtensorMap q, k, v;
+  CUtensorMap o;      // dense d <= 128: O in boxes of 64 columns x 32 rows
+  WinParams prm;
+  int grid;           // paged: CTAs (the partial slots and desc are sized for it)
+  cudaStream_t stream;
+};
+
+template <int ELEM, int D, bool PAGED>
+cudaError_t launch_attn_window(const WinLaunch& L) {
+  using C = WinCfg<ELEM, D, PAGED>;
+  auto kern = attn_window_kernel<ELEM, D, PAGED>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  // per function and device: the shared memory limit, and that the register
+  // split fits what the kernel is launched with (the growing warpgroups
+  // would otherwise wait for registers that never come)
+  static int ready[64] = {};
+  if (ready[dev] == 0) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM_BYTES);
+    if (e != cudaSuccess) return e;
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, kern);
+    if (e != cudaSuccess) return e;
+    const bool fits = !C::REALLOC || at.numRegs * C::THREADS >= 128 * C::CTRL_REGS + C::SOFTMAX_WARPS * 32 * C::SOFTMAX_REGS;
+    ready[dev] = fits ? 1 : -1;
+  }
+  if (ready[dev] != 1) return cudaErrorInvalidConfiguration;
+  WinParams prm = L.prm;
+  long long grid = L.grid;
+  if constexpr (!PAGED) {
+    grid = (long long)prm.BH * ((prm.N + C::NQT * kBM - 1) / (C::NQT * kBM));
+    // chunks of heads whose keys and values fill about half of L2, as in attn_fwd.cuh
+    prm.head_chunk = prm.BH;
+    const long long kv_head_bytes = 2LL * prm.Nk * C::ROW_BYTES;
+    const int qgroup = prm.Hq / prm.Hkv;
+    long long chunk = ((64LL << 20) / (kv_head_bytes > 0 ? kv_head_bytes : 1)) * qgroup;
+    if (chunk < qgroup) chunk = qgroup;
+    if (chunk < prm.BH) prm.head_chunk = (int)chunk;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid, 1, 1);
+  cfg.blockDim = dim3(C::THREADS, 1, 1);
+  cfg.dynamicSmemBytes = C::SMEM_BYTES;
+  cfg.stream = L.stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 1;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kern, L.q, L.k, L.v, L.o, prm);
+  if (e != cudaSuccess) return e;
+  return cudaGetLastError();
+}
+
+}  // namespace fa

@@ -13,7 +13,8 @@
 namespace fa {
 
 // Device error word values (read back by fa_check_device_error).
-enum : int { FA_DEVERR_NONE = 0, FA_DEVERR_TIMEOUT = 1 };
+// FA_DEVERR_INDEX is a bit of its own, set beside a timeout's.
+enum : int { FA_DEVERR_NONE = 0, FA_DEVERR_TIMEOUT = 1, FA_DEVERR_INDEX = 2 };
 
 // Wait budget of one pipeline wait, in nanoseconds of %globaltimer.
 #ifndef FA_WAIT_LIMIT_NS
@@ -109,6 +110,16 @@ __device__ __forceinline__ void tma_load_3d_hint(void* smem_dst, const CUtensorM
       "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
       " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(smem_dst)),
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+      : "memory");
+}
+
+// The same for a 4-D map.
+__device__ __forceinline__ void tma_load_4d_hint(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int c0,
+                                                 int c1, int c2, int c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(smem_dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
       : "memory");
 }
 

@@ -50,7 +50,9 @@ typedef enum {
     FA_ERR_UNSUPPORTED = 2,   /* head dimension or device not supported                            */
     FA_ERR_CUDA = 3,          /* a CUDA runtime/driver call or kernel launch failed                 */
     FA_ERR_TIMEOUT = 4,       /* a kernel's pipeline wait ran out of time (see fa_check_device_error) */
-    FA_ERR_SCRATCH_LIMIT = 5  /* problem larger than the library's static scratch (no-allocation entry point) */
+    FA_ERR_SCRATCH_LIMIT = 5, /* problem larger than the library's static scratch (no-allocation entry point) */
+    FA_ERR_INDEX = 6          /* a length, position or page number read from device memory was out of range
+                                 (see fa_check_device_error)                                                 */
 } fa_status;
 
 typedef enum {
@@ -394,14 +396,155 @@ fa_status fa_quant_fp8_per_tensor_noalloc(const float* x, void* x8, float* desca
                                           int64_t B, int64_t H, int64_t N, int64_t d,
                                           const int8_t* hadamard_signs, cudaStream_t stream);
 
+/*
+ * ---- sliding window with sinks, and the paged key/value cache ----
+ *
+ * Visibility.  A query at position p of its sequence sees key j iff
+ *     j <= p  and  (j > p - window  or  j < sinks):
+ * the last `window` keys up to its own, and the first `sinks` keys of the
+ * sequence.  window >= 1 (any value of at least the sequence length makes the
+ * mask plain causal), sinks >= 0.  Key tiles without a visible key are
+ * neither read nor multiplied.  A query that sees no key gets O = 0 and
+ * LSE = -inf.
+ */
+
+/*
+ * fa_fwd_window -- fa_fwd_gqa under a sliding window with sinks.
+ *   q [B, Hq, Nq, d], k, v [B, Hkv, Nk, d], o [B, Hq, Nq, d], lse [B, Hq, Nq]
+ *   as fa_fwd_gqa (contiguous, bf16 or fp16, Hq a multiple of Hkv).  Query i
+ *   sits at position p = i + Nk - Nq (the sequence ends with the last query).
+ * Numerics, ownership and non-finite inputs as fa_fwd: a NaN or infinity in
+ * element (j, c) of V may also reach column c of rows that do not see key j
+ * but share its 128-key tile with rows that do.
+ * Errors: as fa_fwd_gqa, FA_ERR_INVALID_ARG also for window < 1 or sinks < 0,
+ * FA_ERR_UNSUPPORTED also for Nq or Nk above 2^30.
+ */
+fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse,
+                        int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d,
+                        int64_t window, int64_t sinks, float scale, int dtype, cudaStream_t stream);
+
+/*
+ * A paged key/value cache: num_pages pages of page_size tokens for each of
+ * `heads` key/value heads.  Element (page, head, token, c) of k (and of v)
+ * lies at k + page * page_stride + head * head_stride + token * token_stride
+ * + c, strides in elements: [pages, heads, page_size, d] and [pages,
+ * page_size, heads, d] are both such layouts, as are k and v interleaved in
+ * one allocation.
+ *   k, v       DEVICE pointers, 16-byte aligned, owned by the caller
+ *   page_size  a power of two, 16 to 1024;  d 64, 128 or 256
+ *   strides    multiples of 8 and at least d (a stride whose size is 1 is not
+ *              looked at)
+ */
+typedef struct {
+    void* k;
+    void* v;
+    int64_t num_pages, page_size, heads, d;
+    int64_t page_stride, head_stride, token_stride;
+    int dtype;
+} fa_kv_cache;
+
+/*
+ * A ragged batch over a cache, as fa_fwd_paged and fa_cache_append take it.
+ * Sequence b brings the new tokens cu_q[b] .. cu_q[b + 1] - 1 of the packed
+ * token arrays and has seq_k[b] keys, those of its new tokens included and
+ * last: new token i of n sits at position seq_k[b] - n + i.  Key j lies at
+ * row j % page_size of page block_table[b * table_stride + j / page_size].
+ *   block_table  [B, max_pages] int32 (device), rows table_stride apart; only
+ *                the entries of pages with a visible key (fa_fwd_paged) or a
+ *                new token (fa_cache_append) are read
+ *   cu_q         [B + 1] int32 (device), not decreasing, cu_q[B] <= T.  Rows
+ *                of the packed arrays outside every sequence are neither
+ *                written nor used
+ *   seq_k        [B] int32 (device)
+ * All three are device data, read by the kernels when they run, so a captured
+ * graph follows their contents.  The host cannot refuse what they hold; the
+ * kernels do: a length is cut to the arrays it would overrun, a page number
+ * out of range reads as zeros (fa_fwd_paged) or drops the token
+ * (fa_cache_append), nothing out of bounds is touched, and
+ * fa_check_device_error then returns FA_ERR_INDEX.
+ */
+
+/*
+ * fa_fwd_paged -- attention of the new tokens of a ragged batch (one token or
+ * a chunk per sequence, mixed freely) over a paged cache that already holds
+ * their keys and values, under a sliding window with sinks.
+ *   q          [T, Hq, d] of the cache's dtype (device), tokens q_stride
+ *              elements apart (a multiple of 8, at least Hq * d), heads d apart
+ *   o          [T, Hq, d] contiguous (device, written);  lse [T, Hq] fp32
+ *   Hq         a multiple of cache->heads, at most 128 query heads to each
+ *   max_q      the most new tokens any sequence brings, 0 if not known.  A
+ *              hint: it sizes the query tiles; results are right for any value
+ *   window, sinks, scale  as fa_fwd_window (pages that left every query's
+ *              window, sinks apart, may be freed: they are not read)
+ *   workspace  DEVICE pointer, 256-byte aligned, owned by the caller, at least
+ *              fa_paged_workspace_bytes(d) bytes; overwritten; calls sharing
+ *              it must not overlap on the GPU (two captured graphs included)
+ * Rows of the cache behind a sequence's end, and pages it does not see, may
+ * hold anything (NaN included).  Two kernels on `stream`, no allocation.  The
+ * result of one sequence may differ in its last bits with the rest of the
+ * batch (the work is cut evenly over the GPU and the pieces are joined), but
+ * is the same from run to run.
+ * Errors: FA_ERR_INVALID_ARG for bad pointers, alignment, sizes, strides,
+ * window, sinks, scale or workspace; FA_ERR_UNSUPPORTED for d, page_size or
+ * head counts outside the above, more than 2^24 sequences, lengths above
+ * 2^30, or a device other than sm_103.  B * T * Hq = 0 is a no-op.
+ */
+fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse,
+                       const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                       const int32_t* cu_q, const int32_t* seq_k,
+                       int64_t B, int64_t T, int64_t Hq, int64_t q_stride, int64_t max_q,
+                       int64_t window, int64_t sinks, float scale,
+                       void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fa_paged_workspace_bytes -- bytes of device workspace fa_fwd_paged needs on
+ * the current device for head dimension d, whatever the batch: two partial
+ * results of one query tile pair per SM (about 40 MB at d = 128).
+ */
+fa_status fa_paged_workspace_bytes(int64_t d, size_t* bytes);
+
+/*
+ * fa_cache_append -- writes the new tokens' keys and values of a ragged batch
+ * into their pages, after a rotary position embedding of the keys, and
+ * rotates the new tokens' queries by the same angles: the step before
+ * fa_fwd_paged.
+ *   k, v       [T, heads, d] of the cache's dtype (device, read only), tokens
+ *              k_stride / v_stride elements apart (multiples of 8, at least
+ *              heads * d): slices of one fused projection are such arrays
+ *   q          [T, Hq, d] likewise (q_stride), or NULL with Hq = 0
+ *   q_out      [T, Hq, d] contiguous (device, written).  q_out = q is allowed
+ *              when q is contiguous; any other overlap of an input with an
+ *              output is not
+ *   rope_cos, rope_sin  [rope_len, d/2] fp32 (device, read only, 16-byte
+ *              aligned); row p holds the angles of position p
+ *   rope_layout  0: no rotation (keys and queries are copied), or
+ *              FA_ROPE_INTERLEAVED / FA_ROPE_HALF as in fa_quant_fp8_rope:
+ *              pair (a, b) becomes (a*c - b*s, a*s + b*c), each product
+ *              rounded to fp32 before the sum, the sum once to the dtype
+ * A token whose position is negative, behind its table row or the angle
+ * tables, or whose page is out of range, is dropped (no key, value or query
+ * of it is written) and reported by fa_check_device_error as FA_ERR_INDEX.
+ * If two tokens share a cache row, which of them it holds is not defined.
+ * Errors: as fa_fwd_paged, FA_ERR_INVALID_ARG also for a missing or
+ * misaligned table or an unknown layout.  B * T = 0 is a no-op.
+ */
+fa_status fa_cache_append(const fa_kv_cache* cache, const void* q, const void* k, const void* v, void* q_out,
+                          int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                          const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                          const int32_t* cu_q, const int32_t* seq_k, int64_t B, int64_t T, int64_t Hq,
+                          const float* rope_cos, const float* rope_sin, int64_t rope_len, int rope_layout,
+                          cudaStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fa_status_string(fa_status status);
 
 /*
  * fa_check_device_error -- synchronises `stream`, then reports and clears the
  * library's device error word on the current device: FA_ERR_TIMEOUT if a
- * kernel gave up on a pipeline wait since the last check, FA_ERR_CUDA if the
- * synchronisation itself failed, else FA_OK.
+ * kernel gave up on a pipeline wait since the last check, FA_ERR_INDEX if a
+ * kernel met an index out of range in device memory (fa_fwd_paged,
+ * fa_cache_append), FA_ERR_CUDA if the synchronisation itself failed, else
+ * FA_OK.
  */
 fa_status fa_check_device_error(cudaStream_t stream);
 
