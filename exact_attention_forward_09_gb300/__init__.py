@@ -17,7 +17,7 @@ import torch
 
 from .build import LIB as _LIB_PATH
 
-__all__ = ["fwd_host", "fwd_host_workspace_bytes", "bwd", "bwd_workspace_bytes", "fwd_splitkv", "splitkv_workspace_bytes", "fwd", "fwd_gqa", "fwd_window",
+__all__ = ["fwd_host", "fwd_host_workspace_bytes", "bwd", "bwd_workspace_bytes", "fwd_splitkv", "splitkv_workspace_bytes", "fwd", "fwd_gqa", "fwd_window", "bwd_window", "bwd_window_workspace_bytes",
            "fwd_paged", "paged_workspace_bytes", "cache_append", "fwd_fp8", "fwd_fp8_gqa", "quant_fp8", "quant_fp8_per_tensor_noalloc", "check_device_error", "lib",
            "FaError", "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
            "FA_ERR_SCRATCH_LIMIT", "FA_ERR_INDEX", "FA_DTYPE_BF16", "FA_DTYPE_FP16", "FP8_BLOCK_ROWS",
@@ -93,6 +93,10 @@ def _lib():
         cache = ctypes.POINTER(_KvCache)
         lib.fa_fwd_window.argtypes = [vp, vp, vp, vp, vp] + [i64] * 8 + [f32, i32, vp]
         lib.fa_fwd_window.restype = i32
+        lib.fa_bwd_window.argtypes = [vp] * 9 + [i64] * 8 + [f32, i32, vp, ctypes.c_size_t, vp]
+        lib.fa_bwd_window.restype = i32
+        lib.fa_bwd_window_workspace_bytes.argtypes = [i64] * 8 + [ctypes.POINTER(ctypes.c_size_t)]
+        lib.fa_bwd_window_workspace_bytes.restype = i32
         lib.fa_paged_workspace_bytes.argtypes = [i64, ctypes.POINTER(ctypes.c_size_t)]
         lib.fa_paged_workspace_bytes.restype = i32
         lib.fa_fwd_paged.argtypes = [vp, cache, vp, vp, vp, i64, i64, vp, vp] + [i64] * 7 + [f32, vp, ctypes.c_size_t, vp]
@@ -354,6 +358,48 @@ def fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, s
                                   B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks), _scale(scale, d), dt, _stream(q))
     _check(st, "fa_fwd_window")
     return out, lse
+
+
+def bwd_window_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int, window: int, sinks: int = 0) -> int:
+    """Bytes of device workspace ``bwd_window`` needs for this shape."""
+    n = ctypes.c_size_t(0)
+    _check(_lib().fa_bwd_window_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks), ctypes.byref(n)),
+           "fa_bwd_window_workspace_bytes")
+    return int(n.value)
+
+
+def bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
+               dout: torch.Tensor, window: int, sinks: int = 0, scale: float | None = None,
+               dq: torch.Tensor | None = None, dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+               workspace: torch.Tensor | None = None):
+    """Gradients of sum(dout * O) for ``fwd_window`` (``fa_bwd_window``): q,
+    out, dout [B, Hq, Nq, d], k/v [B, Hkv, Nk, d], lse [B, Hq, Nq] fp32 from
+    the forward with the same window, sinks and scale; d 64 or 128.  Returns
+    (dq, dk, dv)."""
+    _check_gqa(q, k, v, (torch.bfloat16, torch.float16))
+    B, Hq, Nq, d = q.shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    for name, t in (("out", out), ("dout", dout)):
+        _check_out(name, t, q.shape, q.dtype, q.device)
+    _check_out("lse", lse, (B, Hq, Nq), torch.float32, q.device)
+    grads = []
+    for name, t, x in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
+        if t is None:
+            t = torch.empty_like(x)
+        else:
+            _check_out(name, t, x.shape, x.dtype, x.device)
+        grads.append(t)
+    dt = FA_DTYPE_BF16 if q.dtype == torch.bfloat16 else FA_DTYPE_FP16
+    with torch.cuda.device(q.device):
+        if workspace is None:
+            need = bwd_window_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, window, sinks)
+            workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=q.device)
+        st = _lib().fa_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                                  dout.data_ptr(), *[t.data_ptr() for t in grads], B, Hq, Hkv, Nq, Nk, d,
+                                  int(window), int(sinks), _scale(scale, d), dt, workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _stream(q))
+    _check(st, "fa_bwd_window")
+    return tuple(grads)
 
 
 def _cache(k_pages, v_pages):

@@ -789,9 +789,14 @@ fa_status fa_bwd_workspace_bytes(int64_t B, int64_t Hq, int64_t Nq, int64_t d, s
   return FA_OK;
 }
 
-fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
-                 void* dq, void* dk, void* dv, int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d,
-                 int causal, float scale, int dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+}  // extern "C"
+
+namespace {
+// fa_bwd (window 0) and fa_bwd_window (window >= 1, causal).
+fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
+                   void* dq, void* dk, void* dv, int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d,
+                   int causal, int64_t window, int64_t sinks, float scale, int dtype, void* workspace,
+                   size_t workspace_bytes, cudaStream_t stream) {
   if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_FP16) return FA_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
   if (B < 0 || Hq < 0 || Hkv < 0 || Nq < 0 || Nk < 0 || d < 0) return FA_ERR_INVALID_ARG;
@@ -823,7 +828,9 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
   // the preprocessing kernel runs one block per 8 padded query rows
   if ((B * Hq * fa::bwd_records_per_head(Nq, (int)d) * 64 + 7) / 8 > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   size_t need = 0;
-  if ((st = fa_bwd_workspace_bytes(B, Hq, Nq, d, &need)) != FA_OK) return st;
+  if ((st = window > 0 ? fa_bwd_window_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, window, sinks, &need)
+                       : fa_bwd_workspace_bytes(B, Hq, Nq, d, &need)) != FA_OK)
+    return st;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < need)
     return FA_ERR_INVALID_ARG;
   if ((st = device_setup(&dev, &err)) != FA_OK) return st;
@@ -866,7 +873,17 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
   L.prm.drop_step = (g_inject.exchange(0) & 1) ? 1 : -1;
   L.stream = stream;
   cudaError_t e;
-  if (d == 64) {
+  if (window > 0) {
+    const fa::BwdWindow w = fa::bwd_window_plan(B, Hq, Hkv, Nq, Nk, (int)d, window, sinks);
+    L.prm.window = w.window;
+    L.prm.sinks = w.sinks;
+    L.prm.sink_tiles = w.sink_tiles;
+    L.prm.sink_split = w.split;
+    if (w.split > 1) L.prm.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (need - w.part_bytes));
+    if (d == 64) e = f16 ? fa::launch_attn_bwd<1, 64, true, true>(L) : fa::launch_attn_bwd<0, 64, true, true>(L);
+    else e = f16 ? fa::launch_attn_bwd<1, 128, true, true>(L) : fa::launch_attn_bwd<0, 128, true, true>(L);
+    if (e == cudaSuccess && w.split > 1) e = fa::launch_bwd_sink_sum(L.prm, (int)d, f16, stream);
+  } else if (d == 64) {
     if (f16) e = causal ? fa::launch_attn_bwd<1, 64, true>(L) : fa::launch_attn_bwd<1, 64, false>(L);
     else e = causal ? fa::launch_attn_bwd<0, 64, true>(L) : fa::launch_attn_bwd<0, 64, false>(L);
   } else {
@@ -877,6 +894,42 @@ fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, con
   if (fa::launch_bwd_dq_convert(dq_acc, dq, scale, (long long)(rows * d), f16, stream) != cudaSuccess)
     return FA_ERR_CUDA;
   return FA_OK;
+}
+}  // namespace
+
+extern "C" {
+
+fa_status fa_bwd(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
+                 void* dq, void* dk, void* dv, int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d,
+                 int causal, float scale, int dtype, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return bwd_impl(q, k, v, o, lse, dout, dq, dk, dv, B, Hq, Hkv, Nq, Nk, d, causal, 0, 0, scale, dtype, workspace,
+                  workspace_bytes, stream);
+}
+
+fa_status fa_bwd_window_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d,
+                                        int64_t window, int64_t sinks, size_t* bytes) {
+  if (!bytes) return FA_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (Hkv < 0 || Nk < 0 || window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+  size_t base = 0;
+  const fa_status st = fa_bwd_workspace_bytes(B, Hq, Nq, d, &base);
+  if (st != FA_OK) return st;
+  if (d == 256) return FA_ERR_UNSUPPORTED;  // the backward kernel covers d = 64 and 128
+  if (B == 0 || Hq == 0) return FA_OK;
+  if (Hkv == 0 || Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
+  if (Nq > ((int64_t)1 << 30) || Nk > ((int64_t)1 << 30) || B * Hkv > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
+  *bytes = base + fa::bwd_window_plan(B, Hq, Hkv, Nq, Nk, (int)d, window, sinks).part_bytes;
+  return FA_OK;
+}
+
+fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* dout,
+                        void* dq, void* dk, void* dv, int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk,
+                        int64_t d, int64_t window, int64_t sinks, float scale, int dtype, void* workspace,
+                        size_t workspace_bytes, cudaStream_t stream) {
+  if (window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+  if (Nq > ((int64_t)1 << 30) || Nk > ((int64_t)1 << 30)) return FA_ERR_UNSUPPORTED;
+  return bwd_impl(q, k, v, o, lse, dout, dq, dk, dv, B, Hq, Hkv, Nq, Nk, d, 1, window, sinks, scale, dtype, workspace,
+                  workspace_bytes, stream);
 }
 
 const char* fa_status_string(fa_status status) {

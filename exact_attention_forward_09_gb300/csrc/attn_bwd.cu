@@ -32,6 +32,13 @@
 // so the tensor core runs them while the compute warpgroup works on tile t.
 // A preprocessing kernel forms D and clears the dQ accumulator; a last
 // kernel scales it and converts it to the element type.
+//
+// WIN instances: the causal kernel under a sliding window with sinks (key j
+// visible to position p iff j <= p and (j > p - window or j < sinks)).  A key
+// tile's walk ends with the last query whose window reaches it; the tiles
+// that hold a sink are seen by every later query, so their walk is shared out
+// over several CTAs that start first and leave fp32 dK and dV parts
+// (BwdWindow), which a small kernel sums in a fixed order.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -173,13 +180,14 @@ __device__ __forceinline__ void settle(uint64_t* bar, uint32_t parity) {
   }
 }
 
-template <int ELEM, int D, bool CAUSAL>
+template <int ELEM, int D, bool CAUSAL, bool WIN>
 __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                     const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const __grid_constant__ CUtensorMap tm_dq, const __grid_constant__ CUtensorMap tm_dk,
                     const __grid_constant__ CUtensorMap tm_dv, const BwdParams prm) {
   using C = BwdCfg<ELEM, D, CAUSAL>;
+  static_assert(CAUSAL || !WIN, "windows are causal");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   BwdBars* bars = reinterpret_cast<BwdBars*>(smem + C::OFF_BAR);
@@ -199,7 +207,20 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
   // CTA -> (key/value head, key tile).  Causal: key-tile-major, so the tiles
   // with the most visible queries (the first ones) start first.
   int bkv, kt;
-  if constexpr (CAUSAL) {
+  int part = -1;  // WIN: which share of a sink tile's steps (-1: all of a tile's)
+  if constexpr (WIN) {
+    // the shares of the sink tiles first, then the other tiles in order
+    const int sink_ctas = prm.sink_tiles * prm.sink_split * prm.BHkv;
+    int x = (int)blockIdx.x;
+    bkv = x % prm.BHkv;
+    if (x < sink_ctas) {
+      x /= prm.BHkv;
+      kt = x / prm.sink_split;
+      part = prm.sink_split > 1 ? x % prm.sink_split : -1;
+    } else {
+      kt = prm.sink_tiles + (x - sink_ctas) / prm.BHkv;
+    }
+  } else if constexpr (CAUSAL) {
     kt = (int)blockIdx.x / prm.BHkv;
     bkv = (int)blockIdx.x % prm.BHkv;
   } else {
@@ -213,9 +234,24 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
     const int first = k0 - koff;
     qt0 = first > 0 ? first / C::BQ : 0;
   }
-  const int per_head = nqt > qt0 ? nqt - qt0 : 0;
-  const int T = grp * per_head;  // steps of this CTA
+  int qt1 = nqt;  // behind the last query tile that sees a key of this tile
+  if constexpr (WIN) {
+    if (kt >= prm.sink_tiles) {
+      const int last = min(k0 + kBK, Nk) - 1 + prm.window - 1 - koff;  // last query whose window reaches the tile
+      qt1 = last < 0 ? 0 : min(nqt, last / C::BQ + 1);
+    }
+  }
+  const int per_head = qt1 > qt0 ? qt1 - qt0 : 0;
+  int T = grp * per_head;  // steps of this CTA
+  int step0 = 0;           // WIN: first of them
+  if constexpr (WIN) {
+    if (part >= 0) {
+      step0 = (int)((long long)T * part / prm.sink_split);
+      T = (int)((long long)T * (part + 1) / prm.sink_split) - step0;
+    }
+  }
   auto step_of = [&](int t, int& bhq, int& q0) {
+    if constexpr (WIN) t += step0;
     bhq = bq_head0 + t / per_head;
     q0 = (qt0 + t % per_head) * C::BQ;
   };
@@ -424,6 +460,13 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
         lim = key - koff - q0 - cb;
         need_mask = (k0 + kBK - 1 - koff - q0 - cb) > 0;  // same for the whole warpgroup
       }
+      // WIN: columns lim .. lim + reach are queries that see the key (the
+      // window has left it behind them; a sink stays)
+      uint32_t reach = 0;
+      if constexpr (WIN) {
+        reach = key < prm.sinks ? 0x7fffffffu : (uint32_t)(prm.window - 1);
+        need_mask = need_mask || k0 + prm.window - 1 - koff - q0 - cb < C::HALF_Q - 1;
+      }
       constexpr int PW = C::PIECE;
 #pragma unroll
       for (int sub = 0; sub < C::NSUB; ++sub) {
@@ -452,10 +495,10 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
           float p0 = ex2(x01.x), p1 = ex2(x01.y), p2 = ex2(x23.x), p3 = ex2(x23.y);
           if (CAUSAL && need_mask) {
             const int c = PW * sub + i;
-            p0 = (c < lim) ? 0.0f : p0;
-            p1 = (c + 1 < lim) ? 0.0f : p1;
-            p2 = (c + 2 < lim) ? 0.0f : p2;
-            p3 = (c + 3 < lim) ? 0.0f : p3;
+            p0 = (WIN ? (uint32_t)(c - lim) > reach : c < lim) ? 0.0f : p0;
+            p1 = (WIN ? (uint32_t)(c + 1 - lim) > reach : c + 1 < lim) ? 0.0f : p1;
+            p2 = (WIN ? (uint32_t)(c + 2 - lim) > reach : c + 2 < lim) ? 0.0f : p2;
+            p3 = (WIN ? (uint32_t)(c + 3 - lim) > reach : c + 3 < lim) ? 0.0f : p3;
           }
           // dS = P (dP - D)
           const float2 g01 = add2(make_float2(__uint_as_float(dr[i]), __uint_as_float(dr[i + 1])),
@@ -508,7 +551,27 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
       have = __all_sync(0xffffffffu, mbar_wait(&bars->acc_full, 0, abort_flag, prm.err));
       if (have) tc_fence_after();
     }
-    if (cg < 2 && bar_and(2 + cg, 128, have)) {
+    if (WIN && part >= 0) {
+      // this share's dV (warpgroup 0) or unscaled dK (warpgroup 1), fp32: one
+      // key row per thread
+      if (cg < 2 && have) {
+        float* dst = prm.part + (((((size_t)kt * prm.BHkv + bkv) * prm.sink_split + part) * 2 + (cg ? 0 : 1)) * kBK + r) * D;
+        const uint32_t col = cg ? C::COL_DK : C::COL_DV;
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          uint32_t a[32];
+          if (T > 0) {
+            tmem_ld32(tmem + lane_addr + col + c0, a);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) a[i] = 0u;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) st_global_v8(dst + c0 + 8 * i, a + 8 * i);
+        }
+      }
+    } else if (cg < 2 && bar_and(2 + cg, 128, have)) {
       const uint32_t col = cg ? C::COL_DK : C::COL_DV;
       const float mult = cg ? prm.scale : 1.0f;
       uint8_t* stg = smem + C::OFF_ST + cg * C::KV_BYTES;  // kBK rows x D, NCH panels
@@ -734,6 +797,40 @@ __global__ void __launch_bounds__(256) zero_fill_kernel(uint4* __restrict__ p, l
     p[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
+// One warp per key row of a sink tile and gradient (dK, dV): the sum of the
+// shares' parts in order, scaled (dK), rounded once.
+template <int D, bool F16>
+__global__ void __launch_bounds__(256) bwd_sink_sum_kernel(const BwdParams prm) {
+  constexpr int E = D / 32;
+  const long long x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int row = (int)(x % kBK);
+  const int which = (int)(x / kBK % 2);                     // 0: dK, 1: dV
+  const long long unit = x / (2 * kBK);                     // tile * BHkv + bkv
+  const long long kt = unit / prm.BHkv, bkv = unit % prm.BHkv;
+  const long long key = kt * kBK + row;
+  if (kt >= prm.sink_tiles || key >= prm.Nk) return;
+  float acc[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+  const float* src = prm.part + ((unit * prm.sink_split * 2 + which) * kBK + row) * D + lane * E;
+  for (int s = 0; s < prm.sink_split; ++s, src += 2LL * kBK * D) {
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(src + e);
+      acc[e] += v.x;
+      acc[e + 1] += v.y;
+    }
+  }
+  const float mult = which ? 1.0f : prm.scale;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(which ? prm.dv : prm.dk) + ((bkv * prm.Nk + key) * D + lane * E) / 2;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    if constexpr (F16) dst[e / 2] = pack_f16x2(acc[e] * mult, acc[e + 1] * mult);
+    else dst[e / 2] = pack_bf16x2(acc[e] * mult, acc[e + 1] * mult);
+  }
+}
+
 // grid for a grid-stride loop over n items: at most 8 blocks of 256 per SM
 unsigned stride_grid(long long n) {
   int dev = 0, sms = 148;
@@ -746,10 +843,10 @@ unsigned stride_grid(long long n) {
 
 }  // namespace
 
-template <int ELEM, int D, bool CAUSAL>
+template <int ELEM, int D, bool CAUSAL, bool WIN>
 cudaError_t launch_attn_bwd(const BwdLaunch& L) {
   using C = BwdCfg<ELEM, D, CAUSAL>;
-  auto kern = attn_bwd_kernel<ELEM, D, CAUSAL>;
+  auto kern = attn_bwd_kernel<ELEM, D, CAUSAL, WIN>;
   static bool attr_done[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -760,7 +857,8 @@ cudaError_t launch_attn_bwd(const BwdLaunch& L) {
     if (dev >= 0 && dev < 64) attr_done[dev] = true;
   }
   const long long nkt = (L.prm.Nk + kBK - 1) / kBK;
-  const long long ctas = (long long)L.prm.BHkv * nkt;
+  long long ctas = (long long)L.prm.BHkv * nkt;
+  if constexpr (WIN) ctas += (long long)L.prm.BHkv * L.prm.sink_tiles * (L.prm.sink_split - 1);
   kern<<<(unsigned)ctas, C::THREADS, C::SMEM_BYTES, L.stream>>>(L.q, L.dout, L.k, L.v, L.dq_acc, L.dk, L.dv,
                                                                L.prm);
   return cudaGetLastError();
@@ -774,6 +872,10 @@ template cudaError_t launch_attn_bwd<0, 64, false>(const BwdLaunch&);
 template cudaError_t launch_attn_bwd<0, 64, true>(const BwdLaunch&);
 template cudaError_t launch_attn_bwd<1, 64, false>(const BwdLaunch&);
 template cudaError_t launch_attn_bwd<1, 64, true>(const BwdLaunch&);
+template cudaError_t launch_attn_bwd<0, 128, true, true>(const BwdLaunch&);
+template cudaError_t launch_attn_bwd<1, 128, true, true>(const BwdLaunch&);
+template cudaError_t launch_attn_bwd<0, 64, true, true>(const BwdLaunch&);
+template cudaError_t launch_attn_bwd<1, 64, true, true>(const BwdLaunch&);
 
 // Query rows per step of the kernel for head dimension d (the Q / dO TMA
 // box height) and the 64-row LSE / D records it needs per query head.
@@ -781,6 +883,45 @@ int bwd_step_rows(int d) { return d == 64 ? BwdCfg<0, 64>::BQ : BwdCfg<0, 128>::
 long long bwd_records_per_head(long long nq, int d) {
   const long long bq = bwd_step_rows(d);
   return (nq + bq - 1) / bq * (bq / kRec);
+}
+
+BwdWindow bwd_window_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int d, int64_t window,
+                          int64_t sinks) {
+  BwdWindow w;
+  w.window = (int)(window < Nk ? window : (Nk > 1 ? Nk : 1));  // a longer one hides nothing
+  w.sinks = (int)(sinks < Nk ? sinks : Nk);
+  w.sink_tiles = (w.sinks + kBK - 1) / kBK;
+  w.split = 1;
+  w.part_bytes = 0;
+  if (w.sink_tiles == 0 || Nq == 0) return w;
+  const int64_t bq = bwd_step_rows(d), nqt = (Nq + bq - 1) / bq, grp = Hq / Hkv;
+  // steps of a tile without sinks, of the first sink tile, and as many shares
+  // as bring the second down to the first (at least 8 steps each), while the
+  // shares do not outnumber what fills the GPU several times
+  int64_t usual = (kBK - 1 + w.window + bq - 1) / bq + 1;
+  if (usual > nqt) usual = nqt;
+  usual *= grp;
+  if (usual < 8) usual = 8;
+  int64_t split = (grp * nqt + usual - 1) / usual;
+  const int64_t most = 1024 / (w.sink_tiles * B * Hkv);
+  if (split > most) split = most;
+  w.split = (int)(split < 1 ? 1 : split);
+  if (w.split > 1) w.part_bytes = (size_t)w.sink_tiles * B * Hkv * w.split * 2 * kBK * d * 4;
+  return w;
+}
+
+cudaError_t launch_bwd_sink_sum(const BwdParams& prm, int d, bool f16, cudaStream_t stream) {
+  const unsigned blocks = (unsigned)((long long)prm.sink_tiles * prm.BHkv * 2 * kBK / 8);
+  if (d == 64) {
+    if (f16) bwd_sink_sum_kernel<64, true><<<blocks, 256, 0, stream>>>(prm);
+    else bwd_sink_sum_kernel<64, false><<<blocks, 256, 0, stream>>>(prm);
+  } else if (d == 128) {
+    if (f16) bwd_sink_sum_kernel<128, true><<<blocks, 256, 0, stream>>>(prm);
+    else bwd_sink_sum_kernel<128, false><<<blocks, 256, 0, stream>>>(prm);
+  } else {
+    return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
 }
 
 cudaError_t launch_bwd_prep(const void* o, const void* dout, const float* lse, float* vecs, float* dq_acc,

@@ -1,6 +1,7 @@
 // attn_bwd.h -- launch interface of the attention backward kernels.
 #pragma once
 
+#include <cstddef>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_runtime.h>
@@ -22,7 +23,23 @@ struct BwdParams {
   float scale_log2;    // scale * log2(e)
   float scale;         // dK = scale * dS^T Q
   int drop_step;       // test hook: step whose Q/dO stage CTA 0 never fills (-1: none)
+  // sliding window with sinks (the WIN instances): see BwdWindow
+  int window, sinks;
+  int sink_tiles, sink_split;
+  float* part;         // sink_split > 1: [sink_tiles][BHkv][sink_split][dK, dV][128][D] fp32
 };
+
+// How the windowed backward treats the key tiles that hold a sink: every
+// query from their first key on sees them, where the other tiles are seen by
+// about window / 128 + 1 query tiles, so their query steps are shared out
+// over `split` CTAs each, which leave fp32 dK and dV to be summed.
+struct BwdWindow {
+  int window, sinks;
+  int sink_tiles, split;
+  size_t part_bytes;
+};
+BwdWindow bwd_window_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int d, int64_t window,
+                          int64_t sinks);
 
 struct BwdLaunch {
   CUtensorMap q, dout;  // [BHq, Nq, D], 64-row boxes
@@ -34,8 +51,12 @@ struct BwdLaunch {
 };
 
 // ELEM: 0 bf16, 1 f16 (the forward's element kinds)
-template <int ELEM, int D, bool CAUSAL>
+template <int ELEM, int D, bool CAUSAL, bool WIN = false>
 cudaError_t launch_attn_bwd(const BwdLaunch& L);
+
+// dK = scale * sum of the parts' dK, dV = sum of their dV, rows below Nk of
+// the sink tiles.
+cudaError_t launch_bwd_sink_sum(const BwdParams& prm, int d, bool f16, cudaStream_t stream);
 
 // Records of -LSE_i * log2(e) and -D_i (D_i = dO_i . O_i) for every query
 // row, padded to nrec 64-row records per head, and dq_acc := 0.

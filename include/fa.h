@@ -424,6 +424,33 @@ fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, fl
                         int64_t window, int64_t sinks, float scale, int dtype, cudaStream_t stream);
 
 /*
+ * fa_bwd_window -- gradients of sum(dout * O) for O = fa_fwd_window(q, k, v)
+ * with the same window, sinks and scale: fa_bwd's arguments, formulas and
+ * layouts (d 64 or 128) with P restricted to the visible keys.
+ *   lse        [B, Hq, Nq] fp32 as fa_fwd_window wrote it
+ *   workspace  at least fa_bwd_window_workspace_bytes(...) bytes, 256-byte
+ *              aligned; overwritten; calls sharing it must not overlap
+ * dk and dv are the same from run to run; dq, as in fa_bwd, is accumulated
+ * across key tiles with fp32 reduce-adds whose order may change its rounding.
+ * Errors: as fa_bwd, FA_ERR_INVALID_ARG also for window < 1 or sinks < 0,
+ * FA_ERR_UNSUPPORTED also for Nq or Nk above 2^30.
+ */
+fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                        const void* dout, void* dq, void* dk, void* dv,
+                        int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d,
+                        int64_t window, int64_t sinks, float scale, int dtype,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * fa_bwd_window_workspace_bytes -- bytes of device workspace fa_bwd_window
+ * needs: fa_bwd's, and fp32 dK and dV parts of the key tiles that hold a sink
+ * when their queries are shared out (at most 128 MiB at d = 128).  Same checks
+ * as fa_bwd_window.
+ */
+fa_status fa_bwd_window_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d,
+                                        int64_t window, int64_t sinks, size_t* bytes);
+
+/*
  * A paged key/value cache: num_pages pages of page_size tokens for each of
  * `heads` key/value heads.  Element (page, head, token, c) of k (and of v)
  * lies at k + page * page_stride + head * head_stride + token * token_stride

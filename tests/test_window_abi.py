@@ -36,6 +36,40 @@ def test_fwd_window_refusals(fa):
     assert _window(fa, Nq=0, q=None, o=None, lse=None) == fa.FA_OK
 
 
+def _bwd(fa, **kw):
+    a = dict(q=P, k=P, v=P, o=P, lse=P, do=P, dq=P, dk=P, dv=P, B=1, Hq=4, Hkv=2, Nq=8, Nk=16, d=64, window=4, sinks=1, scale=0.1,
+             dtype=0, ws=P, ws_bytes=1 << 30)
+    a.update(kw)
+    return fa.lib().fa_bwd_window(*a.values(), None)
+
+
+def test_bwd_window_refusals(fa):
+    bad, unsup = fa.FA_ERR_INVALID_ARG, fa.FA_ERR_UNSUPPORTED
+    for kw in (dict(window=0), dict(sinks=-1), dict(scale=NAN), dict(dtype=2), dict(B=-1), dict(Hq=5), dict(Hkv=0), dict(Nk=0),
+               dict(q=None), dict(do=P + 8), dict(dk=None), dict(dv=P + 4), dict(lse=P + 4), dict(ws=None), dict(ws=P + 16),
+               dict(ws_bytes=100)):
+        assert _bwd(fa, **kw) == bad, kw
+    for kw in (dict(d=96), dict(d=256), dict(Nk=(1 << 30) + 1)):
+        assert _bwd(fa, **kw) == unsup, kw
+    none = {n: None for n in ("q", "k", "v", "o", "lse", "do", "dq", "dk", "dv", "ws")}
+    assert _bwd(fa, **none, B=0) == fa.FA_OK
+    n = ctypes.c_size_t(3)
+    size = fa.lib().fa_bwd_window_workspace_bytes
+    assert size(1, 4, 2, 8, 16, 64, 0, 0, ctypes.byref(n)) == bad
+    assert size(1, 4, 2, 8, 16, 64, 4, -1, ctypes.byref(n)) == bad
+    assert size(1, 4, 3, 8, 16, 64, 4, 0, ctypes.byref(n)) == bad
+    assert size(1, 4, 2, 8, 16, 256, 4, 0, ctypes.byref(n)) == unsup
+    assert size(1, 4, 2, 8, 16, 64, 4, 0, None) == bad
+    # without sinks, or where a window covers everything: what the causal backward needs
+    base = fa.bwd_workspace_bytes(2, 8, 3000, 128)
+    assert fa.bwd_window_workspace_bytes(2, 8, 2, 3000, 3000, 128, 100, 0) == base
+    assert fa.bwd_window_workspace_bytes(2, 8, 2, 3000, 3000, 128, 3000, 4) == base
+    # with them: shares of the sink tiles, bounded whatever the sizes
+    for args in ((2, 8, 2, 3000, 3000, 128, 100, 4), (1, 8, 8, 100000, 100000, 128, 1, 1), (1, 8, 1, 9000, 9000, 64, 10, 9000)):
+        more = fa.bwd_window_workspace_bytes(*args) - fa.bwd_workspace_bytes(args[0], args[1], args[3], args[5])
+        assert 0 <= more <= 128 << 20
+
+
 def _cache(fa, **kw):
     a = dict(k=P, v=P, num_pages=10, page_size=16, heads=2, d=64, page_stride=2 * 16 * 64, head_stride=16 * 64,
              token_stride=64, dtype=0)

@@ -117,3 +117,44 @@ class Paged:
 
 def ints(values, device="cuda"):
     return torch.tensor(values, dtype=torch.int32, device=device)
+
+
+def check_backward(got, q, k, v, do, o, window, sinks, scale, ref, dtype, what):
+    """Element-wise bounds of dQ, dK, dV (one batch entry; o: the forward's
+    rounded output, which D is formed from).
+
+    P is off by a factor within e = 4 delta + 2^-18 (scores, exp2, the LSE's
+    own error; delta as in check_forward) and rounded to the element type (u)
+    as dV's left operand; dP by d 2^-23 sum|do||v|; D by sum |do||o - O| and
+    its fp32 sum; dS = P (dP - D) is rounded to the element type (u); every
+    gradient is a sum of such products in fp32 (2^-18 of the absolute sum)
+    and rounded once (u).  In fp16, P and dS below 2^-14 lie on a grid whose
+    half step is 2^-25."""
+    u = HALF_STEP[dtype]
+    H, Nq, d = q.shape
+    Hkv, Nk = k.shape[0], k.shape[1]
+    g = H // Hkv
+    q, do, o = q.double(), do.double(), o.double()
+    k, v = (x.double().repeat_interleave(g, 0) for x in (k, v))
+    see = visible(Nq, Nk, window, sinks, q.device)
+    lse = torch.where(ref["some"], ref["LSE"], torch.zeros_like(ref["LSE"]))
+    p = torch.where(see, torch.exp((q @ k.transpose(1, 2)) * scale - lse[..., None]), torch.zeros(1, dtype=torch.float64, device=q.device))
+    ds = p * (do @ v.transpose(1, 2) - (do * ref["O"]).sum(-1, keepdim=True))
+    e = (4 * d * 2.0 ** -23 * ref["S"] + 2.0 ** -18)[..., None]
+    tiny = 2.0 ** -25 if dtype == torch.float16 else 0.0
+    edp = d * 2.0 ** -23 * (do.abs() @ v.abs().transpose(1, 2))
+    eD = (do.abs() * (o - ref["O"]).abs()).sum(-1, keepdim=True) + d * 2.0 ** -23 * (do.abs() * o.abs()).sum(-1, keepdim=True)
+    eP = torch.where(see, (u + e) * p + tiny, torch.zeros_like(p))
+    eS = torch.where(see, (1 + u) * (e * ds.abs() + (1 + e) * p * (edp + eD)) + u * ds.abs() + tiny, torch.zeros_like(p))
+    fold = lambda x: x.view(Hkv, g, Nk, d).sum(1)  # noqa: E731
+    aP, aS = p + eP, ds.abs() + eS
+    bounds = (abs(scale) * (eS @ k.abs() + 2.0 ** -18 * (aS @ k.abs())),
+              abs(scale) * fold(eS.transpose(1, 2) @ q.abs() + 2.0 ** -18 * (aS.transpose(1, 2) @ q.abs())),
+              fold(eP.transpose(1, 2) @ do.abs() + 2.0 ** -18 * (aP.transpose(1, 2) @ do.abs())))
+    for name, x, b in zip(("dQ", "dK", "dV"), got, bounds):
+        x, r = x.double(), ref[name]
+        assert bool(torch.isfinite(x).all()), f"{what} {name}: non-finite"
+        tol = b + u * (r.abs() + b) + tiny
+        bad = (x - r).abs() > tol
+        assert not bool(bad.any()), f"{what} {name}: {int(bad.sum())} of {bad.numel()} outside, worst excess " \
+                                    f"{float(((x - r).abs() - tol).max()):.3e}"
