@@ -9,6 +9,7 @@ the computation runs in the library's kernels; there is no other code path.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -325,6 +326,23 @@ def fwd_gqa(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = Fa
     return out, lse
 
 
+# The calls below are often small, and then the time on the host counts: they
+# ask for the current stream and switch devices only as far as needed.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_NO_GUARD = contextlib.nullcontext()
+
+
+def _current_stream(index: int) -> int:
+    return _raw_stream(index) if _raw_stream is not None else torch.cuda.current_stream(index).cuda_stream
+
+
+def _guard(index: int):
+    return _NO_GUARD if torch.cuda.current_device() == index else torch.cuda.device(index)
+
+
+_TYPES = {torch.bfloat16: FA_DTYPE_BF16, torch.float16: FA_DTYPE_FP16}
+
+
 def _scale(scale, d):
     return 1.0 / math.sqrt(d) if scale is None else float(scale)
 
@@ -352,10 +370,11 @@ def fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, s
         lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
     else:
         _check_out("lse", lse, (B, Hq, Nq), torch.float32, q.device)
-    dt = FA_DTYPE_BF16 if q.dtype == torch.bfloat16 else FA_DTYPE_FP16
-    with torch.cuda.device(q.device):
+    index = q.get_device()
+    with _guard(index):
         st = _lib().fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                  B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks), _scale(scale, d), dt, _stream(q))
+                                  B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks), _scale(scale, d), _TYPES[q.dtype],
+                                  _current_stream(index))
     _check(st, "fa_fwd_window")
     return out, lse
 
@@ -389,15 +408,15 @@ def bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
         else:
             _check_out(name, t, x.shape, x.dtype, x.device)
         grads.append(t)
-    dt = FA_DTYPE_BF16 if q.dtype == torch.bfloat16 else FA_DTYPE_FP16
-    with torch.cuda.device(q.device):
+    index = q.get_device()
+    with _guard(index):
         if workspace is None:
             need = bwd_window_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, window, sinks)
             workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=q.device)
         st = _lib().fa_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                                   dout.data_ptr(), *[t.data_ptr() for t in grads], B, Hq, Hkv, Nq, Nk, d,
-                                  int(window), int(sinks), _scale(scale, d), dt, workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _stream(q))
+                                  int(window), int(sinks), _scale(scale, d), _TYPES[q.dtype], workspace.data_ptr(),
+                                  workspace.numel() * workspace.element_size(), _current_stream(index))
     _check(st, "fa_bwd_window")
     return tuple(grads)
 
@@ -408,7 +427,7 @@ def _cache(k_pages, v_pages):
     for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
         if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
             raise ValueError(f"{name} must be a [num_pages, heads, page_size, d] CUDA tensor")
-        if t.dtype not in (torch.bfloat16, torch.float16):
+        if t.dtype not in _TYPES:
             raise ValueError(f"{name} has dtype {t.dtype}; expected bf16 or fp16")
         if t.stride(3) != 1:
             raise ValueError(f"{name} must have its last dimension contiguous")
@@ -417,8 +436,7 @@ def _cache(k_pages, v_pages):
         raise ValueError("k_pages and v_pages must share shape, strides, dtype and device")
     n, h, ps, d = k_pages.shape
     sp, sh, st, _ = k_pages.stride()
-    dt = FA_DTYPE_BF16 if k_pages.dtype == torch.bfloat16 else FA_DTYPE_FP16
-    return _KvCache(k_pages.data_ptr(), v_pages.data_ptr(), n, ps, h, d, sp, sh, st, dt)
+    return _KvCache(k_pages.data_ptr(), v_pages.data_ptr(), n, ps, h, d, sp, sh, st, _TYPES[k_pages.dtype])
 
 
 def _check_batch(block_table, cu_q, seq_k, device):
@@ -478,14 +496,15 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, blo
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
     else:
         _check_out("lse", lse, (T, Hq), torch.float32, dev)
-    with torch.cuda.device(dev):
+    index = k_pages.get_device()
+    with _guard(index):
         if workspace is None:
             workspace = torch.empty((paged_workspace_bytes(d),), dtype=torch.uint8, device=dev)
         st = _lib().fa_fwd_paged(q.data_ptr(), ctypes.byref(cache), out.data_ptr(), lse.data_ptr(),
                                  block_table.data_ptr(), table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(),
                                  B, T, Hq, q_stride, int(max_q), 1 << 30 if window is None else int(window),
                                  int(sinks), _scale(scale, d), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _stream(k_pages))
+                                 workspace.numel() * workspace.element_size(), _current_stream(index))
     _check(st, "fa_fwd_paged")
     return out, lse
 
@@ -530,10 +549,11 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
         if layout not in (FA_ROPE_INTERLEAVED, FA_ROPE_HALF):
             raise ValueError("rope layout must be FA_ROPE_INTERLEAVED or FA_ROPE_HALF")
         cp, sp = cos.data_ptr(), sin.data_ptr()
-    with torch.cuda.device(dev):
+    index = k_pages.get_device()
+    with _guard(index):
         st = _lib().fa_cache_append(ctypes.byref(cache), qp, k.data_ptr(), v.data_ptr(), op, qs, ks, vs,
                                     block_table.data_ptr(), table_stride, max_pages, cu_q.data_ptr(),
-                                    seq_k.data_ptr(), B, T, Hq, cp, sp, n, int(layout), _stream(k_pages))
+                                    seq_k.data_ptr(), B, T, Hq, cp, sp, n, int(layout), _current_stream(index))
     _check(st, "fa_cache_append")
     return q_out
 

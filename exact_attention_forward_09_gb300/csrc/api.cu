@@ -882,7 +882,8 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, c
     if (w.split > 1) L.prm.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (need - w.part_bytes));
     if (d == 64) e = f16 ? fa::launch_attn_bwd<1, 64, true, true>(L) : fa::launch_attn_bwd<0, 64, true, true>(L);
     else e = f16 ? fa::launch_attn_bwd<1, 128, true, true>(L) : fa::launch_attn_bwd<0, 128, true, true>(L);
-    if (e == cudaSuccess && w.split > 1) e = fa::launch_bwd_sink_sum(L.prm, (int)d, f16, stream);
+    if (e == cudaSuccess) e = fa::launch_bwd_window_finish(L.prm, dq, (long long)(rows * d), (int)d, f16, stream);
+    return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
   } else if (d == 64) {
     if (f16) e = causal ? fa::launch_attn_bwd<1, 64, true>(L) : fa::launch_attn_bwd<1, 64, false>(L);
     else e = causal ? fa::launch_attn_bwd<0, 64, true>(L) : fa::launch_attn_bwd<0, 64, false>(L);

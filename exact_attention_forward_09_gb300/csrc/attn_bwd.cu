@@ -277,6 +277,12 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
     tmem_alloc(&bars->tmem_base, C::TMEM_COLS);
     tmem_relinquish();
   }
+  if constexpr (WIN) {
+    // launched while the preprocessing kernel ends, and letting the last
+    // kernel be launched: each waits where it needs the one before
+    pdl_launch();
+    pdl_wait();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -797,12 +803,31 @@ __global__ void __launch_bounds__(256) zero_fill_kernel(uint4* __restrict__ p, l
     p[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// One warp per key row of a sink tile and gradient (dK, dV): the sum of the
-// shares' parts in order, scaled (dK), rounded once.
+// The end of the windowed backward, one launch: blocks below conv_blocks
+// scale and convert dQ (grid-stride), the others sum the sink tiles' shares,
+// one warp per key row and gradient (dK, dV), the parts in order, scaled
+// (dK), rounded once.
 template <int D, bool F16>
-__global__ void __launch_bounds__(256) bwd_sink_sum_kernel(const BwdParams prm) {
+__global__ void __launch_bounds__(256) bwd_window_finish_kernel(const BwdParams prm, void* __restrict__ dq, long long n8,
+                                                                int conv_blocks) {
+  pdl_wait();
+  if ((int)blockIdx.x < conv_blocks) {
+    const float4* a4 = reinterpret_cast<const float4*>(prm.dq_acc);
+    uint4* out = reinterpret_cast<uint4*>(dq);
+    const float f = prm.scale;
+    for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n8; i += (long long)conv_blocks * 256) {
+      const float4 x = a4[2 * i], y = a4[2 * i + 1];
+      if constexpr (F16)
+        out[i] = make_uint4(pack_f16x2(x.x * f, x.y * f), pack_f16x2(x.z * f, x.w * f), pack_f16x2(y.x * f, y.y * f),
+                            pack_f16x2(y.z * f, y.w * f));
+      else
+        out[i] = make_uint4(pack_bf16x2(x.x * f, x.y * f), pack_bf16x2(x.z * f, x.w * f), pack_bf16x2(y.x * f, y.y * f),
+                            pack_bf16x2(y.z * f, y.w * f));
+    }
+    return;
+  }
   constexpr int E = D / 32;
-  const long long x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const long long x = (long long)(blockIdx.x - conv_blocks) * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
   const int row = (int)(x % kBK);
   const int which = (int)(x / kBK % 2);                     // 0: dK, 1: dV
@@ -814,6 +839,7 @@ __global__ void __launch_bounds__(256) bwd_sink_sum_kernel(const BwdParams prm) 
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
   const float* src = prm.part + ((unit * prm.sink_split * 2 + which) * kBK + row) * D + lane * E;
+#pragma unroll 4
   for (int s = 0; s < prm.sink_split; ++s, src += 2LL * kBK * D) {
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
@@ -859,6 +885,19 @@ cudaError_t launch_attn_bwd(const BwdLaunch& L) {
   const long long nkt = (L.prm.Nk + kBK - 1) / kBK;
   long long ctas = (long long)L.prm.BHkv * nkt;
   if constexpr (WIN) ctas += (long long)L.prm.BHkv * L.prm.sink_tiles * (L.prm.sink_split - 1);
+  if constexpr (WIN) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    cfg.blockDim = dim3(C::THREADS, 1, 1);
+    cfg.dynamicSmemBytes = C::SMEM_BYTES;
+    cfg.stream = L.stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, L.q, L.dout, L.k, L.v, L.dq_acc, L.dk, L.dv, L.prm);
+  }
   kern<<<(unsigned)ctas, C::THREADS, C::SMEM_BYTES, L.stream>>>(L.q, L.dout, L.k, L.v, L.dq_acc, L.dk, L.dv,
                                                                L.prm);
   return cudaGetLastError();
@@ -910,18 +949,27 @@ BwdWindow bwd_window_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_
   return w;
 }
 
-cudaError_t launch_bwd_sink_sum(const BwdParams& prm, int d, bool f16, cudaStream_t stream) {
-  const unsigned blocks = (unsigned)((long long)prm.sink_tiles * prm.BHkv * 2 * kBK / 8);
-  if (d == 64) {
-    if (f16) bwd_sink_sum_kernel<64, true><<<blocks, 256, 0, stream>>>(prm);
-    else bwd_sink_sum_kernel<64, false><<<blocks, 256, 0, stream>>>(prm);
-  } else if (d == 128) {
-    if (f16) bwd_sink_sum_kernel<128, true><<<blocks, 256, 0, stream>>>(prm);
-    else bwd_sink_sum_kernel<128, false><<<blocks, 256, 0, stream>>>(prm);
-  } else {
-    return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
+cudaError_t launch_bwd_window_finish(const BwdParams& prm, void* dq, long long elems, int d, bool f16,
+                                     cudaStream_t stream) {
+  const long long n8 = elems / 8;
+  const int conv = (int)stride_grid(n8);
+  const long long sum = prm.sink_split > 1 ? (long long)prm.sink_tiles * prm.BHkv * 2 * kBK / 8 : 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(conv + sum), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (d == 64)
+    return cudaLaunchKernelEx(&cfg, f16 ? bwd_window_finish_kernel<64, true> : bwd_window_finish_kernel<64, false>, prm, dq,
+                              n8, conv);
+  if (d == 128)
+    return cudaLaunchKernelEx(&cfg, f16 ? bwd_window_finish_kernel<128, true> : bwd_window_finish_kernel<128, false>, prm,
+                              dq, n8, conv);
+  return cudaErrorInvalidValue;
 }
 
 cudaError_t launch_bwd_prep(const void* o, const void* dout, const float* lse, float* vecs, float* dq_acc,

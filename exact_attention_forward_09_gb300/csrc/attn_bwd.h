@@ -54,9 +54,10 @@ struct BwdLaunch {
 template <int ELEM, int D, bool CAUSAL, bool WIN = false>
 cudaError_t launch_attn_bwd(const BwdLaunch& L);
 
-// dK = scale * sum of the parts' dK, dV = sum of their dV, rows below Nk of
-// the sink tiles.
-cudaError_t launch_bwd_sink_sum(const BwdParams& prm, int d, bool f16, cudaStream_t stream);
+// The end of the windowed backward: dq = RN(scale * dq_acc), and for the sink
+// tiles (rows below Nk) dK = scale * sum of the shares' dK, dV = sum of theirs.
+cudaError_t launch_bwd_window_finish(const BwdParams& prm, void* dq, long long elems, int d, bool f16,
+                                     cudaStream_t stream);
 
 // Records of -LSE_i * log2(e) and -D_i (D_i = dO_i . O_i) for every query
 // row, padded to nrec 64-row records per head, and dq_acc := 0.

@@ -298,6 +298,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
   // paged: this CTA's run [line0, line0 + line_n) of the line of key tiles
   long long line_per = 0, line0 = 0, line_n = 0;
   if constexpr (PAGED) {
+    pdl_launch();  // the join can be launched; it waits for this kernel's end
     // rows of a query tile that no TMA box covers (128 % g != 0) are zeros
     if (rpt < kBM) {
       for (int i = threadIdx.x; i < C::NQT * C::NCH * (kBM - rpt) * 8; i += C::THREADS) {

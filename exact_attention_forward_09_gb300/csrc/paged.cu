@@ -15,10 +15,39 @@ namespace {
 // ---------------------------------------------------------------- join --
 // Softmax over disjoint key sets is the LSE-weighted mean of the parts: with
 // m = max_s LSE_s and w_s = e^(LSE_s - m), O = sum_s w_s O_s / sum_s w_s and
-// LSE = m + ln sum_s w_s.  One block per row of a cut unit: its 8 warps take
-// the parts in turn (a single long context is cut into as many parts as half
-// the GPU has SMs), lane l holding columns l*E .. l*E+E-1, and meet in shared
-// memory in a fixed order.
+// LSE = m + ln sum_s w_s, summed in a fixed order.  Lane l holds columns l*E
+// .. l*E+E-1 of a row.  A unit cut in a few parts (chunks: up to 256 rows, two
+// or three parts) takes one warp per row; one cut in many (a single long
+// context: a few rows, as many parts as the GPU has SMs per head) takes a
+// block per row, whose warps share the parts and meet in shared memory.  The
+// bytes are the parts, just written and still in L2.
+constexpr int kFewParts = 8;
+
+// acc += sum over i < n of w_i * part s0 + i * step, lane i holding w_i
+template <int E, typename At>
+__device__ __forceinline__ void add_parts(float (&acc)[E], const float* __restrict__ o_part, At at, int s0, int step,
+                                          int n, float w, int D, int lane) {
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float wi = __shfl_sync(0xffffffffu, w, i);
+    const float* src = o_part + at(s0 + i * step) * D + lane * E;
+    float x[E];
+    if constexpr (E == 2) {
+      *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(x + e) = *reinterpret_cast<const float4*>(src + e);
+    }
+    // (a part without visible keys has weight 0 and zeros; one of a NaN row
+    // has weight NaN, and the row stays NaN)
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, x[e], acc[e]);
+  }
+}
+
+// e^(l - m), 0 for a part without visible keys
+__device__ __forceinline__ float part_weight(float l, float m) { return l == -INFINITY ? 0.0f : expf(l - m); }
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) paged_combine_kernel(const float* __restrict__ o_part,
                                                             const float* __restrict__ lse_part,
@@ -27,43 +56,72 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const float* __restr
   constexpr int E = D / 32;
   __shared__ float red[8][D];
   __shared__ float red_w[8];
+  pdl_wait();  // the parts and desc are the previous kernel's
   const int4 u = desc[blockIdx.x];
-  const int parts = u.x;
+  const int parts = u.x, rows = u.w;
+  if (parts == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  for (int row = blockIdx.y; parts > 0 && row < u.w; row += gridDim.y) {
-    auto at = [&](int s) -> long long {
-      const long long slot = s == 0 ? 2LL * blockIdx.x + 1 : 2LL * (blockIdx.x + s);
-      return slot * slot_rows + row;
-    };
+  int row = 0;
+  auto at = [&](int s) -> long long {
+    const long long slot = s == 0 ? 2LL * blockIdx.x + 1 : 2LL * (blockIdx.x + s);
+    return slot * slot_rows + row;
+  };
+  auto out_row = [&]() -> long long { return (long long)(u.y + row / g) * Hq + u.z * g + row % g; };
+  float acc[E];
+  if (parts <= kFewParts) {
+    for (row = blockIdx.y * 8 + warp; row < rows; row += gridDim.y * 8) {
+      const float l = lane < parts ? lse_part[at(lane)] : -INFINITY;
+      float m = l;
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      m = __shfl_sync(0xffffffffu, m, 0);  // (lanes 0 .. 7 hold all parts)
+      const float w = lane < parts ? part_weight(l, m) : 0.0f;
+      float total = w;
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
+      total = __shfl_sync(0xffffffffu, total, 0);
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+      add_parts<E>(acc, o_part, at, 0, 1, parts, w, D, lane);
+      const float inv = total != 0.0f ? 1.0f / total : 0.0f;
+      const long long r = out_row();
+      uint32_t pk[E / 2];
+#pragma unroll
+      for (int e = 0; e < E; e += 2)
+        pk[e / 2] = F16 ? pack_f16x2(acc[e] * inv, acc[e + 1] * inv) : pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(o) + r * (D / 2) + lane * (E / 2);
+      if constexpr (E == 2) dst[0] = pk[0];
+      else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(pk);
+      else *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<uint4*>(pk);
+      if (lane == 0) lse[r] = total == 0.0f ? -INFINITY : m + logf(total);
+    }
+    return;
+  }
+  for (row = blockIdx.y; row < rows; row += gridDim.y) {
     float m = -INFINITY;
     for (int s = lane; s < parts; s += 32) m = fmaxf(m, lse_part[at(s)]);
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float acc[E], wsum = 0.0f;
+    float wsum = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int s = warp; s < parts; s += 8) {
-      const float ls = lse_part[at(s)];
-      if (ls == -INFINITY) continue;  // a run without visible keys; a NaN row stays NaN
-      const float w = expf(ls - m);
+    for (int s0 = warp; s0 < parts; s0 += 8 * 32) {  // this warp's parts, 32 at a time
+      const int n = min(32, (parts - s0 + 7) / 8);
+      const float w = lane < n ? part_weight(lse_part[at(s0 + 8 * lane)], m) : 0.0f;
       wsum += w;
-      const float* src = o_part + at(s) * D + lane * E;
-#pragma unroll
-      for (int e = 0; e < E; e += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(src + e);
-        acc[e] = fmaf(w, x.x, acc[e]);
-        acc[e + 1] = fmaf(w, x.y, acc[e + 1]);
-      }
+      add_parts<E>(acc, o_part, at, s0, 8, n, w, D, lane);
     }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, d);
 #pragma unroll
     for (int e = 0; e < E; ++e) red[warp][lane * E + e] = acc[e];
     if (lane == 0) red_w[warp] = wsum;
     __syncthreads();
-    const long long orow = (long long)(u.y + row / g) * Hq + u.z * g + row % g;
     float total = 0.0f;
 #pragma unroll
     for (int w = 0; w < 8; ++w) total += red_w[w];
     const float inv = total != 0.0f ? 1.0f / total : 0.0f;
+    const long long r = out_row();
     if (threadIdx.x < D / 2) {
       float a = 0.0f, b = 0.0f;
 #pragma unroll
@@ -71,10 +129,10 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const float* __restr
         a += red[w][2 * threadIdx.x];
         b += red[w][2 * threadIdx.x + 1];
       }
-      reinterpret_cast<uint32_t*>(o)[orow * (D / 2) + threadIdx.x] =
+      reinterpret_cast<uint32_t*>(o)[r * (D / 2) + threadIdx.x] =
           F16 ? pack_f16x2(a * inv, b * inv) : pack_bf16x2(a * inv, b * inv);
     }
-    if (threadIdx.x == 0) lse[orow] = total == 0.0f ? -INFINITY : m + logf(total);
+    if (threadIdx.x == 0) lse[r] = total == 0.0f ? -INFINITY : m + logf(total);
     __syncthreads();  // red is read before the next row's sums
   }
 }
@@ -82,7 +140,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const float* __restr
 // -------------------------------------------------------------- append --
 // All bytes: each new q, k and v row is read once and written once.  One
 // block per token: its threads are D/16 column chunks (16 columns each: the
-// two 8-column halves of 8 rotary pairs) times 256/(D/16) heads, so a thread
+// two 8-column halves of 8 rotary pairs) times 128/(D/16) heads, so a thread
 // loads the 8 angles of its chunk once and uses them for every head it
 // takes.  The pair (a, b) becomes (a c - b s, a s + b c) in fp32, each
 // product rounded before the sum, rounded once to the element type.
@@ -113,11 +171,37 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 }
 
 template <int D, bool F16, int LAYOUT>  // LAYOUT 0: no rotation
-__global__ void __launch_bounds__(256) cache_append_kernel(const AppendParams prm) {
+__global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams prm) {
   constexpr int CL = D / 16;        // column chunks
-  constexpr int HL = 256 / CL;      // heads at a time
+  constexpr int HL = 128 / CL;      // heads at a time
+  constexpr int MORE = 4;           // rows in flight per thread
   const int t = blockIdx.x;
   const int lane = threadIdx.x & 31;
+  const int c = threadIdx.x % CL, h0 = threadIdx.x / CL;
+  // columns of the two 8-element pieces of this chunk
+  const int x0 = LAYOUT == FA_ROPE_HALF ? 8 * c : 16 * c;
+  const int x1 = LAYOUT == FA_ROPE_HALF ? D / 2 + 8 * c : 16 * c + 8;
+  const int rows = prm.Hq + 2 * prm.Hkv;
+  auto source = [&](int r) -> const uint16_t* {
+    if (r < prm.Hq) return prm.q + t * prm.q_stride + (long long)r * D;
+    r -= prm.Hq;
+    return r < prm.Hkv ? prm.k + t * prm.k_stride + (long long)r * D : prm.v + t * prm.v_stride + (long long)(r - prm.Hkv) * D;
+  };
+  uint4 u[MORE], w[MORE];
+  auto load = [&](int r0) {
+#pragma unroll
+    for (int i = 0; i < MORE; ++i) {
+      const int r = r0 + i * HL;
+      if (r < rows) {
+        const uint16_t* src = source(r);
+        u[i] = *reinterpret_cast<const uint4*>(src + x0);
+        w[i] = *reinterpret_cast<const uint4*>(src + x1);
+      }
+    }
+  };
+  // the first rows do not depend on where they go: their latency and that of
+  // the three dependent look-ups (sequence, lengths, page) pass together
+  load(h0);
   const int b = find_sequence(prm.cu_q, prm.B, t, lane);
   const int q0 = prm.cu_q[b], q1 = prm.cu_q[b + 1];
   if (t < q0 || t >= q1) return;  // a row that belongs to no sequence
@@ -130,10 +214,6 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendParams pr
     if (threadIdx.x == 0) atomicOr(prm.err, FA_DEVERR_INDEX);
     return;
   }
-  const int c = threadIdx.x % CL, h0 = threadIdx.x / CL;
-  // columns of the two 8-element pieces of this chunk
-  const int x0 = LAYOUT == FA_ROPE_HALF ? 8 * c : 16 * c;
-  const int x1 = LAYOUT == FA_ROPE_HALF ? D / 2 + 8 * c : 16 * c + 8;
   float cs[8], sn[8];
   if constexpr (LAYOUT != 0) {
     const float4* pc = reinterpret_cast<const float4*>(prm.cos + pos * (D / 2) + 8 * c);
@@ -144,68 +224,60 @@ __global__ void __launch_bounds__(256) cache_append_kernel(const AppendParams pr
     *reinterpret_cast<float4*>(sn + 4) = ps[1];
   }
   const long long slot = page * prm.page_stride + (pos & ((1 << prm.page_shift) - 1)) * prm.token_stride;
-  const int rows = prm.Hq + 2 * prm.Hkv;
-  for (int r = h0; r < rows; r += HL) {
-    const uint16_t* src;
-    uint16_t* dst;
-    bool turn = LAYOUT != 0;
-    if (r < prm.Hq) {
-      src = prm.q + t * prm.q_stride + (long long)r * D;
-      dst = prm.q_out + ((long long)t * prm.Hq + r) * D;
-    } else if (r < prm.Hq + prm.Hkv) {
-      const int h = r - prm.Hq;
-      src = prm.k + t * prm.k_stride + (long long)h * D;
-      dst = prm.k_pages + slot + h * prm.head_stride;
-    } else {
-      const int h = r - prm.Hq - prm.Hkv;
-      src = prm.v + t * prm.v_stride + (long long)h * D;
-      dst = prm.v_pages + slot + h * prm.head_stride;
-      turn = false;
-    }
-    uint4 u = *reinterpret_cast<const uint4*>(src + x0), w = *reinterpret_cast<const uint4*>(src + x1);
-    if (turn) {
-      uint32_t uu[4] = {u.x, u.y, u.z, u.w}, ww[4] = {w.x, w.y, w.z, w.w};
-      float a[8], z[8];  // the pairs' first and second elements
+  for (int r0 = h0; r0 < rows; r0 += MORE * HL) {
+    if (r0 != h0) load(r0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 f = unpack2<F16>(uu[i]), h = unpack2<F16>(ww[i]);
-        if constexpr (LAYOUT == FA_ROPE_HALF) {
-          a[2 * i] = f.x, a[2 * i + 1] = f.y, z[2 * i] = h.x, z[2 * i + 1] = h.y;
-        } else {
-          a[i] = f.x, z[i] = f.y, a[4 + i] = h.x, z[4 + i] = h.y;
+    for (int j = 0; j < MORE; ++j) {
+      const int r = r0 + j * HL;
+      if (r >= rows) break;
+      uint16_t* dst;
+      if (r < prm.Hq) dst = prm.q_out + ((long long)t * prm.Hq + r) * D;
+      else if (r < prm.Hq + prm.Hkv) dst = prm.k_pages + slot + (r - prm.Hq) * prm.head_stride;
+      else dst = prm.v_pages + slot + (r - prm.Hq - prm.Hkv) * prm.head_stride;
+      if (LAYOUT != 0 && r < prm.Hq + prm.Hkv) {
+        uint32_t uu[4] = {u[j].x, u[j].y, u[j].z, u[j].w}, ww[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+        float a[8], z[8];  // the pairs' first and second elements
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 f = unpack2<F16>(uu[i]), h = unpack2<F16>(ww[i]);
+          if constexpr (LAYOUT == FA_ROPE_HALF) {
+            a[2 * i] = f.x, a[2 * i + 1] = f.y, z[2 * i] = h.x, z[2 * i + 1] = h.y;
+          } else {
+            a[i] = f.x, z[i] = f.y, a[4 + i] = h.x, z[4 + i] = h.y;
+          }
         }
-      }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float p = __fsub_rn(__fmul_rn(a[i], cs[i]), __fmul_rn(z[i], sn[i]));
-        const float q = __fadd_rn(__fmul_rn(a[i], sn[i]), __fmul_rn(z[i], cs[i]));
-        a[i] = p;
-        z[i] = q;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if constexpr (LAYOUT == FA_ROPE_HALF) {
-          uu[i] = pack2<F16>(a[2 * i], a[2 * i + 1]);
-          ww[i] = pack2<F16>(z[2 * i], z[2 * i + 1]);
-        } else {
-          uu[i] = pack2<F16>(a[i], z[i]);
-          ww[i] = pack2<F16>(a[4 + i], z[4 + i]);
+        for (int i = 0; i < 8; ++i) {
+          const float p = __fsub_rn(__fmul_rn(a[i], cs[i]), __fmul_rn(z[i], sn[i]));
+          const float q = __fadd_rn(__fmul_rn(a[i], sn[i]), __fmul_rn(z[i], cs[i]));
+          a[i] = p;
+          z[i] = q;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (LAYOUT == FA_ROPE_HALF) {
+            uu[i] = pack2<F16>(a[2 * i], a[2 * i + 1]);
+            ww[i] = pack2<F16>(z[2 * i], z[2 * i + 1]);
+          } else {
+            uu[i] = pack2<F16>(a[i], z[i]);
+            ww[i] = pack2<F16>(a[4 + i], z[4 + i]);
+          }
+        }
+        u[j] = make_uint4(uu[0], uu[1], uu[2], uu[3]);
+        w[j] = make_uint4(ww[0], ww[1], ww[2], ww[3]);
       }
-      u = make_uint4(uu[0], uu[1], uu[2], uu[3]);
-      w = make_uint4(ww[0], ww[1], ww[2], ww[3]);
+      *reinterpret_cast<uint4*>(dst + x0) = u[j];
+      *reinterpret_cast<uint4*>(dst + x1) = w[j];
     }
-    *reinterpret_cast<uint4*>(dst + x0) = u;
-    *reinterpret_cast<uint4*>(dst + x1) = w;
   }
 }
 
 template <int D, bool F16>
 cudaError_t append_layout(const AppendParams& prm, int layout, cudaStream_t stream) {
   const unsigned grid = (unsigned)prm.T;
-  if (layout == 0) cache_append_kernel<D, F16, 0><<<grid, 256, 0, stream>>>(prm);
-  else if (layout == FA_ROPE_HALF) cache_append_kernel<D, F16, FA_ROPE_HALF><<<grid, 256, 0, stream>>>(prm);
-  else cache_append_kernel<D, F16, FA_ROPE_INTERLEAVED><<<grid, 256, 0, stream>>>(prm);
+  if (layout == 0) cache_append_kernel<D, F16, 0><<<grid, 128, 0, stream>>>(prm);
+  else if (layout == FA_ROPE_HALF) cache_append_kernel<D, F16, FA_ROPE_HALF><<<grid, 128, 0, stream>>>(prm);
+  else cache_append_kernel<D, F16, FA_ROPE_INTERLEAVED><<<grid, 128, 0, stream>>>(prm);
   return cudaGetLastError();
 }
 
@@ -223,15 +295,25 @@ cudaError_t launch_cache_append(const AppendParams& prm, int d, bool f16, int la
 cudaError_t launch_paged_combine(const float* o_part, const float* lse_part, const int4* desc, void* o, float* lse,
                                  int ctas, int slot_rows, int max_rows, int g, int Hq, int d, bool f16,
                                  cudaStream_t stream) {
-  const dim3 grid((unsigned)ctas, (unsigned)(max_rows < 32 ? max_rows : 32), 1);
-  auto go = [&](auto kern) { kern<<<grid, 256, 0, stream>>>(o_part, lse_part, desc, o, lse, slot_rows, g, Hq); };
+  // launched while the attention kernel still runs; it waits for it itself
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(max_rows < 32 ? max_rows : 32), 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  auto go = [&](auto kern) {
+    return cudaLaunchKernelEx(&cfg, kern, o_part, lse_part, desc, o, lse, slot_rows, g, Hq);
+  };
   switch (d) {
-    case 64: f16 ? go(paged_combine_kernel<64, true>) : go(paged_combine_kernel<64, false>); break;
-    case 128: f16 ? go(paged_combine_kernel<128, true>) : go(paged_combine_kernel<128, false>); break;
-    case 256: f16 ? go(paged_combine_kernel<256, true>) : go(paged_combine_kernel<256, false>); break;
+    case 64: return f16 ? go(paged_combine_kernel<64, true>) : go(paged_combine_kernel<64, false>);
+    case 128: return f16 ? go(paged_combine_kernel<128, true>) : go(paged_combine_kernel<128, false>);
+    case 256: return f16 ? go(paged_combine_kernel<256, true>) : go(paged_combine_kernel<256, false>);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace fa

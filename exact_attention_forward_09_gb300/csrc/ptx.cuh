@@ -190,6 +190,15 @@ __device__ __forceinline__ void bar_sync_n(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// --------------------------------------------------- dependent launches --
+// In a kernel launched with programmatic stream serialisation: waits until
+// the kernel before it in the stream has ended and its writes are visible
+// (returns at once otherwise).
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel of the stream be launched, if it was asked for so,
+// once every CTA of this one has come here or ended.
+__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ------------------------------------------------- register reallocation --
 // Executed by all threads of a warpgroup: shrink / grow its per-thread
 // register budget (multiples of 8 in [24, 256]).

@@ -232,7 +232,7 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   p.page_shift = shift_of(cache->page_size);
   p.g = (int)g;
   p.tpt = (int)tpt;
-  p.min_tiles = 4;
+  p.min_tiles = 1;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   p.o_part = reinterpret_cast<float*>(w);
   p.lse_part = reinterpret_cast<float*>(w + ws.lse_at);
