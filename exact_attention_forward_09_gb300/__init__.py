@@ -347,10 +347,32 @@ def _scale(scale, d):
     return 1.0 / math.sqrt(d) if scale is None else float(scale)
 
 
-def _check_out(name, t, shape, dtype, device):
-    if not isinstance(t, torch.Tensor) or tuple(t.shape) != tuple(shape) or t.dtype != dtype \
-            or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on {device}")
+def _check_out(name, t, shape, dtype, index):
+    if not isinstance(t, torch.Tensor) or t.shape != shape or t.dtype is not dtype or t.get_device() != index \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)} tensor on cuda:{index}")
+
+
+def _workspace(t, index):
+    """The address and size of a caller's workspace."""
+    if not isinstance(t, torch.Tensor) or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{index}")
+    return t.data_ptr(), t.nbytes
+
+
+def _dense(q, k, v):
+    """(B, Hq, Nq, d, Hkv, Nk, device index) of checked dense q, k, v."""
+    if isinstance(q, torch.Tensor) and isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor):
+        sq, sk, dt, index = q.shape, k.shape, q.dtype, q.get_device()
+        if len(sq) == 4 and len(sk) == 4 and v.shape == sk and dt in _TYPES and k.dtype is dt and v.dtype is dt \
+                and index >= 0 and k.get_device() == index and v.get_device() == index and q.is_contiguous() \
+                and k.is_contiguous() and v.is_contiguous():
+            B, Hq, Nq, d = sq
+            Bk, Hkv, Nk, dk = sk
+            if Bk == B and dk == d and Hkv > 0 and Hq % Hkv == 0:
+                return B, Hq, Nq, d, Hkv, Nk, index
+    _check_gqa(q, k, v, (torch.bfloat16, torch.float16))  # says what is wrong
+    raise ValueError("q, k and v are not dense 16-bit CUDA tensors of one device")
 
 
 def fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, sinks: int = 0,
@@ -359,23 +381,21 @@ def fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, s
     Hq, Nq, d], k/v [B, Hkv, Nk, d]; query i at position p = i + Nk - Nq sees
     key j iff j <= p and (j > p - window or j < sinks).  Returns
     (O [B, Hq, Nq, d], LSE [B, Hq, Nq])."""
-    _check_gqa(q, k, v, (torch.bfloat16, torch.float16))
-    B, Hq, Nq, d = q.shape
-    Hkv, Nk = k.shape[1], k.shape[2]
+    B, Hq, Nq, d, Hkv, Nk, index = _dense(q, k, v)
     if out is None:
         out = torch.empty_like(q)
     else:
-        _check_out("out", out, q.shape, q.dtype, q.device)
+        _check_out("out", out, (B, Hq, Nq, d), q.dtype, index)
     if lse is None:
         lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
     else:
-        _check_out("lse", lse, (B, Hq, Nq), torch.float32, q.device)
-    index = q.get_device()
+        _check_out("lse", lse, (B, Hq, Nq), torch.float32, index)
     with _guard(index):
         st = _lib().fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                                   B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks), _scale(scale, d), _TYPES[q.dtype],
                                   _current_stream(index))
-    _check(st, "fa_fwd_window")
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_window")
     return out, lse
 
 
@@ -384,7 +404,7 @@ def bwd_window_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: i
     n = ctypes.c_size_t(0)
     _check(_lib().fa_bwd_window_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks), ctypes.byref(n)),
            "fa_bwd_window_workspace_bytes")
-    return int(n.value)
+    return n.value
 
 
 def bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
@@ -395,77 +415,86 @@ def bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
     out, dout [B, Hq, Nq, d], k/v [B, Hkv, Nk, d], lse [B, Hq, Nq] fp32 from
     the forward with the same window, sinks and scale; d 64 or 128.  Returns
     (dq, dk, dv)."""
-    _check_gqa(q, k, v, (torch.bfloat16, torch.float16))
-    B, Hq, Nq, d = q.shape
-    Hkv, Nk = k.shape[1], k.shape[2]
-    for name, t in (("out", out), ("dout", dout)):
-        _check_out(name, t, q.shape, q.dtype, q.device)
-    _check_out("lse", lse, (B, Hq, Nq), torch.float32, q.device)
-    grads = []
-    for name, t, x in (("dq", dq, q), ("dk", dk, k), ("dv", dv, v)):
-        if t is None:
-            t = torch.empty_like(x)
-        else:
-            _check_out(name, t, x.shape, x.dtype, x.device)
-        grads.append(t)
-    index = q.get_device()
+    B, Hq, Nq, d, Hkv, Nk, index = _dense(q, k, v)
+    dt = q.dtype
+    _check_out("out", out, q.shape, dt, index)
+    _check_out("dout", dout, q.shape, dt, index)
+    _check_out("lse", lse, (B, Hq, Nq), torch.float32, index)
+    if dq is None:
+        dq = torch.empty_like(q)
+    else:
+        _check_out("dq", dq, q.shape, dt, index)
+    if dk is None:
+        dk = torch.empty_like(k)
+    else:
+        _check_out("dk", dk, k.shape, dt, index)
+    if dv is None:
+        dv = torch.empty_like(v)
+    else:
+        _check_out("dv", dv, v.shape, dt, index)
     with _guard(index):
         if workspace is None:
             need = bwd_window_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, window, sinks)
-            workspace = torch.empty((max(need, 1),), dtype=torch.uint8, device=q.device)
+            workspace = torch.empty((need or 1,), dtype=torch.uint8, device=q.device)
         st = _lib().fa_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                  dout.data_ptr(), *[t.data_ptr() for t in grads], B, Hq, Hkv, Nq, Nk, d,
-                                  int(window), int(sinks), _scale(scale, d), _TYPES[q.dtype], workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), _current_stream(index))
-    _check(st, "fa_bwd_window")
-    return tuple(grads)
+                                  dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Nq, Nk, d,
+                                  int(window), int(sinks), _scale(scale, d), _TYPES[dt],
+                                  *_workspace(workspace, index), _current_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_bwd_window")
+    return dq, dk, dv
 
 
 def _cache(k_pages, v_pages):
     """The ``fa_kv_cache`` of two [num_pages, heads, page_size, d] tensors (or
-    views of that shape with other strides)."""
-    for name, t in (("k_pages", k_pages), ("v_pages", v_pages)):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 4:
-            raise ValueError(f"{name} must be a [num_pages, heads, page_size, d] CUDA tensor")
-        if t.dtype not in _TYPES:
-            raise ValueError(f"{name} has dtype {t.dtype}; expected bf16 or fp16")
-        if t.stride(3) != 1:
-            raise ValueError(f"{name} must have its last dimension contiguous")
-    if k_pages.shape != v_pages.shape or k_pages.stride() != v_pages.stride() or k_pages.dtype != v_pages.dtype \
-            or k_pages.device != v_pages.device:
-        raise ValueError("k_pages and v_pages must share shape, strides, dtype and device")
-    n, h, ps, d = k_pages.shape
-    sp, sh, st, _ = k_pages.stride()
-    return _KvCache(k_pages.data_ptr(), v_pages.data_ptr(), n, ps, h, d, sp, sh, st, _TYPES[k_pages.dtype])
+    views of that shape with other strides), and their device index."""
+    if isinstance(k_pages, torch.Tensor) and isinstance(v_pages, torch.Tensor):
+        shape, stride, dt, index = k_pages.shape, k_pages.stride(), k_pages.dtype, k_pages.get_device()
+        if len(shape) == 4 and index >= 0 and dt in _TYPES and stride[3] == 1 and v_pages.shape == shape \
+                and v_pages.stride() == stride and v_pages.dtype is dt and v_pages.get_device() == index:
+            n, h, ps, d = shape
+            return _KvCache(k_pages.data_ptr(), v_pages.data_ptr(), n, ps, h, d, stride[0], stride[1], stride[2],
+                            _TYPES[dt]), index
+    raise ValueError("k_pages and v_pages must be bf16 or fp16 [num_pages, heads, page_size, d] CUDA tensors of one shape, "
+                     "dtype, device and strides, their last dimension contiguous")
 
 
-def _check_batch(block_table, cu_q, seq_k, device):
+def _check_batch(block_table, cu_q, seq_k, index):
     """(B, table stride, table width) of a ragged batch's index tensors."""
-    for name, t, dim in (("block_table", block_table, 2), ("cu_q", cu_q, 1), ("seq_k", seq_k, 1)):
-        if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != dim or t.device != device \
-                or (t.numel() > 0 and t.stride(-1) != 1):
-            raise ValueError(f"{name} must be a {dim}-D int32 tensor on {device} with its last dimension contiguous")
-    B = seq_k.shape[0]
-    if block_table.shape[0] != B or cu_q.shape[0] != B + 1:
-        raise ValueError("block_table must be [B, max_pages], cu_q [B + 1] and seq_k [B]")
-    return B, block_table.stride(0), block_table.shape[1]
+    if isinstance(block_table, torch.Tensor) and isinstance(cu_q, torch.Tensor) and isinstance(seq_k, torch.Tensor):
+        i32, st, sc, sk = torch.int32, block_table.shape, cu_q.shape, seq_k.shape
+        if len(st) == 2 and len(sc) == 1 and len(sk) == 1 and block_table.dtype is i32 and cu_q.dtype is i32 \
+                and seq_k.dtype is i32 and block_table.get_device() == index and cu_q.get_device() == index \
+                and seq_k.get_device() == index and st[0] == sk[0] and sc[0] == sk[0] + 1 and cu_q.is_contiguous() \
+                and seq_k.is_contiguous() and (st[1] < 2 or block_table.stride(1) == 1):
+            return sk[0], block_table.stride(0), st[1]
+    raise ValueError(f"block_table [B, max_pages], cu_q [B + 1] and seq_k [B] must be int32 tensors on cuda:{index}, "
+                     "cu_q and seq_k contiguous, and so each row of block_table")
 
 
-def _check_tokens(name, t, T, heads, d, dtype, device):
+def _check_tokens(name, t, T, heads, d, dtype, index):
     """The token stride of a packed [T, heads, d] tensor."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype != dtype or t.device != device \
-            or t.shape[0] != T or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be a {dtype} [T, heads, d] tensor on {device}")
-    if t.numel() > 0 and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != d)):
-        raise ValueError(f"{name} must have each token's heads contiguous")
-    return t.stride(0)
+    if isinstance(t, torch.Tensor):
+        shape = t.shape
+        if len(shape) == 3 and t.dtype is dtype and t.get_device() == index and shape[0] == T and shape[1] == heads \
+                and shape[2] == d:
+            stride = t.stride()
+            if t.numel() == 0 or (stride[2] == 1 and (heads == 1 or stride[1] == d)):
+                return stride[0]
+    raise ValueError(f"{name} must be a {dtype} [{T}, {heads}, {d}] tensor on cuda:{index}, the heads of a token contiguous")
+
+
+_PAGED_BYTES = {}  # by device index and head dimension
 
 
 def paged_workspace_bytes(d: int) -> int:
     """Bytes of device workspace ``fwd_paged`` needs on the current device."""
-    n = ctypes.c_size_t(0)
-    _check(_lib().fa_paged_workspace_bytes(d, ctypes.byref(n)), "fa_paged_workspace_bytes")
-    return int(n.value)
+    key = (torch.cuda.current_device(), d)
+    if key not in _PAGED_BYTES:
+        n = ctypes.c_size_t(0)
+        _check(_lib().fa_paged_workspace_bytes(d, ctypes.byref(n)), "fa_paged_workspace_bytes")
+        _PAGED_BYTES[key] = n.value
+    return _PAGED_BYTES[key]
 
 
 def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
@@ -479,33 +508,33 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, blo
     ``window`` None: every key up to a query's own.  ``max_q``: the most new
     tokens of any sequence, if known.  Returns (O [T, Hq, d], LSE [T, Hq]);
     rows outside every sequence are left as they were."""
-    cache = _cache(k_pages, v_pages)
-    dev = k_pages.device
+    cache, index = _cache(k_pages, v_pages)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [T, Hq, d] CUDA tensor")
     T, Hq, d = q.shape
-    q_stride = _check_tokens("q", q, T, None, cache.d, k_pages.dtype, dev)
-    B, table_stride, max_pages = _check_batch(block_table, cu_q, seq_k, dev)
+    dt = k_pages.dtype
+    q_stride = _check_tokens("q", q, T, Hq, cache.d, dt, index)
+    B, table_stride, max_pages = _check_batch(block_table, cu_q, seq_k, index)
     if cache.heads == 0 or Hq % cache.heads != 0:
         raise ValueError("the number of query heads must be a multiple of the number of key/value heads")
+    dev = k_pages.device
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=q.dtype, device=dev)
+        out = torch.empty((T, Hq, d), dtype=dt, device=dev)
     else:
-        _check_out("out", out, (T, Hq, d), q.dtype, dev)
+        _check_out("out", out, (T, Hq, d), dt, index)
     if lse is None:
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
     else:
-        _check_out("lse", lse, (T, Hq), torch.float32, dev)
-    index = k_pages.get_device()
+        _check_out("lse", lse, (T, Hq), torch.float32, index)
     with _guard(index):
         if workspace is None:
             workspace = torch.empty((paged_workspace_bytes(d),), dtype=torch.uint8, device=dev)
-        st = _lib().fa_fwd_paged(q.data_ptr(), ctypes.byref(cache), out.data_ptr(), lse.data_ptr(),
-                                 block_table.data_ptr(), table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(),
-                                 B, T, Hq, q_stride, int(max_q), 1 << 30 if window is None else int(window),
-                                 int(sinks), _scale(scale, d), workspace.data_ptr(),
-                                 workspace.numel() * workspace.element_size(), _current_stream(index))
-    _check(st, "fa_fwd_paged")
+        st = _lib().fa_fwd_paged(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
+                                 table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), B, T, Hq, q_stride,
+                                 int(max_q), 1 << 30 if window is None else int(window), int(sinks), _scale(scale, d),
+                                 *_workspace(workspace, index), _current_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_fwd_paged")
     return out, lse
 
 
@@ -519,42 +548,42 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     Hq, d] if given, are rotated by their positions first.  k, v and q may be
     slices of one projection.  Returns the rotated queries (``q_out``), or
     None without q."""
-    cache = _cache(k_pages, v_pages)
-    dev, dt = k_pages.device, k_pages.dtype
+    cache, index = _cache(k_pages, v_pages)
+    dt, d, heads = k_pages.dtype, cache.d, cache.heads
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be a [T, heads, d] CUDA tensor")
     T = k.shape[0]
-    ks = _check_tokens("k", k, T, cache.heads, cache.d, dt, dev)
-    vs = _check_tokens("v", v, T, cache.heads, cache.d, dt, dev)
-    B, table_stride, max_pages = _check_batch(block_table, cu_q, seq_k, dev)
+    ks = _check_tokens("k", k, T, heads, d, dt, index)
+    vs = _check_tokens("v", v, T, heads, d, dt, index)
+    B, table_stride, max_pages = _check_batch(block_table, cu_q, seq_k, index)
     Hq, qs, qp, op = 0, 0, None, None
     if q is not None:
-        qs = _check_tokens("q", q, T, None, cache.d, dt, dev)
-        Hq = q.shape[1]
+        Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
+        qs = _check_tokens("q", q, T, Hq, d, dt, index)
         if q_out is None:
-            q_out = torch.empty((T, Hq, cache.d), dtype=dt, device=dev)
+            q_out = torch.empty((T, Hq, d), dtype=dt, device=k_pages.device)
         else:
-            _check_out("q_out", q_out, (T, Hq, cache.d), dt, dev)
+            _check_out("q_out", q_out, (T, Hq, d), dt, index)
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
     cp, sp, n, layout = None, None, 0, 0
     if rope is not None:
         cos, sin, layout = rope
-        n = cos.shape[0]
-        for nm, t in (("cos", cos), ("sin", sin)):
-            if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_contiguous() \
-                    or tuple(t.shape) != (n, cache.d // 2) or t.device != dev:
-                raise ValueError(f"rope {nm} must be a contiguous fp32 [positions, d/2] tensor on {dev}")
         if layout not in (FA_ROPE_INTERLEAVED, FA_ROPE_HALF):
             raise ValueError("rope layout must be FA_ROPE_INTERLEAVED or FA_ROPE_HALF")
+        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+            raise ValueError("rope cos must be a [positions, d/2] tensor")
+        n = cos.shape[0]
+        _check_out("rope cos", cos, (n, d // 2), torch.float32, index)
+        _check_out("rope sin", sin, (n, d // 2), torch.float32, index)
         cp, sp = cos.data_ptr(), sin.data_ptr()
-    index = k_pages.get_device()
     with _guard(index):
-        st = _lib().fa_cache_append(ctypes.byref(cache), qp, k.data_ptr(), v.data_ptr(), op, qs, ks, vs,
-                                    block_table.data_ptr(), table_stride, max_pages, cu_q.data_ptr(),
-                                    seq_k.data_ptr(), B, T, Hq, cp, sp, n, int(layout), _current_stream(index))
-    _check(st, "fa_cache_append")
+        st = _lib().fa_cache_append(cache, qp, k.data_ptr(), v.data_ptr(), op, qs, ks, vs, block_table.data_ptr(),
+                                    table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), B, T, Hq, cp, sp, n,
+                                    int(layout), _current_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_append")
     return q_out
 
 

@@ -259,7 +259,9 @@ def test_paged_refusals(fa):
     for kw in (dict(q=q.float()), dict(q=q[:, :3]), dict(q=q[:, :, :64]), dict(k_pages=c.k.half()), dict(cu_q=cu.long()),
                dict(cu_q=cu[:2]), dict(seq_k=sk.cpu()), dict(block_table=c.table[:1]), dict(q=q.transpose(0, 1)),
                dict(out=torch.empty((2, 4, 128), dtype=torch.bfloat16, device="cuda")),
-               dict(lse=torch.empty((3, 4), dtype=torch.float64, device="cuda"))):
+               dict(lse=torch.empty((3, 4), dtype=torch.float64, device="cuda")),
+               dict(workspace=torch.empty((1 << 28,), dtype=torch.uint8)),
+               dict(workspace=torch.empty((1,), dtype=torch.uint8, device="cuda").expand(1 << 28))):
         with pytest.raises(ValueError):
             ok(**kw)
     for kw in (dict(window=0), dict(sinks=-1), dict(scale=math.nan), dict(max_q=-1),
