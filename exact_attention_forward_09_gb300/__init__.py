@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 import os
 
@@ -399,6 +400,7 @@ def fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, s
     return out, lse
 
 
+@functools.lru_cache(maxsize=256)
 def bwd_window_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int, window: int, sinks: int = 0) -> int:
     """Bytes of device workspace ``bwd_window`` needs for this shape."""
     n = ctypes.c_size_t(0)

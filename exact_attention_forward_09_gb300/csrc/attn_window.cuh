@@ -108,6 +108,7 @@ struct WinParams {
   int N, Nk;          // query rows / keys per head
   int BH;             // batch x query heads
   int head_chunk;     // heads taken together, heaviest units first (see attn_fwd.cuh)
+  int pair_units;     // units that hold two query tiles; the groups behind them run as units of one
   // paged
   const int* cu_q;    // [B + 1] first token of each sequence in q
   const int* seq_k;   // [B] keys per sequence, the new tokens' included
@@ -118,7 +119,7 @@ struct WinParams {
   int num_pages, page_shift;
   int g;              // query heads per key/value head
   int tpt;            // tokens per query tile (tpt * g <= 128)
-  int min_tiles;      // a CTA's run of the line is at least this long
+  int min_places;     // a CTA's run of the line is at least this long
   float* o_part;      // [2 * grid][NQT * 128][D] partial results of cut units
   float* lse_part;    // [2 * grid][NQT * 128]
   int4* desc;         // [grid] cut units: {parts, first token, kv head, rows}
@@ -187,12 +188,12 @@ struct WinPart {
   int sa, la, lb;
   __device__ __forceinline__ WinPart(const WinUnit& w, int t)
       : sa(t ? w.sa[1] : w.sa[0]), la(t ? w.la[1] : w.la[0]), lb(t ? w.lb[1] : w.lb[0]) {}
-  __device__ __forceinline__ bool has(int l) const { return l < sa || (l >= la && l < lb); }
   __device__ __forceinline__ int count(int r0, int r1) const {  // of [r0, r1)
     return max(0, min(r1, sa) - r0) + max(0, min(r1, lb) - max(r0, la));
   }
+  // the first of them at or behind l, where there is one
+  __device__ __forceinline__ int from(int l) const { return l < sa || l >= la ? l : la; }
 };
-__device__ __forceinline__ bool win_active(const WinUnit& w, int t, int l) { return WinPart(w, t).has(l); }
 __device__ __forceinline__ int win_count(const WinUnit& w, int t) { return WinPart(w, t).count(w.r0, w.r1); }
 
 template <int NS>
@@ -207,10 +208,10 @@ struct WinBars {
   uint64_t unit_full[2], unit_empty[2];
   alignas(16) uint32_t clc_resp[4];
   WinUnit unit[2];
-  // the line of work (paged): per-warp sums, then where this CTA's run starts
-  long long warp_sum[12];
-  long long start_off;
-  int start_b;
+  // the line of work (paged): per-warp sums, then the unit this CTA's run starts in
+  uint32_t warp_sum[12];
+  int start_b, start_tok0, start_nq, start_nk, start_group, start_len, start_at;
+  uint32_t start_off;
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -221,9 +222,8 @@ struct WinBars {
 struct WinSeq {
   int tok0, nq, nk;
 };
-__device__ __forceinline__ WinSeq win_seq(const WinParams& prm, int b, bool* bad) {
+__device__ __forceinline__ WinSeq win_seq(const WinParams& prm, int a, int e, int n, bool* bad) {
   WinSeq s;
-  const int a = prm.cu_q[b], e = prm.cu_q[b + 1], n = prm.seq_k[b];
   s.tok0 = min(max(a, 0), prm.T);
   const int end = min(max(e, s.tok0), prm.T);
   s.nq = end - s.tok0;
@@ -243,10 +243,40 @@ __device__ __forceinline__ int win_group_len(const WinParams& prm, const WinSeq&
   const int len = w1 - max(0, w0 - sk);
   return len > 0 ? len : 1;
 }
+// Places on the line of a unit of `len` key tiles: two to a tile when both
+// query tiles are in use (such a step takes 1.8 times a single one's time),
+// one otherwise, rounded up to even, so that CTAs, which start at even
+// places, start at whole tiles.  (One query tile per CTA, d = 256: one each.)
+template <int NQT>
+__device__ __forceinline__ uint32_t win_places(int len, int ntok, int tpt) {
+  if (NQT == 1) return (uint32_t)len;
+  return ntok > tpt ? 2u * (uint32_t)len : ((uint32_t)len + 1u) & ~1u;
+}
 
 // bits [0, n) of a 32-bit word, n clamped to 0..32
 __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : (0xffffffffu >> (32 - (n < 32 ? n : 32)));
+}
+
+// Waits for the V tile at ring position pv and, where `dead`, zeroes this
+// thread's row of it (row: its shared-memory address in slot 0); made visible
+// to the tensor core.  Out of line: it runs once or twice per unit.
+template <typename C, typename Bars>
+__device__ __noinline__ bool clear_v_row(Bars* bars, uint32_t row, int pv, bool dead, int* err) {
+  for (int sp = 0; sp < C::SPT; ++sp)
+    if (!__all_sync(0xffffffffu, mbar_wait(&bars->full[(pv + sp) % C::NS], (uint32_t)(((pv + sp) / C::NS) & 1),
+                                           &bars->abort_flag, err)))
+      return false;
+  if (dead) {
+#pragma unroll 1
+    for (int ch = 0; ch < C::NCH; ++ch) {
+      const uint32_t at = row + ((pv + ch / C::SLOT_CH) % C::NS) * C::SLOT_BYTES + (ch % C::SLOT_CH) * C::CHUNK_BYTES;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) st_shared_v4(at + 16 * i, 0u, 0u, 0u, 0u);
+    }
+  }
+  fence_proxy_async_smem();
+  return true;
 }
 
 template <int ELEM, int D, bool PAGED>
@@ -269,6 +299,16 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
   const int rpt = tpt * g;                 // rows per query tile
   const int tpg = C::NQT * tpt;            // tokens per unit
 
+  // paged: the lengths of this thread's first sequence are asked for first,
+  // so that their latency passes during the set-up below
+  int seq_a = 0, seq_e = 0, seq_n = 0;
+  const int seq_share = PAGED ? (prm.B + C::THREADS - 1) / C::THREADS : 0;  // sequences per thread
+  const int seq_b0 = PAGED ? min(prm.B, (int)threadIdx.x * seq_share) : 0;
+  if (PAGED && seq_b0 < prm.B) {
+    seq_a = prm.cu_q[seq_b0];
+    seq_e = prm.cu_q[seq_b0 + 1];
+    seq_n = prm.seq_k[seq_b0];
+  }
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
@@ -295,8 +335,17 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
     tmem_relinquish();
   }
 
-  // paged: this CTA's run [line0, line0 + line_n) of the line of key tiles
-  long long line_per = 0, line0 = 0, line_n = 0;
+  if (warp == C::LOAD_WARP && lane == 0) {
+    tma_prefetch_desc(&tm_q);
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+  }
+
+  // paged: this CTA's run [line0, line0 + line_n) of the line of work.  (The
+  // host refuses batches whose line could pass 2^31 places; token ranges that
+  // overlap, against the contract, may wrap it: the results are then wrong,
+  // but every index below is checked where it is used.)
+  uint32_t line_per = 0, line0 = 0, line_n = 0;
   if constexpr (PAGED) {
     pdl_launch();  // the join can be launched; it waits for this kernel's end
     // rows of a query tile that no TMA box covers (128 % g != 0) are zeros
@@ -308,46 +357,67 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
       fence_proxy_async_smem();
     }
     if (threadIdx.x == 0) prm.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
-    // each thread sums the key tiles of a contiguous share of the sequences
+    // each thread sums the places of a contiguous share of the sequences
     bool bad = false;
-    const int share = (prm.B + C::THREADS - 1) / C::THREADS;
-    const int b0 = min(prm.B, (int)threadIdx.x * share), b1 = min(prm.B, b0 + share);
-    auto seq_len = [&](int b) -> long long {
-      const WinSeq s = win_seq(prm, b, &bad);
-      long long n = 0;
-      for (int i = 0; i * tpg < s.nq; ++i) n += win_group_len(prm, s, tpg, i);
-      return n * prm.Hkv;
+    const int b1 = min(prm.B, seq_b0 + seq_share);
+    auto seq_of = [&](int b) -> WinSeq {
+      if (b == seq_b0) return win_seq(prm, seq_a, seq_e, seq_n, &bad);
+      return win_seq(prm, prm.cu_q[b], prm.cu_q[b + 1], prm.seq_k[b], &bad);
     };
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += seq_len(b);
-    long long incl = mine;
+    auto group_places = [&](const WinSeq& q, int i) -> uint32_t {
+      return win_places<C::NQT>(win_group_len(prm, q, tpg, i), min(tpg, q.nq - i * tpg), tpt) * (uint32_t)prm.Hkv;
+    };
+    auto seq_places = [&](const WinSeq& q) -> uint32_t {
+      uint32_t n = 0;
+      for (int i = 0; i * tpg < q.nq; ++i) n += group_places(q, i);
+      return n;
+    };
+    uint32_t mine = 0;
+    for (int b = seq_b0; b < b1; ++b) mine += seq_places(seq_of(b));
+    uint32_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const long long x = __shfl_up_sync(0xffffffffu, incl, d);
+      const uint32_t x = __shfl_up_sync(0xffffffffu, incl, d);
       if (lane >= d) incl += x;
     }
     if (lane == 31) bars->warp_sum[warp] = incl;
     __syncthreads();
-    long long before = 0, total = 0;
+    uint32_t before = 0, total = 0;
 #pragma unroll
     for (int w = 0; w < C::THREADS / 32; ++w) {
-      const long long x = bars->warp_sum[w];
+      const uint32_t x = bars->warp_sum[w];
       if (w < warp) before += x;
       total += x;
     }
     line_per = (total + gridDim.x - 1) / gridDim.x;
-    if (line_per < prm.min_tiles) line_per = prm.min_tiles;
+    if (line_per < (uint32_t)prm.min_places) line_per = prm.min_places;
+    line_per = (line_per + 1) & ~1u;
     line0 = line_per * blockIdx.x;
-    line_n = total - line0 < line_per ? total - line0 : line_per;
-    long long at = before + incl - mine;
-    if (line0 >= at && line0 < at + mine) {
-      int b = b0;
-      for (; b < b1; ++b) {
-        const long long n = seq_len(b);
-        if (line0 < at + n) break;
+    line_n = line0 >= total ? 0u : min(line_per, total - line0);
+    uint32_t at = before + incl - mine;
+    if (line_n > 0 && line0 >= at && line0 - at < mine) {
+      // this thread's sequences hold the start of the run: find the unit
+      WinSeq q = seq_of(seq_b0);
+      int b = seq_b0;
+      for (;;) {
+        const uint32_t n = b1 - seq_b0 == 1 ? mine : seq_places(q);
+        if (line0 - at < n || b + 1 >= b1) break;
         at += n;
+        q = seq_of(++b);
+      }
+      int i = 0;
+      while ((i + 1) * tpg < q.nq) {
+        const uint32_t n = group_places(q, i);
+        if (line0 - at < n) break;
+        at += n;
+        ++i;
       }
       bars->start_b = b;
+      bars->start_tok0 = q.tok0;
+      bars->start_nq = q.nq;
+      bars->start_nk = q.nk;
+      bars->start_group = i;
+      bars->start_len = win_group_len(prm, q, tpg, i);
       bars->start_off = line0 - at;
     }
     if (bad && blockIdx.x == 0) atomicOr(prm.err, FA_DEVERR_INDEX);
@@ -357,29 +427,12 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
-  // Unit number r of this CTA from the queue; the slot is released by one
-  // lane per consuming warp.
-  auto fetch_unit = [&](int r, bool arrive, bool& okr) -> WinUnit {
-    const int slot = r & 1;
-    okr = mbar_wait(&bars->unit_full[slot], (uint32_t)((r >> 1) & 1), abort_flag, prm.err);
-    WinUnit w = bars->unit[slot];
-    if (!okr) w.kz = -1;
-    __syncwarp();  // every lane has read the slot before one of them releases it
-    if (arrive) mbar_arrive(&bars->unit_empty[slot]);
-    return w;
-  };
-
   if (warp >= C::SOFTMAX_WARPS) {
     if constexpr (C::REALLOC) regs_dec<C::CTRL_REGS>();
     if (warp == C::LOAD_WARP) {
       // ---------------------------------------------------------- load --
       // The whole warp runs the loop; lane 0 waits, arms barriers and
       // publishes units; paged boxes are issued one per lane.
-      if (lane == 0) {
-        tma_prefetch_desc(&tm_q);
-        tma_prefetch_desc(&tm_k);
-        tma_prefetch_desc(&tm_v);
-      }
       const uint64_t pol_kv = policy_evict_last();
       const uint64_t pol_q = policy_evict_first();
       int pos = 0;    // ring position (continues across units)
@@ -506,33 +559,34 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
       if constexpr (PAGED) {
         int r = 0;
         if (line_n > 0) {
-          long long rem = line_n, at = line0;
-          int b = bars->start_b, i = 0;
-          long long off = bars->start_off;
+          uint32_t rem = line_n, at = line0;
+          int b = bars->start_b, i = bars->start_group, len = bars->start_len;
+          WinSeq s = {bars->start_tok0, bars->start_nq, bars->start_nk};
+          int ntok = min(tpg, s.nq - i * tpg);
+          uint32_t places = win_places<C::NQT>(len, ntok, tpt);
+          int head = (int)(bars->start_off / places);
+          uint32_t off = bars->start_off % places;
           bool bad = false;
-          WinSeq s = win_seq(prm, b, &bad);
-          int len = win_group_len(prm, s, tpg, 0);
-          while (off >= (long long)len * prm.Hkv) {
-            off -= (long long)len * prm.Hkv;
-            len = win_group_len(prm, s, tpg, ++i);
-          }
-          int head = (int)(off / len), r0 = (int)(off % len);
-          while (ok && rem > 0) {
-            const int run = (int)(rem < len - r0 ? rem : len - r0);
+          while (ok) {
+            // [off, off + run) of the unit's places are this CTA's
+            const uint32_t run = min(rem, places - off);
+            const int per_tile = C::NQT == 2 && ntok > tpt ? 2 : 1;
+            const bool begins = off == 0, ends = off + run == places;
             w.kz = head;
             w.q_row = i * tpg;
             w.qz = s.tok0 + w.q_row;
             w.p0 = s.nk - s.nq + w.q_row;
-            w.ntok = min(tpg, s.nq - w.q_row);
+            w.ntok = ntok;
             w.nk = s.nk;
             w.lo = max(0, w.p0 - prm.window + 1);
             const WinTiles u = win_tiles(w.p0, w.ntok, tpt, C::NQT, prm.window, prm.sinks);
             take_tiles(u);
-            w.r0 = r0;
-            w.r1 = min(u.len, r0 + run);  // (len counts a unit without keys as one tile)
-            w.part = (r0 == 0 && run == len) ? -1 : 2 * (int)blockIdx.x + (r0 > 0 ? 0 : 1);
-            if (r0 == 0 && run < len && lane == 0) {
-              const long long last = (at + len - 1) / line_per;  // CTA that holds the unit's last tile
+            w.r0 = min(u.len, (int)off / per_tile);
+            w.r1 = ends ? u.len : min(u.len, (int)(off + run) / per_tile);
+            w.part = begins && ends ? -1 : 2 * (int)blockIdx.x + (begins ? 1 : 0);
+            if (begins && !ends && lane == 0) {
+              // parts: up to the CTA that holds the unit's last place
+              const uint32_t last = min((at + places - 1) / line_per, gridDim.x - 1);
               prm.desc[blockIdx.x] = make_int4((int)(last - blockIdx.x) + 1, w.qz, head, w.ntok * g);
             }
             ok = publish(r++, w);
@@ -540,16 +594,20 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
             rem -= run;
             at += run;
             if (rem == 0) break;
-            r0 = 0;
+            off = 0;
             if (++head == prm.Hkv) {
               head = 0;
               if (++i * tpg >= s.nq) {
                 i = 0;
                 do {
-                  s = win_seq(prm, ++b, &bad);
-                } while (s.nq == 0 && b + 1 < prm.B);
+                  if (++b >= prm.B) break;
+                  s = win_seq(prm, prm.cu_q[b], prm.cu_q[b + 1], prm.seq_k[b], &bad);
+                } while (s.nq == 0);
+                if (b >= prm.B) break;
               }
               len = win_group_len(prm, s, tpg, i);
+              ntok = min(tpg, s.nq - i * tpg);
+              places = win_places<C::NQT>(len, ntok, tpt);
             }
           }
         }
@@ -558,29 +616,33 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
       } else {
         // dense: one unit per launched CTA, heaviest first within chunks of
         // heads; a CTA about to finish takes over the next CTA that has not
-        // started (cluster launch control), so its loads overlap the tail
+        // started (cluster launch control), so its loads overlap the tail.
+        // Units [0, pair_units) hold both query tiles of a group, the groups
+        // behind them run as two units of one query tile each.
         const int n_groups = (prm.N + tpg - 1) / tpg;
-        const int units = prm.BH * n_groups;
+        const int units = prm.pair_units + C::NQT * (prm.BH * n_groups - prm.pair_units);
         const int qgroup = prm.Hq / prm.Hkv;
         int n_req = 0;
         bool more = true;
-        auto decode = [&](int v) {
+        auto decode = [&](int x) {
+          const bool single = x >= prm.pair_units;
+          const int v = single ? prm.pair_units + (x - prm.pair_units) / C::NQT : x;
           const int per_chunk = prm.head_chunk * n_groups;
           const int c = v / per_chunk;
           const int idx = v - c * per_chunk;
           const int heads_here = min(prm.head_chunk, prm.BH - c * prm.head_chunk);
           const int bh = c * prm.head_chunk + idx % heads_here;
-          w.q_row = (n_groups - 1 - idx / heads_here) * tpg;
+          w.q_row = (n_groups - 1 - idx / heads_here) * tpg + (single ? (x - prm.pair_units) % C::NQT * kBM : 0);
           w.qz = bh;
           w.kz = (bh / prm.Hq) * prm.Hkv + (bh % prm.Hq) / qgroup;
           w.p0 = w.q_row + prm.Nk - prm.N;
-          w.ntok = min(tpg, prm.N - w.q_row);
+          w.ntok = max(0, min(single ? kBM : tpg, prm.N - w.q_row));  // (0: a group's missing second tile)
           w.nk = prm.Nk;
           w.lo = max(0, w.p0 - prm.window + 1);
           const WinTiles u = win_tiles(w.p0, w.ntok, tpt, C::NQT, prm.window, prm.sinks);
           take_tiles(u);
           w.r0 = 0;
-          w.r1 = u.len;
+          w.r1 = w.ntok > 0 ? u.len : 0;
           w.part = -1;
         };
         int u = (int)blockIdx.x;
@@ -681,9 +743,12 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
         }
       };
       for (int r = 0; ok; ++r) {
-        const WinUnit w = fetch_unit(r, lane == 0, ok);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok || w.kz < 0) break;
+        ok = warp_wait(&bars->unit_full[r & 1], (uint32_t)((r >> 1) & 1));
+        if (!ok) break;
+        const WinUnit w = bars->unit[r & 1];
+        __syncwarp();  // every lane has read the slot before one of them releases it
+        if (lane == 0) mbar_arrive(&bars->unit_empty[r & 1]);
+        if (w.kz < 0) break;
         if (w.r1 <= w.r0) continue;
         ok = warp_wait(&bars->q_full, (uint32_t)(k & 1));
         if (!ok) break;
@@ -694,13 +759,16 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           if (--qk_left == 0) mma_commit_elect(&bars->q_empty);  // the unit's Q has been read
         };
         if constexpr (C::NQT == 2) {
+          // per query tile: P V still to issue, and the next list index
+          const WinPart part[2] = {WinPart(w, 0), WinPart(w, 1)};
           int left[2] = {n0, n1};
+          int next[2] = {part[0].from(w.r0), part[1].from(w.r0)};
           bool begun[2] = {false, false};
           ok = wait_tile(pos);
           if (!ok) break;
 #pragma unroll
           for (int t = 0; t < 2; ++t)
-            if (win_active(w, t, w.r0)) {
+            if (left[t] > 0 && next[t] == w.r0) {
               issue_qk(t, t, pos);
               mma_commit_elect(&bars->s_full[t]);
               qk_issued();
@@ -709,12 +777,11 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           pos += C::SPT;
           for (int l = w.r0; l < w.r1 && ok; ++l) {
             const int pv_pos = pos, k_pos = pos + C::SPT;  // V_l, K_{l+1}
-            const bool more = l + 1 < w.r1;
             bool v_ready = false, k_ready = false;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               if (!ok) break;
-              if (win_active(w, t, l)) {
+              if (left[t] > 0 && next[t] == l) {
                 if (!v_ready) {
                   ok = wait_tile(pv_pos);
                   v_ready = true;
@@ -730,9 +797,10 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
                 if (!ok) break;
                 ++pc[t];
                 begun[t] = true;
+                next[t] = part[t].from(l + 1);
                 if (--left[t] == 0) mma_commit_elect(&bars->o_full[t]);
               }
-              if (more && win_active(w, t, l + 1)) {
+              if (left[t] > 0 && next[t] == l + 1) {
                 if (!k_ready) {
                   ok = wait_tile(k_pos);
                   k_ready = true;
@@ -747,7 +815,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
             // (every list index has a query tile that takes part in it)
             release_tile(pv_pos);
             pos += C::SPT;
-            if (more) {
+            if (l + 1 < w.r1) {
               release_tile(k_pos);
               pos += C::SPT;
             }
@@ -819,30 +887,34 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
     bool ok = true;
 
     for (int rr = 0; ok; ++rr) {
-      bool okr = true;
-      const WinUnit w = fetch_unit(rr, lane == 0, okr);
-      ok = __all_sync(0xffffffffu, okr);
-      if (!ok || w.kz < 0) break;
-      const int nrun = w.r1 > w.r0 ? w.r1 - w.r0 : 0;
+      // The unit is read where it stands in the queue, and its slot released
+      // at the unit's end: what only the epilogue needs does not weigh on the
+      // key-tile loop's registers.
+      ok = __all_sync(0xffffffffu, mbar_wait(&bars->unit_full[rr & 1], (uint32_t)((rr >> 1) & 1), abort_flag, prm.err));
+      if (!ok) break;
+      const WinUnit& w = bars->unit[rr & 1];
+      if (w.kz < 0) break;
+      const int r0 = w.r0, r1 = w.r1;
+      const int nrun = r1 > r0 ? r1 - r0 : 0;
       const int ring0 = ring;
       ring += 2 * nrun * C::SPT;
+      const int rows = min(rpt, (w.ntok - t * tpt) * g);  // valid rows of this tile
+      const bool valid = r_in < rows;
+      const int tok = t * tpt + (PAGED ? r_in / g : r_in);   // token within the unit
+      // where this row's results go
+      auto out_row_of = [&]() -> size_t {
+        if (w.part >= 0) return (size_t)w.part * (C::NQT * kBM) + t * rpt + r_in;
+        if (PAGED) return (size_t)(w.qz + tok) * prm.Hq + w.kz * g + r_in % g;
+        return (size_t)w.qz * prm.N + w.q_row + tok;
+      };
       do {  // one unit (skipped when this tile has no valid row)
-        const int rows = min(rpt, (w.ntok - t * tpt) * g);  // valid rows of this tile
         if (rows <= 0) break;
-        const bool valid = r_in < rows;
-        const int tok = t * tpt + (PAGED ? r_in / g : r_in);   // token within the unit
-        // where this row's results go
-        size_t out_row = 0;
-        if (valid) {
-          if (w.part >= 0) out_row = (size_t)w.part * (C::NQT * kBM) + t * rpt + r_in;
-          else if (PAGED) out_row = (size_t)(w.qz + tok) * prm.Hq + w.kz * g + r_in % g;
-          else out_row = (size_t)w.qz * prm.N + w.q_row + tok;
-        }
         const WinPart mine(w, t);
-        const int n = C::NQT == 2 ? mine.count(w.r0, w.r1) : nrun;
+        const int n = C::NQT == 2 ? mine.count(r0, r1) : nrun;
         if (n == 0) {
           // no row of this tile sees a key of this run: O = 0, LSE = -inf
           if (valid) {
+            const size_t out_row = out_row_of();
             if (w.part >= 0) {
               float4* dst = reinterpret_cast<float4*>(prm.o_part + out_row * D);
 #pragma unroll 1
@@ -858,6 +930,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           break;
         }
         // this row's last and first (window) visible key; the tile's strictest ones
+        const int ns = w.ns, skip = w.skip;
         const int last = min(w.p0 + tok, w.nk - 1);
         const int lo = w.p0 + tok - prm.window + 1;
         const int tile_last = w.p0 + t * tpt;                              // of its first row
@@ -875,9 +948,8 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           }
           return true;
         };
-        int j = 0;  // tiles done by this query tile
-        for (int l = w.r0; l < w.r1 && ok; ++l) {
-          if (C::NQT == 2 && !mine.has(l)) continue;
+        int l = C::NQT == 2 ? mine.from(r0) : r0;  // list index
+        for (int j = 0; j < n && ok; ++j, l = C::NQT == 2 ? mine.from(l + 1) : l + 1) {
           const int x = it + j;
           const int buf = C::NQT == 2 ? t : (x & 1);
           const uint32_t ph = C::NQT == 2 ? (uint32_t)(sc & 1) : (uint32_t)((x >> 1) & 1);
@@ -894,8 +966,31 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
             }
           }
           const uint32_t s_addr = tmem + lane_addr + buf * kBN;
-          const int col0 = (l < w.ns ? l : l + w.skip) * kBN;
+          const int col0 = (l < ns ? l : l + skip) * kBN;
           const bool need_mask = col0 + kBN - 1 > tile_last || (col0 < tile_lo && col0 + kBN > prm.sinks);
+          if constexpr (PAGED) {
+            // Rows of the V tile that no query of the unit may see can hold
+            // anything; P = 0 there would still give NaN from a NaN, so they
+            // become zeros before P is handed over (here, while few registers are
+            // live).  Thread r clears key r; both query tiles do so (the writes
+            // are the same), each before its own P V.
+            const bool gap = w.lo > prm.sinks && col0 < w.lo && col0 + kBN > prm.sinks;
+            if (col0 + kBN > w.nk || gap) {
+              // (one query tile: the slot's previous fill may still be the V tile
+              // before, so that one's P V is waited for first; with two, K of
+              // this tile lies between)
+              if (C::NQT == 1 && j > 0 && !consume_o(x - 1)) {
+                ok = false;
+                break;
+              }
+              const int v_at = C::NQT == 2 ? 2 * (l - r0) + 1 : j + min(j + 2, n);
+              const int key = col0 + r_in;
+              const bool dead = key >= w.nk || (key < w.lo && key >= prm.sinks);
+              ok = clear_v_row<C, Bars>(bars, smem_u32(smem + C::OFF_RING) + r_in * 128, ring0 + v_at * C::SPT, dead,
+                                        prm.err);
+              if (!ok) break;
+            }
+          }
           float s[kBN];
           {
             uint32_t u[32];
@@ -956,41 +1051,6 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
             }
             rescale_o_cols<D>(tmem + lane_addr + C::O_COL0 + t * D, alpha);
           }
-          if constexpr (PAGED) {
-            // Rows of the V tile that no query of the unit may see can hold
-            // anything; P = 0 there would still give NaN from a NaN, so they
-            // become zeros before P is handed over.  Thread r clears key r;
-            // both query tiles do so (the writes are the same), each before
-            // its own P V.
-            const bool gap = w.lo > prm.sinks && col0 < w.lo && col0 + kBN > prm.sinks;
-            if (col0 + kBN > w.nk || gap) {
-              // (one query tile: the slot's previous fill may still be the V tile
-              // before, so that one's P V is waited for first; with two, K of
-              // this tile lies between)
-              if (C::NQT == 1 && j > 0 && !consume_o(x - 1)) {
-                ok = false;
-                break;
-              }
-              const int v_at = C::NQT == 2 ? 2 * (l - w.r0) + 1 : j + min(j + 2, n);
-              const int pv = ring0 + v_at * C::SPT;
-#pragma unroll
-              for (int sp = 0; sp < C::SPT; ++sp)
-                ok = ok && __all_sync(0xffffffffu, mbar_wait(&bars->full[(pv + sp) % C::NS],
-                                                             (uint32_t)(((pv + sp) / C::NS) & 1), abort_flag, prm.err));
-              if (!ok) break;
-              const int key = col0 + r_in;
-              if (key >= w.nk || (key < w.lo && key >= prm.sinks)) {
-#pragma unroll 1
-                for (int ch = 0; ch < C::NCH; ++ch) {
-                  const uint32_t row = smem_u32(smem + C::OFF_RING) + ((pv + ch / C::SLOT_CH) % C::NS) * C::SLOT_BYTES +
-                                       (ch % C::SLOT_CH) * C::CHUNK_BYTES + r_in * 128;
-#pragma unroll
-                  for (int i = 0; i < 8; ++i) st_shared_v4(row + 16 * i, 0u, 0u, 0u, 0u);
-                }
-              }
-              fence_proxy_async_smem();
-            }
-          }
           // P = 2^(s*cj - m); a masked score gives 2^-inf = 0 (a row without
           // a visible key yet takes 0 in place of -m)
           const float2 cj2 = make_float2(cj, cj);
@@ -1026,7 +1086,6 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           tmem_wait_st();
           tc_fence_before();
           mbar_arrive(&bars->p_full[buf][1]);
-          ++j;
         }
 
         // -------------------------------------------------------- epilogue --
@@ -1038,6 +1097,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
         const float f = (l_run > 0.0f) ? (1.0f / l_run) : 0.0f;
         const float lse_row = (m_run + lg2(l_run)) * 0.69314718055994530942f;
         const uint32_t o_addr = tmem + lane_addr + C::O_COL0 + t * D;
+        const size_t out_row = valid ? out_row_of() : 0;
         if (w.part >= 0) {
           // fp32 partial: O normalised over this run's keys and the run's LSE
           float* prow = prm.o_part + out_row * D;
@@ -1117,6 +1177,8 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
         tc_fence_before();
       } while (0);
       if constexpr (C::NQT == 1) it += nrun;
+      __syncwarp();  // every lane is done with the slot
+      if (lane == 0) mbar_arrive(&bars->unit_empty[rr & 1]);
     }
   }
   // the epilogue's bulk stores have completed before the CTA ends
@@ -1162,7 +1224,18 @@ cudaError_t launch_attn_window(const WinLaunch& L) {
   WinParams prm = L.prm;
   long long grid = L.grid;
   if constexpr (!PAGED) {
-    grid = (long long)prm.BH * ((prm.N + C::NQT * kBM - 1) / (C::NQT * kBM));
+    // Groups of two query tiles.  When the last wave of SMs is at most half
+    // full its groups run as two units of one tile, each of which takes 0.55
+    // to 0.6 of a pair's time; a call of less than half a wave runs so whole.
+    static int sms[64] = {};
+    if (sms[dev] == 0) {
+      e = cudaDeviceGetAttribute(&sms[dev], cudaDevAttrMultiProcessorCount, dev);
+      if (e != cudaSuccess) return e;
+    }
+    const long long groups = (long long)prm.BH * ((prm.N + C::NQT * kBM - 1) / (C::NQT * kBM));
+    const long long rem = groups % sms[dev];
+    prm.pair_units = (int)(C::NQT == 2 && rem > 0 && 2 * rem <= sms[dev] ? groups - rem : groups);
+    grid = prm.pair_units + C::NQT * (groups - prm.pair_units);
     // chunks of heads whose keys and values fill about half of L2, as in attn_fwd.cuh
     prm.head_chunk = prm.BH;
     const long long kv_head_bytes = 2LL * prm.Nk * C::ROW_BYTES;

@@ -514,7 +514,8 @@ typedef struct {
  * Errors: FA_ERR_INVALID_ARG for bad pointers, alignment, sizes, strides,
  * window, sinks, scale or workspace; FA_ERR_UNSUPPORTED for d, page_size or
  * head counts outside the above, more than 2^24 sequences, lengths above
- * 2^30, or a device other than sm_103.  B * T * Hq = 0 is a no-op.
+ * 2^30, work that could pass 2^30 key tiles by the host's sizes (T, B,
+ * max_pages, window), or a device other than sm_103.  B * T * Hq = 0 is a no-op.
  */
 fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse,
                        const int32_t* block_table, int64_t table_stride, int64_t max_pages,
