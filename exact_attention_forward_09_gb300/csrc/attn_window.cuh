@@ -76,10 +76,17 @@ struct WinCfg {
   static constexpr int SOFTMAX_WARPS = 4 * NQT;
   static constexpr int MMA_WARP = SOFTMAX_WARPS;
   static constexpr int LOAD_WARP = SOFTMAX_WARPS + 1;
+  // paged: a second load warp takes the V tiles.  A box is one page's rows of
+  // one 128-byte column chunk, and a warp issues one about every 80 clocks: at
+  // 16-token pages a K and a V tile of d = 128 are 32 boxes, as long to issue
+  // as the tiles' arithmetic takes (chunks over 16-token pages: 652 -> 590 us
+  // for 4 x 2048 new tokens over 4000 to 10000 keys).
+  static constexpr int LOADV_WARP = PAGED ? LOAD_WARP + 1 : -1;
+  static constexpr int UNIT_READERS = SOFTMAX_WARPS + 1 + (PAGED ? 1 : 0);  // warps that release a unit's slot
   // two query tiles: a third, control warpgroup gives registers to the
   // softmax warpgroups (the split of attn_fwd.cuh)
   static constexpr bool REALLOC = NQT == 2;
-  static constexpr int THREADS = REALLOC ? 32 * (SOFTMAX_WARPS + 4) : 32 * (SOFTMAX_WARPS + 2);
+  static constexpr int THREADS = REALLOC ? 32 * (SOFTMAX_WARPS + 4) : 32 * (SOFTMAX_WARPS + (PAGED ? 3 : 2));
   static constexpr int CTRL_REGS = 104;
   static constexpr int SOFTMAX_REGS = 200;
   static constexpr float TAU = 8.0f;                       // lazy-rescale threshold, log2 units
@@ -178,7 +185,8 @@ struct alignas(16) WinUnit {
   int sa[2], la[2], lb[2];
   int part;     // -1: whole unit, written to o; else the partial slot
   int lo;       // keys in [sinks, lo) are visible to no query of the unit
-  int pad[2];
+  int seq;      // paged: sequence
+  int pad;
 };
 static_assert(sizeof(WinUnit) == 80, "WinUnit is copied in 16-byte pieces");
 
@@ -299,16 +307,6 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
   const int rpt = tpt * g;                 // rows per query tile
   const int tpg = C::NQT * tpt;            // tokens per unit
 
-  // paged: the lengths of this thread's first sequence are asked for first,
-  // so that their latency passes during the set-up below
-  int seq_a = 0, seq_e = 0, seq_n = 0;
-  const int seq_share = PAGED ? (prm.B + C::THREADS - 1) / C::THREADS : 0;  // sequences per thread
-  const int seq_b0 = PAGED ? min(prm.B, (int)threadIdx.x * seq_share) : 0;
-  if (PAGED && seq_b0 < prm.B) {
-    seq_a = prm.cu_q[seq_b0];
-    seq_e = prm.cu_q[seq_b0 + 1];
-    seq_n = prm.seq_k[seq_b0];
-  }
   if (threadIdx.x == 0) {
     mbar_init(&bars->q_full, 1);
     mbar_init(&bars->q_empty, 1);
@@ -323,7 +321,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
       mbar_init(&bars->o_ready[t], 1);
       mbar_init(&bars->o_full[t], 1);
       mbar_init(&bars->unit_full[t], 1);
-      mbar_init(&bars->unit_empty[t], 1 + C::SOFTMAX_WARPS);
+      mbar_init(&bars->unit_empty[t], C::UNIT_READERS);
     }
     mbar_init(&bars->drain, 1);
     mbar_init(&bars->clc_bar, 1);
@@ -341,6 +339,17 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
     tma_prefetch_desc(&tm_v);
   }
 
+  // launched while the kernel before it ends; nothing above touched global memory
+  if constexpr (PAGED) pdl_wait();
+  // paged: the lengths of this thread's first sequence
+  int seq_a = 0, seq_e = 0, seq_n = 0;
+  const int seq_share = PAGED ? (prm.B + C::THREADS - 1) / C::THREADS : 0;  // sequences per thread
+  const int seq_b0 = PAGED ? min(prm.B, (int)threadIdx.x * seq_share) : 0;
+  if (PAGED && seq_b0 < prm.B) {
+    seq_a = prm.cu_q[seq_b0];
+    seq_e = prm.cu_q[seq_b0 + 1];
+    seq_n = prm.seq_k[seq_b0];
+  }
   // paged: this CTA's run [line0, line0 + line_n) of the line of work.  (The
   // host refuses batches whose line could pass 2^31 places; token ranges that
   // overlap, against the contract, may wrap it: the results are then wrong,
@@ -391,7 +400,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
     }
     line_per = (total + gridDim.x - 1) / gridDim.x;
     if (line_per < (uint32_t)prm.min_places) line_per = prm.min_places;
-    line_per = (line_per + 1) & ~1u;
+    if (C::NQT == 2) line_per = (line_per + 1) & ~1u;
     line0 = line_per * blockIdx.x;
     line_n = line0 >= total ? 0u : min(line_per, total - line0);
     uint32_t at = before + incl - mine;
@@ -427,9 +436,101 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
 
+  // The two load warps' common parts.  Page numbers of list index l: lane i
+  // holds that of box i (-1: no visible key, or out of range: reads as zeros).
+  auto pages_of = [&](const WinUnit& w, int l) -> int {
+    int id = -1;
+    const int box_shift = prm.page_shift < 7 ? prm.page_shift : 7;  // rows of a box: a page's, at most a tile's
+    if (PAGED && lane < (kBN >> box_shift) && l < w.r1) {
+      const int box_rows = 1 << box_shift;
+      const int tile = l < w.ns ? l : l + w.skip;
+      const int key = tile * kBN + lane * box_rows;
+      if (key < w.nk && (key < prm.sinks || key + box_rows > w.lo)) {
+        id = prm.table[(long long)w.seq * prm.table_stride + (key >> prm.page_shift)];
+        if ((unsigned)id >= (unsigned)prm.num_pages) {
+          atomicOr(prm.err, FA_DEVERR_INDEX);
+          id = -1;
+        }
+      }
+    }
+    return id;
+  };
+  // One K or V tile into the ring from position pos on (SPT slots).
+  auto load_tile = [&](const WinUnit& w, const CUtensorMap* map, int pos, int l, int ids, uint64_t policy) -> bool {
+    const int key0 = (l < w.ns ? l : l + w.skip) * kBN;
+    for (int sp = 0; sp < C::SPT; ++sp, ++pos) {
+      const int slot = pos % C::NS;
+      const uint32_t ph = (uint32_t)((pos / C::NS) & 1);
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars->empty[slot], ph ^ 1u, abort_flag, prm.err))) return false;
+      // failure-injection hook (tests only): this slot is never filled, so
+      // the MMA warp's wait on it runs out and the kernel aborts
+      if (pos == prm.drop_pos && blockIdx.x == 0) continue;
+      uint8_t* dst = smem + C::OFF_RING + slot * C::SLOT_BYTES;
+      if (lane == 0) mbar_arrive_expect_tx(&bars->full[slot], C::SLOT_BYTES);
+      __syncwarp();
+      if constexpr (PAGED) {
+        // one box per lane
+        const int box_shift = prm.page_shift < 7 ? prm.page_shift : 7;
+        const int box = lane & ((kBN >> box_shift) - 1), ch = lane >> (7 - box_shift);
+        const int id = __shfl_sync(0xffffffffu, ids, box);
+        const int row = box << box_shift;
+        if (ch < C::SLOT_CH)
+          tma_load_4d_hint(dst + ch * C::CHUNK_BYTES + row * 128, map, &bars->full[slot],
+                           (sp * C::SLOT_CH + ch) * C::CH_ELEMS, (key0 + row) & ((1 << prm.page_shift) - 1), w.kz, id,
+                           policy);
+      } else if (lane < C::SLOT_CH) {
+        tma_load_3d_hint(dst + lane * C::CHUNK_BYTES, map, &bars->full[slot], (sp * C::SLOT_CH + lane) * C::CH_ELEMS,
+                         key0, w.kz, policy);
+      }
+    }
+    return true;
+  };
+  // Ring positions within a unit of n tiles, in the order in which the MMA
+  // warp consumes them: K0 V0 K1 V1 ... (two query tiles), K0 K1 V0 K2 V1 ...
+  auto k_at = [&](int j) -> int { return (C::NQT == 2 ? 2 * j : (j < 2 ? j : 2 * j - 1)) * C::SPT; };
+  auto v_at = [&](int j, int n) -> int { return (C::NQT == 2 ? 2 * j + 1 : j + min(j + 2, n)) * C::SPT; };
+  // Never leave with copies in flight: the last fills of the slots used (pos
+  // positions so far).  After a wait ran out some of them were never issued;
+  // those that were land within microseconds.
+  auto settle_ring = [&](int pos) {
+    const int used = pos < C::NS ? pos : C::NS;
+    for (int i = 0; i < used; ++i) {
+      const int p_last = pos - 1 - i;
+      const uint64_t t0 = globaltimer();
+      while (!mbar_try_wait(&bars->full[p_last % C::NS], (uint32_t)((p_last / C::NS) & 1)) &&
+             globaltimer() - t0 < (*abort_flag ? 2000000ull : FA_WAIT_LIMIT_NS)) {
+      }
+    }
+  };
+
   if (warp >= C::SOFTMAX_WARPS) {
     if constexpr (C::REALLOC) regs_dec<C::CTRL_REGS>();
-    if (warp == C::LOAD_WARP) {
+    if (PAGED && warp == C::LOADV_WARP) {
+      // -------------------------------------------------------- load V --
+      const uint64_t pol_kv = policy_evict_last();
+      int pos = 0;
+      bool ok = true;
+      for (int r = 0; ok; ++r) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&bars->unit_full[r & 1], (uint32_t)((r >> 1) & 1), abort_flag, prm.err));
+        if (!ok) break;
+        const WinUnit w = bars->unit[r & 1];
+        __syncwarp();  // every lane has read the slot before one of them releases it
+        if (lane == 0) mbar_arrive(&bars->unit_empty[r & 1]);
+        if (w.kz < 0) break;
+        const int n = w.r1 - w.r0;
+        if (n <= 0) continue;
+        int ids = pages_of(w, w.r0), ids1 = pages_of(w, w.r0 + 1);
+        for (int j = 0; j < n && ok; ++j) {
+          const int ids2 = pages_of(w, w.r0 + j + 2);  // two tiles ahead: its latency hides behind the loads
+          ok = load_tile(w, &tm_v, pos + v_at(j, n), w.r0 + j, ids, pol_kv);
+          ids = ids1;
+          ids1 = ids2;
+        }
+        pos += 2 * n * C::SPT;
+      }
+      settle_ring(pos);
+      __syncwarp();
+    } else if (warp == C::LOAD_WARP) {
       // ---------------------------------------------------------- load --
       // The whole warp runs the loop; lane 0 waits, arms barriers and
       // publishes units; paged boxes are issued one per lane.
@@ -451,57 +552,11 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
         }
         return __shfl_sync(0xffffffffu, (int)good, 0) != 0;
       };
-      // page numbers of list index l: lane i holds that of box i (-1: read as zeros)
-      const int page_rows = PAGED ? 1 << prm.page_shift : 0;
-      const int box_rows = page_rows < kBN ? page_rows : kBN;
-      const int nbox = PAGED ? kBN / box_rows : 1;
-      auto pages_of = [&](const WinUnit& w, const int* table, int l) -> int {
-        int id = -1;
-        if (PAGED && lane < nbox && l < w.r1) {
-          const int tile = l < w.ns ? l : l + w.skip;
-          const int key = tile * kBN + lane * box_rows;
-          if (key < w.nk && (key < prm.sinks || key + box_rows > w.lo)) {
-            id = table[key >> prm.page_shift];
-            if ((unsigned)id >= (unsigned)prm.num_pages) {
-              atomicOr(prm.err, FA_DEVERR_INDEX);
-              id = -1;
-            }
-          }
-        }
-        return id;
-      };
-      // one K or V tile (SPT ring slots) into the ring
-      auto load_tile = [&](const WinUnit& w, bool is_v, int l, int ids) {
-        const CUtensorMap* map = is_v ? &tm_v : &tm_k;
-        const int key0 = (l < w.ns ? l : l + w.skip) * kBN;
-        for (int sp = 0; sp < C::SPT && ok; ++sp, ++pos) {
-          const int slot = pos % C::NS;
-          const uint32_t ph = (uint32_t)((pos / C::NS) & 1);
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->empty[slot], ph ^ 1u, abort_flag, prm.err));
-          if (!ok) break;
-          // failure-injection hook (tests only): this slot is never filled,
-          // so the MMA warp's wait on it runs out and the kernel aborts
-          if (pos == prm.drop_pos && blockIdx.x == 0) continue;
-          uint8_t* dst = smem + C::OFF_RING + slot * C::SLOT_BYTES;
-          if (lane == 0) mbar_arrive_expect_tx(&bars->full[slot], C::SLOT_BYTES);
-          __syncwarp();
-          if constexpr (PAGED) {
-            const int box = lane % nbox, ch = lane / nbox;
-            const int id = __shfl_sync(0xffffffffu, ids, box);
-            if (ch < C::SLOT_CH)
-              tma_load_4d_hint(dst + ch * C::CHUNK_BYTES + box * box_rows * 128, map, &bars->full[slot],
-                               (sp * C::SLOT_CH + ch) * C::CH_ELEMS, (key0 + box * box_rows) & (page_rows - 1), w.kz, id,
-                               pol_kv);
-          } else if (lane < C::SLOT_CH) {
-            tma_load_3d_hint(dst + lane * C::CHUNK_BYTES, map, &bars->full[slot],
-                             (sp * C::SLOT_CH + lane) * C::CH_ELEMS, key0, w.kz, pol_kv);
-          }
-        }
-      };
-      // Q tiles and every key/value tile of a unit
-      auto load_unit = [&](const WinUnit& w, const int* table) {
-        if (w.r1 <= w.r0) return;  // no visible key: nothing to load
-        int ids = pages_of(w, table, w.r0), ids1 = pages_of(w, table, w.r0 + 1), ids2 = -1;
+      // Q tiles and every key tile of a unit (dense: and every value tile)
+      auto load_unit = [&](const WinUnit& w) {
+        const int n = w.r1 - w.r0;
+        if (n <= 0) return;  // no visible key: nothing to load
+        int ids = pages_of(w, w.r0), ids1 = pages_of(w, w.r0 + 1);
         const int n0 = win_count(w, 0), n1 = C::NQT == 2 ? win_count(w, 1) : 0;
         // the Q buffer is free once the previous unit's last Q K^T finished
         if (k > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (uint32_t)((k - 1) & 1), abort_flag, prm.err));
@@ -521,27 +576,19 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           }
         }
         __syncwarp();
-        if constexpr (C::NQT == 2) {
-          // K0 V0 K1 V1 ...
-          for (int l = w.r0; l < w.r1 && ok; ++l) {
-            ids2 = pages_of(w, table, l + 2);  // two tiles ahead: its latency hides behind the loads
-            load_tile(w, false, l, ids);
-            load_tile(w, true, l, ids);
-            ids = ids1;
-            ids1 = ids2;
+        for (int j = 0; j < n && ok; ++j) {
+          const int ids2 = pages_of(w, w.r0 + j + 2);
+          ok = load_tile(w, &tm_k, pos + k_at(j), w.r0 + j, ids, pol_kv);
+          if (!PAGED && ok) {
+            // this warp issues V too, in ring order
+            if (C::NQT == 2) ok = load_tile(w, &tm_v, pos + v_at(j, n), w.r0 + j, 0, pol_kv);
+            else if (j >= 1) ok = load_tile(w, &tm_v, pos + v_at(j - 1, n), w.r0 + j - 1, 0, pol_kv);
           }
-        } else {
-          // K0 K1 V0 K2 V1 K3 V2 ...
-          load_tile(w, false, w.r0, ids);
-          if (w.r0 + 1 < w.r1) load_tile(w, false, w.r0 + 1, ids1);
-          for (int l = w.r0; l < w.r1 && ok; ++l) {
-            ids2 = pages_of(w, table, l + 2);
-            load_tile(w, true, l, ids);
-            if (l + 2 < w.r1) load_tile(w, false, l + 2, ids2);
-            ids = ids1;
-            ids1 = ids2;
-          }
+          ids = ids1;
+          ids1 = ids2;
         }
+        if (!PAGED && C::NQT == 1 && ok) ok = load_tile(w, &tm_v, pos + v_at(n - 1, n), w.r0 + n - 1, 0, pol_kv);
+        pos += 2 * n * C::SPT;
         ++k;
       };
       WinUnit w;
@@ -555,7 +602,8 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           w.lb[t] = u.lb[t];
         }
       };
-      w.pad[0] = w.pad[1] = 0;
+      w.pad = 0;
+      w.seq = 0;
       if constexpr (PAGED) {
         int r = 0;
         if (line_n > 0) {
@@ -573,6 +621,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
             const int per_tile = C::NQT == 2 && ntok > tpt ? 2 : 1;
             const bool begins = off == 0, ends = off + run == places;
             w.kz = head;
+            w.seq = b;
             w.q_row = i * tpg;
             w.qz = s.tok0 + w.q_row;
             w.p0 = s.nk - s.nq + w.q_row;
@@ -590,7 +639,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
               prm.desc[blockIdx.x] = make_int4((int)(last - blockIdx.x) + 1, w.qz, head, w.ntok * g);
             }
             ok = publish(r++, w);
-            if (ok) load_unit(w, prm.table + (long long)b * prm.table_stride);
+            if (ok) load_unit(w);
             rem -= run;
             at += run;
             if (rem == 0) break;
@@ -649,7 +698,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
         decode(u);
         ok = publish(0, w);
         for (int r = 0; ok; ++r) {
-          load_unit(w, nullptr);
+          load_unit(w);
           if (!ok) break;
           int nu = -1;
           if (more) {
@@ -674,16 +723,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           if (nu < 0) break;
         }
       }
-      // never leave with copies in flight: the last fill of every used slot
-      // and the last Q tiles
-      const int used = pos < C::NS ? pos : C::NS;
-      for (int i = 0; i < used; ++i) {
-        const int p_last = pos - 1 - i;
-        const uint64_t t0 = globaltimer();
-        while (!mbar_try_wait(&bars->full[p_last % C::NS], (uint32_t)((p_last / C::NS) & 1)) &&
-               globaltimer() - t0 < FA_WAIT_LIMIT_NS) {
-        }
-      }
+      settle_ring(pos);
       if (k > 0) {
         const uint64_t t0 = globaltimer();
         while (!mbar_try_wait(&bars->q_full, (uint32_t)((k - 1) & 1)) && globaltimer() - t0 < FA_WAIT_LIMIT_NS) {
@@ -930,7 +970,6 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           break;
         }
         // this row's last and first (window) visible key; the tile's strictest ones
-        const int ns = w.ns, skip = w.skip;
         const int last = min(w.p0 + tok, w.nk - 1);
         const int lo = w.p0 + tok - prm.window + 1;
         const int tile_last = w.p0 + t * tpt;                              // of its first row
@@ -966,7 +1005,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
             }
           }
           const uint32_t s_addr = tmem + lane_addr + buf * kBN;
-          const int col0 = (l < ns ? l : l + skip) * kBN;
+          const int col0 = (l < w.ns ? l : l + w.skip) * kBN;
           const bool need_mask = col0 + kBN - 1 > tile_last || (col0 < tile_lo && col0 + kBN > prm.sinks);
           if constexpr (PAGED) {
             // Rows of the V tile that no query of the unit may see can hold
@@ -983,11 +1022,10 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
                 ok = false;
                 break;
               }
-              const int v_at = C::NQT == 2 ? 2 * (l - r0) + 1 : j + min(j + 2, n);
               const int key = col0 + r_in;
               const bool dead = key >= w.nk || (key < w.lo && key >= prm.sinks);
-              ok = clear_v_row<C, Bars>(bars, smem_u32(smem + C::OFF_RING) + r_in * 128, ring0 + v_at * C::SPT, dead,
-                                        prm.err);
+              ok = clear_v_row<C, Bars>(bars, smem_u32(smem + C::OFF_RING) + r_in * 128, ring0 + v_at(C::NQT == 2 ? l - r0 : j, n),
+                                        dead, prm.err);
               if (!ok) break;
             }
           }
@@ -1250,10 +1288,15 @@ cudaError_t launch_attn_window(const WinLaunch& L) {
   cfg.dynamicSmemBytes = C::SMEM_BYTES;
   cfg.stream = L.stream;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 1;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  if constexpr (PAGED) {
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+  } else {
+    attr[0].id = cudaLaunchAttributeClusterDimension;  // work stealing asks for whole clusters
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+  }
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   e = cudaLaunchKernelEx(&cfg, kern, L.q, L.k, L.v, L.o, prm);

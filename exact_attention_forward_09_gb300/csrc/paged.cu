@@ -56,6 +56,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const float* __restr
   constexpr int E = D / 32;
   __shared__ float red[8][D];
   __shared__ float red_w[8];
+  pdl_launch();
   pdl_wait();  // the parts and desc are the previous kernel's
   const int4 u = desc[blockIdx.x];
   const int parts = u.x, rows = u.w;

@@ -232,7 +232,7 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   p.page_shift = shift_of(cache->page_size);
   p.g = (int)g;
   p.tpt = (int)tpt;
-  p.min_places = 2;
+  p.min_places = 1;
   // the line of work: at most this many units, each of at most this many
   // key tiles, two places to a tile
   const int64_t unit_tok = (slot_rows_of(d) / fa::kBM) * tpt;
