@@ -89,6 +89,11 @@ struct WinCfg {
   static constexpr int THREADS = REALLOC ? 32 * (SOFTMAX_WARPS + 4) : 32 * (SOFTMAX_WARPS + (PAGED ? 3 : 2));
   static constexpr int CTRL_REGS = 104;
   static constexpr int SOFTMAX_REGS = 200;
+  // A few sinks are usually all that is seen of tile 0: then only its first
+  // NARROW keys are multiplied and exponentiated (an MMA with N = 32 runs at
+  // 40% of the N = 128 rate, so the tile costs a third of a full one).
+  static constexpr int NARROW = 32;
+  static constexpr uint32_t IDESC_QK_NARROW = instr_desc(ELEM == kBF16 ? 1u : 0u, ELEM == kBF16 ? 1u : 0u, 0, 0, 128, NARROW);
   static constexpr float TAU = 8.0f;                       // lazy-rescale threshold, log2 units
   static constexpr uint32_t FMT = ELEM == kBF16 ? 1u : 0u;
   static constexpr uint32_t IDESC_QK = instr_desc(FMT, FMT, 0, 0, 128, kBN);
@@ -186,7 +191,7 @@ struct alignas(16) WinUnit {
   int part;     // -1: whole unit, written to o; else the partial slot
   int lo;       // keys in [sinks, lo) are visible to no query of the unit
   int seq;      // paged: sequence
-  int pad;
+  int narrow;   // tile 0 is visited for its sinks alone, which lie in its first NARROW columns
 };
 static_assert(sizeof(WinUnit) == 80, "WinUnit is copied in 16-byte pieces");
 
@@ -264,6 +269,44 @@ __device__ __forceinline__ uint32_t win_places(int len, int ntok, int tpt) {
 // bits [0, n) of a 32-bit word, n clamped to 0..32
 __device__ __forceinline__ uint32_t low_bits(int n) {
   return n <= 0 ? 0u : (0xffffffffu >> (32 - (n < 32 ? n : 32)));
+}
+
+// Which of the 32 keys from c0 on the query at position p sees: those up to
+// its own, and from its window's first on or below `sinks`.
+__device__ __forceinline__ uint32_t win_visible(int p, int window, int sinks, int c0) {
+  return low_bits(p + 1 - c0) & (~low_bits(p - window + 1 - c0) | low_bits(sinks - c0));
+}
+
+// The softmax of a narrow tile, the first one of its rows: 32 columns of S at
+// s_addr, of which `see` are visible; P is written back over them.  Returns
+// the row's maximum (log2 units) and sum.  Out of line, so that the full
+// tile's loop keeps its registers.
+template <int ELEM>
+__device__ __noinline__ float2 narrow_softmax(uint32_t s_addr, uint32_t see, float cj) {
+  const float mask_val = cj < 0.0f ? INFINITY : -INFINITY;
+  uint32_t u[32];
+  tmem_ld32(s_addr, u);
+  tmem_wait_ld();
+  float mx = mask_val;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const float x = (see & (1u << i)) ? __uint_as_float(u[i]) : mask_val;
+    u[i] = __float_as_uint(x);
+    mx = cj < 0.0f ? fminf(mx, x) : fmaxf(mx, x);
+  }
+  const float m = mx * cj;
+  const float nm = m == -INFINITY ? 0.0f : -m;
+  float l = 0.0f;
+  uint32_t pk[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    const float a = ex2(fmaf(__uint_as_float(u[2 * i]), cj, nm)), b = ex2(fmaf(__uint_as_float(u[2 * i + 1]), cj, nm));
+    l += a + b;
+    pk[i] = ELEM == kBF16 ? pack_bf16x2(a, b) : pack_f16x2(a, b);
+  }
+  tmem_st16(s_addr, pk);
+  tmem_wait_st();
+  return make_float2(m, l);
 }
 
 // Waits for the V tile at ring position pv and, where `dead`, zeroes this
@@ -601,8 +644,8 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           w.la[t] = u.la[t];
           w.lb[t] = u.lb[t];
         }
+        w.narrow = u.skip > 0 && u.ns == 1 && prm.sinks <= C::NARROW ? 1 : 0;
       };
-      w.pad = 0;
       w.seq = 0;
       if constexpr (PAGED) {
         int r = 0;
@@ -757,7 +800,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
       const uint64_t ring_v_desc0 = smem_desc(ring_s, C::CHUNK_BYTES, 1024, 2);  // V slots, MN-major
       auto slot_off = [&](int p) -> uint32_t { return (uint32_t)(p % C::NS) * C::SLOT_BYTES; };
       // S_buf = Q_t K^T for the K tile at ring position p
-      auto issue_qk = [&](int t, int buf, int p) {
+      auto issue_qk_of = [&](int t, int buf, int p, auto idesc) {
         const uint64_t a0 = q_desc0 + (uint64_t)((t * C::NCH * C::CHUNK_BYTES) >> 4);
         uint64_t b0[C::SPT];
 #pragma unroll
@@ -767,8 +810,21 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           const int ch = ks / 4, in_ch = (ks % 4) * 32;
           const uint64_t a = a0 + (uint64_t)((ch * C::CHUNK_BYTES + in_ch) >> 4);
           const uint64_t b = b0[ch / C::SLOT_CH] + (uint64_t)(((ch % C::SLOT_CH) * C::CHUNK_BYTES + in_ch) >> 4);
-          mma_ss_elect<0>(tmem + buf * kBN, a, b, C::IDESC_QK, ks > 0 ? 1u : 0u);
+          mma_ss_elect<0>(tmem + buf * kBN, a, b, decltype(idesc)::value, ks > 0 ? 1u : 0u);
         }
+      };
+      auto issue_qk = [&](int t, int buf, int p) { issue_qk_of(t, buf, p, std::integral_constant<uint32_t, C::IDESC_QK>()); };
+      // a narrow tile: S for its first keys, and their P V (all in half 0)
+      auto issue_qk_narrow = [&](int t, int buf, int p) {
+        issue_qk_of(t, buf, p, std::integral_constant<uint32_t, C::IDESC_QK_NARROW>());
+      };
+      auto issue_pv_narrow = [&](int t, int buf, int p) {
+#pragma unroll
+        for (int sp = 0; sp < C::SPT; ++sp)
+#pragma unroll
+          for (int ks = 0; ks < C::NARROW / 16; ++ks)
+            mma_ts_elect<0>(tmem + C::O_COL0 + t * D + sp * C::SLOT_D, tmem + buf * kBN + ks * 8,
+                            ring_v_desc0 + (uint64_t)((slot_off(p + sp) + ks * 2048) >> 4), C::IDESC_PV, ks > 0 ? 1u : 0u);
       };
       // O_t (+)= P_buf V for half h of the keys of the V tile at ring position p
       auto issue_pv = [&](int t, int buf, int p, bool acc, int h) {
@@ -806,16 +862,59 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           bool begun[2] = {false, false};
           ok = wait_tile(pos);
           if (!ok) break;
+          int l0 = w.r0;
+          if (w.narrow && l0 == 0) {
+            // both query tiles' narrow tile first; it is every valid tile's first
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-            if (left[t] > 0 && next[t] == w.r0) {
-              issue_qk(t, t, pos);
-              mma_commit_elect(&bars->s_full[t]);
-              qk_issued();
+            for (int t = 0; t < 2; ++t)
+              if (left[t] > 0 && next[t] == 0) {
+                issue_qk_narrow(t, t, pos);
+                mma_commit_elect(&bars->s_full[t]);
+                qk_issued();
+              }
+            release_tile(pos);
+            pos += C::SPT;
+            const int v_pos = pos, k_pos = pos + C::SPT;
+            ok = wait_tile(v_pos) && (w.r1 == 1 || wait_tile(k_pos));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (!ok) break;
+              if (left[t] > 0 && next[t] == 0) {
+                ok = warp_wait(&bars->p_full[t][0], (uint32_t)(pc[t] & 1)) && warp_wait(&bars->p_full[t][1], (uint32_t)(pc[t] & 1));
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv_narrow(t, t, v_pos);
+                ++pc[t];
+                begun[t] = true;
+                next[t] = part[t].from(1);
+                if (--left[t] == 0) mma_commit_elect(&bars->o_full[t]);
+              }
+              if (left[t] > 0 && next[t] == 1) {
+                issue_qk(t, t, k_pos);
+                mma_commit_elect(&bars->s_full[t]);
+                qk_issued();
+              }
             }
+            if (!ok) break;
+            release_tile(v_pos);
+            pos += C::SPT;
+            l0 = 1;
+            if (l0 >= w.r1) {
+              ++k;
+              continue;
+            }
+          } else {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              if (left[t] > 0 && next[t] == l0) {
+                issue_qk(t, t, pos);
+                mma_commit_elect(&bars->s_full[t]);
+                qk_issued();
+              }
+          }
           release_tile(pos);
           pos += C::SPT;
-          for (int l = w.r0; l < w.r1 && ok; ++l) {
+          for (int l = l0; l < w.r1 && ok; ++l) {
             const int pv_pos = pos, k_pos = pos + C::SPT;  // V_l, K_{l+1}
             bool v_ready = false, k_ready = false;
 #pragma unroll
@@ -863,10 +962,12 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
         } else {
           // one query tile, S double-buffered: S(0), S(1), then PV(j), S(j+2)
           const int n = w.r1 - w.r0;
+          const bool narrow = w.narrow && w.r0 == 0;
           for (int j = 0; j < 2 && j < n && ok; ++j) {
             ok = wait_tile(pos);
             if (!ok) break;
-            issue_qk(0, (it + j) & 1, pos);
+            if (j == 0 && narrow) issue_qk_narrow(0, it & 1, pos);
+            else issue_qk(0, (it + j) & 1, pos);
             mma_commit_elect(&bars->s_full[(it + j) & 1]);
             qk_issued();
             release_tile(pos);
@@ -876,12 +977,19 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
             const int x = it + j, b = x & 1;
             ok = wait_tile(pos);  // V_j
             if (!ok) break;
-#pragma unroll
-            for (int h = 0; h < 2 && ok; ++h) {
-              ok = warp_wait(&bars->p_full[b][h], (uint32_t)((x >> 1) & 1));
+            if (j == 0 && narrow) {
+              ok = warp_wait(&bars->p_full[b][0], (uint32_t)((x >> 1) & 1)) && warp_wait(&bars->p_full[b][1], (uint32_t)((x >> 1) & 1));
               if (!ok) break;
               tc_fence_after();
-              issue_pv(0, b, pos, j > 0, h);
+              issue_pv_narrow(0, b, pos);
+            } else {
+#pragma unroll
+              for (int h = 0; h < 2 && ok; ++h) {
+                ok = warp_wait(&bars->p_full[b][h], (uint32_t)((x >> 1) & 1));
+                if (!ok) break;
+                tc_fence_after();
+                issue_pv(0, b, pos, j > 0, h);
+              }
             }
             if (!ok) break;
             mma_commit_elect(&bars->o_ready[b]);
@@ -969,9 +1077,9 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           }
           break;
         }
-        // this row's last and first (window) visible key; the tile's strictest ones
-        const int last = min(w.p0 + tok, w.nk - 1);
-        const int lo = w.p0 + tok - prm.window + 1;
+        // this row's last visible key, its own position (a valid row's lies in
+        // the sequence); the tile's strictest last and first (window) ones
+        const int last = w.p0 + tok;
         const int tile_last = w.p0 + t * tpt;                              // of its first row
         const int tile_lo = w.p0 + t * tpt + (rows - 1) / g - prm.window + 1;  // of its last row
         float m_run = -INFINITY;  // reference maximum, log2 units
@@ -988,7 +1096,35 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           return true;
         };
         int l = C::NQT == 2 ? mine.from(r0) : r0;  // list index
-        for (int j = 0; j < n && ok; ++j, l = C::NQT == 2 ? mine.from(l + 1) : l + 1) {
+        int j = 0;                                 // tiles done by this query tile
+        if (w.narrow && l == 0) {
+          const int buf = C::NQT == 2 ? t : (it & 1);
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], (uint32_t)((C::NQT == 2 ? sc : it >> 1) & 1),
+                                                 abort_flag, prm.err));
+          ++sc;
+          if (!ok) break;
+          tc_fence_after();
+          if (C::NQT == 1 && it >= 2 && !consume_o(it - 2)) {
+            ok = false;
+            break;
+          }
+          if constexpr (PAGED) {
+            // the keys behind the sinks have left the window (see below)
+            ok = clear_v_row<C, Bars>(bars, smem_u32(smem + C::OFF_RING) + r_in * 128, ring0 + v_at(0, n),
+                                      r_in >= prm.sinks, prm.err);
+            if (!ok) break;
+          }
+          const float2 ml = narrow_softmax<ELEM>(tmem + lane_addr + buf * kBN,
+                                                 win_visible(last, prm.window, prm.sinks, 0), cj);
+          m_run = ml.x;
+          l_run = ml.y;
+          tc_fence_before();
+          mbar_arrive(&bars->p_full[buf][0]);
+          mbar_arrive(&bars->p_full[buf][1]);
+          j = 1;
+          l = C::NQT == 2 ? mine.from(1) : 1;
+        }
+        for (; j < n && ok; ++j, l = C::NQT == 2 ? mine.from(l + 1) : l + 1) {
           const int x = it + j;
           const int buf = C::NQT == 2 ? t : (x & 1);
           const uint32_t ph = C::NQT == 2 ? (uint32_t)(sc & 1) : (uint32_t)((x >> 1) & 1);
@@ -1041,12 +1177,10 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
             tmem_wait_ld();
           }
           if (need_mask) {
-            // visible columns of this row as four words: up to `last`, and
-            // from `lo` on or below `sinks`
+            // visible columns of this row as four words
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int c0 = col0 + 32 * q;
-              const uint32_t see = low_bits(last + 1 - c0) & (~low_bits(lo - c0) | low_bits(prm.sinks - c0));
+              const uint32_t see = win_visible(last, prm.window, prm.sinks, col0 + 32 * q);
 #pragma unroll
               for (int i = 0; i < 32; ++i) s[32 * q + i] = (see & (1u << i)) ? s[32 * q + i] : mask_val;
             }
