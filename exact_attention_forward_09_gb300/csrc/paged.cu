@@ -17,35 +17,26 @@ namespace {
 // m = max_s LSE_s and w_s = e^(LSE_s - m), O = sum_s w_s O_s / sum_s w_s and
 // LSE = m + ln sum_s w_s, summed in a fixed order.  Lane l holds columns l*E
 // .. l*E+E-1 of a row.  A unit cut in a few parts (chunks: up to 256 rows, two
-// or three parts) takes one warp per row; one cut in many (a single long
+// or three parts) takes a warp per two rows; one cut in many (a single long
 // context: a few rows, as many parts as the GPU has SMs per head) takes a
 // block per row, whose warps share the parts and meet in shared memory.  The
-// bytes are the parts, just written and still in L2.
-constexpr int kFewParts = 8;
+// parts were just written and lie in L2, and what is left is latency: the
+// loads of a row's parts go out before the weights they meet are known.
+constexpr int kFewParts = 4;
 
-// acc += sum over i < n of w_i * part s0 + i * step, lane i holding w_i
-template <int E, typename At>
-__device__ __forceinline__ void add_parts(float (&acc)[E], const float* __restrict__ o_part, At at, int s0, int step,
-                                          int n, float w, int D, int lane) {
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float wi = __shfl_sync(0xffffffffu, w, i);
-    const float* src = o_part + at(s0 + i * step) * D + lane * E;
-    float x[E];
-    if constexpr (E == 2) {
-      *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
-    } else {
+// x = columns lane*E .. of a row of parts
+template <int E>
+__device__ __forceinline__ void load_cols(float (&x)[E], const float* src) {
+  if constexpr (E == 2) {
+    *reinterpret_cast<float2*>(x) = *reinterpret_cast<const float2*>(src);
+  } else {
 #pragma unroll
-      for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(x + e) = *reinterpret_cast<const float4*>(src + e);
-    }
-    // (a part without visible keys has weight 0 and zeros; one of a NaN row
-    // has weight NaN, and the row stays NaN)
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, x[e], acc[e]);
+    for (int e = 0; e < E; e += 4) *reinterpret_cast<float4*>(x + e) = *reinterpret_cast<const float4*>(src + e);
   }
 }
 
-// e^(l - m), 0 for a part without visible keys
+// e^(l - m), 0 for a part without visible keys (its columns are zeros); a part
+// of a NaN row has weight NaN, and the row stays NaN
 __device__ __forceinline__ float part_weight(float l, float m) { return l == -INFINITY ? 0.0f : expf(l - m); }
 
 template <int D, bool F16>
@@ -62,55 +53,85 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const float* __restr
   const int parts = u.x, rows = u.w;
   if (parts == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int row = 0;
-  auto at = [&](int s) -> long long {
+  auto at = [&](int s, int row) -> long long {
     const long long slot = s == 0 ? 2LL * blockIdx.x + 1 : 2LL * (blockIdx.x + s);
     return slot * slot_rows + row;
   };
-  auto out_row = [&]() -> long long { return (long long)(u.y + row / g) * Hq + u.z * g + row % g; };
-  float acc[E];
+  auto out_row = [&](int row) -> long long { return (long long)(u.y + row / g) * Hq + u.z * g + row % g; };
   if (parts <= kFewParts) {
-    for (row = blockIdx.y * 8 + warp; row < rows; row += gridDim.y * 8) {
-      const float l = lane < parts ? lse_part[at(lane)] : -INFINITY;
-      float m = l;
+    for (int row0 = (blockIdx.y * 8 + warp) * 2; row0 < rows; row0 += gridDim.y * 16) {
+      float x[2][kFewParts][E], l[2];
 #pragma unroll
-      for (int d = 4; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      m = __shfl_sync(0xffffffffu, m, 0);  // (lanes 0 .. 7 hold all parts)
-      const float w = lane < parts ? part_weight(l, m) : 0.0f;
-      float total = w;
+      for (int i = 0; i < 2; ++i) {
+        const int row = min(row0 + i, rows - 1);
+        l[i] = lane < parts ? lse_part[at(lane, row)] : -INFINITY;
 #pragma unroll
-      for (int d = 4; d > 0; d >>= 1) total += __shfl_xor_sync(0xffffffffu, total, d);
-      total = __shfl_sync(0xffffffffu, total, 0);
+        for (int s = 0; s < kFewParts; ++s)
+          if (s < parts) load_cols<E>(x[i][s], o_part + at(s, row) * D + lane * E);
+      }
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-      add_parts<E>(acc, o_part, at, 0, 1, parts, w, D, lane);
-      const float inv = total != 0.0f ? 1.0f / total : 0.0f;
-      const long long r = out_row();
-      uint32_t pk[E / 2];
+      for (int i = 0; i < 2; ++i) {
+        if (row0 + i >= rows) break;
+        float m = l[i];
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        m = __shfl_sync(0xffffffffu, m, 0);  // (lanes 0 .. 3 hold all parts)
+        const float w = lane < parts ? part_weight(l[i], m) : 0.0f;
+        float acc[E], total = 0.0f;
 #pragma unroll
-      for (int e = 0; e < E; e += 2)
-        pk[e / 2] = F16 ? pack_f16x2(acc[e] * inv, acc[e + 1] * inv) : pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-      uint32_t* dst = reinterpret_cast<uint32_t*>(o) + r * (D / 2) + lane * (E / 2);
-      if constexpr (E == 2) dst[0] = pk[0];
-      else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(pk);
-      else *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<uint4*>(pk);
-      if (lane == 0) lse[r] = total == 0.0f ? -INFINITY : m + logf(total);
+        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kFewParts; ++s) {
+          if (s < parts) {
+            const float ws = __shfl_sync(0xffffffffu, w, s);
+            total += ws;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(ws, x[i][s][e], acc[e]);
+          }
+        }
+        const float inv = total != 0.0f ? 1.0f / total : 0.0f;
+        const long long r = out_row(row0 + i);
+        uint32_t pk[E / 2];
+#pragma unroll
+        for (int e = 0; e < E; e += 2)
+          pk[e / 2] = F16 ? pack_f16x2(acc[e] * inv, acc[e + 1] * inv) : pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+        uint32_t* dst = reinterpret_cast<uint32_t*>(o) + r * (D / 2) + lane * (E / 2);
+        if constexpr (E == 2) dst[0] = pk[0];
+        else if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<uint2*>(pk);
+        else *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<uint4*>(pk);
+        if (lane == 0) lse[r] = total == 0.0f ? -INFINITY : m + logf(total);
+      }
     }
     return;
   }
-  for (row = blockIdx.y; row < rows; row += gridDim.y) {
+  constexpr int AHEAD = E <= 4 ? 8 : 4;  // parts in flight per warp
+  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
     float m = -INFINITY;
-    for (int s = lane; s < parts; s += 32) m = fmaxf(m, lse_part[at(s)]);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-    float wsum = 0.0f;
+    for (int s = lane; s < parts; s += 32) m = fmaxf(m, lse_part[at(s, row)]);
+    float acc[E], wsum = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int s0 = warp; s0 < parts; s0 += 8 * 32) {  // this warp's parts, 32 at a time
-      const int n = min(32, (parts - s0 + 7) / 8);
-      const float w = lane < n ? part_weight(lse_part[at(s0 + 8 * lane)], m) : 0.0f;
+    for (int s0 = warp; s0 < parts; s0 += 8 * AHEAD) {  // this warp's parts: s0, s0 + 8, ...
+      const int n = min(AHEAD, (parts - s0 + 7) / 8);
+      float x[AHEAD][E];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i)
+        if (i < n) load_cols<E>(x[i], o_part + at(s0 + 8 * i, row) * D + lane * E);
+      const float l = lane < n ? lse_part[at(s0 + 8 * lane, row)] : -INFINITY;
+      if (s0 == warp) {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+      }
+      const float w = lane < n ? part_weight(l, m) : 0.0f;
       wsum += w;
-      add_parts<E>(acc, o_part, at, s0, 8, n, w, D, lane);
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const float wi = __shfl_sync(0xffffffffu, w, i);
+        if (i < n) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, x[i][e], acc[e]);
+        }
+      }
     }
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, d);
@@ -122,7 +143,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const float* __restr
 #pragma unroll
     for (int w = 0; w < 8; ++w) total += red_w[w];
     const float inv = total != 0.0f ? 1.0f / total : 0.0f;
-    const long long r = out_row();
+    const long long r = out_row(row);
     if (threadIdx.x < D / 2) {
       float a = 0.0f, b = 0.0f;
 #pragma unroll
@@ -133,6 +154,7 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const float* __restr
       reinterpret_cast<uint32_t*>(o)[r * (D / 2) + threadIdx.x] =
           F16 ? pack_f16x2(a * inv, b * inv) : pack_bf16x2(a * inv, b * inv);
     }
+    // (warp 0 has a part, so thread 0's maximum is the row's)
     if (threadIdx.x == 0) lse[r] = total == 0.0f ? -INFINITY : m + logf(total);
     __syncthreads();  // red is read before the next row's sums
   }
@@ -298,7 +320,9 @@ cudaError_t launch_paged_combine(const float* o_part, const float* lse_part, con
                                  cudaStream_t stream) {
   // launched while the attention kernel still runs; it waits for it itself
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(max_rows < 32 ? max_rows : 32), 1);
+  // a block takes 16 rows of a unit cut in few parts, or one of a unit cut in many
+  const int few = (max_rows + 15) / 16, many = max_rows < 8 ? max_rows : 8;
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(few > many ? few : many), 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
