@@ -14,6 +14,7 @@ import ctypes
 import functools
 import math
 import os
+import struct
 
 import torch
 
@@ -42,11 +43,16 @@ class FaError(RuntimeError):
 
 
 class _KvCache(ctypes.Structure):
-    """``fa_kv_cache``."""
+    """``fa_kv_cache``.  (The operators below pass its bytes, packed in one
+    step: filling a ctypes structure field by field takes longer than their
+    launch.)"""
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("num_pages", ctypes.c_int64),
                 ("page_size", ctypes.c_int64), ("heads", ctypes.c_int64), ("d", ctypes.c_int64),
                 ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
                 ("dtype", ctypes.c_int)]
+
+
+_KV_PACK = struct.Struct("@PPqqqqqqqi4x").pack
 
 
 _LIB = None
@@ -92,7 +98,7 @@ def _lib():
         lib.fa_bwd.restype = i32
         lib.fa_bwd_workspace_bytes.argtypes = [i64, i64, i64, i64, ctypes.POINTER(ctypes.c_size_t)]
         lib.fa_bwd_workspace_bytes.restype = i32
-        cache = ctypes.POINTER(_KvCache)
+        cache = ctypes.c_char_p  # the bytes of an fa_kv_cache
         lib.fa_fwd_window.argtypes = [vp, vp, vp, vp, vp] + [i64] * 8 + [f32, i32, vp]
         lib.fa_fwd_window.restype = i32
         lib.fa_bwd_window.argtypes = [vp] * 9 + [i64] * 8 + [f32, i32, vp, ctypes.c_size_t, vp]
@@ -449,14 +455,15 @@ def bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
 
 def _cache(k_pages, v_pages):
     """The ``fa_kv_cache`` of two [num_pages, heads, page_size, d] tensors (or
-    views of that shape with other strides), and their device index."""
+    views of that shape with other strides), their heads, head dimension,
+    dtype and device index."""
     if isinstance(k_pages, torch.Tensor) and isinstance(v_pages, torch.Tensor):
         shape, stride, dt, index = k_pages.shape, k_pages.stride(), k_pages.dtype, k_pages.get_device()
         if len(shape) == 4 and index >= 0 and dt in _TYPES and stride[3] == 1 and v_pages.shape == shape \
                 and v_pages.stride() == stride and v_pages.dtype is dt and v_pages.get_device() == index:
             n, h, ps, d = shape
-            return _KvCache(k_pages.data_ptr(), v_pages.data_ptr(), n, ps, h, d, stride[0], stride[1], stride[2],
-                            _TYPES[dt]), index
+            return _KV_PACK(k_pages.data_ptr(), v_pages.data_ptr(), n, ps, h, d, stride[0], stride[1], stride[2],
+                            _TYPES[dt]), h, d, dt, index
     raise ValueError("k_pages and v_pages must be bf16 or fp16 [num_pages, heads, page_size, d] CUDA tensors of one shape, "
                      "dtype, device and strides, their last dimension contiguous")
 
@@ -491,12 +498,9 @@ _PAGED_BYTES = {}  # by device index and head dimension
 
 def paged_workspace_bytes(d: int) -> int:
     """Bytes of device workspace ``fwd_paged`` needs on the current device."""
-    key = (torch.cuda.current_device(), d)
-    if key not in _PAGED_BYTES:
-        n = ctypes.c_size_t(0)
-        _check(_lib().fa_paged_workspace_bytes(d, ctypes.byref(n)), "fa_paged_workspace_bytes")
-        _PAGED_BYTES[key] = n.value
-    return _PAGED_BYTES[key]
+    n = ctypes.c_size_t(0)
+    _check(_lib().fa_paged_workspace_bytes(d, ctypes.byref(n)), "fa_paged_workspace_bytes")
+    return n.value
 
 
 def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
@@ -510,14 +514,13 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, blo
     ``window`` None: every key up to a query's own.  ``max_q``: the most new
     tokens of any sequence, if known.  Returns (O [T, Hq, d], LSE [T, Hq]);
     rows outside every sequence are left as they were."""
-    cache, index = _cache(k_pages, v_pages)
+    cache, heads, d, dt, index = _cache(k_pages, v_pages)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [T, Hq, d] CUDA tensor")
-    T, Hq, d = q.shape
-    dt = k_pages.dtype
-    q_stride = _check_tokens("q", q, T, Hq, cache.d, dt, index)
+    T, Hq, _ = q.shape
+    q_stride = _check_tokens("q", q, T, Hq, d, dt, index)
     B, table_stride, max_pages = _check_batch(block_table, cu_q, seq_k, index)
-    if cache.heads == 0 or Hq % cache.heads != 0:
+    if heads == 0 or Hq % heads != 0:
         raise ValueError("the number of query heads must be a multiple of the number of key/value heads")
     dev = k_pages.device
     if out is None:
@@ -530,7 +533,10 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, blo
         _check_out("lse", lse, (T, Hq), torch.float32, index)
     with _guard(index):
         if workspace is None:
-            workspace = torch.empty((paged_workspace_bytes(d),), dtype=torch.uint8, device=dev)
+            need = _PAGED_BYTES.get((index, d))
+            if need is None:
+                need = _PAGED_BYTES[index, d] = paged_workspace_bytes(d)
+            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
         st = _lib().fa_fwd_paged(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
                                  table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), B, T, Hq, q_stride,
                                  int(max_q), 1 << 30 if window is None else int(window), int(sinks), _scale(scale, d),
@@ -550,8 +556,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     Hq, d] if given, are rotated by their positions first.  k, v and q may be
     slices of one projection.  Returns the rotated queries (``q_out``), or
     None without q."""
-    cache, index = _cache(k_pages, v_pages)
-    dt, d, heads = k_pages.dtype, cache.d, cache.heads
+    cache, heads, d, dt, index = _cache(k_pages, v_pages)
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be a [T, heads, d] CUDA tensor")
     T = k.shape[0]
@@ -563,7 +568,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
         Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
         qs = _check_tokens("q", q, T, Hq, d, dt, index)
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=dt, device=k_pages.device)
+            q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
         else:
             _check_out("q_out", q_out, (T, Hq, d), dt, index)
         qp, op = q.data_ptr(), q_out.data_ptr()

@@ -144,7 +144,7 @@ fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, fl
   L.prm.Hq = (int)Hq;
   L.prm.Hkv = (int)Hkv;
   L.prm.o_vec32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
-  L.prm.drop_pos = fa::internal_take_inject() ? 3 : -1;
+  L.prm.drop_pos = fa::internal_take_inject() ? 1 : -1;  // (a slot that any unit with a key uses)
   L.prm.N = (int)Nq;
   L.prm.Nk = (int)Nk;
   L.prm.BH = (int)(B * Hq);
@@ -220,7 +220,7 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   p.Hq = (int)Hq;
   p.Hkv = (int)Hkv;
   p.o_vec32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
-  p.drop_pos = fa::internal_take_inject() ? 3 : -1;
+  p.drop_pos = fa::internal_take_inject() ? 1 : -1;
   p.cu_q = cu_q;
   p.seq_k = seq_k;
   p.table = block_table;

@@ -578,13 +578,13 @@ fa_status fa_check_device_error(cudaStream_t stream);
 
 /*
  * fa_debug_inject -- TEST HOOK for the failure path; not for production use.
- * flags bit 0: the next fa_fwd / fa_fwd_fp8 launch has its first CTA leave
- * one K/V ring slot unfilled (the next fa_bwd launch: one Q/dO stage of its
- * first CTA's second step), so the bounded waits on it run out (about 2 s):
+ * flags bit 0: the next fa_fwd / fa_fwd_fp8 / fa_fwd_window / fa_fwd_paged
+ * launch has its first CTA leave one K/V ring slot unfilled (the next fa_bwd
+ * or fa_bwd_window launch: one Q/dO stage of its first CTA's second step), so the bounded waits on it run out (about 2 s):
  * the kernel then stops every role, frees its tensor memory and ends, and
  * fa_check_device_error() returns FA_ERR_TIMEOUT.  The output of that
  * launch is incomplete.  The flag is consumed by the next fa_fwd*,
- * fa_fwd_fp8* or fa_bwd call.
+ * fa_fwd_fp8* or fa_bwd* call.
  * flags bit 1: the same for the next quantiser call (fa_quant_fp8,
  * fa_quant_fp8_rope or fa_quant_fp8_per_tensor_noalloc): the first CTA of its
  * first launch leaves one input slot unfilled; the blocks it cannot finish

@@ -415,3 +415,25 @@ def test_append_then_attend_in_chunks_matches_dense(fa):
         ref = reference(qd[b], keys[b], vals[b], window, sinks, d ** -0.5)
         check_forward(o[b].transpose(0, 1), lse[b].transpose(0, 1), ref, torch.bfloat16, d, N, f"paged, sequence {b}")
         check_forward(od[b], ld[b], ref, torch.bfloat16, d, N, f"dense, sequence {b}")
+
+
+@pytest.mark.parametrize("sinks", [1, 32, 33])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_few_sinks_far_from_the_window(fa, sinks, d):
+    _run(fa, [(1, 1900), (70, 900), (3, 2500)], 4, 2, d, torch.bfloat16, 16, window=150, sinks=sinks)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_paged_wait_that_runs_out_is_reported(fa, d):
+    lens = [(200, 900), (1, 3000)]
+    q, c, cu, sk, seqs = _batch(lens, 4, 2, d, torch.bfloat16, 16)
+    want = fa.fwd_paged(q, c.k, c.v, c.table, cu, sk)
+    fa.check_device_error()
+    assert fa.lib().fa_debug_inject(1) == fa.FA_OK
+    fa.fwd_paged(q, c.k, c.v, c.table, cu, sk)
+    with pytest.raises(fa.FaError) as e:
+        fa.check_device_error()
+    assert e.value.status == fa.FA_ERR_TIMEOUT
+    got = fa.fwd_paged(q, c.k, c.v, c.table, cu, sk)
+    fa.check_device_error()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

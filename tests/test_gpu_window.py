@@ -139,3 +139,28 @@ def test_window_forward_in_a_graph_and_on_a_stream(fa):
     torch.cuda.synchronize()
     want = fa.fwd_window(q2, k, v, *case[6:])
     assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
+@pytest.mark.parametrize("sinks", [1, 31, 32, 33, 64, 127, 128])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_few_sinks_far_from_the_window(fa, sinks, d):
+    # up to 32 sinks in a tile of their own take a narrower path
+    _check(fa, (1, 3, 1, 700, 1900, d, 150, sinks), torch.bfloat16)
+    _check(fa, (1, 2, 1, 1, 900, d, 3, sinks), torch.float16, scale=-0.1)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_window_wait_that_runs_out_is_reported(fa, d):
+    # a ring slot that the kernel leaves unfilled: the waits on it end after
+    # their limit, the call is reported, and the next one is right
+    q, k, v = _inputs(1, 2, 2, 900, 900, d, 41, torch.bfloat16)
+    want = fa.fwd_window(q, k, v, 400, 4)
+    fa.check_device_error()
+    assert fa.lib().fa_debug_inject(1) == fa.FA_OK
+    fa.fwd_window(q, k, v, 400, 4)
+    with pytest.raises(fa.FaError) as e:
+        fa.check_device_error()
+    assert e.value.status == fa.FA_ERR_TIMEOUT
+    got = fa.fwd_window(q, k, v, 400, 4)
+    fa.check_device_error()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

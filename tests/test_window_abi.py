@@ -77,6 +77,11 @@ def _cache(fa, **kw):
     return fa._KvCache(*a.values())
 
 
+def test_the_packed_cache_is_the_structure(fa):
+    v = (P, 2 * P, 10, 16, 2, 64, 2048, 1024, 64, 1)
+    assert fa._KV_PACK(*v) == bytes(fa._KvCache(*v)) and len(fa._KV_PACK(*v)) == ctypes.sizeof(fa._KvCache)
+
+
 BAD_CACHES = [dict(k=None), dict(v=None), dict(k=P + 8), dict(num_pages=0), dict(heads=0), dict(page_size=0), dict(dtype=3),
               dict(token_stride=60), dict(token_stride=68), dict(head_stride=1020), dict(head_stride=0), dict(page_stride=-64),
               dict(token_stride=32)]
@@ -88,7 +93,7 @@ def _paged(fa, cache=None, **kw):
     a = dict(q=P, cache=None, o=P, lse=P, table=P, table_stride=4, max_pages=4, cu_q=P, seq_k=P, B=2, T=5, Hq=4, q_stride=256,
              max_q=0, window=1 << 30, sinks=0, scale=0.1, ws=P, ws_bytes=1 << 40)
     a.update(kw)
-    a["cache"] = ctypes.byref(_cache(fa, **(cache or {})))
+    a["cache"] = bytes(_cache(fa, **(cache or {})))
     return fa.lib().fa_fwd_paged(*a.values(), None)
 
 
@@ -118,7 +123,7 @@ def _append(fa, cache=None, **kw):
     a = dict(cache=None, q=P, k=P, v=P, q_out=P, q_stride=256, k_stride=128, v_stride=128, table=P, table_stride=4, max_pages=4,
              cu_q=P, seq_k=P, B=2, T=5, Hq=4, cos=P, sin=P, rope_len=100, layout=fa.FA_ROPE_HALF)
     a.update(kw)
-    a["cache"] = ctypes.byref(_cache(fa, **(cache or {})))
+    a["cache"] = bytes(_cache(fa, **(cache or {})))
     return fa.lib().fa_cache_append(*a.values(), None)
 
 
