@@ -25,7 +25,7 @@ UNITS = ["api.cu", "attn_bf16.cu", "attn_fp16.cu", "attn_fp8.cu", "quant_fp8.cu"
          "attn_window_fp16.cu", "attn_paged_bf16.cu", "attn_paged_fp16.cu", "paged.cu"]
 ABLATE_UNITS = ["ablate_api.cu", "ablate_bf16.cu", "ablate_bf16_causal.cu", "ablate_fp8.cu", "ablate_d64.cu"]
 HEADERS = ["ptx.cuh", "attn_fwd.cuh", "quant_fp8.h", "attn_bwd.h", "splitkv.h", "ablate_inst.h", "api_internal.h",
-           "attn_window.cuh", "paged.h"]
+           "attn_window.cuh", "paged.h", "ptx_window.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -18,6 +18,7 @@
 #include "splitkv.h"
 #include "quant_fp8.h"
 #include "attn_bwd.h"
+#include "ptx_window.cuh"
 
 // The attention kernels are instantiated in their own translation units
 // (attn_bf16.cu, attn_fp16.cu, attn_fp8.cu, attn_split_*.cu), compiled in

@@ -46,7 +46,7 @@
 #include <cuda_runtime.h>
 
 #include "attn_bwd.h"
-#include "ptx.cuh"
+#include "ptx_window.cuh"
 
 namespace fa {
 namespace {

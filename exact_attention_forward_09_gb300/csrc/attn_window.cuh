@@ -42,7 +42,7 @@
 #include <cuda_fp16.h>
 
 #include "attn_fwd.cuh"
-#include "ptx.cuh"
+#include "ptx_window.cuh"
 
 namespace fa {
 

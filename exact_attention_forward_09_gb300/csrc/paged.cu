@@ -7,7 +7,7 @@
 
 #include "fa.h"
 #include "paged.h"
-#include "ptx.cuh"
+#include "ptx_window.cuh"
 
 namespace fa {
 namespace {

@@ -13,8 +13,7 @@
 namespace fa {
 
 // Device error word values (read back by fa_check_device_error).
-// FA_DEVERR_INDEX is a bit of its own, set beside a timeout's.
-enum : int { FA_DEVERR_NONE = 0, FA_DEVERR_TIMEOUT = 1, FA_DEVERR_INDEX = 2 };
+enum : int { FA_DEVERR_NONE = 0, FA_DEVERR_TIMEOUT = 1 };
 
 // Wait budget of one pipeline wait, in nanoseconds of %globaltimer.
 #ifndef FA_WAIT_LIMIT_NS
@@ -113,16 +112,6 @@ __device__ __forceinline__ void tma_load_3d_hint(void* smem_dst, const CUtensorM
       : "memory");
 }
 
-// The same for a 4-D map.
-__device__ __forceinline__ void tma_load_4d_hint(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int c0,
-                                                 int c1, int c2, int c3, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "l"(policy)
-      : "memory");
-}
-
 __device__ __forceinline__ uint64_t policy_evict_last() {
   uint64_t p;
   asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(p));
@@ -189,15 +178,6 @@ __device__ __forceinline__ bool bar_and(uint32_t id, uint32_t nthreads, bool pre
 __device__ __forceinline__ void bar_sync_n(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
-
-// --------------------------------------------------- dependent launches --
-// In a kernel launched with programmatic stream serialisation: waits until
-// the kernel before it in the stream has ended and its writes are visible
-// (returns at once otherwise).
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-// Lets the next kernel of the stream be launched, if it was asked for so,
-// once every CTA of this one has come here or ended.
-__device__ __forceinline__ void pdl_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // ------------------------------------------------- register reallocation --
 // Executed by all threads of a warpgroup: shrink / grow its per-thread
