@@ -17,12 +17,20 @@ namespace {
 // m = max_s LSE_s and w_s = e^(LSE_s - m), O = sum_s w_s O_s / sum_s w_s and
 // LSE = m + ln sum_s w_s, summed in a fixed order.  Lane l holds columns l*E
 // .. l*E+E-1 of a row.  A unit cut in a few parts (chunks: up to 256 rows, two
-// or three parts) takes a warp per two rows; one cut in many (a single long
-// context: a few rows, as many parts as the GPU has SMs per head) takes a
-// block per row, whose warps share the parts and meet in shared memory.  The
-// parts were just written and lie in L2, and what is left is latency: the
-// loads of a row's parts go out before the weights they meet are known.
+// or three parts) takes a warp per two rows; of one cut in many (a long
+// context: as many parts as the GPU has SMs per head) a block takes up to
+// eight rows at once, so that its rows take few rounds, and each row's share
+// of the warps splits the parts and meets in shared memory.  The parts were
+// just written and lie in L2, and what is left is latency: the loads of a
+// row's parts go out before the weights they meet are known, and the blocks of
+// a call with few units go to its cut units alone.
+//   d = 128, one sequence of 12000 keys, 32/2 heads, 8 new tokens (128 rows
+//   per head): 15.2 us in all; 25.0 with blocks spread over all CTAs' units, 40.9
+//   with a whole block for one row after the other.  (Ranking the cut units
+//   costs 0.5 us, so calls with many units or few rows keep a block per CTA.)
 constexpr int kFewParts = 4;
+constexpr int kThreads = 256;
+constexpr int kMaxCtas = 2 * kThreads;
 
 // x = columns lane*E .. of a row of parts
 template <int E>
@@ -40,22 +48,56 @@ __device__ __forceinline__ void load_cols(float (&x)[E], const float* src) {
 __device__ __forceinline__ float part_weight(float l, float m) { return l == -INFINITY ? 0.0f : expf(l - m); }
 
 template <int D, bool F16>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const float* __restrict__ o_part,
-                                                            const float* __restrict__ lse_part,
-                                                            const int4* __restrict__ desc, void* __restrict__ o,
-                                                            float* __restrict__ lse, int slot_rows, int g, int Hq) {
+__global__ void __launch_bounds__(kThreads) paged_combine_kernel(
+    const float* __restrict__ o_part, const float* __restrict__ lse_part, const int4* __restrict__ desc,
+    void* __restrict__ o, float* __restrict__ lse, int ctas, int slot_rows, int g, int Hq) {
   constexpr int E = D / 32;
   __shared__ float red[8][D];
   __shared__ float red_w[8];
+  __shared__ int warp_cut[8];
+  __shared__ int4 shared_u;
+  __shared__ int shared_cta;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_launch();
   pdl_wait();  // the parts and desc are the previous kernel's
-  const int4 u = desc[blockIdx.x];
-  const int parts = u.x, rows = u.w;
+  int4 u;
+  int cta = blockIdx.x;
+  if (gridDim.x == ctas) {
+    u = desc[cta];
+  } else {
+    // fewer units than CTAs: the k-th cut unit goes to blocks (k, y)
+    int4 mine[2];
+    uint32_t has[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int c = i * kThreads + threadIdx.x;
+      mine[i] = c < ctas ? desc[c] : make_int4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) has[i] = __ballot_sync(0xffffffffu, mine[i].x != 0);
+    if (lane == 0) warp_cut[warp] = __popc(has[0]) + __popc(has[1]);
+    if (threadIdx.x == 0) shared_u = make_int4(0, 0, 0, 0);
+    __syncthreads();
+    int rank = 0;
+#pragma unroll
+    for (int w = 0; w < 8; ++w)
+      if (w < warp) rank += warp_cut[w];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (mine[i].x != 0 && rank + __popc(has[i] & ((1u << lane) - 1)) == blockIdx.x) {
+        shared_u = mine[i];
+        shared_cta = i * kThreads + threadIdx.x;
+      }
+      rank += __popc(has[i]);
+    }
+    __syncthreads();
+    u = shared_u;
+    cta = shared_cta;
+  }
+  const int parts = u.x, rows = u.w, slot0 = 2 * cta;
   if (parts == 0) return;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   auto at = [&](int s, int row) -> long long {
-    const long long slot = s == 0 ? 2LL * blockIdx.x + 1 : 2LL * (blockIdx.x + s);
-    return slot * slot_rows + row;
+    return (long long)(s == 0 ? slot0 + 1 : slot0 + 2 * s) * slot_rows + row;
   };
   auto out_row = [&](int row) -> long long { return (long long)(u.y + row / g) * Hq + u.z * g + row % g; };
   if (parts <= kFewParts) {
@@ -105,31 +147,40 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const float* __restr
     return;
   }
   constexpr int AHEAD = E <= 4 ? 8 : 4;  // parts in flight per warp
-  for (int row = blockIdx.y; row < rows; row += gridDim.y) {
+  // rows that the block takes at once: enough for one round, at most a row per warp
+  int lg = 0;
+  while (lg < 3 && (int)(gridDim.y << lg) < rows) ++lg;
+  const int share = 8 >> lg;  // warps per row
+  const int sub = warp / share, first = warp % share;
+  for (int base = blockIdx.y; base < rows; base += gridDim.y << lg) {
+    const int row = base + sub * gridDim.y;
+    const bool valid = row < rows;
     float m = -INFINITY;
-    for (int s = lane; s < parts; s += 32) m = fmaxf(m, lse_part[at(s, row)]);
     float acc[E], wsum = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    for (int s0 = warp; s0 < parts; s0 += 8 * AHEAD) {  // this warp's parts: s0, s0 + 8, ...
-      const int n = min(AHEAD, (parts - s0 + 7) / 8);
-      float x[AHEAD][E];
+    if (valid) {
+      for (int s = lane; s < parts; s += 32) m = fmaxf(m, lse_part[at(s, row)]);
+      for (int s0 = first; s0 < parts; s0 += share * AHEAD) {  // this warp's parts: s0, s0 + share, ...
+        const int n = min(AHEAD, (parts - s0 + share - 1) / share);
+        float x[AHEAD][E];
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i)
-        if (i < n) load_cols<E>(x[i], o_part + at(s0 + 8 * i, row) * D + lane * E);
-      const float l = lane < n ? lse_part[at(s0 + 8 * lane, row)] : -INFINITY;
-      if (s0 == warp) {
+        for (int i = 0; i < AHEAD; ++i)
+          if (i < n) load_cols<E>(x[i], o_part + at(s0 + share * i, row) * D + lane * E);
+        const float l = lane < n ? lse_part[at(s0 + share * lane, row)] : -INFINITY;
+        if (s0 == first) {
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-      }
-      const float w = lane < n ? part_weight(l, m) : 0.0f;
-      wsum += w;
+          for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        }
+        const float w = lane < n ? part_weight(l, m) : 0.0f;
+        wsum += w;
 #pragma unroll
-      for (int i = 0; i < AHEAD; ++i) {
-        const float wi = __shfl_sync(0xffffffffu, w, i);
-        if (i < n) {
+        for (int i = 0; i < AHEAD; ++i) {
+          const float wi = __shfl_sync(0xffffffffu, w, i);
+          if (i < n) {
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, x[i][e], acc[e]);
+            for (int e = 0; e < E; ++e) acc[e] = fmaf(wi, x[i][e], acc[e]);
+          }
         }
       }
     }
@@ -139,24 +190,24 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const float* __restr
     for (int e = 0; e < E; ++e) red[warp][lane * E + e] = acc[e];
     if (lane == 0) red_w[warp] = wsum;
     __syncthreads();
-    float total = 0.0f;
-#pragma unroll
-    for (int w = 0; w < 8; ++w) total += red_w[w];
-    const float inv = total != 0.0f ? 1.0f / total : 0.0f;
-    const long long r = out_row(row);
-    if (threadIdx.x < D / 2) {
-      float a = 0.0f, b = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) {
-        a += red[w][2 * threadIdx.x];
-        b += red[w][2 * threadIdx.x + 1];
+    if (valid) {
+      float total = 0.0f;
+      for (int w = 0; w < share; ++w) total += red_w[sub * share + w];
+      const float inv = total != 0.0f ? 1.0f / total : 0.0f;
+      const long long r = out_row(row);
+      for (int c = first * 32 + lane; c < D / 2; c += share * 32) {
+        float x = 0.0f, y = 0.0f;
+        for (int w = 0; w < share; ++w) {
+          x += red[sub * share + w][2 * c];
+          y += red[sub * share + w][2 * c + 1];
+        }
+        reinterpret_cast<uint32_t*>(o)[r * (D / 2) + c] =
+            F16 ? pack_f16x2(x * inv, y * inv) : pack_bf16x2(x * inv, y * inv);
       }
-      reinterpret_cast<uint32_t*>(o)[r * (D / 2) + threadIdx.x] =
-          F16 ? pack_f16x2(a * inv, b * inv) : pack_bf16x2(a * inv, b * inv);
+      // (a row's first warp has a part, so its maximum is the row's)
+      if (first == 0 && lane == 0) lse[r] = total == 0.0f ? -INFINITY : m + logf(total);
     }
-    // (warp 0 has a part, so thread 0's maximum is the row's)
-    if (threadIdx.x == 0) lse[r] = total == 0.0f ? -INFINITY : m + logf(total);
-    __syncthreads();  // red is read before the next row's sums
+    __syncthreads();  // red is read before the next rows' sums
   }
 }
 
@@ -321,14 +372,23 @@ cudaError_t launch_cache_append(const AppendParams& prm, int d, bool f16, int la
 }
 
 cudaError_t launch_paged_combine(const float* o_part, const float* lse_part, const int4* desc, void* o, float* lse,
-                                 int ctas, int slot_rows, int max_rows, int g, int Hq, int d, bool f16,
-                                 cudaStream_t stream) {
+                                 int sms, int ctas, int max_units, int slot_rows, int max_rows, int g, int Hq, int d,
+                                 bool f16, cudaStream_t stream) {
   // launched while the attention kernel still runs; it waits for it itself
   cudaLaunchConfig_t cfg = {};
-  // a block takes 16 rows of a unit cut in few parts, or one of a unit cut in many
+  if (ctas > kMaxCtas) return cudaErrorInvalidValue;
+  // a block per CTA and 16 rows of a unit cut in few parts, or one row of a
+  // unit cut in many; with so few units that their blocks would leave SMs
+  // idle, a block per unit and as many rows as fill the GPU four times
   const int few = (max_rows + 15) / 16, many = max_rows < 8 ? max_rows : 8;
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(few > many ? few : many), 1);
-  cfg.blockDim = dim3(256, 1, 1);
+  int x = ctas, y = few > many ? few : many;
+  const int spread = 4 * sms / (max_units < ctas ? max_units : ctas);
+  if (spread > y && max_rows > y) {
+    x = max_units;
+    y = spread < max_rows ? spread : max_rows;
+  }
+  cfg.gridDim = dim3((unsigned)x, (unsigned)y, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -336,7 +396,7 @@ cudaError_t launch_paged_combine(const float* o_part, const float* lse_part, con
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   auto go = [&](auto kern) {
-    return cudaLaunchKernelEx(&cfg, kern, o_part, lse_part, desc, o, lse, slot_rows, g, Hq);
+    return cudaLaunchKernelEx(&cfg, kern, o_part, lse_part, desc, o, lse, ctas, slot_rows, g, Hq);
   };
   switch (d) {
     case 64: return f16 ? go(paged_combine_kernel<64, true>) : go(paged_combine_kernel<64, false>);

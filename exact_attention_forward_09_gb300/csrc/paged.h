@@ -11,10 +11,11 @@ namespace fa {
 // lies in slot 2 c + 1 and part s >= 1 in slot 2 (c + s); a slot holds
 // slot_rows rows of o_part ([d] fp32) and lse_part.  Row r of the unit goes
 // to token first + r / g, head kv_head * g + r % g of o [T, Hq, d] and lse
-// [T, Hq].  max_rows: the most rows a unit can have.
+// [T, Hq].  max_units: the most units the call can have; max_rows: the rows a
+// unit is expected to have at most (more are joined, if slower).
 cudaError_t launch_paged_combine(const float* o_part, const float* lse_part, const int4* desc, void* o, float* lse,
-                                 int ctas, int slot_rows, int max_rows, int g, int Hq, int d, bool f16,
-                                 cudaStream_t stream);
+                                 int sms, int ctas, int max_units, int slot_rows, int max_rows, int g, int Hq, int d,
+                                 bool f16, cudaStream_t stream);
 
 struct AppendParams {
   const uint16_t *q, *k, *v;   // new tokens: [T, heads, d], rows of a token contiguous

@@ -239,7 +239,8 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   const int64_t keys = max_pages * cache->page_size < kMaxLen ? max_pages * cache->page_size : kMaxLen;
   int64_t tiles = keys / fa::kBN + 1;
   if (p.window + (int64_t)p.sinks + unit_tok < keys) tiles = (p.window + (int64_t)p.sinks + unit_tok) / fa::kBN + 4;
-  if ((T / unit_tok + B) * Hkv >= (int64_t)0x7fffffff / (2 * (tiles + 1))) return FA_ERR_UNSUPPORTED;
+  const int64_t units = (T / unit_tok + B) * Hkv;
+  if (units >= (int64_t)0x7fffffff / (2 * (tiles + 1))) return FA_ERR_UNSUPPORTED;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   p.o_part = reinterpret_cast<float*>(w);
   p.lse_part = reinterpret_cast<float*>(w + ws.lse_at);
@@ -248,8 +249,9 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   L.stream = stream;
   if ((st = launch_window<true>(L, d, cache->dtype)) != FA_OK) return st;
   const int64_t most = (max_q > 0 && max_q < unit_tok ? max_q : unit_tok) * g;
-  return fa::launch_paged_combine(p.o_part, p.lse_part, p.desc, o, lse, ctas, slot_rows_of(d), (int)most, (int)g,
-                                  (int)Hq, (int)d, cache->dtype == FA_DTYPE_FP16, stream) == cudaSuccess
+  return fa::launch_paged_combine(p.o_part, p.lse_part, p.desc, o, lse, ctas, ctas, (int)units, slot_rows_of(d),
+                                  (int)most, (int)g, (int)Hq, (int)d, cache->dtype == FA_DTYPE_FP16, stream) ==
+                 cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
 }
