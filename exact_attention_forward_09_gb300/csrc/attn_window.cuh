@@ -46,14 +46,30 @@
 
 namespace fa {
 
-template <int ELEM, int D, bool PAGED>
+// PAIR: two query tiles per CTA, one CTA per SM (d <= 128).  Without it one
+// query tile per CTA: d = 256, whose S is double-buffered instead, and a paged
+// d = 64 form with two CTAs per SM, for batches whose sequences mostly bring
+// few rows.  With one query tile in use a key tile's chain (S, softmax, P V) is
+// all that runs, and at d = 64 its 32 KB take less time to arrive than the
+// chain: two independent CTAs read 64 sequences of 2000 to 16000 keys (one
+// token each, 32/8 heads) in 220 us, 5.6 TB/s, a pair in 310; at d = 128 one
+// chain keeps up with the memory.  On long chunks the pair is faster (500
+// against 566 us for 4 x 2048 tokens over 4000 to 10000 keys): it reads each
+// key tile once for two query tiles.
+template <int ELEM, int D, bool PAGED, bool PAIR = (D <= 128)>
 struct WinCfg {
   static_assert(ELEM == kBF16 || ELEM == kFP16, "16-bit operands");
   static constexpr int ROW_BYTES = D * 2;
   static constexpr int CH_ELEMS = 64;                      // elements per 128-byte chunk
   static constexpr int NCH = D / CH_ELEMS;
   static constexpr int CHUNK_BYTES = 128 * 128;            // 128 rows x 128 bytes
-  static constexpr int NQT = D <= 128 ? 2 : 1;             // query tiles per CTA
+  static constexpr int NQT = PAIR ? 2 : 1;                 // query tiles per CTA
+  static constexpr bool ALT = D <= 128;                    // one S buffer per query tile; ring K0 V0 K1 V1 ...
+  static constexpr int OCC = ALT && !PAIR ? 2 : 1;         // CTAs per SM
+  static_assert(!PAIR || ALT, "two query tiles of d = 256 exceed tensor memory");
+  static_assert(OCC == 1 || PAGED, "dense calls use pairs");
+  // shared memory of a CTA: what two per SM leave beside their reserves
+  static constexpr int SMEM_LIMIT = OCC == 2 ? 115712 : kSmemLimit;
   static constexpr int TILE_BYTES = kBN * ROW_BYTES;
   static constexpr int SLOT_BYTES = TILE_BYTES < 32768 ? TILE_BYTES : 32768;
   static constexpr int SPT = TILE_BYTES / SLOT_BYTES;      // ring slots per tile
@@ -66,27 +82,28 @@ struct WinCfg {
   static constexpr bool EPI_TMA = !PAGED && D <= 128;
   static constexpr int EPI_WARP_BYTES = 32 * 64 * 2;
   static constexpr int EPI_BYTES = EPI_TMA ? 4 * NQT * EPI_WARP_BYTES : 0;
-  static constexpr int NS_MAX = (kSmemLimit - 2048 - EPI_BYTES - Q_BYTES) / SLOT_BYTES;
+  static constexpr int NS_MAX = (SMEM_LIMIT - 2048 - EPI_BYTES - Q_BYTES) / SLOT_BYTES;
   static constexpr int NS = NS_MAX > 8 ? 8 : NS_MAX;
   static_assert(NS >= 2 * SPT, "ring too shallow");
   static constexpr int P_COLS = kBN / 2;
-  static constexpr uint32_t TMEM_COLS = 512;
-  static constexpr uint32_t O_COL0 = 256;                  // S / P buffers at 0 and 128
+  static constexpr uint32_t TMEM_COLS = 512 / OCC;
+  static constexpr uint32_t O_COL0 = OCC == 2 ? 128 : 256;  // behind the S / P buffers at 0 and (but for OCC 2) 128
   static_assert(O_COL0 + NQT * D <= TMEM_COLS, "TMEM budget");
   static constexpr int SOFTMAX_WARPS = 4 * NQT;
   static constexpr int MMA_WARP = SOFTMAX_WARPS;
   static constexpr int LOAD_WARP = SOFTMAX_WARPS + 1;
-  // paged: a second load warp takes the V tiles.  A box is one page's rows of
-  // one 128-byte column chunk, and a warp issues one about every 80 clocks: at
-  // 16-token pages a K and a V tile of d = 128 are 32 boxes, as long to issue
-  // as the tiles' arithmetic takes (chunks over 16-token pages: 652 -> 590 us
-  // for 4 x 2048 new tokens over 4000 to 10000 keys).
-  static constexpr int LOADV_WARP = PAGED ? LOAD_WARP + 1 : -1;
-  static constexpr int UNIT_READERS = SOFTMAX_WARPS + 1 + (PAGED ? 1 : 0);  // warps that release a unit's slot
+  // paged, one CTA per SM: a second load warp takes the V tiles.  A box is one
+  // page's rows of one 128-byte column chunk, and a warp issues one about every
+  // 80 clocks: at 16-token pages a K and a V tile of d = 128 are 32 boxes, as
+  // long to issue as the tiles' arithmetic takes (chunks over 16-token pages:
+  // 652 -> 590 us for 4 x 2048 new tokens over 4000 to 10000 keys).
+  static constexpr bool V_WARP = PAGED && OCC == 1;
+  static constexpr int LOADV_WARP = V_WARP ? LOAD_WARP + 1 : -1;
+  static constexpr int UNIT_READERS = SOFTMAX_WARPS + 1 + (V_WARP ? 1 : 0);  // warps that release a unit's slot
   // two query tiles: a third, control warpgroup gives registers to the
   // softmax warpgroups (the split of attn_fwd.cuh)
-  static constexpr bool REALLOC = NQT == 2;
-  static constexpr int THREADS = REALLOC ? 32 * (SOFTMAX_WARPS + 4) : 32 * (SOFTMAX_WARPS + (PAGED ? 3 : 2));
+  static constexpr bool REALLOC = PAIR;
+  static constexpr int THREADS = REALLOC ? 32 * (SOFTMAX_WARPS + 4) : 32 * (SOFTMAX_WARPS + (V_WARP ? 3 : 2));
   static constexpr int CTRL_REGS = 104;
   static constexpr int SOFTMAX_REGS = 200;
   // A few sinks are usually all that is seen of tile 0: then only its first
@@ -104,7 +121,7 @@ struct WinCfg {
   static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
   static_assert(OFF_EPI % 1024 == 0 && OFF_BAR % 1024 == 0, "1024-byte swizzle atoms");
   static constexpr int SMEM_BYTES = OFF_BAR + 1024 + 1024;  // + barriers + alignment slack
-  static_assert(SMEM_BYTES <= kSmemLimit, "shared memory budget");
+  static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
 };
 
 struct WinParams {
@@ -132,8 +149,8 @@ struct WinParams {
   int g;              // query heads per key/value head
   int tpt;            // tokens per query tile (tpt * g <= 128)
   int min_places;     // a CTA's run of the line is at least this long
-  float* o_part;      // [2 * grid][NQT * 128][D] partial results of cut units
-  float* lse_part;    // [2 * grid][NQT * 128]
+  float* o_part;      // [2 * grid][slot rows][D] partial results of cut units
+  float* lse_part;    // [2 * grid][slot rows], NQT * 128 of them
   int4* desc;         // [grid] cut units: {parts, first token, kv head, rows}
 };
 
@@ -330,12 +347,12 @@ __device__ __noinline__ bool clear_v_row(Bars* bars, uint32_t row, int pv, bool 
   return true;
 }
 
-template <int ELEM, int D, bool PAGED>
-__global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
+template <int ELEM, int D, bool PAGED, bool PAIR>
+__global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, PAIR>::THREADS, WinCfg<ELEM, D, PAGED, PAIR>::OCC)
     attn_window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                        const WinParams prm) {
-  using C = WinCfg<ELEM, D, PAGED>;
+  using C = WinCfg<ELEM, D, PAGED, PAIR>;
   using Bars = WinBars<C::NS>;
   static_assert(sizeof(Bars) <= 1024, "barrier area");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -529,9 +546,9 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
     return true;
   };
   // Ring positions within a unit of n tiles, in the order in which the MMA
-  // warp consumes them: K0 V0 K1 V1 ... (two query tiles), K0 K1 V0 K2 V1 ...
-  auto k_at = [&](int j) -> int { return (C::NQT == 2 ? 2 * j : (j < 2 ? j : 2 * j - 1)) * C::SPT; };
-  auto v_at = [&](int j, int n) -> int { return (C::NQT == 2 ? 2 * j + 1 : j + min(j + 2, n)) * C::SPT; };
+  // warp consumes them: K0 V0 K1 V1 ..., or (S double-buffered) K0 K1 V0 K2 V1 ...
+  auto k_at = [&](int j) -> int { return (C::ALT ? 2 * j : (j < 2 ? j : 2 * j - 1)) * C::SPT; };
+  auto v_at = [&](int j, int n) -> int { return (C::ALT ? 2 * j + 1 : j + min(j + 2, n)) * C::SPT; };
   // Never leave with copies in flight: the last fills of the slots used (pos
   // positions so far).  After a wait ran out some of them were never issued;
   // those that were land within microseconds.
@@ -548,7 +565,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
 
   if (warp >= C::SOFTMAX_WARPS) {
     if constexpr (C::REALLOC) regs_dec<C::CTRL_REGS>();
-    if (PAGED && warp == C::LOADV_WARP) {
+    if (C::V_WARP && warp == C::LOADV_WARP) {
       // -------------------------------------------------------- load V --
       const uint64_t pol_kv = policy_evict_last();
       int pos = 0;
@@ -595,7 +612,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
         }
         return __shfl_sync(0xffffffffu, (int)good, 0) != 0;
       };
-      // Q tiles and every key tile of a unit (dense: and every value tile)
+      // Q tiles and every key tile of a unit (and, without a V warp, every value tile)
       auto load_unit = [&](const WinUnit& w) {
         const int n = w.r1 - w.r0;
         if (n <= 0) return;  // no visible key: nothing to load
@@ -622,15 +639,15 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
         for (int j = 0; j < n && ok; ++j) {
           const int ids2 = pages_of(w, w.r0 + j + 2);
           ok = load_tile(w, &tm_k, pos + k_at(j), w.r0 + j, ids, pol_kv);
-          if (!PAGED && ok) {
+          if (!C::V_WARP && ok) {
             // this warp issues V too, in ring order
-            if (C::NQT == 2) ok = load_tile(w, &tm_v, pos + v_at(j, n), w.r0 + j, 0, pol_kv);
+            if (C::ALT) ok = load_tile(w, &tm_v, pos + v_at(j, n), w.r0 + j, ids, pol_kv);
             else if (j >= 1) ok = load_tile(w, &tm_v, pos + v_at(j - 1, n), w.r0 + j - 1, 0, pol_kv);
           }
           ids = ids1;
           ids1 = ids2;
         }
-        if (!PAGED && C::NQT == 1 && ok) ok = load_tile(w, &tm_v, pos + v_at(n - 1, n), w.r0 + n - 1, 0, pol_kv);
+        if (!C::V_WARP && !C::ALT && ok) ok = load_tile(w, &tm_v, pos + v_at(n - 1, n), w.r0 + n - 1, 0, pol_kv);
         pos += 2 * n * C::SPT;
         ++k;
       };
@@ -780,8 +797,8 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
       const uint32_t ring_s = smem_u32(smem + C::OFF_RING);
       int pos = 0;          // ring position of the next tile to consume
       int k = 0;            // units with keys processed
-      int pc[2] = {0, 0};   // two query tiles: P handshakes consumed per tile
-      int it = 0;           // one query tile: S/P iterations so far (buffer = it & 1)
+      int pc[2] = {0, 0};   // P handshakes consumed per query tile
+      int it = 0;           // S double-buffered: S/P iterations so far (buffer = it & 1)
       bool ok = true;
       auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
         return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, prm.err));
@@ -854,7 +871,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
         auto qk_issued = [&]() {
           if (--qk_left == 0) mma_commit_elect(&bars->q_empty);  // the unit's Q has been read
         };
-        if constexpr (C::NQT == 2) {
+        if constexpr (C::ALT) {
           // per query tile: P V still to issue, and the next list index
           const WinPart part[2] = {WinPart(w, 0), WinPart(w, 1)};
           int left[2] = {n0, n1};
@@ -1027,10 +1044,10 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
     const bool neg = prm.scale_log2 < 0.0f;
     const float mask_val = neg ? INFINITY : -INFINITY;
     const float cj = prm.scale_log2;
-    int sc = 0;        // two query tiles: S handshakes consumed (this tile)
-    int it = 0;        // one query tile: iterations so far
+    int sc = 0;        // S handshakes consumed
+    int it = 0;        // S double-buffered: iterations so far
     int oc = 0;        // o_full phases consumed
-    int pv_seen = 0;   // one query tile: P V completions consumed
+    int pv_seen = 0;   // S double-buffered: P V completions consumed
     int ring = 0;      // ring position of the unit's first tile
     bool ok = true;
 
@@ -1084,7 +1101,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
         const int tile_lo = w.p0 + t * tpt + (rows - 1) / g - prm.window + 1;  // of its last row
         float m_run = -INFINITY;  // reference maximum, log2 units
         float l_run = 0.0f;
-        // one query tile: consume o_ready completions up to the P V of
+        // S double-buffered: consume o_ready completions up to the P V of
         // iteration x (they complete in order)
         auto consume_o = [&](int x) -> bool {
           while (pv_seen <= x) {
@@ -1098,13 +1115,13 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
         int l = C::NQT == 2 ? mine.from(r0) : r0;  // list index
         int j = 0;                                 // tiles done by this query tile
         if (w.narrow && l == 0) {
-          const int buf = C::NQT == 2 ? t : (it & 1);
-          ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], (uint32_t)((C::NQT == 2 ? sc : it >> 1) & 1),
+          const int buf = C::ALT ? t : (it & 1);
+          ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], (uint32_t)((C::ALT ? sc : it >> 1) & 1),
                                                  abort_flag, prm.err));
           ++sc;
           if (!ok) break;
           tc_fence_after();
-          if (C::NQT == 1 && it >= 2 && !consume_o(it - 2)) {
+          if (!C::ALT && it >= 2 && !consume_o(it - 2)) {
             ok = false;
             break;
           }
@@ -1126,13 +1143,13 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
         }
         for (; j < n && ok; ++j, l = C::NQT == 2 ? mine.from(l + 1) : l + 1) {
           const int x = it + j;
-          const int buf = C::NQT == 2 ? t : (x & 1);
-          const uint32_t ph = C::NQT == 2 ? (uint32_t)(sc & 1) : (uint32_t)((x >> 1) & 1);
+          const int buf = C::ALT ? t : (x & 1);
+          const uint32_t ph = C::ALT ? (uint32_t)(sc & 1) : (uint32_t)((x >> 1) & 1);
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], ph, abort_flag, prm.err));
           ++sc;
           if (!ok) break;
           tc_fence_after();
-          if constexpr (C::NQT == 1) {
+          if constexpr (!C::ALT) {
             // P V(x-2) was issued before S(x): consume its o_ready phase to
             // keep at most one pending per buffer
             if (x >= 2 && !consume_o(x - 2)) {
@@ -1151,10 +1168,10 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
             // are the same), each before its own P V.
             const bool gap = w.lo > prm.sinks && col0 < w.lo && col0 + kBN > prm.sinks;
             if (col0 + kBN > w.nk || gap) {
-              // (one query tile: the slot's previous fill may still be the V tile
-              // before, so that one's P V is waited for first; with two, K of
+              // (S double-buffered: the slot's previous fill may still be the V tile
+              // before, so that one's P V is waited for first; else K of
               // this tile lies between)
-              if (C::NQT == 1 && j > 0 && !consume_o(x - 1)) {
+              if (!C::ALT && j > 0 && !consume_o(x - 1)) {
                 ok = false;
                 break;
               }
@@ -1213,7 +1230,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
           }
           l_run *= alpha;
           if (j > 0 && __any_sync(0xffffffffu, move)) {
-            if constexpr (C::NQT == 1) {
+            if constexpr (!C::ALT) {
               // O holds P V(x-1): wait for it
               if (!consume_o(x - 1)) {
                 ok = false;
@@ -1348,7 +1365,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED>::THREADS, 1)
         // the MMA warp issues after this tile's next P arrives
         tc_fence_before();
       } while (0);
-      if constexpr (C::NQT == 1) it += nrun;
+      if constexpr (!C::ALT) it += nrun;
       __syncwarp();  // every lane is done with the slot
       if (lane == 0) mbar_arrive(&bars->unit_empty[rr & 1]);
     }
@@ -1371,10 +1388,10 @@ struct WinLaunch {
   cudaStream_t stream;
 };
 
-template <int ELEM, int D, bool PAGED>
+template <int ELEM, int D, bool PAGED, bool PAIR = (D <= 128)>
 cudaError_t launch_attn_window(const WinLaunch& L) {
-  using C = WinCfg<ELEM, D, PAGED>;
-  auto kern = attn_window_kernel<ELEM, D, PAGED>;
+  using C = WinCfg<ELEM, D, PAGED, PAIR>;
+  auto kern = attn_window_kernel<ELEM, D, PAGED, PAIR>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

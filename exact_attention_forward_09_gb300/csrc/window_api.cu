@@ -24,6 +24,8 @@ FA_EXTERN_WINDOW(kFP16, false)
 FA_EXTERN_WINDOW(kBF16, true)
 FA_EXTERN_WINDOW(kFP16, true)
 #undef FA_EXTERN_WINDOW
+extern template cudaError_t launch_attn_window<kBF16, 64, true, false>(const WinLaunch&);
+extern template cudaError_t launch_attn_window<kFP16, 64, true, false>(const WinLaunch&);
 }  // namespace fa
 
 namespace {
@@ -60,18 +62,17 @@ CUtensorMapDataType map_type(int dtype) {
   return dtype == FA_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
 }
 
-// Query rows of one paged unit (both query tiles) for head dimension d.
-int slot_rows_of(int64_t d) { return d <= 128 ? 2 * fa::kBM : fa::kBM; }
-
+// Two partial results of all query rows that an SM works on (a pair of query
+// tiles, or two CTAs of one), their LSE, and a descriptor per CTA.
 struct PagedWorkspace {
   size_t lse_at, desc_at, bytes;
 };
-PagedWorkspace paged_workspace(int ctas, int64_t d) {
-  const size_t rows = (size_t)2 * ctas * slot_rows_of(d);
+PagedWorkspace paged_workspace(int sms, int64_t d) {
+  const size_t rows = (size_t)2 * sms * (d <= 128 ? 2 : 1) * fa::kBM;
   PagedWorkspace w;
   w.lse_at = rows * d * 4;
   w.desc_at = w.lse_at + rows * 4;
-  w.bytes = w.desc_at + (size_t)ctas * sizeof(int4);
+  w.bytes = w.desc_at + (size_t)2 * sms * sizeof(int4);
   return w;
 }
 
@@ -181,8 +182,8 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   int dev = 0;
   int* err = nullptr;
   if ((st = fa::internal_device_setup(&dev, &err)) != FA_OK) return st;
-  const int ctas = fa::internal_sm_count(dev);
-  const PagedWorkspace ws = paged_workspace(ctas, d);
+  const int sms = fa::internal_sm_count(dev);
+  const PagedWorkspace ws = paged_workspace(sms, d);
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || workspace_bytes < ws.bytes)
     return FA_ERR_INVALID_ARG;
 
@@ -191,6 +192,16 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   const int64_t g = Hq / Hkv;
   int64_t tpt = fa::kBM / g;  // tokens whose g heads fit a query tile
   if (max_q > 0 && max_q < tpt) tpt = max_q;
+  // Query tiles per CTA (see WinCfg): at d = 64 one where sequences bring few
+  // rows on average; or up to a tile's, if there are enough of them that few
+  // are cut or if the longest is far above the average, so that most are short.
+  // (One tile against a pair, 16/4 heads: 32 x 1 token over 3000 keys 32 and 37
+  // us; 33 sequences, 30 of them one token, 31 and 36; but 32 x 24 tokens over
+  // 1100 keys, cut into twice as many parts, 24 and 19.)
+  const bool pair = d == 128 || (d == 64 && (T * g > fa::kBM * B || (T * g > 32 * B && B * Hkv < 2 * sms &&
+                                                                     (max_q < T ? max_q : T) * B <= 4 * T)));
+  const int ctas = d == 64 && !pair ? 2 * sms : sms;
+  const int slot_rows = (pair ? 2 : 1) * fa::kBM;
   const CUtensorMapDataType dt = map_type(cache->dtype);
   {
     const uint64_t dims[3] = {(uint64_t)d, (uint64_t)Hq, (uint64_t)T};
@@ -235,7 +246,7 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   p.min_places = 1;
   // the line of work: at most this many units, each of at most this many
   // key tiles, two places to a tile
-  const int64_t unit_tok = (slot_rows_of(d) / fa::kBM) * tpt;
+  const int64_t unit_tok = (pair ? 2 : 1) * tpt;
   const int64_t keys = max_pages * cache->page_size < kMaxLen ? max_pages * cache->page_size : kMaxLen;
   int64_t tiles = keys / fa::kBN + 1;
   if (p.window + (int64_t)p.sinks + unit_tok < keys) tiles = (p.window + (int64_t)p.sinks + unit_tok) / fa::kBN + 4;
@@ -247,11 +258,16 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   p.desc = reinterpret_cast<int4*>(w + ws.desc_at);
   L.grid = ctas;
   L.stream = stream;
-  if ((st = launch_window<true>(L, d, cache->dtype)) != FA_OK) return st;
+  if (d == 64 && !pair) {
+    const cudaError_t e = cache->dtype == FA_DTYPE_BF16 ? fa::launch_attn_window<fa::kBF16, 64, true, false>(L)
+                                                        : fa::launch_attn_window<fa::kFP16, 64, true, false>(L);
+    if (e != cudaSuccess) return FA_ERR_CUDA;
+  } else if ((st = launch_window<true>(L, d, cache->dtype)) != FA_OK) {
+    return st;
+  }
   const int64_t most = (max_q > 0 && max_q < unit_tok ? max_q : unit_tok) * g;
-  return fa::launch_paged_combine(p.o_part, p.lse_part, p.desc, o, lse, ctas, ctas, (int)units, slot_rows_of(d),
-                                  (int)most, (int)g, (int)Hq, (int)d, cache->dtype == FA_DTYPE_FP16, stream) ==
-                 cudaSuccess
+  return fa::launch_paged_combine(p.o_part, p.lse_part, p.desc, o, lse, sms, ctas, (int)units, slot_rows, (int)most,
+                                  (int)g, (int)Hq, (int)d, cache->dtype == FA_DTYPE_FP16, stream) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
 }

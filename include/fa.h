@@ -527,7 +527,7 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
 /*
  * fa_paged_workspace_bytes -- bytes of device workspace fa_fwd_paged needs on
  * the current device for head dimension d, whatever the batch: two partial
- * results of one query tile pair per SM (about 40 MB at d = 128).
+ * results of 256 query rows (d = 256: 128) per SM, about 40 MB at d = 128.
  */
 fa_status fa_paged_workspace_bytes(int64_t d, size_t* bytes);
 
