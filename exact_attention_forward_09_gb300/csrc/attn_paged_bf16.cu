@@ -4,6 +4,7 @@
 namespace fa {
 template cudaError_t launch_attn_window<kBF16, 64, true>(const WinLaunch&);
 template cudaError_t launch_attn_window<kBF16, 64, true, false>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 128, true, false>(const WinLaunch&);
 template cudaError_t launch_attn_window<kBF16, 128, true>(const WinLaunch&);
 template cudaError_t launch_attn_window<kBF16, 256, true>(const WinLaunch&);
 }  // namespace fa

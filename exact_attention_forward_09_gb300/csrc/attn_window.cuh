@@ -46,16 +46,16 @@
 
 namespace fa {
 
-// PAIR: two query tiles per CTA, one CTA per SM (d <= 128).  Without it one
-// query tile per CTA: d = 256, whose S is double-buffered instead, and a paged
-// d = 64 form with two CTAs per SM, for batches whose sequences mostly bring
-// few rows.  With one query tile in use a key tile's chain (S, softmax, P V) is
-// all that runs, and at d = 64 its 32 KB take less time to arrive than the
-// chain: two independent CTAs read 64 sequences of 2000 to 16000 keys (one
-// token each, 32/8 heads) in 220 us, 5.6 TB/s, a pair in 310; at d = 128 one
-// chain keeps up with the memory.  On long chunks the pair is faster (500
-// against 566 us for 4 x 2048 tokens over 4000 to 10000 keys): it reads each
-// key tile once for two query tiles.
+// PAIR: two query tiles per CTA (d <= 128).  Without it one: d = 256, and the
+// paged forms for batches whose sequences mostly bring few rows.  There one
+// query tile is in use, and a key tile's chain (S, softmax, P V) is all that
+// runs in a pair's CTA.  So d = 128 takes the room of the second query tile for
+// a second S buffer, as d = 256 does (one token each, 32/8 heads: 256 sequences
+// under a window of 1024 278 -> 227 us, one of 131000 keys 36.0 -> 32.9), and
+// d = 64 runs two CTAs per SM: two chains (64 sequences of 2000 to 16000 keys
+// 310 -> 220 us, 5.6 TB/s).  On long chunks the pair is faster (500 against 566
+// us for 4 x 2048 tokens over 4000 to 10000 keys, d = 64): it reads each key
+// tile once for two query tiles.
 template <int ELEM, int D, bool PAGED, bool PAIR = (D <= 128)>
 struct WinCfg {
   static_assert(ELEM == kBF16 || ELEM == kFP16, "16-bit operands");
@@ -64,9 +64,9 @@ struct WinCfg {
   static constexpr int NCH = D / CH_ELEMS;
   static constexpr int CHUNK_BYTES = 128 * 128;            // 128 rows x 128 bytes
   static constexpr int NQT = PAIR ? 2 : 1;                 // query tiles per CTA
-  static constexpr bool ALT = D <= 128;                    // one S buffer per query tile; ring K0 V0 K1 V1 ...
+  static constexpr bool ALT = PAIR || D == 64;             // one S buffer per query tile; ring K0 V0 K1 V1 ...
   static constexpr int OCC = ALT && !PAIR ? 2 : 1;         // CTAs per SM
-  static_assert(!PAIR || ALT, "two query tiles of d = 256 exceed tensor memory");
+  static_assert(!PAIR || D <= 128, "two query tiles of d = 256 exceed tensor memory");
   static_assert(OCC == 1 || PAGED, "dense calls use pairs");
   // shared memory of a CTA: what two per SM leave beside their reserves
   static constexpr int SMEM_LIMIT = OCC == 2 ? 115712 : kSmemLimit;

@@ -24,8 +24,12 @@ FA_EXTERN_WINDOW(kFP16, false)
 FA_EXTERN_WINDOW(kBF16, true)
 FA_EXTERN_WINDOW(kFP16, true)
 #undef FA_EXTERN_WINDOW
-extern template cudaError_t launch_attn_window<kBF16, 64, true, false>(const WinLaunch&);
-extern template cudaError_t launch_attn_window<kFP16, 64, true, false>(const WinLaunch&);
+#define FA_EXTERN_ONE_TILE(E)                                                     \
+  extern template cudaError_t launch_attn_window<E, 64, true, false>(const WinLaunch&); \
+  extern template cudaError_t launch_attn_window<E, 128, true, false>(const WinLaunch&);
+FA_EXTERN_ONE_TILE(kBF16)
+FA_EXTERN_ONE_TILE(kFP16)
+#undef FA_EXTERN_ONE_TILE
 }  // namespace fa
 
 namespace {
@@ -43,17 +47,18 @@ float log2_scale(float scale) {
   return s == 0.0f ? 1e-30f : s;
 }
 
-template <bool PAGED>
+// PAIR: two query tiles per CTA at d = 64 and 128
+template <bool PAGED, bool PAIR>
 fa_status launch_window(const fa::WinLaunch& L, int64_t d, int dtype) {
   cudaError_t e = cudaErrorInvalidValue;
   if (dtype == FA_DTYPE_BF16) {
-    if (d == 64) e = fa::launch_attn_window<fa::kBF16, 64, PAGED>(L);
-    else if (d == 128) e = fa::launch_attn_window<fa::kBF16, 128, PAGED>(L);
-    else if (d == 256) e = fa::launch_attn_window<fa::kBF16, 256, PAGED>(L);
+    if (d == 64) e = fa::launch_attn_window<fa::kBF16, 64, PAGED, PAIR>(L);
+    else if (d == 128) e = fa::launch_attn_window<fa::kBF16, 128, PAGED, PAIR>(L);
+    else if (d == 256) e = fa::launch_attn_window<fa::kBF16, 256, PAGED, false>(L);
   } else {
-    if (d == 64) e = fa::launch_attn_window<fa::kFP16, 64, PAGED>(L);
-    else if (d == 128) e = fa::launch_attn_window<fa::kFP16, 128, PAGED>(L);
-    else if (d == 256) e = fa::launch_attn_window<fa::kFP16, 256, PAGED>(L);
+    if (d == 64) e = fa::launch_attn_window<fa::kFP16, 64, PAGED, PAIR>(L);
+    else if (d == 128) e = fa::launch_attn_window<fa::kFP16, 128, PAGED, PAIR>(L);
+    else if (d == 256) e = fa::launch_attn_window<fa::kFP16, 256, PAGED, false>(L);
   }
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
@@ -150,7 +155,7 @@ fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, fl
   L.prm.Nk = (int)Nk;
   L.prm.BH = (int)(B * Hq);
   L.stream = stream;
-  return launch_window<false>(L, d, dtype);
+  return launch_window<false, true>(L, d, dtype);
 }
 
 fa_status fa_paged_workspace_bytes(int64_t d, size_t* bytes) {
@@ -192,14 +197,14 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   const int64_t g = Hq / Hkv;
   int64_t tpt = fa::kBM / g;  // tokens whose g heads fit a query tile
   if (max_q > 0 && max_q < tpt) tpt = max_q;
-  // Query tiles per CTA (see WinCfg): at d = 64 one where sequences bring few
-  // rows on average; or up to a tile's, if there are enough of them that few
-  // are cut or if the longest is far above the average, so that most are short.
-  // (One tile against a pair, 16/4 heads: 32 x 1 token over 3000 keys 32 and 37
-  // us; 33 sequences, 30 of them one token, 31 and 36; but 32 x 24 tokens over
-  // 1100 keys, cut into twice as many parts, 24 and 19.)
-  const bool pair = d == 128 || (d == 64 && (T * g > fa::kBM * B || (T * g > 32 * B && B * Hkv < 2 * sms &&
-                                                                     (max_q < T ? max_q : T) * B <= 4 * T)));
+  // Query tiles per CTA (see WinCfg): one where sequences bring few rows on
+  // average; or up to a tile's, if there are enough of them that few are cut or
+  // if the longest is far above the average, so that most are short.
+  // (One tile against a pair at d = 64, 16/4 heads: 32 x 1 token over 3000 keys
+  // 32 and 37 us; 33 sequences, 30 of them one token, 31 and 36; but 32 x 24
+  // tokens over 1100 keys, cut into twice as many parts, 24 and 19.)
+  const bool pair = d <= 128 && (T * g > fa::kBM * B || (T * g > 32 * B && B * Hkv < 2 * sms &&
+                                                         (max_q < T ? max_q : T) * B <= 4 * T));
   const int ctas = d == 64 && !pair ? 2 * sms : sms;
   const int slot_rows = (pair ? 2 : 1) * fa::kBM;
   const CUtensorMapDataType dt = map_type(cache->dtype);
@@ -258,13 +263,8 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   p.desc = reinterpret_cast<int4*>(w + ws.desc_at);
   L.grid = ctas;
   L.stream = stream;
-  if (d == 64 && !pair) {
-    const cudaError_t e = cache->dtype == FA_DTYPE_BF16 ? fa::launch_attn_window<fa::kBF16, 64, true, false>(L)
-                                                        : fa::launch_attn_window<fa::kFP16, 64, true, false>(L);
-    if (e != cudaSuccess) return FA_ERR_CUDA;
-  } else if ((st = launch_window<true>(L, d, cache->dtype)) != FA_OK) {
-    return st;
-  }
+  st = pair ? launch_window<true, true>(L, d, cache->dtype) : launch_window<true, false>(L, d, cache->dtype);
+  if (st != FA_OK) return st;
   const int64_t most = (max_q > 0 && max_q < unit_tok ? max_q : unit_tok) * g;
   return fa::launch_paged_combine(p.o_part, p.lse_part, p.desc, o, lse, sms, ctas, (int)units, slot_rows, (int)most,
                                   (int)g, (int)Hq, (int)d, cache->dtype == FA_DTYPE_FP16, stream) == cudaSuccess
