@@ -328,7 +328,8 @@ __device__ __noinline__ float2 narrow_softmax(uint32_t s_addr, uint32_t see, flo
 
 // Waits for the V tile at ring position pv and, where `dead`, zeroes this
 // thread's row of it (row: its shared-memory address in slot 0); made visible
-// to the tensor core.  Out of line: it runs once or twice per unit.
+// to the tensor core.  Neighbouring threads start at different 16-byte pieces,
+// as equal ones share their banks.  Out of line: it runs once or twice per unit.
 template <typename C, typename Bars>
 __device__ __noinline__ bool clear_v_row(Bars* bars, uint32_t row, int pv, bool dead, int* err) {
   for (int sp = 0; sp < C::SPT; ++sp)
@@ -340,7 +341,7 @@ __device__ __noinline__ bool clear_v_row(Bars* bars, uint32_t row, int pv, bool 
     for (int ch = 0; ch < C::NCH; ++ch) {
       const uint32_t at = row + ((pv + ch / C::SLOT_CH) % C::NS) * C::SLOT_BYTES + (ch % C::SLOT_CH) * C::CHUNK_BYTES;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) st_shared_v4(at + 16 * i, 0u, 0u, 0u, 0u);
+      for (int i = 0; i < 8; ++i) st_shared_v4(at + 16 * ((i + threadIdx.x) & 7), 0u, 0u, 0u, 0u);
     }
   }
   fence_proxy_async_smem();
@@ -1098,7 +1099,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, PAIR>::THREADS, WinCfg<
         // the sequence); the tile's strictest last and first (window) ones
         const int last = w.p0 + tok;
         const int tile_last = w.p0 + t * tpt;                              // of its first row
-        const int tile_lo = w.p0 + t * tpt + (rows - 1) / g - prm.window + 1;  // of its last row
+        const int tile_lo = w.p0 + min(w.ntok, (t + 1) * tpt) - prm.window;    // of its last row
         float m_run = -INFINITY;  // reference maximum, log2 units
         float l_run = 0.0f;
         // S double-buffered: consume o_ready completions up to the P V of
