@@ -1042,6 +1042,8 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, PAIR>::THREADS, WinCfg<
     const int wq = warp % 4;                 // TMEM lane quarter
     const int r_in = wq * 32 + lane;         // row within the tile, and key row of a V tile
     const uint32_t lane_addr = (uint32_t)(wq * 32) << 16;
+    const int tok_in = PAGED ? r_in / g : r_in;  // token within the tile
+    const int head_in = r_in - tok_in * g;
     const bool neg = prm.scale_log2 < 0.0f;
     const float mask_val = neg ? INFINITY : -INFINITY;
     const float cj = prm.scale_log2;
@@ -1066,11 +1068,11 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, PAIR>::THREADS, WinCfg<
       ring += 2 * nrun * C::SPT;
       const int rows = min(rpt, (w.ntok - t * tpt) * g);  // valid rows of this tile
       const bool valid = r_in < rows;
-      const int tok = t * tpt + (PAGED ? r_in / g : r_in);   // token within the unit
+      const int tok = t * tpt + tok_in;                      // token within the unit
       // where this row's results go
       auto out_row_of = [&]() -> size_t {
         if (w.part >= 0) return (size_t)w.part * (C::NQT * kBM) + t * rpt + r_in;
-        if (PAGED) return (size_t)(w.qz + tok) * prm.Hq + w.kz * g + r_in % g;
+        if (PAGED) return (size_t)(w.qz + tok) * prm.Hq + w.kz * g + head_in;
         return (size_t)w.qz * prm.N + w.q_row + tok;
       };
       do {  // one unit (skipped when this tile has no valid row)
