@@ -3,8 +3,11 @@
 
 namespace fa {
 template cudaError_t launch_attn_window<kBF16, 64, true>(const WinLaunch&);
-template cudaError_t launch_attn_window<kBF16, 64, true, false>(const WinLaunch&);
-template cudaError_t launch_attn_window<kBF16, 128, true, false>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 64, true, WIN_ONE>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 128, true, WIN_ONE>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 256, true, WIN_FEW>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 128, true, WIN_FEW>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 64, true, WIN_FEW>(const WinLaunch&);
 template cudaError_t launch_attn_window<kBF16, 128, true>(const WinLaunch&);
 template cudaError_t launch_attn_window<kBF16, 256, true>(const WinLaunch&);
 }  // namespace fa

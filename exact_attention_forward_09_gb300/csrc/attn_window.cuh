@@ -46,18 +46,35 @@
 
 namespace fa {
 
-// PAIR: two query tiles per CTA (d <= 128).  Without it one: d = 256, and the
-// paged forms for batches whose sequences mostly bring few rows.  There one
-// query tile is in use, and a key tile's chain (S, softmax, P V) is all that
-// runs in a pair's CTA.  So d = 128 takes the room of the second query tile for
-// a second S buffer, as d = 256 does (one token each, 32/8 heads: 256 sequences
-// under a window of 1024 278 -> 227 us, one of 131000 keys 36.0 -> 32.9), and
-// d = 64 runs two CTAs per SM: two chains (64 sequences of 2000 to 16000 keys
-// 310 -> 220 us, 5.6 TB/s).  On long chunks the pair is faster (500 against 566
-// us for 4 x 2048 tokens over 4000 to 10000 keys, d = 64): it reads each key
-// tile once for two query tiles.
-template <int ELEM, int D, bool PAGED, bool PAIR = (D <= 128)>
+// The kernel's forms.
+// WIN_PAIR (d <= 128): two query tiles per CTA.  On long chunks and dense calls
+// the fastest: it reads each key tile once for two query tiles (500 against 566
+// us for 4 x 2048 tokens over 4000 to 10000 keys, d = 64).
+// WIN_ONE: one query tile per CTA; all of d = 256, and paged batches whose
+// sequences mostly bring few rows.  There one query tile of a pair would be in
+// use, and a key tile's chain (S, softmax, P V) be all that runs in its CTA.
+// So d = 128 takes the room of the second query tile for a second S buffer, as
+// d = 256 does (one token each, 32/8 heads: 256 sequences under a window of
+// 1024 278 -> 227 us, one of 131000 keys 36.0 -> 32.9), and d = 64 runs two
+// CTAs per SM: two chains (64 sequences of 2000 to 16000 keys 310 -> 220 us).
+// WIN_FEW: as WIN_ONE, for units of at most kFewRows rows (a token's g heads,
+// or a few tokens').  One softmax warp would do the work of a whole key tile
+// for a few rows while three work on rows that do not exist.  So the rows lie
+// four times in the query tile, at rows 0, 32, 64 and 96, and with that in the
+// TMEM lanes of each warp; warp w exponentiates columns 32 w .. 32 w + 31 alone,
+// for its copy, and hands over zeros for the others.  The four copies are
+// attention over disjoint keys, joined by their maxima and sums when the unit
+// ends.  (One token each, 32/8 heads, against WIN_ONE: 256 sequences
+// under a window of 1024 at d = 64, 128, 256: 149 -> 107, 224 -> 186, 430 -> 367
+// us; of 50 to 600 keys 78 -> 62, 125 -> 115, 190 -> 168; 64 of 2000 to 16000
+// at d = 64 224 -> 195, 6.5 TB/s.)  An infinite value in a row of V that is
+// seen can give NaN, as the copies that do not take its key weigh it with 0.
+enum WinForm { WIN_FEW, WIN_ONE, WIN_PAIR };
+constexpr int kFewRows = 16;
+
+template <int ELEM, int D, bool PAGED, int FORM = (D <= 128 ? WIN_PAIR : WIN_ONE)>
 struct WinCfg {
+  static constexpr bool PAIR = FORM == WIN_PAIR, FEW = FORM == WIN_FEW;
   static_assert(ELEM == kBF16 || ELEM == kFP16, "16-bit operands");
   static constexpr int ROW_BYTES = D * 2;
   static constexpr int CH_ELEMS = 64;                      // elements per 128-byte chunk
@@ -67,7 +84,8 @@ struct WinCfg {
   static constexpr bool ALT = PAIR || D == 64;             // one S buffer per query tile; ring K0 V0 K1 V1 ...
   static constexpr int OCC = ALT && !PAIR ? 2 : 1;         // CTAs per SM
   static_assert(!PAIR || D <= 128, "two query tiles of d = 256 exceed tensor memory");
-  static_assert(OCC == 1 || PAGED, "dense calls use pairs");
+  static_assert((OCC == 1 && !FEW) || PAGED, "dense calls use pairs");
+  static constexpr int ML_BYTES = FEW ? 4 * kFewRows * 8 : 0;
   // shared memory of a CTA: what two per SM leave beside their reserves
   static constexpr int SMEM_LIMIT = OCC == 2 ? 115712 : kSmemLimit;
   static constexpr int TILE_BYTES = kBN * ROW_BYTES;
@@ -82,7 +100,7 @@ struct WinCfg {
   static constexpr bool EPI_TMA = !PAGED && D <= 128;
   static constexpr int EPI_WARP_BYTES = 32 * 64 * 2;
   static constexpr int EPI_BYTES = EPI_TMA ? 4 * NQT * EPI_WARP_BYTES : 0;
-  static constexpr int NS_MAX = (SMEM_LIMIT - 2048 - EPI_BYTES - Q_BYTES) / SLOT_BYTES;
+  static constexpr int NS_MAX = (SMEM_LIMIT - 2048 - ML_BYTES - EPI_BYTES - Q_BYTES) / SLOT_BYTES;
   static constexpr int NS = NS_MAX > 8 ? 8 : NS_MAX;
   static_assert(NS >= 2 * SPT, "ring too shallow");
   static constexpr int P_COLS = kBN / 2;
@@ -120,7 +138,8 @@ struct WinCfg {
   static constexpr int OFF_EPI = OFF_RING + NS * SLOT_BYTES;
   static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
   static_assert(OFF_EPI % 1024 == 0 && OFF_BAR % 1024 == 0, "1024-byte swizzle atoms");
-  static constexpr int SMEM_BYTES = OFF_BAR + 1024 + 1024;  // + barriers + alignment slack
+  static constexpr int OFF_ML = OFF_BAR + 1024;                // WIN_FEW: maxima and sums, [row][warp]
+  static constexpr int SMEM_BYTES = OFF_ML + ML_BYTES + 1024;  // + alignment slack
   static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
 };
 
@@ -348,12 +367,12 @@ __device__ __noinline__ bool clear_v_row(Bars* bars, uint32_t row, int pv, bool 
   return true;
 }
 
-template <int ELEM, int D, bool PAGED, bool PAIR>
-__global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, PAIR>::THREADS, WinCfg<ELEM, D, PAGED, PAIR>::OCC)
+template <int ELEM, int D, bool PAGED, int FORM>
+__global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<ELEM, D, PAGED, FORM>::OCC)
     attn_window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                        const WinParams prm) {
-  using C = WinCfg<ELEM, D, PAGED, PAIR>;
+  using C = WinCfg<ELEM, D, PAGED, FORM>;
   using Bars = WinBars<C::NS>;
   static_assert(sizeof(Bars) <= 1024, "barrier area");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -419,7 +438,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, PAIR>::THREADS, WinCfg<
   if constexpr (PAGED) {
     pdl_launch();  // the join can be launched; it waits for this kernel's end
     // rows of a query tile that no TMA box covers (128 % g != 0) are zeros
-    if (rpt < kBM) {
+    if (!C::FEW && rpt < kBM) {
       for (int i = threadIdx.x; i < C::NQT * C::NCH * (kBM - rpt) * 8; i += C::THREADS) {
         const int c = i / ((kBM - rpt) * 8), x = i % ((kBM - rpt) * 8);
         *reinterpret_cast<uint4*>(smem + C::OFF_Q + c * C::CHUNK_BYTES + rpt * 128 + x * 16) = make_uint4(0u, 0u, 0u, 0u);
@@ -622,7 +641,15 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, PAIR>::THREADS, WinCfg<
         // the Q buffer is free once the previous unit's last Q K^T finished
         if (k > 0) ok = __all_sync(0xffffffffu, mbar_wait(&bars->q_empty, (uint32_t)((k - 1) & 1), abort_flag, prm.err));
         if (!ok) return;
-        if (lane == 0) {
+        if (C::FEW) {
+          // the rows' four copies: lane = copy and column chunk
+          if (lane == 0) mbar_arrive_expect_tx(&bars->q_full, (uint32_t)(4 * rpt * C::ROW_BYTES));
+          __syncwarp();
+          const int c = lane / C::NCH, ch = lane % C::NCH;
+          if (c < 4)
+            tma_load_3d_hint(smem + C::OFF_Q + ch * C::CHUNK_BYTES + c * 32 * 128, &tm_q, &bars->q_full,
+                             ch * C::CH_ELEMS, w.kz * g, w.qz, pol_q);
+        } else if (lane == 0) {
           const uint32_t tile = (uint32_t)(rpt * C::ROW_BYTES);
           mbar_arrive_expect_tx(&bars->q_full, (n0 > 0 ? tile : 0u) + (n1 > 0 ? tile : 0u));
           for (int t = 0; t < C::NQT; ++t) {
@@ -1044,6 +1071,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, PAIR>::THREADS, WinCfg<
     const uint32_t lane_addr = (uint32_t)(wq * 32) << 16;
     const int tok_in = PAGED ? r_in / g : r_in;  // token within the tile
     const int head_in = r_in - tok_in * g;
+    const int row_tok = C::FEW ? lane / g : tok_in;  // WIN_FEW: rows are lanes
     const bool neg = prm.scale_log2 < 0.0f;
     const float mask_val = neg ? INFINITY : -INFINITY;
     const float cj = prm.scale_log2;
@@ -1053,6 +1081,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, PAIR>::THREADS, WinCfg<
     int pv_seen = 0;   // S double-buffered: P V completions consumed
     int ring = 0;      // ring position of the unit's first tile
     bool ok = true;
+    bool left = false;  // WIN_FEW: the warps found together that one of them gave up
 
     for (int rr = 0; ok; ++rr) {
       // The unit is read where it stands in the queue, and its slot released
@@ -1115,6 +1144,202 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, PAIR>::THREADS, WinCfg<
           }
           return true;
         };
+        if constexpr (C::FEW) {
+          // lane = row, this warp's columns 32 wq .. 32 wq + 31
+          const int nr = w.ntok * g;
+          const int lo = w.p0 + w.ntok - prm.window;  // first key of the last row's window
+          for (int j = 0; j < n && ok; ++j) {
+            const int x = it + j, l = r0 + j;
+            const int buf = C::ALT ? 0 : (x & 1);
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], (uint32_t)((C::ALT ? sc : x >> 1) & 1),
+                                                   abort_flag, prm.err));
+            ++sc;
+            if (!ok) break;
+            tc_fence_after();
+            if (!C::ALT && x >= 2 && !consume_o(x - 2)) {
+              ok = false;
+              break;
+            }
+            const uint32_t s_addr = tmem + lane_addr + buf * kBN;
+            const int col0 = (l < w.ns ? l : l + w.skip) * kBN;
+            const bool narrow = w.narrow && l == 0;
+            // rows of the V tile that no query of the unit sees become zeros, as below
+            const bool gap = w.lo > prm.sinks && col0 < w.lo && col0 + kBN > prm.sinks;
+            if (col0 + kBN > w.nk || gap) {
+              if (!C::ALT && j > 0 && !consume_o(x - 1)) {
+                ok = false;
+                break;
+              }
+              const int key = col0 + r_in;
+              const bool dead = key >= w.nk || (key < w.lo && key >= prm.sinks);
+              ok = clear_v_row<C, Bars>(bars, smem_u32(smem + C::OFF_RING) + r_in * 128, ring0 + v_at(j, n), dead, prm.err);
+              if (!ok) break;
+            }
+            uint32_t pk[16], zero[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) pk[i] = zero[i] = 0u;
+            if (!narrow || wq == 0) {
+              uint32_t u[32];
+              tmem_ld32(s_addr + 32 * wq, u);
+              tmem_wait_ld();
+              const int c0 = col0 + 32 * wq;
+              if (c0 + 31 > w.p0 || (c0 < lo && c0 + 32 > prm.sinks)) {
+                const uint32_t see = win_visible(w.p0 + row_tok, prm.window, prm.sinks, c0);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) u[i] = (see & (1u << i)) ? u[i] : __float_as_uint(mask_val);
+              }
+              float r4[4];
+              if (!neg) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r4[i] = fmaxf(__uint_as_float(u[i]), __uint_as_float(u[4 + i]));
+#pragma unroll
+                for (int c = 8; c < 32; c += 8)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) r4[i] = max3f(r4[i], __uint_as_float(u[c + i]), __uint_as_float(u[c + 4 + i]));
+                r4[0] = fmaxf(max3f(r4[0], r4[1], r4[2]), r4[3]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r4[i] = fminf(__uint_as_float(u[i]), __uint_as_float(u[4 + i]));
+#pragma unroll
+                for (int c = 8; c < 32; c += 8)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) r4[i] = min3f(r4[i], __uint_as_float(u[c + i]), __uint_as_float(u[c + 4 + i]));
+                r4[0] = fminf(min3f(r4[0], r4[1], r4[2]), r4[3]);
+              }
+              // (lanes without a row never move their maximum)
+              const float mx2 = lane < nr ? r4[0] * cj : -INFINITY;
+              float alpha = 1.0f;
+              const bool move = (mx2 > m_run + C::TAU) || (m_run == -INFINITY && mx2 != -INFINITY);
+              if (move) {
+                alpha = ex2(m_run - mx2);  // 0 on the row's first visible columns
+                m_run = mx2;
+              }
+              l_run *= alpha;
+              if (j > 0 && __any_sync(0xffffffffu, move)) {
+                if constexpr (!C::ALT) {
+                  // O holds P V(x-1): wait for it
+                  if (!consume_o(x - 1)) {
+                    ok = false;
+                    break;
+                  }
+                  tc_fence_after();
+                }
+                rescale_o_cols<D>(tmem + lane_addr + C::O_COL0, alpha);
+              }
+              const float nm = m_run == -INFINITY ? 0.0f : -m_run;
+              float2 acc[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float2 e = fma2(make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1])),
+                                      make_float2(cj, cj), make_float2(nm, nm));
+                const float2 q = make_float2(ex2(e.x), ex2(e.y));
+                acc[i & 1] = add2(acc[i & 1], q);
+                pk[i] = (ELEM == kBF16) ? pack_bf16x2(q.x, q.y) : pack_f16x2(q.x, q.y);
+              }
+              const float2 tt = add2(acc[0], acc[1]);
+              l_run += tt.x + tt.y;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (narrow && q > 0) break;  // (its first 32 keys alone are multiplied)
+              if (q == wq) tmem_st16(s_addr + 16 * q, pk);
+              else tmem_st16(s_addr + 16 * q, zero);
+            }
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(&bars->p_full[buf][0]);
+            mbar_arrive(&bars->p_full[buf][1]);
+          }
+          // The copies' join.  O goes through query rows that no copy uses, 16
+          // of each warp's 32: a line of 32 columns per row and column chunk, its
+          // 16-byte pieces permuted by the row; all columns at once for up to 8
+          // rows, which take two lines each, by halves for more.
+          if (ok) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[0], (uint32_t)(oc & 1), abort_flag, prm.err));
+            ++oc;
+          }
+          float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
+          uint8_t* stage = smem + C::OFF_Q + kFewRows * 128;
+          const bool once = nr <= kFewRows / 2;
+          auto put = [&](int h) {
+#pragma unroll
+            for (int ch = 0; ch < C::NCH; ++ch) {
+              uint32_t u[32];
+              tmem_ld32(tmem + lane_addr + C::O_COL0 + h * (D / 2) + ch * 32, u);
+              tmem_wait_ld();
+              if (lane < nr) {
+                const int at = once ? lane + h * (kFewRows / 2) : lane;
+                uint4* line = reinterpret_cast<uint4*>(stage + ch * C::CHUNK_BYTES + (wq * 32 + at) * 128);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                  line[i ^ (at & 7)] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+              }
+            }
+          };
+          if (ok) {
+            tc_fence_after();
+            if (lane < nr) ml[lane * 4 + wq] = make_float2(m_run, l_run);
+            put(0);
+            if (once) put(1);
+            // this warp's reads of O (with more rows: of half of it; the others
+            // come before the last barrier) are ordered before the next unit's S
+            tc_fence_before();
+          }
+          // (a warp that gave up meets the others here or at its end, so no one waits for it)
+          ok = bar_and(1, 128, ok);
+          if (!ok) {
+            left = true;
+            break;
+          }
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1 && !once) {
+              bar_sync_n(1, 128);
+              put(1);
+              tc_fence_before();
+              bar_sync_n(1, 128);
+            }
+            for (int i = threadIdx.x; i < nr * (D / 8); i += 128) {
+              const int row = i / (D / 8), c = i % (D / 8);  // 4 columns, from h * D / 2 + 4 c on
+              float2 v[4];
+              float m_all = -INFINITY, l_all = 0.0f;
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                v[q] = ml[row * 4 + q];
+                m_all = fmaxf(m_all, v[q].x);
+              }
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                v[q].x = v[q].x == -INFINITY ? 0.0f : ex2(v[q].x - m_all);
+                l_all = fmaf(v[q].x, v[q].y, l_all);
+              }
+              const float f = l_all > 0.0f ? 1.0f / l_all : 0.0f;
+              const int at = once ? row + h * (kFewRows / 2) : row;
+              float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const float4 b = reinterpret_cast<const float4*>(stage + (c / 8) * C::CHUNK_BYTES +
+                                                                 (q * 32 + at) * 128)[(c % 8) ^ (at & 7)];
+                a.x = fmaf(v[q].x, b.x, a.x);
+                a.y = fmaf(v[q].x, b.y, a.y);
+                a.z = fmaf(v[q].x, b.z, a.z);
+                a.w = fmaf(v[q].x, b.w, a.w);
+              }
+              const size_t o_row = w.part >= 0 ? (size_t)w.part * kBM + row
+                                               : (size_t)(w.qz + row / g) * prm.Hq + w.kz * g + row % g;
+              const size_t o_at = o_row * D + h * (D / 2) + 4 * c;
+              if (w.part >= 0) {
+                *reinterpret_cast<float4*>(prm.o_part + o_at) = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+              } else {
+                const uint2 pk = ELEM == kFP16 ? make_uint2(pack_f16x2(a.x * f, a.y * f), pack_f16x2(a.z * f, a.w * f))
+                                               : make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+                *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(prm.o) + o_at) = pk;
+              }
+              if (h == 0 && c == 0)
+                (w.part >= 0 ? prm.lse_part : prm.lse)[o_row] = (m_all + lg2(l_all)) * 0.69314718055994530942f;
+            }
+          }
+          break;
+        }
         int l = C::NQT == 2 ? mine.from(r0) : r0;  // list index
         int j = 0;                                 // tiles done by this query tile
         if (w.narrow && l == 0) {
@@ -1372,6 +1597,8 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, PAIR>::THREADS, WinCfg<
       __syncwarp();  // every lane is done with the slot
       if (lane == 0) mbar_arrive(&bars->unit_empty[rr & 1]);
     }
+    // a warp that others may wait for at their unit's join meets them there
+    if (C::FEW && !left) bar_and(1, 128, false);
   }
   // the epilogue's bulk stores have completed before the CTA ends
   if (C::EPI_TMA && warp < C::SOFTMAX_WARPS && lane == 0) bulk_wait_all();
@@ -1391,10 +1618,10 @@ struct WinLaunch {
   cudaStream_t stream;
 };
 
-template <int ELEM, int D, bool PAGED, bool PAIR = (D <= 128)>
+template <int ELEM, int D, bool PAGED, int FORM = (D <= 128 ? WIN_PAIR : WIN_ONE)>
 cudaError_t launch_attn_window(const WinLaunch& L) {
-  using C = WinCfg<ELEM, D, PAGED, PAIR>;
-  auto kern = attn_window_kernel<ELEM, D, PAGED, PAIR>;
+  using C = WinCfg<ELEM, D, PAGED, FORM>;
+  auto kern = attn_window_kernel<ELEM, D, PAGED, FORM>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

@@ -24,9 +24,12 @@ FA_EXTERN_WINDOW(kFP16, false)
 FA_EXTERN_WINDOW(kBF16, true)
 FA_EXTERN_WINDOW(kFP16, true)
 #undef FA_EXTERN_WINDOW
-#define FA_EXTERN_ONE_TILE(E)                                                     \
-  extern template cudaError_t launch_attn_window<E, 64, true, false>(const WinLaunch&); \
-  extern template cudaError_t launch_attn_window<E, 128, true, false>(const WinLaunch&);
+#define FA_EXTERN_ONE_TILE(E)                                                        \
+  extern template cudaError_t launch_attn_window<E, 64, true, WIN_ONE>(const WinLaunch&);  \
+  extern template cudaError_t launch_attn_window<E, 128, true, WIN_ONE>(const WinLaunch&); \
+  extern template cudaError_t launch_attn_window<E, 64, true, WIN_FEW>(const WinLaunch&);  \
+  extern template cudaError_t launch_attn_window<E, 128, true, WIN_FEW>(const WinLaunch&); \
+  extern template cudaError_t launch_attn_window<E, 256, true, WIN_FEW>(const WinLaunch&);
 FA_EXTERN_ONE_TILE(kBF16)
 FA_EXTERN_ONE_TILE(kFP16)
 #undef FA_EXTERN_ONE_TILE
@@ -47,18 +50,19 @@ float log2_scale(float scale) {
   return s == 0.0f ? 1e-30f : s;
 }
 
-// PAIR: two query tiles per CTA at d = 64 and 128
-template <bool PAGED, bool PAIR>
+// FORM at d = 64 and 128 (d = 256 has no pairs)
+template <bool PAGED, int FORM>
 fa_status launch_window(const fa::WinLaunch& L, int64_t d, int dtype) {
+  constexpr int FORM256 = FORM == fa::WIN_PAIR ? fa::WIN_ONE : FORM;
   cudaError_t e = cudaErrorInvalidValue;
   if (dtype == FA_DTYPE_BF16) {
-    if (d == 64) e = fa::launch_attn_window<fa::kBF16, 64, PAGED, PAIR>(L);
-    else if (d == 128) e = fa::launch_attn_window<fa::kBF16, 128, PAGED, PAIR>(L);
-    else if (d == 256) e = fa::launch_attn_window<fa::kBF16, 256, PAGED, false>(L);
+    if (d == 64) e = fa::launch_attn_window<fa::kBF16, 64, PAGED, FORM>(L);
+    else if (d == 128) e = fa::launch_attn_window<fa::kBF16, 128, PAGED, FORM>(L);
+    else if (d == 256) e = fa::launch_attn_window<fa::kBF16, 256, PAGED, FORM256>(L);
   } else {
-    if (d == 64) e = fa::launch_attn_window<fa::kFP16, 64, PAGED, PAIR>(L);
-    else if (d == 128) e = fa::launch_attn_window<fa::kFP16, 128, PAGED, PAIR>(L);
-    else if (d == 256) e = fa::launch_attn_window<fa::kFP16, 256, PAGED, false>(L);
+    if (d == 64) e = fa::launch_attn_window<fa::kFP16, 64, PAGED, FORM>(L);
+    else if (d == 128) e = fa::launch_attn_window<fa::kFP16, 128, PAGED, FORM>(L);
+    else if (d == 256) e = fa::launch_attn_window<fa::kFP16, 256, PAGED, FORM256>(L);
   }
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
@@ -155,7 +159,7 @@ fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, fl
   L.prm.Nk = (int)Nk;
   L.prm.BH = (int)(B * Hq);
   L.stream = stream;
-  return launch_window<false, true>(L, d, dtype);
+  return launch_window<false, fa::WIN_PAIR>(L, d, dtype);
 }
 
 fa_status fa_paged_workspace_bytes(int64_t d, size_t* bytes) {
@@ -197,13 +201,17 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   const int64_t g = Hq / Hkv;
   int64_t tpt = fa::kBM / g;  // tokens whose g heads fit a query tile
   if (max_q > 0 && max_q < tpt) tpt = max_q;
+  // The form (see WinForm).  Few rows: as many tokens per unit as a few rows
+  // hold, if no sequence brings more, or on average each brings one.
+  const bool few = g <= fa::kFewRows && (max_q > 0 ? max_q <= fa::kFewRows / g : T <= B);
+  if (few && tpt > fa::kFewRows / g) tpt = fa::kFewRows / g;
   // Query tiles per CTA (see WinCfg): one where sequences bring few rows on
   // average; or up to a tile's, if there are enough of them that few are cut or
   // if the longest is far above the average, so that most are short.
   // (One tile against a pair at d = 64, 16/4 heads: 32 x 1 token over 3000 keys
   // 32 and 37 us; 33 sequences, 30 of them one token, 31 and 36; but 32 x 24
   // tokens over 1100 keys, cut into twice as many parts, 24 and 19.)
-  const bool pair = d <= 128 && (T * g > fa::kBM * B || (T * g > 32 * B && B * Hkv < 2 * sms &&
+  const bool pair = !few && d <= 128 && (T * g > fa::kBM * B || (T * g > 32 * B && B * Hkv < 2 * sms &&
                                                          (max_q < T ? max_q : T) * B <= 4 * T));
   const int ctas = d == 64 && !pair ? 2 * sms : sms;
   const int slot_rows = (pair ? 2 : 1) * fa::kBM;
@@ -263,7 +271,9 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   p.desc = reinterpret_cast<int4*>(w + ws.desc_at);
   L.grid = ctas;
   L.stream = stream;
-  st = pair ? launch_window<true, true>(L, d, cache->dtype) : launch_window<true, false>(L, d, cache->dtype);
+  st = few ? launch_window<true, fa::WIN_FEW>(L, d, cache->dtype)
+       : pair ? launch_window<true, fa::WIN_PAIR>(L, d, cache->dtype)
+              : launch_window<true, fa::WIN_ONE>(L, d, cache->dtype);
   if (st != FA_OK) return st;
   const int64_t most = (max_q > 0 && max_q < unit_tok ? max_q : unit_tok) * g;
   return fa::launch_paged_combine(p.o_part, p.lse_part, p.desc, o, lse, sms, ctas, (int)units, slot_rows, (int)most,
