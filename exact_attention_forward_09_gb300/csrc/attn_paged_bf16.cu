@@ -2,12 +2,13 @@
 #include "attn_window.cuh"
 
 namespace fa {
-template cudaError_t launch_attn_window<kBF16, 64, true>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 64, true, WIN_FEW2>(const WinLaunch&);
 template cudaError_t launch_attn_window<kBF16, 64, true, WIN_ONE>(const WinLaunch&);
-template cudaError_t launch_attn_window<kBF16, 128, true, WIN_ONE>(const WinLaunch&);
-template cudaError_t launch_attn_window<kBF16, 256, true, WIN_FEW>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 64, true, WIN_PAIR>(const WinLaunch&);
 template cudaError_t launch_attn_window<kBF16, 128, true, WIN_FEW>(const WinLaunch&);
-template cudaError_t launch_attn_window<kBF16, 64, true, WIN_FEW>(const WinLaunch&);
-template cudaError_t launch_attn_window<kBF16, 128, true>(const WinLaunch&);
-template cudaError_t launch_attn_window<kBF16, 256, true>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 128, true, WIN_FEW2>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 128, true, WIN_ONE>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 128, true, WIN_PAIR>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 256, true, WIN_FEW>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 256, true, WIN_ONE>(const WinLaunch&);
 }  // namespace fa

@@ -57,43 +57,53 @@ namespace fa {
 // d = 256 does (one token each, 32/8 heads: 256 sequences under a window of
 // 1024 278 -> 227 us, one of 131000 keys 36.0 -> 32.9), and d = 64 runs two
 // CTAs per SM: two chains (64 sequences of 2000 to 16000 keys 310 -> 220 us).
-// WIN_FEW: as WIN_ONE, for units of at most kFewRows rows (a token's g heads,
+// WIN_FEW: as WIN_ONE, for units of at most FEW_ROWS rows (a token's g heads,
 // or a few tokens').  One softmax warp would do the work of a whole key tile
 // for a few rows while three work on rows that do not exist.  So the rows lie
 // four times in the query tile, at rows 0, 32, 64 and 96, and with that in the
 // TMEM lanes of each warp; warp w exponentiates columns 32 w .. 32 w + 31 alone,
 // for its copy, and hands over zeros for the others.  The four copies are
 // attention over disjoint keys, joined by their maxima and sums when the unit
-// ends.  (One token each, 32/8 heads, against WIN_ONE: 256 sequences
-// under a window of 1024 at d = 64, 128, 256: 149 -> 107, 224 -> 186, 430 -> 367
-// us; of 50 to 600 keys 78 -> 62, 125 -> 115, 190 -> 168; 64 of 2000 to 16000
-// at d = 64 224 -> 195, 6.5 TB/s.)  An infinite value in a row of V that is
-// seen can give NaN, as the copies that do not take its key weigh it with 0.
-enum WinForm { WIN_FEW, WIN_ONE, WIN_PAIR };
-constexpr int kFewRows = 16;
+// ends.  (One token each, 32/8 heads, against WIN_ONE: 256 sequences under a
+// window of 1024 at d = 64, 128, 256: 149 -> 107, 224 -> 186, 430 -> 367 us; of
+// 50 to 600 keys 78 -> 62, 125 -> 115, 190 -> 168; 64 of 2000 to 16000 at d = 64
+// 224 -> 195, 6.5 TB/s.)  An infinite value in a row of V that is seen can give
+// NaN, as the copies that do not take its key weigh it with 0.
+// WIN_FEW2 (d <= 128): the same with two CTAs per SM, where a unit's start and
+// end pass while the other CTA works.  At d = 128 it takes units of up to 8 rows
+// and half the tiles in flight, and pays where units are many (256 of 50 to 600
+// keys 116 -> 96 us, 64 of 2000 to 16000 373 -> 360; under the window of 1024
+// 185 -> 194) and not where few are cut in many parts (one of 131000 keys, 16/2
+// heads, 32.2 against 34.8).
+enum WinForm { WIN_FEW, WIN_FEW2, WIN_ONE, WIN_PAIR };
+constexpr int few_rows(int d, int form) { return form == WIN_FEW2 && d == 128 ? 8 : 16; }
 
 template <int ELEM, int D, bool PAGED, int FORM = (D <= 128 ? WIN_PAIR : WIN_ONE)>
 struct WinCfg {
-  static constexpr bool PAIR = FORM == WIN_PAIR, FEW = FORM == WIN_FEW;
+  static constexpr bool PAIR = FORM == WIN_PAIR, FEW = FORM == WIN_FEW || FORM == WIN_FEW2;
   static_assert(ELEM == kBF16 || ELEM == kFP16, "16-bit operands");
   static constexpr int ROW_BYTES = D * 2;
   static constexpr int CH_ELEMS = 64;                      // elements per 128-byte chunk
   static constexpr int NCH = D / CH_ELEMS;
   static constexpr int CHUNK_BYTES = 128 * 128;            // 128 rows x 128 bytes
   static constexpr int NQT = PAIR ? 2 : 1;                 // query tiles per CTA
-  static constexpr bool ALT = PAIR || D == 64;             // one S buffer per query tile; ring K0 V0 K1 V1 ...
+  static constexpr bool ALT = PAIR || FORM == WIN_FEW2 || D == 64;             // one S buffer per query tile; ring K0 V0 K1 V1 ...
   static constexpr int OCC = ALT && !PAIR ? 2 : 1;         // CTAs per SM
   static_assert(!PAIR || D <= 128, "two query tiles of d = 256 exceed tensor memory");
   static_assert((OCC == 1 && !FEW) || PAGED, "dense calls use pairs");
-  static constexpr int ML_BYTES = FEW ? 4 * kFewRows * 8 : 0;
+  static constexpr int FEW_ROWS = few_rows(D, FORM);
+  static constexpr int ML_BYTES = FEW ? 4 * FEW_ROWS * 8 : 0;
+  // WIN_FEW2, d = 128: the column chunks of the query tile lie in each other's unused rows
+  static constexpr bool Q_PACKED = FEW && FEW_ROWS == 8;
   // shared memory of a CTA: what two per SM leave beside their reserves
   static constexpr int SMEM_LIMIT = OCC == 2 ? 115712 : kSmemLimit;
   static constexpr int TILE_BYTES = kBN * ROW_BYTES;
-  static constexpr int SLOT_BYTES = TILE_BYTES < 32768 ? TILE_BYTES : 32768;
+  static constexpr int SLOT_BYTES = TILE_BYTES < 32768 ? TILE_BYTES : (OCC == 2 ? 16384 : 32768);
   static constexpr int SPT = TILE_BYTES / SLOT_BYTES;      // ring slots per tile
   static constexpr int SLOT_CH = SLOT_BYTES / CHUNK_BYTES;
   static constexpr int SLOT_D = SLOT_CH * CH_ELEMS;
-  static constexpr int Q_BYTES = NQT * kBM * ROW_BYTES;
+  static constexpr int Q_CHUNK = Q_PACKED ? FEW_ROWS * 128 : CHUNK_BYTES;
+  static constexpr int Q_BYTES = Q_PACKED ? CHUNK_BYTES + Q_CHUNK : NQT * kBM * ROW_BYTES;
   // dense d <= 128: O goes out through per-warp staging boxes and bulk tensor
   // copies (as attn_fwd.cuh); a paged row tile ends inside its neighbours'
   // rows, so there every thread stores its own row
@@ -115,7 +125,7 @@ struct WinCfg {
   // 80 clocks: at 16-token pages a K and a V tile of d = 128 are 32 boxes, as
   // long to issue as the tiles' arithmetic takes (chunks over 16-token pages:
   // 652 -> 590 us for 4 x 2048 new tokens over 4000 to 10000 keys).
-  static constexpr bool V_WARP = PAGED && OCC == 1;
+  static constexpr bool V_WARP = PAGED && (OCC == 1 || D == 128);
   static constexpr int LOADV_WARP = V_WARP ? LOAD_WARP + 1 : -1;
   static constexpr int UNIT_READERS = SOFTMAX_WARPS + 1 + (V_WARP ? 1 : 0);  // warps that release a unit's slot
   // two query tiles: a third, control warpgroup gives registers to the
@@ -647,7 +657,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
           __syncwarp();
           const int c = lane / C::NCH, ch = lane % C::NCH;
           if (c < 4)
-            tma_load_3d_hint(smem + C::OFF_Q + ch * C::CHUNK_BYTES + c * 32 * 128, &tm_q, &bars->q_full,
+            tma_load_3d_hint(smem + C::OFF_Q + ch * C::Q_CHUNK + c * 32 * 128, &tm_q, &bars->q_full,
                              ch * C::CH_ELEMS, w.kz * g, w.qz, pol_q);
         } else if (lane == 0) {
           const uint32_t tile = (uint32_t)(rpt * C::ROW_BYTES);
@@ -853,7 +863,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
 #pragma unroll
         for (int ks = 0; ks < D / 16; ++ks) {
           const int ch = ks / 4, in_ch = (ks % 4) * 32;
-          const uint64_t a = a0 + (uint64_t)((ch * C::CHUNK_BYTES + in_ch) >> 4);
+          const uint64_t a = a0 + (uint64_t)((ch * C::Q_CHUNK + in_ch) >> 4);
           const uint64_t b = b0[ch / C::SLOT_CH] + (uint64_t)(((ch % C::SLOT_CH) * C::CHUNK_BYTES + in_ch) >> 4);
           mma_ss_elect<0>(tmem + buf * kBN, a, b, decltype(idesc)::value, ks > 0 ? 1u : 0u);
         }
@@ -1252,15 +1262,15 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
           }
           // The copies' join.  O goes through query rows that no copy uses, 16
           // of each warp's 32: a line of 32 columns per row and column chunk, its
-          // 16-byte pieces permuted by the row; all columns at once for up to 8
-          // rows, which take two lines each, by halves for more.
+          // 16-byte pieces permuted by the row; all columns at once where they fit
+          // (up to 8 rows of two lines each), else by halves.
           if (ok) {
             ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[0], (uint32_t)(oc & 1), abort_flag, prm.err));
             ++oc;
           }
           float2* ml = reinterpret_cast<float2*>(smem + C::OFF_ML);
-          uint8_t* stage = smem + C::OFF_Q + kFewRows * 128;
-          const bool once = nr <= kFewRows / 2;
+          uint8_t* stage = smem + C::OFF_Q + 16 * 128;
+          const bool once = !C::Q_PACKED && nr <= C::FEW_ROWS / 2;
           auto put = [&](int h) {
 #pragma unroll
             for (int ch = 0; ch < C::NCH; ++ch) {
@@ -1268,8 +1278,8 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
               tmem_ld32(tmem + lane_addr + C::O_COL0 + h * (D / 2) + ch * 32, u);
               tmem_wait_ld();
               if (lane < nr) {
-                const int at = once ? lane + h * (kFewRows / 2) : lane;
-                uint4* line = reinterpret_cast<uint4*>(stage + ch * C::CHUNK_BYTES + (wq * 32 + at) * 128);
+                const int at = once ? lane + h * (C::FEW_ROWS / 2) : lane;
+                uint4* line = reinterpret_cast<uint4*>(stage + ch * C::Q_CHUNK + (wq * 32 + at) * 128);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                   line[i ^ (at & 7)] = make_uint4(u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
@@ -1313,11 +1323,11 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
                 l_all = fmaf(v[q].x, v[q].y, l_all);
               }
               const float f = l_all > 0.0f ? 1.0f / l_all : 0.0f;
-              const int at = once ? row + h * (kFewRows / 2) : row;
+              const int at = once ? row + h * (C::FEW_ROWS / 2) : row;
               float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
               for (int q = 0; q < 4; ++q) {
-                const float4 b = reinterpret_cast<const float4*>(stage + (c / 8) * C::CHUNK_BYTES +
+                const float4 b = reinterpret_cast<const float4*>(stage + (c / 8) * C::Q_CHUNK +
                                                                  (q * 32 + at) * 128)[(c % 8) ^ (at & 7)];
                 a.x = fmaf(v[q].x, b.x, a.x);
                 a.y = fmaf(v[q].x, b.y, a.y);

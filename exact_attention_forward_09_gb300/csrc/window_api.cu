@@ -15,24 +15,24 @@
 #include "paged.h"
 
 namespace fa {
-#define FA_EXTERN_WINDOW(E, P)                                                \
-  extern template cudaError_t launch_attn_window<E, 64, P>(const WinLaunch&);  \
-  extern template cudaError_t launch_attn_window<E, 128, P>(const WinLaunch&); \
-  extern template cudaError_t launch_attn_window<E, 256, P>(const WinLaunch&);
-FA_EXTERN_WINDOW(kBF16, false)
-FA_EXTERN_WINDOW(kFP16, false)
-FA_EXTERN_WINDOW(kBF16, true)
-FA_EXTERN_WINDOW(kFP16, true)
+#define FA_EXTERN_WINDOW(E, D, P, F) extern template cudaError_t launch_attn_window<E, D, P, F>(const WinLaunch&);
+#define FA_EXTERN_ELEM(E)                 \
+  FA_EXTERN_WINDOW(E, 64, false, WIN_PAIR)  \
+  FA_EXTERN_WINDOW(E, 128, false, WIN_PAIR) \
+  FA_EXTERN_WINDOW(E, 256, false, WIN_ONE)  \
+  FA_EXTERN_WINDOW(E, 64, true, WIN_FEW2)   \
+  FA_EXTERN_WINDOW(E, 64, true, WIN_ONE)    \
+  FA_EXTERN_WINDOW(E, 64, true, WIN_PAIR)   \
+  FA_EXTERN_WINDOW(E, 128, true, WIN_FEW)   \
+  FA_EXTERN_WINDOW(E, 128, true, WIN_FEW2)  \
+  FA_EXTERN_WINDOW(E, 128, true, WIN_ONE)   \
+  FA_EXTERN_WINDOW(E, 128, true, WIN_PAIR)  \
+  FA_EXTERN_WINDOW(E, 256, true, WIN_FEW)   \
+  FA_EXTERN_WINDOW(E, 256, true, WIN_ONE)
+FA_EXTERN_ELEM(kBF16)
+FA_EXTERN_ELEM(kFP16)
+#undef FA_EXTERN_ELEM
 #undef FA_EXTERN_WINDOW
-#define FA_EXTERN_ONE_TILE(E)                                                        \
-  extern template cudaError_t launch_attn_window<E, 64, true, WIN_ONE>(const WinLaunch&);  \
-  extern template cudaError_t launch_attn_window<E, 128, true, WIN_ONE>(const WinLaunch&); \
-  extern template cudaError_t launch_attn_window<E, 64, true, WIN_FEW>(const WinLaunch&);  \
-  extern template cudaError_t launch_attn_window<E, 128, true, WIN_FEW>(const WinLaunch&); \
-  extern template cudaError_t launch_attn_window<E, 256, true, WIN_FEW>(const WinLaunch&);
-FA_EXTERN_ONE_TILE(kBF16)
-FA_EXTERN_ONE_TILE(kFP16)
-#undef FA_EXTERN_ONE_TILE
 }  // namespace fa
 
 namespace {
@@ -50,19 +50,29 @@ float log2_scale(float scale) {
   return s == 0.0f ? 1e-30f : s;
 }
 
-// FORM at d = 64 and 128 (d = 256 has no pairs)
-template <bool PAGED, int FORM>
-fa_status launch_window(const fa::WinLaunch& L, int64_t d, int dtype) {
-  constexpr int FORM256 = FORM == fa::WIN_PAIR ? fa::WIN_ONE : FORM;
+template <int ELEM>
+fa_status launch_dense(const fa::WinLaunch& L, int64_t d) {
+  const cudaError_t e = d == 64    ? fa::launch_attn_window<ELEM, 64, false, fa::WIN_PAIR>(L)
+                        : d == 128 ? fa::launch_attn_window<ELEM, 128, false, fa::WIN_PAIR>(L)
+                                   : fa::launch_attn_window<ELEM, 256, false, fa::WIN_ONE>(L);
+  return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int ELEM>
+fa_status launch_paged(const fa::WinLaunch& L, int64_t d, int form) {
   cudaError_t e = cudaErrorInvalidValue;
-  if (dtype == FA_DTYPE_BF16) {
-    if (d == 64) e = fa::launch_attn_window<fa::kBF16, 64, PAGED, FORM>(L);
-    else if (d == 128) e = fa::launch_attn_window<fa::kBF16, 128, PAGED, FORM>(L);
-    else if (d == 256) e = fa::launch_attn_window<fa::kBF16, 256, PAGED, FORM256>(L);
+  if (d == 64) {
+    if (form == fa::WIN_FEW2) e = fa::launch_attn_window<ELEM, 64, true, fa::WIN_FEW2>(L);
+    if (form == fa::WIN_ONE) e = fa::launch_attn_window<ELEM, 64, true, fa::WIN_ONE>(L);
+    if (form == fa::WIN_PAIR) e = fa::launch_attn_window<ELEM, 64, true, fa::WIN_PAIR>(L);
+  } else if (d == 128) {
+    if (form == fa::WIN_FEW) e = fa::launch_attn_window<ELEM, 128, true, fa::WIN_FEW>(L);
+    if (form == fa::WIN_FEW2) e = fa::launch_attn_window<ELEM, 128, true, fa::WIN_FEW2>(L);
+    if (form == fa::WIN_ONE) e = fa::launch_attn_window<ELEM, 128, true, fa::WIN_ONE>(L);
+    if (form == fa::WIN_PAIR) e = fa::launch_attn_window<ELEM, 128, true, fa::WIN_PAIR>(L);
   } else {
-    if (d == 64) e = fa::launch_attn_window<fa::kFP16, 64, PAGED, FORM>(L);
-    else if (d == 128) e = fa::launch_attn_window<fa::kFP16, 128, PAGED, FORM>(L);
-    else if (d == 256) e = fa::launch_attn_window<fa::kFP16, 256, PAGED, FORM256>(L);
+    if (form == fa::WIN_FEW) e = fa::launch_attn_window<ELEM, 256, true, fa::WIN_FEW>(L);
+    if (form == fa::WIN_ONE) e = fa::launch_attn_window<ELEM, 256, true, fa::WIN_ONE>(L);
   }
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
@@ -159,7 +169,7 @@ fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, fl
   L.prm.Nk = (int)Nk;
   L.prm.BH = (int)(B * Hq);
   L.stream = stream;
-  return launch_window<false, fa::WIN_PAIR>(L, d, dtype);
+  return dtype == FA_DTYPE_BF16 ? launch_dense<fa::kBF16>(L, d) : launch_dense<fa::kFP16>(L, d);
 }
 
 fa_status fa_paged_workspace_bytes(int64_t d, size_t* bytes) {
@@ -201,19 +211,26 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   const int64_t g = Hq / Hkv;
   int64_t tpt = fa::kBM / g;  // tokens whose g heads fit a query tile
   if (max_q > 0 && max_q < tpt) tpt = max_q;
-  // The form (see WinForm).  Few rows: as many tokens per unit as a few rows
-  // hold, if no sequence brings more, or on average each brings one.
-  const bool few = g <= fa::kFewRows && (max_q > 0 ? max_q <= fa::kFewRows / g : T <= B);
-  if (few && tpt > fa::kFewRows / g) tpt = fa::kFewRows / g;
-  // Query tiles per CTA (see WinCfg): one where sequences bring few rows on
-  // average; or up to a tile's, if there are enough of them that few are cut or
-  // if the longest is far above the average, so that most are short.
+  // The form (see WinForm).  Few rows: no sequence brings more than their
+  // tokens, or each brings one on average.  Two CTAs per SM with units for all.
+  auto few_of = [&](int form) {
+    const int64_t tokens = fa::few_rows((int)d, form) / g;
+    return tokens > 0 && (max_q > 0 ? max_q <= tokens : T <= B) ? tokens : 0;
+  };
+  int64_t few = d == 64 || (d == 128 && B * Hkv >= sms) ? few_of(fa::WIN_FEW2) : 0;
+  const bool few2 = few > 0;
+  if (!few2) few = d == 64 ? 0 : few_of(fa::WIN_FEW);
+  if (few > 0 && few < tpt) tpt = few;
+  // Else query tiles per CTA: one where sequences bring few rows on average; or
+  // up to a tile's, if there are enough of them that few are cut or if the
+  // longest is far above the average, so that most are short.
   // (One tile against a pair at d = 64, 16/4 heads: 32 x 1 token over 3000 keys
   // 32 and 37 us; 33 sequences, 30 of them one token, 31 and 36; but 32 x 24
   // tokens over 1100 keys, cut into twice as many parts, 24 and 19.)
-  const bool pair = !few && d <= 128 && (T * g > fa::kBM * B || (T * g > 32 * B && B * Hkv < 2 * sms &&
-                                                         (max_q < T ? max_q : T) * B <= 4 * T));
-  const int ctas = d == 64 && !pair ? 2 * sms : sms;
+  const bool pair = few == 0 && d <= 128 && (T * g > fa::kBM * B || (T * g > 32 * B && B * Hkv < 2 * sms &&
+                                                                    (max_q < T ? max_q : T) * B <= 4 * T));
+  const int form = few2 ? fa::WIN_FEW2 : few > 0 ? fa::WIN_FEW : pair ? fa::WIN_PAIR : fa::WIN_ONE;
+  const int ctas = few2 || (form == fa::WIN_ONE && d == 64) ? 2 * sms : sms;
   const int slot_rows = (pair ? 2 : 1) * fa::kBM;
   const CUtensorMapDataType dt = map_type(cache->dtype);
   {
@@ -271,9 +288,7 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   p.desc = reinterpret_cast<int4*>(w + ws.desc_at);
   L.grid = ctas;
   L.stream = stream;
-  st = few ? launch_window<true, fa::WIN_FEW>(L, d, cache->dtype)
-       : pair ? launch_window<true, fa::WIN_PAIR>(L, d, cache->dtype)
-              : launch_window<true, fa::WIN_ONE>(L, d, cache->dtype);
+  st = cache->dtype == FA_DTYPE_BF16 ? launch_paged<fa::kBF16>(L, d, form) : launch_paged<fa::kFP16>(L, d, form);
   if (st != FA_OK) return st;
   const int64_t most = (max_q > 0 && max_q < unit_tok ? max_q : unit_tok) * g;
   return fa::launch_paged_combine(p.o_part, p.lse_part, p.desc, o, lse, sms, ctas, (int)units, slot_rows, (int)most,
