@@ -38,7 +38,9 @@
 // tile's walk ends with the last query whose window reaches it; the tiles
 // that hold a sink are seen by every later query, so their walk is shared out
 // over several CTAs that start first and leave fp32 dK and dV parts
-// (BwdWindow), which a small kernel sums in a fixed order.
+// (BwdWindow), which a small kernel sums in a fixed order.  The other tiles'
+// walks, of all query heads of a group, are shared out likewise where the
+// tiles are too few to fill the GPU.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -180,6 +182,11 @@ __device__ __forceinline__ void settle(uint64_t* bar, uint32_t parity) {
   }
 }
 
+// WIN: the sink tiles' parts, which come before the other tiles'
+__device__ __forceinline__ size_t bwd_sink_parts(const BwdParams& prm) {
+  return prm.sink_split > 1 ? (size_t)prm.sink_tiles * prm.BHkv * prm.sink_split : 0;
+}
+
 template <int ELEM, int D, bool CAUSAL, bool WIN>
 __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
     attn_bwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
@@ -207,18 +214,20 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
   // CTA -> (key/value head, key tile).  Causal: key-tile-major, so the tiles
   // with the most visible queries (the first ones) start first.
   int bkv, kt;
-  int part = -1;  // WIN: which share of a sink tile's steps (-1: all of a tile's)
+  int part = -1;  // WIN: which share of the tile's steps (-1: all)
   if constexpr (WIN) {
-    // the shares of the sink tiles first, then the other tiles in order
+    // the shares of the sink tiles first, then those of the other tiles in order
     const int sink_ctas = prm.sink_tiles * prm.sink_split * prm.BHkv;
     int x = (int)blockIdx.x;
     bkv = x % prm.BHkv;
     if (x < sink_ctas) {
       x /= prm.BHkv;
       kt = x / prm.sink_split;
-      part = prm.sink_split > 1 ? x % prm.sink_split : -1;
+      if (prm.sink_split > 1) part = x % prm.sink_split;
     } else {
-      kt = prm.sink_tiles + (x - sink_ctas) / prm.BHkv;
+      x = (x - sink_ctas) / prm.BHkv;
+      kt = prm.sink_tiles + x / prm.tile_split;
+      if (prm.tile_split > 1) part = x % prm.tile_split;
     }
   } else if constexpr (CAUSAL) {
     kt = (int)blockIdx.x / prm.BHkv;
@@ -246,8 +255,9 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
   int step0 = 0;           // WIN: first of them
   if constexpr (WIN) {
     if (part >= 0) {
-      step0 = (int)((long long)T * part / prm.sink_split);
-      T = (int)((long long)T * (part + 1) / prm.sink_split) - step0;
+      const int shares = kt < prm.sink_tiles ? prm.sink_split : prm.tile_split;
+      step0 = (int)((long long)T * part / shares);
+      T = (int)((long long)T * (part + 1) / shares) - step0;
     }
   }
   auto step_of = [&](int t, int& bhq, int& q0) {
@@ -561,7 +571,11 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
       // this share's dV (warpgroup 0) or unscaled dK (warpgroup 1), fp32: one
       // key row per thread
       if (cg < 2 && have) {
-        float* dst = prm.part + (((((size_t)kt * prm.BHkv + bkv) * prm.sink_split + part) * 2 + (cg ? 0 : 1)) * kBK + r) * D;
+        const size_t slot =
+            kt < prm.sink_tiles
+                ? ((size_t)kt * prm.BHkv + bkv) * prm.sink_split + part
+                : bwd_sink_parts(prm) + ((size_t)(kt - prm.sink_tiles) * prm.BHkv + bkv) * prm.tile_split + part;
+        float* dst = prm.part + ((slot * 2 + (cg ? 0 : 1)) * kBK + r) * D;
         const uint32_t col = cg ? C::COL_DK : C::COL_DV;
 #pragma unroll 1
         for (int c0 = 0; c0 < D; c0 += 32) {
@@ -804,7 +818,7 @@ __global__ void __launch_bounds__(256) zero_fill_kernel(uint4* __restrict__ p, l
 }
 
 // The end of the windowed backward, one launch: blocks below conv_blocks
-// scale and convert dQ (grid-stride), the others sum the sink tiles' shares,
+// scale and convert dQ (grid-stride), the others sum the shared tiles' parts,
 // one warp per key row and gradient (dK, dV), the parts in order, scaled
 // (dK), rounded once.
 template <int D, bool F16>
@@ -831,16 +845,19 @@ __global__ void __launch_bounds__(256) bwd_window_finish_kernel(const BwdParams 
   const int lane = threadIdx.x & 31;
   const int row = (int)(x % kBK);
   const int which = (int)(x / kBK % 2);                     // 0: dK, 1: dV
-  const long long unit = x / (2 * kBK);                     // tile * BHkv + bkv
-  const long long kt = unit / prm.BHkv, bkv = unit % prm.BHkv;
+  const long long unit = x / (2 * kBK);                     // shared tile * BHkv + bkv
+  const long long kt = unit / prm.BHkv + (prm.sink_split > 1 ? 0 : prm.sink_tiles), bkv = unit % prm.BHkv;
   const long long key = kt * kBK + row;
-  if (kt >= prm.sink_tiles || key >= prm.Nk) return;
+  if (key >= prm.Nk) return;
+  const int shares = kt < prm.sink_tiles ? prm.sink_split : prm.tile_split;
+  const long long slot = kt < prm.sink_tiles ? (kt * prm.BHkv + bkv) * shares
+                                             : (long long)bwd_sink_parts(prm) + ((kt - prm.sink_tiles) * prm.BHkv + bkv) * shares;
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-  const float* src = prm.part + ((unit * prm.sink_split * 2 + which) * kBK + row) * D + lane * E;
+  const float* src = prm.part + ((slot * 2 + which) * kBK + row) * D + lane * E;
 #pragma unroll 4
-  for (int s = 0; s < prm.sink_split; ++s, src += 2LL * kBK * D) {
+  for (int s = 0; s < shares; ++s, src += 2LL * kBK * D) {
 #pragma unroll
     for (int e = 0; e < E; e += 2) {
       const float2 v = *reinterpret_cast<const float2*>(src + e);
@@ -884,7 +901,8 @@ cudaError_t launch_attn_bwd(const BwdLaunch& L) {
   }
   const long long nkt = (L.prm.Nk + kBK - 1) / kBK;
   long long ctas = (long long)L.prm.BHkv * nkt;
-  if constexpr (WIN) ctas += (long long)L.prm.BHkv * L.prm.sink_tiles * (L.prm.sink_split - 1);
+  if constexpr (WIN)
+    ctas = L.prm.BHkv * ((long long)L.prm.sink_tiles * L.prm.sink_split + (nkt - L.prm.sink_tiles) * L.prm.tile_split);
   if constexpr (WIN) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
@@ -930,22 +948,44 @@ BwdWindow bwd_window_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_
   w.window = (int)(window < Nk ? window : (Nk > 1 ? Nk : 1));  // a longer one hides nothing
   w.sinks = (int)(sinks < Nk ? sinks : Nk);
   w.sink_tiles = (w.sinks + kBK - 1) / kBK;
-  w.split = 1;
+  w.split = w.tile_split = 1;
   w.part_bytes = 0;
-  if (w.sink_tiles == 0 || Nq == 0) return w;
+  if (Nq == 0) return w;
   const int64_t bq = bwd_step_rows(d), nqt = (Nq + bq - 1) / bq, grp = Hq / Hkv;
-  // steps of a tile without sinks, of the first sink tile, and as many shares
-  // as bring the second down to the first (at least 8 steps each), while the
-  // shares do not outnumber what fills the GPU several times
-  int64_t usual = (kBK - 1 + w.window + bq - 1) / bq + 1;
+  const int64_t tiles = (Nk + kBK - 1) / kBK - w.sink_tiles;  // those without sinks
+  int64_t usual = (kBK - 1 + w.window + bq - 1) / bq + 1;      // steps of such a tile and head
   if (usual > nqt) usual = nqt;
   usual *= grp;
-  if (usual < 8) usual = 8;
-  int64_t split = (grp * nqt + usual - 1) / usual;
-  const int64_t most = 1024 / (w.sink_tiles * B * Hkv);
-  if (split > most) split = most;
-  w.split = (int)(split < 1 ? 1 : split);
-  if (w.split > 1) w.part_bytes = (size_t)w.sink_tiles * B * Hkv * w.split * 2 * kBK * d * 4;
+  // Shares of the tiles without sinks: what a model of the time asks for, in
+  // steps: waves of shares, each of so many steps and what a CTA takes to start
+  // and to end, and the parts' way to memory and back.  Whole call with the
+  // forward, one share and shared: 4096 tokens, 16/1 heads, d = 128, window 1024
+  // 455 and 173 us; 1023 tokens, 32/4 heads, window 977 206 and 84.  (A window
+  // over everything stays fa_bwd bit for bit, and so unshared.)
+  const int64_t sms = 152, most_parts = 1024, bhkv = B * Hkv;
+  const int64_t most_shares = w.window < Nk ? 16 : 1;
+  double best = 0.0;
+  for (int64_t n = 1; n <= most_shares && n <= usual && (n == 1 || n * tiles * bhkv <= most_parts); ++n) {
+    const int64_t ctas = n * tiles * bhkv;
+    const double t = (double)((ctas + sms - 1) / sms) * ((double)((usual + n - 1) / n) + 3.0) +
+                     (n > 1 ? 2.0 + (double)ctas * d / 8192.0 : 0.0);
+    if (n == 1 || t < 0.9 * best) {
+      best = t;
+      w.tile_split = (int)n;
+    }
+  }
+  if (w.sink_tiles > 0) {
+    // of a sink tile as many shares as bring one down to the others' (at least
+    // 8 steps each), while they do not outnumber what fills the GPU several times
+    int64_t share = (usual + w.tile_split - 1) / w.tile_split;
+    if (share < 8) share = 8;
+    int64_t split = (grp * nqt + share - 1) / share;
+    const int64_t most = most_parts / (w.sink_tiles * bhkv);
+    if (split > most) split = most;
+    w.split = (int)(split < 1 ? 1 : split);
+  }
+  const int64_t parts = (w.split > 1 ? w.sink_tiles * w.split : 0) + (w.tile_split > 1 ? tiles * w.tile_split : 0);
+  w.part_bytes = (size_t)parts * bhkv * 2 * kBK * d * 4;
   return w;
 }
 
@@ -953,7 +993,9 @@ cudaError_t launch_bwd_window_finish(const BwdParams& prm, void* dq, long long e
                                      cudaStream_t stream) {
   const long long n8 = elems / 8;
   const int conv = (int)stride_grid(n8);
-  const long long sum = prm.sink_split > 1 ? (long long)prm.sink_tiles * prm.BHkv * 2 * kBK / 8 : 0;
+  const long long nkt = (prm.Nk + kBK - 1) / kBK;
+  const long long shared = (prm.sink_split > 1 ? prm.sink_tiles : 0) + (prm.tile_split > 1 ? nkt - prm.sink_tiles : 0);
+  const long long sum = shared * prm.BHkv * 2 * kBK / 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(conv + sum), 1, 1);
   cfg.blockDim = dim3(256, 1, 1);

@@ -25,17 +25,19 @@ struct BwdParams {
   int drop_step;       // test hook: step whose Q/dO stage CTA 0 never fills (-1: none)
   // sliding window with sinks (the WIN instances): see BwdWindow
   int window, sinks;
-  int sink_tiles, sink_split;
-  float* part;         // sink_split > 1: [sink_tiles][BHkv][sink_split][dK, dV][128][D] fp32
+  int sink_tiles, sink_split, tile_split;
+  // sink_split > 1: [sink_tiles][BHkv][sink_split][dK, dV][128][D] fp32, then
+  // tile_split > 1: [other tiles][BHkv][tile_split][dK, dV][128][D]
+  float* part;
 };
 
-// How the windowed backward treats the key tiles that hold a sink: every
-// query from their first key on sees them, where the other tiles are seen by
-// about window / 128 + 1 query tiles, so their query steps are shared out
-// over `split` CTAs each, which leave fp32 dK and dV to be summed.
+// How the windowed backward shares out its key tiles' query steps, over CTAs
+// that leave fp32 dK and dV to be summed.  The tiles that hold a sink are seen
+// by every query from their first key on, the others by about window / 128 + 1
+// query tiles: `split` shares of each of the first, `tile_split` of the others.
 struct BwdWindow {
   int window, sinks;
-  int sink_tiles, split;
+  int sink_tiles, split, tile_split;
   size_t part_bytes;
 };
 BwdWindow bwd_window_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int d, int64_t window,
@@ -54,7 +56,7 @@ struct BwdLaunch {
 template <int ELEM, int D, bool CAUSAL, bool WIN = false>
 cudaError_t launch_attn_bwd(const BwdLaunch& L);
 
-// The end of the windowed backward: dq = RN(scale * dq_acc), and for the sink
+// The end of the windowed backward: dq = RN(scale * dq_acc), and for the shared
 // tiles (rows below Nk) dK = scale * sum of the shares' dK, dV = sum of theirs.
 cudaError_t launch_bwd_window_finish(const BwdParams& prm, void* dq, long long elems, int d, bool f16,
                                      cudaStream_t stream);

@@ -443,9 +443,8 @@ fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void*
 
 /*
  * fa_bwd_window_workspace_bytes -- bytes of device workspace fa_bwd_window
- * needs: fa_bwd's, and fp32 dK and dV parts of the key tiles that hold a sink
- * when their queries are shared out (at most 128 MiB at d = 128).  Same checks
- * as fa_bwd_window.
+ * needs: fa_bwd's, and fp32 dK and dV parts of the key tiles whose queries are
+ * shared out (at most 256 MiB at d = 128).  Same checks as fa_bwd_window.
  */
 fa_status fa_bwd_window_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d,
                                         int64_t window, int64_t sinks, size_t* bytes);
