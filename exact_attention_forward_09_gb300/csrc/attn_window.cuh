@@ -75,24 +75,32 @@ namespace fa {
 // keys 116 -> 96 us, 64 of 2000 to 16000 373 -> 360; under the window of 1024
 // 185 -> 194) and not where few are cut in many parts (one of 131000 keys, 16/2
 // heads, 32.2 against 34.8).
-enum WinForm { WIN_FEW, WIN_FEW2, WIN_ONE, WIN_PAIR };
+// WIN_SPLIT (dense): one query tile per cluster, whose CTAs take runs of its key
+// tiles and join their results through each other's shared memory, for calls
+// of so few query tiles that most SMs would idle.  (d = 128, 8/2 heads over 8000
+// keys without a window: 1 query 81.4 -> 14.5 us, 100 82.0 -> 16.5, 1000 82.0 ->
+// 38.7; 12 heads, window 500, 1 and 100 queries: 13.4 -> 9.4, 15.4 -> 10.8.)
+enum WinForm { WIN_FEW, WIN_FEW2, WIN_ONE, WIN_PAIR, WIN_SPLIT };
 constexpr int few_rows(int d, int form) { return form == WIN_FEW2 && d == 128 ? 8 : 16; }
 
 template <int ELEM, int D, bool PAGED, int FORM = (D <= 128 ? WIN_PAIR : WIN_ONE)>
 struct WinCfg {
-  static constexpr bool PAIR = FORM == WIN_PAIR, FEW = FORM == WIN_FEW || FORM == WIN_FEW2;
+  static constexpr bool PAIR = FORM == WIN_PAIR, FEW = FORM == WIN_FEW || FORM == WIN_FEW2,
+                        SPLIT = FORM == WIN_SPLIT;
   static_assert(ELEM == kBF16 || ELEM == kFP16, "16-bit operands");
+  static constexpr int D_ = D, ELEM_ = ELEM;
   static constexpr int ROW_BYTES = D * 2;
   static constexpr int CH_ELEMS = 64;                      // elements per 128-byte chunk
   static constexpr int NCH = D / CH_ELEMS;
   static constexpr int CHUNK_BYTES = 128 * 128;            // 128 rows x 128 bytes
   static constexpr int NQT = PAIR ? 2 : 1;                 // query tiles per CTA
-  static constexpr bool ALT = PAIR || FORM == WIN_FEW2 || D == 64;             // one S buffer per query tile; ring K0 V0 K1 V1 ...
+  static constexpr bool ALT = PAIR || FORM == WIN_FEW2 || (D == 64 && !SPLIT);             // one S buffer per query tile; ring K0 V0 K1 V1 ...
   static constexpr int OCC = ALT && !PAIR ? 2 : 1;         // CTAs per SM
   static_assert(!PAIR || D <= 128, "two query tiles of d = 256 exceed tensor memory");
   static_assert((OCC == 1 && !FEW) || PAGED, "dense calls use pairs");
+  static_assert(!SPLIT || !PAGED, "paged units are cut along the line of work");
   static constexpr int FEW_ROWS = few_rows(D, FORM);
-  static constexpr int ML_BYTES = FEW ? 4 * FEW_ROWS * 8 : 0;
+  static constexpr int ML_BYTES = FEW ? 4 * FEW_ROWS * 8 : (SPLIT ? kBM * 8 : 0);
   // WIN_FEW2, d = 128: the column chunks of the query tile lie in each other's unused rows
   static constexpr bool Q_PACKED = FEW && FEW_ROWS == 8;
   // shared memory of a CTA: what two per SM leave beside their reserves
@@ -107,7 +115,7 @@ struct WinCfg {
   // dense d <= 128: O goes out through per-warp staging boxes and bulk tensor
   // copies (as attn_fwd.cuh); a paged row tile ends inside its neighbours'
   // rows, so there every thread stores its own row
-  static constexpr bool EPI_TMA = !PAGED && D <= 128;
+  static constexpr bool EPI_TMA = !PAGED && D <= 128 && !SPLIT;
   static constexpr int EPI_WARP_BYTES = 32 * 64 * 2;
   static constexpr int EPI_BYTES = EPI_TMA ? 4 * NQT * EPI_WARP_BYTES : 0;
   static constexpr int NS_MAX = (SMEM_LIMIT - 2048 - ML_BYTES - EPI_BYTES - Q_BYTES) / SLOT_BYTES;
@@ -148,9 +156,11 @@ struct WinCfg {
   static constexpr int OFF_EPI = OFF_RING + NS * SLOT_BYTES;
   static constexpr int OFF_BAR = OFF_EPI + EPI_BYTES;
   static_assert(OFF_EPI % 1024 == 0 && OFF_BAR % 1024 == 0, "1024-byte swizzle atoms");
-  static constexpr int OFF_ML = OFF_BAR + 1024;                // WIN_FEW: maxima and sums, [row][warp]
+  static constexpr int OFF_ML = OFF_BAR + 1024;                // WIN_FEW: maxima and sums, [row][warp]; WIN_SPLIT: [row]
+  static constexpr int OFF_WEIGHT = OFF_Q;                     // WIN_SPLIT: [row][CTA], over Q, which is done with
   static constexpr int SMEM_BYTES = OFF_ML + ML_BYTES + 1024;  // + alignment slack
   static_assert(SMEM_BYTES <= SMEM_LIMIT, "shared memory budget");
+  static_assert(!SPLIT || NS * SLOT_BYTES >= kBM * D * 4, "WIN_SPLIT leaves its part of O in the ring");
 };
 
 struct WinParams {
@@ -375,6 +385,57 @@ __device__ __noinline__ bool clear_v_row(Bars* bars, uint32_t row, int pv, bool 
   }
   fence_proxy_async_smem();
   return true;
+}
+
+// WIN_SPLIT: the join over the cluster's N CTAs of the query tile `w`.  Every
+// CTA takes a share of the (row, 4 columns) items; first each row's weight of
+// each run.
+template <typename C, int N>
+__device__ __forceinline__ void cluster_join(uint8_t* smem, const WinUnit& w, const WinParams& prm) {
+  constexpr int D = C::D_;
+  const int rank = (int)blockIdx.x % N;
+  const uint32_t ml_at = smem_u32(smem + C::OFF_ML), o_at = smem_u32(smem + C::OFF_RING);
+  float* weight = reinterpret_cast<float*>(smem + C::OFF_WEIGHT);  // [row][N], -1: the row sees no key of the run
+  for (int row = threadIdx.x; row < w.ntok; row += C::THREADS) {
+    float2 v[N];
+    float m_all = -INFINITY, l_all = 0.0f;
+#pragma unroll
+    for (int q = 0; q < N; ++q) v[q] = ld_cluster_f2(cluster_addr(ml_at + row * 8, q));
+#pragma unroll
+    for (int q = 0; q < N; ++q) m_all = fmaxf(m_all, v[q].x);
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const float f = v[q].x == -INFINITY ? 1.0f : ex2(v[q].x - m_all);  // (-inf and a sum: NaN scores)
+      l_all = fmaf(f, v[q].y, l_all);
+      v[q].y = v[q].x == -INFINITY && v[q].y == 0.0f ? -1.0f : f;
+    }
+    const float inv = l_all == 0.0f ? 0.0f : 1.0f / l_all;
+#pragma unroll
+    for (int q = 0; q < N; ++q) weight[row * N + q] = v[q].y < 0.0f ? -1.0f : v[q].y * inv;
+    if (rank == 0)
+      prm.lse[(size_t)w.qz * prm.N + w.q_row + row] = (m_all + lg2(l_all)) * 0.69314718055994530942f;
+  }
+  __syncthreads();
+  for (int i = rank * C::THREADS + threadIdx.x; i < w.ntok * (D / 4); i += N * C::THREADS) {
+    const int row = i / (D / 4), c = i % (D / 4);
+    float4 b[N], a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+      b[q] = ld_cluster_f4(cluster_addr(o_at + row * (D * 4) + (((c & ~7) + ((c & 7) ^ (row & 7))) << 4), q));
+#pragma unroll
+    for (int q = 0; q < N; ++q) {
+      const float f = weight[row * N + q];
+      if (f < 0.0f) continue;
+      a.x = fmaf(f, b[q].x, a.x);
+      a.y = fmaf(f, b[q].y, a.y);
+      a.z = fmaf(f, b[q].z, a.z);
+      a.w = fmaf(f, b[q].w, a.w);
+    }
+    const uint2 pk = C::ELEM_ == kFP16 ? make_uint2(pack_f16x2(a.x, a.y), pack_f16x2(a.z, a.w))
+                                       : make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(prm.o) +
+                              ((size_t)w.qz * prm.N + w.q_row + row) * D + 4 * c) = pk;
+  }
 }
 
 template <int ELEM, int D, bool PAGED, int FORM>
@@ -770,7 +831,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
         const int units = prm.pair_units + C::NQT * (prm.BH * n_groups - prm.pair_units);
         const int qgroup = prm.Hq / prm.Hkv;
         int n_req = 0;
-        bool more = true;
+        bool more = !C::SPLIT;
         auto decode = [&](int x) {
           const bool single = x >= prm.pair_units;
           const int v = single ? prm.pair_units + (x - prm.pair_units) / C::NQT : x;
@@ -792,8 +853,16 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
           w.r1 = w.ntok > 0 ? u.len : 0;
           w.part = -1;
         };
-        int u = (int)blockIdx.x;
-        decode(u);
+        if constexpr (C::SPLIT) {
+          // this CTA's run of the cluster's unit
+          const int n_cta = cluster_size(), rank = (int)blockIdx.x % n_cta;
+          decode((int)blockIdx.x / n_cta);
+          const int len = w.r1;
+          w.r0 = (int)((long long)len * rank / n_cta);
+          w.r1 = (int)((long long)len * (rank + 1) / n_cta);
+        } else {
+          decode((int)blockIdx.x);
+        }
         ok = publish(0, w);
         for (int r = 0; ok; ++r) {
           load_unit(w);
@@ -1118,6 +1187,10 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
         if (rows <= 0) break;
         const WinPart mine(w, t);
         const int n = C::NQT == 2 ? mine.count(r0, r1) : nrun;
+        if (C::SPLIT && n == 0) {
+          reinterpret_cast<float2*>(smem + C::OFF_ML)[r_in] = make_float2(-INFINITY, 0.0f);
+          break;
+        }
         if (n == 0) {
           // no row of this tile sees a key of this run: O = 0, LSE = -inf
           if (valid) {
@@ -1521,6 +1594,23 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
         ++oc;
         if (!ok) break;
         tc_fence_after();
+        if constexpr (C::SPLIT) {
+          // for the cluster's join: the row's maximum and sum, and O as it is,
+          // in the ring (no copy or MMA uses it any more), 16-byte pieces
+          // permuted by the row
+          reinterpret_cast<float2*>(smem + C::OFF_ML)[r_in] = make_float2(m_run, l_run);
+          const uint32_t row_at = smem_u32(smem + C::OFF_RING) + r_in * (D * 4);
+#pragma unroll 1
+          for (int c0 = 0; c0 < D; c0 += 32) {
+            uint32_t u[32];
+            tmem_ld32(tmem + lane_addr + C::O_COL0 + c0, u);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              st_shared_v4(row_at + (((c0 >> 2) + (i ^ (lane & 7))) << 4), u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]);
+          }
+          break;
+        }
         const float f = (l_run > 0.0f) ? (1.0f / l_run) : 0.0f;
         const float lse_row = (m_run + lg2(l_run)) * 0.69314718055994530942f;
         const uint32_t o_addr = tmem + lane_addr + C::O_COL0 + t * D;
@@ -1618,6 +1708,16 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
     tc_fence_after();
     tmem_dealloc(tmem, C::TMEM_COLS);
   }
+  if constexpr (C::SPLIT) {
+    // the join; all threads arrive at both barriers, also after a wait that ran out
+    cluster_sync();
+    const WinUnit& w = bars->unit[0];
+    const int n_cta = cluster_size();
+    if (n_cta == 8) cluster_join<C, 8>(smem, w, prm);
+    else if (n_cta == 4) cluster_join<C, 4>(smem, w, prm);
+    else cluster_join<C, 2>(smem, w, prm);
+    cluster_sync();  // the others have read this CTA's shared memory
+  }
 }
 
 struct WinLaunch {
@@ -1625,6 +1725,7 @@ struct WinLaunch {
   CUtensorMap o;      // dense d <= 128: O in boxes of 64 columns x 32 rows
   WinParams prm;
   int grid;           // paged: CTAs (the partial slots and desc are sized for it)
+  int cluster;        // WIN_SPLIT: CTAs per query tile
   cudaStream_t stream;
 };
 
@@ -1665,6 +1766,7 @@ cudaError_t launch_attn_window(const WinLaunch& L) {
     const long long rem = groups % sms[dev];
     prm.pair_units = (int)(C::NQT == 2 && rem > 0 && 2 * rem <= sms[dev] ? groups - rem : groups);
     grid = prm.pair_units + C::NQT * (groups - prm.pair_units);
+    if (C::SPLIT) grid *= L.cluster;
     // chunks of heads whose keys and values fill about half of L2, as in attn_fwd.cuh
     prm.head_chunk = prm.BH;
     const long long kv_head_bytes = 2LL * prm.Nk * C::ROW_BYTES;
@@ -1684,7 +1786,7 @@ cudaError_t launch_attn_window(const WinLaunch& L) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
   } else {
     attr[0].id = cudaLaunchAttributeClusterDimension;  // work stealing asks for whole clusters
-    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.x = C::SPLIT ? L.cluster : 1;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
   }
@@ -1694,5 +1796,9 @@ cudaError_t launch_attn_window(const WinLaunch& L) {
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
+
+// How many WIN_SPLIT clusters of n CTAs (2, 4 or 8) run at once on a device
+// (GB300: 76, 36 and 15, as clusters do not cross its GPCs).
+int window_clusters(int dev, int n);
 
 }  // namespace fa

@@ -2,7 +2,10 @@
 #include "attn_window.cuh"
 
 namespace fa {
-template cudaError_t launch_attn_window<kFP16, 64, false>(const WinLaunch&);
-template cudaError_t launch_attn_window<kFP16, 128, false>(const WinLaunch&);
-template cudaError_t launch_attn_window<kFP16, 256, false>(const WinLaunch&);
+template cudaError_t launch_attn_window<kFP16, 64, false, WIN_PAIR>(const WinLaunch&);
+template cudaError_t launch_attn_window<kFP16, 128, false, WIN_PAIR>(const WinLaunch&);
+template cudaError_t launch_attn_window<kFP16, 256, false, WIN_ONE>(const WinLaunch&);
+template cudaError_t launch_attn_window<kFP16, 64, false, WIN_SPLIT>(const WinLaunch&);
+template cudaError_t launch_attn_window<kFP16, 128, false, WIN_SPLIT>(const WinLaunch&);
+template cudaError_t launch_attn_window<kFP16, 256, false, WIN_SPLIT>(const WinLaunch&);
 }  // namespace fa

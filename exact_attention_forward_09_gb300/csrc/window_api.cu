@@ -20,6 +20,9 @@ namespace fa {
   FA_EXTERN_WINDOW(E, 64, false, WIN_PAIR)  \
   FA_EXTERN_WINDOW(E, 128, false, WIN_PAIR) \
   FA_EXTERN_WINDOW(E, 256, false, WIN_ONE)  \
+  FA_EXTERN_WINDOW(E, 64, false, WIN_SPLIT)  \
+  FA_EXTERN_WINDOW(E, 128, false, WIN_SPLIT) \
+  FA_EXTERN_WINDOW(E, 256, false, WIN_SPLIT) \
   FA_EXTERN_WINDOW(E, 64, true, WIN_FEW2)   \
   FA_EXTERN_WINDOW(E, 64, true, WIN_ONE)    \
   FA_EXTERN_WINDOW(E, 64, true, WIN_PAIR)   \
@@ -52,9 +55,15 @@ float log2_scale(float scale) {
 
 template <int ELEM>
 fa_status launch_dense(const fa::WinLaunch& L, int64_t d) {
-  const cudaError_t e = d == 64    ? fa::launch_attn_window<ELEM, 64, false, fa::WIN_PAIR>(L)
-                        : d == 128 ? fa::launch_attn_window<ELEM, 128, false, fa::WIN_PAIR>(L)
-                                   : fa::launch_attn_window<ELEM, 256, false, fa::WIN_ONE>(L);
+  cudaError_t e;
+  if (L.cluster > 1)
+    e = d == 64    ? fa::launch_attn_window<ELEM, 64, false, fa::WIN_SPLIT>(L)
+        : d == 128 ? fa::launch_attn_window<ELEM, 128, false, fa::WIN_SPLIT>(L)
+                   : fa::launch_attn_window<ELEM, 256, false, fa::WIN_SPLIT>(L);
+  else
+    e = d == 64    ? fa::launch_attn_window<ELEM, 64, false, fa::WIN_PAIR>(L)
+        : d == 128 ? fa::launch_attn_window<ELEM, 128, false, fa::WIN_PAIR>(L)
+                   : fa::launch_attn_window<ELEM, 256, false, fa::WIN_ONE>(L);
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -169,6 +178,14 @@ fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, fl
   L.prm.Nk = (int)Nk;
   L.prm.BH = (int)(B * Hq);
   L.stream = stream;
+  // few query tiles over some key tiles: a cluster for each, as large as all run
+  // at once, a key tile and more per CTA (see WinForm; below 512 keys the join
+  // takes what the split gives)
+  const int64_t tiles = B * Hq * ((Nq + fa::kBM - 1) / fa::kBM);
+  int64_t reach = L.prm.window + (int64_t)L.prm.sinks + fa::kBM;  // keys a query tile sees, and what its edges add
+  if (reach > Nk) reach = Nk;
+  for (int c = 8; c > 1 && L.cluster == 0; c /= 2)
+    if (reach >= 512 && reach >= c * fa::kBN && tiles <= fa::window_clusters(dev, c)) L.cluster = c;
   return dtype == FA_DTYPE_BF16 ? launch_dense<fa::kBF16>(L, d) : launch_dense<fa::kFP16>(L, d);
 }
 
