@@ -506,7 +506,8 @@ typedef struct {
  *              fa_paged_workspace_bytes(d) bytes; overwritten; calls sharing
  *              it must not overlap on the GPU (two captured graphs included)
  * Rows of the cache behind a sequence's end, and pages it does not see, may
- * hold anything (NaN included).  Two kernels on `stream`, no allocation.  The
+ * hold anything (NaN included); an infinity in a value row that is seen may
+ * reach its column of O as NaN.  Two kernels on `stream`, no allocation.  The
  * result of one sequence may differ in its last bits with the rest of the
  * batch (the work is cut evenly over the GPU and the pieces are joined), but
  * is the same from run to run.
