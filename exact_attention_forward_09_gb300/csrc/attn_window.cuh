@@ -128,11 +128,12 @@ struct WinCfg {
   static constexpr int SOFTMAX_WARPS = 4 * NQT;
   static constexpr int MMA_WARP = SOFTMAX_WARPS;
   static constexpr int LOAD_WARP = SOFTMAX_WARPS + 1;
-  // paged, one CTA per SM: a second load warp takes the V tiles.  A box is one
-  // page's rows of one 128-byte column chunk, and a warp issues one about every
-  // 80 clocks: at 16-token pages a K and a V tile of d = 128 are 32 boxes, as
-  // long to issue as the tiles' arithmetic takes (chunks over 16-token pages:
-  // 652 -> 590 us for 4 x 2048 new tokens over 4000 to 10000 keys).
+  // paged: a second load warp takes the V tiles.  A box is one page's rows of
+  // one 128-byte column chunk, and a warp issues one about every 80 clocks: at
+  // 16-token pages a K and a V tile of d = 128 are 32 boxes, as long to issue
+  // as the tiles' arithmetic takes (chunks over 16-token pages: 652 -> 590 us
+  // for 4 x 2048 new tokens over 4000 to 10000 keys).  Two CTAs per SM at d = 64
+  // do without: half the boxes, and registers for no more warps.
   static constexpr bool V_WARP = PAGED && (OCC == 1 || D == 128);
   static constexpr int LOADV_WARP = V_WARP ? LOAD_WARP + 1 : -1;
   static constexpr int UNIT_READERS = SOFTMAX_WARPS + 1 + (V_WARP ? 1 : 0);  // warps that release a unit's slot

@@ -226,6 +226,7 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   fa::WinLaunch L;
   std::memset(&L, 0, sizeof(L));
   const int64_t g = Hq / Hkv;
+  if (max_q < T && max_q * B < T) max_q = 0;  // too low for so many tokens: not a hint to size units by
   int64_t tpt = fa::kBM / g;  // tokens whose g heads fit a query tile
   if (max_q > 0 && max_q < tpt) tpt = max_q;
   // The form (see WinForm).  Few rows: no sequence brings more than their
