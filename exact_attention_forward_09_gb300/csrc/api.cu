@@ -881,6 +881,7 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, c
     L.prm.sink_tiles = w.sink_tiles;
     L.prm.sink_split = w.split;
     L.prm.tile_split = w.tile_split;
+    L.prm.split_kt = w.split_kt;
     if (w.part_bytes > 0) L.prm.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (need - w.part_bytes));
     if (d == 64) e = f16 ? fa::launch_attn_bwd<1, 64, true, true>(L) : fa::launch_attn_bwd<0, 64, true, true>(L);
     else e = f16 ? fa::launch_attn_bwd<1, 128, true, true>(L) : fa::launch_attn_bwd<0, 128, true, true>(L);

@@ -38,9 +38,10 @@
 // tile's walk ends with the last query whose window reaches it; the tiles
 // that hold a sink are seen by every later query, so their walk is shared out
 // over several CTAs that start first and leave fp32 dK and dV parts
-// (BwdWindow), which a small kernel sums in a fixed order.  The other tiles'
-// walks, of all query heads of a group, are shared out likewise where the
-// tiles are too few to fill the GPU.
+// (BwdWindow), which a small kernel sums in a fixed order.  The walks of the
+// other tiles, or of the last of them, over all query heads of a group, are
+// shared out likewise where whole ones would leave much of the GPU idle.
+#include <cmath>
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -216,7 +217,8 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
   int bkv, kt;
   int part = -1;  // WIN: which share of the tile's steps (-1: all)
   if constexpr (WIN) {
-    // the shares of the sink tiles first, then those of the other tiles in order
+    // the shares of the sink tiles first, then the whole tiles in order, then
+    // the shares of the last ones
     const int sink_ctas = prm.sink_tiles * prm.sink_split * prm.BHkv;
     int x = (int)blockIdx.x;
     bkv = x % prm.BHkv;
@@ -225,9 +227,12 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
       kt = x / prm.sink_split;
       if (prm.sink_split > 1) part = x % prm.sink_split;
     } else {
-      x = (x - sink_ctas) / prm.BHkv;
-      kt = prm.sink_tiles + x / prm.tile_split;
-      if (prm.tile_split > 1) part = x % prm.tile_split;
+      kt = prm.sink_tiles + (x - sink_ctas) / prm.BHkv;
+      if (kt >= prm.split_kt) {
+        x = kt - prm.split_kt;
+        kt = prm.split_kt + x / prm.tile_split;
+        part = x % prm.tile_split;
+      }
     }
   } else if constexpr (CAUSAL) {
     kt = (int)blockIdx.x / prm.BHkv;
@@ -574,7 +579,7 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
         const size_t slot =
             kt < prm.sink_tiles
                 ? ((size_t)kt * prm.BHkv + bkv) * prm.sink_split + part
-                : bwd_sink_parts(prm) + ((size_t)(kt - prm.sink_tiles) * prm.BHkv + bkv) * prm.tile_split + part;
+                : bwd_sink_parts(prm) + ((size_t)(kt - prm.split_kt) * prm.BHkv + bkv) * prm.tile_split + part;
         float* dst = prm.part + ((slot * 2 + (cg ? 0 : 1)) * kBK + r) * D;
         const uint32_t col = cg ? C::COL_DK : C::COL_DV;
 #pragma unroll 1
@@ -846,12 +851,15 @@ __global__ void __launch_bounds__(256) bwd_window_finish_kernel(const BwdParams 
   const int row = (int)(x % kBK);
   const int which = (int)(x / kBK % 2);                     // 0: dK, 1: dV
   const long long unit = x / (2 * kBK);                     // shared tile * BHkv + bkv
-  const long long kt = unit / prm.BHkv + (prm.sink_split > 1 ? 0 : prm.sink_tiles), bkv = unit % prm.BHkv;
+  const long long bkv = unit % prm.BHkv;
+  long long kt = unit / prm.BHkv;
+  const int sink_tiles = prm.sink_split > 1 ? prm.sink_tiles : 0;
+  if (kt >= sink_tiles) kt += prm.split_kt - sink_tiles;
   const long long key = kt * kBK + row;
   if (key >= prm.Nk) return;
   const int shares = kt < prm.sink_tiles ? prm.sink_split : prm.tile_split;
   const long long slot = kt < prm.sink_tiles ? (kt * prm.BHkv + bkv) * shares
-                                             : (long long)bwd_sink_parts(prm) + ((kt - prm.sink_tiles) * prm.BHkv + bkv) * shares;
+                                             : (long long)bwd_sink_parts(prm) + ((kt - prm.split_kt) * prm.BHkv + bkv) * shares;
   float acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.0f;
@@ -902,7 +910,8 @@ cudaError_t launch_attn_bwd(const BwdLaunch& L) {
   const long long nkt = (L.prm.Nk + kBK - 1) / kBK;
   long long ctas = (long long)L.prm.BHkv * nkt;
   if constexpr (WIN)
-    ctas = L.prm.BHkv * ((long long)L.prm.sink_tiles * L.prm.sink_split + (nkt - L.prm.sink_tiles) * L.prm.tile_split);
+    ctas = L.prm.BHkv * ((long long)L.prm.sink_tiles * L.prm.sink_split + (L.prm.split_kt - L.prm.sink_tiles) +
+                         (nkt - L.prm.split_kt) * L.prm.tile_split);
   if constexpr (WIN) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas, 1, 1);
@@ -949,6 +958,7 @@ BwdWindow bwd_window_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_
   w.sinks = (int)(sinks < Nk ? sinks : Nk);
   w.sink_tiles = (w.sinks + kBK - 1) / kBK;
   w.split = w.tile_split = 1;
+  w.split_kt = (int)((Nk + kBK - 1) / kBK);
   w.part_bytes = 0;
   if (Nq == 0) return w;
   const int64_t bq = bwd_step_rows(d), nqt = (Nq + bq - 1) / bq, grp = Hq / Hkv;
@@ -956,22 +966,40 @@ BwdWindow bwd_window_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_
   int64_t usual = (kBK - 1 + w.window + bq - 1) / bq + 1;      // steps of such a tile and head
   if (usual > nqt) usual = nqt;
   usual *= grp;
-  // Shares of the tiles without sinks: what a model of the time asks for, in
-  // steps: waves of shares, each of so many steps and what a CTA takes to start
-  // and to end, and the parts' way to memory and back.  Whole call with the
-  // forward, one share and shared: 4096 tokens, 16/1 heads, d = 128, window 1024
-  // 455 and 173 us; 1023 tokens, 32/4 heads, window 977 206 and 84.  (A window
-  // over everything stays fa_bwd bit for bit, and so unshared.)
+  // Shares of the tiles without sinks, of all or of those behind whole waves:
+  // what a model of the time asks for, in steps: CTAs in their order on SMs as
+  // these come free, each of so many steps and what it takes to start and end,
+  // and the parts' way to memory and back.  Whole call with the forward, one
+  // share and shared: 4096 tokens, 16/1 heads, d = 128, window 1024 455 and 173
+  // us; 1023 tokens, 32/4 heads, window 977 206 and 84; the last 48 of 200 tiles
+  // (2 x 3100 tokens, 16/4 heads, window 700) 216 and 187.  (A window over
+  // everything stays fa_bwd bit for bit, and so unshared.)
   const int64_t sms = 152, most_parts = 1024, bhkv = B * Hkv;
-  const int64_t most_shares = w.window < Nk ? 16 : 1;
-  double best = 0.0;
-  for (int64_t n = 1; n <= most_shares && n <= usual && (n == 1 || n * tiles * bhkv <= most_parts); ++n) {
-    const int64_t ctas = n * tiles * bhkv;
-    const double t = (double)((ctas + sms - 1) / sms) * ((double)((usual + n - 1) / n) + 3.0) +
-                     (n > 1 ? 2.0 + (double)ctas * d / 8192.0 : 0.0);
-    if (n == 1 || t < 0.9 * best) {
-      best = t;
-      w.tile_split = (int)n;
+  const double whole = (double)usual + 3.0;
+  auto time_of = [&](int64_t u, int64_t n) {  // u whole tiles, the others in n shares
+    const int64_t full = u * bhkv / sms, over = u * bhkv % sms, parts = (tiles - u) * bhkv * n;
+    if (parts == 0) return (double)(full + (over > 0)) * whole;
+    // rounds of shares on SMs of which `over` are still busy with a whole tile
+    const double share = (double)((usual + n - 1) / n) + 3.0;
+    double t = share * std::ceil(((double)parts + (double)over * whole / share) / (double)sms);
+    if (over > 0 && t < whole) t = whole;
+    return (double)full * whole + t + 2.0 + (double)parts * d / 8192.0;
+  };
+  w.split_kt = w.sink_tiles + (int)tiles;
+  if (w.window < Nk) {
+    double best = 0.9 * time_of(tiles, 1);
+    for (int k = 0; k < 3; ++k) {
+      // all tiles shared, or those behind the last or the last but one whole wave
+      const int64_t waves = tiles * bhkv / sms - (k - 1);
+      const int64_t u = k == 0 ? 0 : waves * sms / bhkv;
+      if (k > 0 && (waves < 1 || u >= tiles)) continue;
+      for (int64_t n = 2; n <= 16 && n <= usual && (tiles - u) * bhkv * n <= most_parts; ++n) {
+        const double t = time_of(u, n);
+        if (t >= best) continue;
+        best = 0.95 * t;
+        w.tile_split = (int)n;
+        w.split_kt = w.sink_tiles + (int)u;
+      }
     }
   }
   if (w.sink_tiles > 0) {
@@ -984,7 +1012,7 @@ BwdWindow bwd_window_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_
     if (split > most) split = most;
     w.split = (int)(split < 1 ? 1 : split);
   }
-  const int64_t parts = (w.split > 1 ? w.sink_tiles * w.split : 0) + (w.tile_split > 1 ? tiles * w.tile_split : 0);
+  const int64_t parts = (w.split > 1 ? w.sink_tiles * w.split : 0) + (w.sink_tiles + tiles - w.split_kt) * w.tile_split;
   w.part_bytes = (size_t)parts * bhkv * 2 * kBK * d * 4;
   return w;
 }
@@ -994,7 +1022,7 @@ cudaError_t launch_bwd_window_finish(const BwdParams& prm, void* dq, long long e
   const long long n8 = elems / 8;
   const int conv = (int)stride_grid(n8);
   const long long nkt = (prm.Nk + kBK - 1) / kBK;
-  const long long shared = (prm.sink_split > 1 ? prm.sink_tiles : 0) + (prm.tile_split > 1 ? nkt - prm.sink_tiles : 0);
+  const long long shared = (prm.sink_split > 1 ? prm.sink_tiles : 0) + (nkt - prm.split_kt);
   const long long sum = shared * prm.BHkv * 2 * kBK / 8;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(conv + sum), 1, 1);

@@ -25,19 +25,22 @@ struct BwdParams {
   int drop_step;       // test hook: step whose Q/dO stage CTA 0 never fills (-1: none)
   // sliding window with sinks (the WIN instances): see BwdWindow
   int window, sinks;
-  int sink_tiles, sink_split, tile_split;
+  int sink_tiles, sink_split;
+  int split_kt, tile_split;  // tiles from split_kt on in tile_split (>= 2) shares
   // sink_split > 1: [sink_tiles][BHkv][sink_split][dK, dV][128][D] fp32, then
-  // tile_split > 1: [other tiles][BHkv][tile_split][dK, dV][128][D]
+  // [tiles from split_kt on][BHkv][tile_split][dK, dV][128][D]
   float* part;
 };
 
 // How the windowed backward shares out its key tiles' query steps, over CTAs
 // that leave fp32 dK and dV to be summed.  The tiles that hold a sink are seen
 // by every query from their first key on, the others by about window / 128 + 1
-// query tiles: `split` shares of each of the first, `tile_split` of the others.
+// query tiles: `split` shares of each of the first, `tile_split` of the others
+// from tile split_kt on.
 struct BwdWindow {
   int window, sinks;
-  int sink_tiles, split, tile_split;
+  int sink_tiles, split;
+  int split_kt, tile_split;
   size_t part_bytes;
 };
 BwdWindow bwd_window_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int d, int64_t window,

@@ -35,6 +35,8 @@ CASES = [
     (1, 24, 1, 513, 513, 300, 260),     # three sink tiles
     (1, 24, 1, 513, 513, 300, 513),     # every tile a sink tile
     (3, 14, 2, 300, 321, 250, 0),
+    (8, 64, 8, 384, 384, 380, 0),       # whole tiles first, the others shared
+    (8, 64, 8, 640, 640, 600, 130),     # with sink tiles before them
     (1, 16, 1, 256, 256, 256, 0),       # a window over everything: not shared
 ]
 
