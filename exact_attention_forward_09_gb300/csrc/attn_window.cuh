@@ -80,7 +80,13 @@ namespace fa {
 // of so few query tiles that most SMs would idle.  (d = 128, 8/2 heads over 8000
 // keys without a window: 1 query 81.4 -> 14.5 us, 100 82.0 -> 16.5, 1000 82.0 ->
 // 38.7; 12 heads, window 500, 1 and 100 queries: 13.4 -> 9.4, 15.4 -> 10.8.)
-enum WinForm { WIN_FEW, WIN_FEW2, WIN_ONE, WIN_PAIR, WIN_SPLIT };
+// WIN_TWO (dense, d = 64): two CTAs of one query tile per SM, for short windows,
+// whose units' starts and ends pass while the other CTA works (2 x 4096 tokens,
+// 16/4 heads, window 128, 256, 512, 1024: 32.2 -> 28.0, 37.5 -> 33.0, 42.7 ->
+// 41.3, 56.3 -> 56.6 us; 64 x 128 tokens, 8 heads 16.1 -> 11.0), where there is
+// more than one query tile per SM (72 tiles of 1025 tokens: +1 us of 9).  At d =
+// 128 it costs 5 to 25%: twice the key tiles from L2, and half the ring each.
+enum WinForm { WIN_FEW, WIN_FEW2, WIN_ONE, WIN_PAIR, WIN_SPLIT, WIN_TWO };
 constexpr int few_rows(int d, int form) { return form == WIN_FEW2 && d == 128 ? 8 : 16; }
 
 template <int ELEM, int D, bool PAGED, int FORM = (D <= 128 ? WIN_PAIR : WIN_ONE)>
@@ -97,7 +103,8 @@ struct WinCfg {
   static constexpr bool ALT = PAIR || FORM == WIN_FEW2 || (D == 64 && !SPLIT);             // one S buffer per query tile; ring K0 V0 K1 V1 ...
   static constexpr int OCC = ALT && !PAIR ? 2 : 1;         // CTAs per SM
   static_assert(!PAIR || D <= 128, "two query tiles of d = 256 exceed tensor memory");
-  static_assert((OCC == 1 && !FEW) || PAGED, "dense calls use pairs");
+  static_assert((OCC == 1 && !FEW) || PAGED || FORM == WIN_TWO, "a paged form");
+  static_assert(FORM != WIN_TWO || (!PAGED && D == 64), "dense calls at d = 64");
   static_assert(!SPLIT || !PAGED, "paged units are cut along the line of work");
   static constexpr int FEW_ROWS = few_rows(D, FORM);
   static constexpr int ML_BYTES = FEW ? 4 * FEW_ROWS * 8 : (SPLIT ? kBM * 8 : 0);

@@ -5,6 +5,7 @@ namespace fa {
 template cudaError_t launch_attn_window<kBF16, 64, false, WIN_PAIR>(const WinLaunch&);
 template cudaError_t launch_attn_window<kBF16, 128, false, WIN_PAIR>(const WinLaunch&);
 template cudaError_t launch_attn_window<kBF16, 256, false, WIN_ONE>(const WinLaunch&);
+template cudaError_t launch_attn_window<kBF16, 64, false, WIN_TWO>(const WinLaunch&);
 template cudaError_t launch_attn_window<kBF16, 64, false, WIN_SPLIT>(const WinLaunch&);
 template cudaError_t launch_attn_window<kBF16, 128, false, WIN_SPLIT>(const WinLaunch&);
 template cudaError_t launch_attn_window<kBF16, 256, false, WIN_SPLIT>(const WinLaunch&);

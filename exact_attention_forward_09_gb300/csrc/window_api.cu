@@ -20,6 +20,7 @@ namespace fa {
   FA_EXTERN_WINDOW(E, 64, false, WIN_PAIR)  \
   FA_EXTERN_WINDOW(E, 128, false, WIN_PAIR) \
   FA_EXTERN_WINDOW(E, 256, false, WIN_ONE)  \
+  FA_EXTERN_WINDOW(E, 64, false, WIN_TWO)    \
   FA_EXTERN_WINDOW(E, 64, false, WIN_SPLIT)  \
   FA_EXTERN_WINDOW(E, 128, false, WIN_SPLIT) \
   FA_EXTERN_WINDOW(E, 256, false, WIN_SPLIT) \
@@ -54,16 +55,19 @@ float log2_scale(float scale) {
 }
 
 template <int ELEM>
-fa_status launch_dense(const fa::WinLaunch& L, int64_t d) {
-  cudaError_t e;
-  if (L.cluster > 1)
-    e = d == 64    ? fa::launch_attn_window<ELEM, 64, false, fa::WIN_SPLIT>(L)
-        : d == 128 ? fa::launch_attn_window<ELEM, 128, false, fa::WIN_SPLIT>(L)
-                   : fa::launch_attn_window<ELEM, 256, false, fa::WIN_SPLIT>(L);
-  else
-    e = d == 64    ? fa::launch_attn_window<ELEM, 64, false, fa::WIN_PAIR>(L)
-        : d == 128 ? fa::launch_attn_window<ELEM, 128, false, fa::WIN_PAIR>(L)
-                   : fa::launch_attn_window<ELEM, 256, false, fa::WIN_ONE>(L);
+fa_status launch_dense(const fa::WinLaunch& L, int64_t d, int form) {
+  cudaError_t e = cudaErrorInvalidValue;
+  if (d == 64) {
+    if (form == fa::WIN_SPLIT) e = fa::launch_attn_window<ELEM, 64, false, fa::WIN_SPLIT>(L);
+    if (form == fa::WIN_TWO) e = fa::launch_attn_window<ELEM, 64, false, fa::WIN_TWO>(L);
+    if (form == fa::WIN_PAIR) e = fa::launch_attn_window<ELEM, 64, false, fa::WIN_PAIR>(L);
+  } else if (d == 128) {
+    if (form == fa::WIN_SPLIT) e = fa::launch_attn_window<ELEM, 128, false, fa::WIN_SPLIT>(L);
+    if (form == fa::WIN_PAIR) e = fa::launch_attn_window<ELEM, 128, false, fa::WIN_PAIR>(L);
+  } else {
+    if (form == fa::WIN_SPLIT) e = fa::launch_attn_window<ELEM, 256, false, fa::WIN_SPLIT>(L);
+    if (form == fa::WIN_ONE) e = fa::launch_attn_window<ELEM, 256, false, fa::WIN_ONE>(L);
+  }
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
@@ -186,7 +190,10 @@ fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, fl
   if (reach > Nk) reach = Nk;
   for (int c = 8; c > 1 && L.cluster == 0; c /= 2)
     if (reach >= 512 && reach >= c * fa::kBN && tiles <= fa::window_clusters(dev, c)) L.cluster = c;
-  return dtype == FA_DTYPE_BF16 ? launch_dense<fa::kBF16>(L, d) : launch_dense<fa::kFP16>(L, d);
+  int form = d == 256 ? fa::WIN_ONE : fa::WIN_PAIR;
+  if (d == 64 && reach <= 6 * fa::kBN && tiles > fa::internal_sm_count(dev)) form = fa::WIN_TWO;
+  if (L.cluster > 0) form = fa::WIN_SPLIT;
+  return dtype == FA_DTYPE_BF16 ? launch_dense<fa::kBF16>(L, d, form) : launch_dense<fa::kFP16>(L, d, form);
 }
 
 fa_status fa_paged_workspace_bytes(int64_t d, size_t* bytes) {
