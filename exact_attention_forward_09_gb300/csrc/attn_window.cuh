@@ -1431,6 +1431,33 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
           }
           break;
         }
+        if constexpr (PAGED && FORM == WIN_ONE && D == 64) {
+          if (wq * 32 >= rows) {
+            // None of this warp's rows exist: it keeps step with the others and
+            // zeroes its rows of V tiles (see below), whatever P then holds, and
+            // leaves its sub-partition to the other CTA (64 sequences of 8 tokens
+            // over 500 to 3000 keys, 32/8 heads 73 -> 65 us; at d = 128, with one
+            // CTA per SM, it gains nothing).
+            for (int j = 0; j < n && ok; ++j, ++sc) {
+              ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[0], (uint32_t)(sc & 1), abort_flag, prm.err));
+              if (!ok) break;
+              const int li = r0 + j, col0 = (li < w.ns ? li : li + w.skip) * kBN;
+              const bool gap = w.lo > prm.sinks && col0 < w.lo && col0 + kBN > prm.sinks;
+              if (col0 + kBN > w.nk || gap) {
+                const int key = col0 + r_in;
+                const bool dead = key >= w.nk || (key < w.lo && key >= prm.sinks);
+                ok = clear_v_row<C, Bars>(bars, smem_u32(smem + C::OFF_RING) + r_in * 128, ring0 + v_at(j, n), dead, prm.err);
+                if (!ok) break;
+              }
+              mbar_arrive(&bars->p_full[0][0]);
+              mbar_arrive(&bars->p_full[0][1]);
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->o_full[0], (uint32_t)(oc & 1), abort_flag, prm.err));
+            ++oc;
+            break;
+          }
+        }
         int l = C::NQT == 2 ? mine.from(r0) : r0;  // list index
         int j = 0;                                 // tiles done by this query tile
         if (w.narrow && l == 0) {
