@@ -841,7 +841,12 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, c
   float* vecs = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (rows * d * 4 + 255) / 256 * 256);
   const bool f16 = dtype == FA_DTYPE_FP16;
   const long long nrec = fa::bwd_records_per_head(Nq, (int)d);
-  if (fa::launch_bwd_prep(o, dout, lse, vecs, dq_acc, (long long)(B * Hq), (int)Nq, (int)nrec, (int)d, f16,
+  fa::BwdEarly early = {};
+  if (window > 0 && window < Nk && Nk - Nq < 32 && B * Hq <= (1 << 24)) {
+    early = {(int)(B * Hq * 4), q, k, v, dout, (int)Hq, (int)Hkv, (int)Nk, (int)window, (int)(sinks < Nk ? sinks : Nk),
+             (float)((double)scale * 1.4426950408889634)};
+  }
+  if (fa::launch_bwd_prep(o, dout, lse, vecs, dq_acc, (long long)(B * Hq), (int)Nq, (int)nrec, (int)d, f16, early,
                           stream) != cudaSuccess)
     return FA_ERR_CUDA;
 

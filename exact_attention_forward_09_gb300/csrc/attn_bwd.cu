@@ -738,18 +738,67 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
 template <int D>
 constexpr int PREP_ROWS = D == 64 ? 8 : 4;
 
+// two 16-bit elements in fp32
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t x) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&x));
+  else return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x));
+}
+
+// D of a row at position p < 32 as sum_j P_j dP_j over its keys (lane = key).
+template <int D, bool F16>
+__device__ __forceinline__ float exact_d(const BwdEarly& e, long long row, long long bhkv, int p, float nlse) {
+  const int j = threadIdx.x & 31;
+  float s = 0.0f, dp = 0.0f;
+  const bool sees = j <= p && (j > p - e.window || j < e.sinks);
+  if (sees) {
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(e.q) + row * D);
+    const uint4* g = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(e.dout) + row * D);
+    const size_t key = ((size_t)bhkv * e.Nk + j) * D;
+    const uint4* k = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(e.k) + key);
+    const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(e.v) + key);
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 a = q[c], b = k[c], x = g[c], y = v[c];
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+      const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float2 a2 = unpack2<F16>(aw[i]), b2 = unpack2<F16>(bw[i]), x2 = unpack2<F16>(xw[i]), y2 = unpack2<F16>(yw[i]);
+        s = fmaf(a2.x, b2.x, fmaf(a2.y, b2.y, s));
+        dp = fmaf(x2.x, y2.x, fmaf(x2.y, y2.y, dp));
+      }
+    }
+  }
+  float sum = sees ? exp2f(fmaf(s, e.scale_log2, nlse)) * dp : 0.0f;
+#pragma unroll
+  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+  return sum;
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(256) bwd_prep_kernel(const void* __restrict__ o, const void* __restrict__ dout,
                                                        const float* __restrict__ lse, float* __restrict__ vecs,
                                                        float* __restrict__ dq_acc, long long prow_total, int nq,
-                                                       int nrec) {
+                                                       int nrec, const BwdEarly early) {
   constexpr int R = PREP_ROWS<D>;
   constexpr int EPL = D / 32;  // elements per lane
   using Vec = std::conditional_t<EPL == 4, uint2, uint32_t>;
   static_assert(sizeof(Vec) == 2 * EPL, "a lane's elements of a row");
   const int lane = threadIdx.x & 31;
+  if (blockIdx.x < early.blocks) {
+    // the first blocks: a warp for each row at a position below 32
+    const long long x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const long long bhq = x / 32;
+    const int p = (int)(x % 32), qp = p - (early.Nk - nq);
+    if (qp < 0 || qp >= nq) return;
+    const long long bhkv = bhq / early.Hq * early.Hkv + bhq % early.Hq / (early.Hq / early.Hkv);
+    const float dsum = exact_d<D, F16>(early, bhq * nq + qp, bhkv, p, -lse[bhq * nq + qp] * 1.4426950408889634f);
+    if (lane == 0) vecs[(bhq * nrec + qp / kRec) * (2 * kRec) + kRec + qp % kRec] = -dsum;
+    return;
+  }
   // (records are whole 64-row blocks, so a warp's rows are of one head)
-  const long long prow = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * R;
+  const long long prow = ((long long)(blockIdx.x - early.blocks) * 8 + (threadIdx.x >> 5)) * R;
   if (prow >= prow_total) return;
   const long long bhq = prow / ((long long)nrec * kRec);
   const int qp0 = (int)(prow % ((long long)nrec * kRec));  // first row within the head, padded
@@ -794,7 +843,8 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const void* __restrict__ 
     for (int m = 16; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
     if (lane == 0) {
       rec[0] = (l[r] == -INFINITY) ? -INFINITY : -l[r] * 1.4426950408889634f;  // a row with no key: P = 0
-      rec[kRec] = -acc;
+      const int p = qp + early.Nk - nq;
+      if (early.blocks == 0 || p < 0 || p >= 32) rec[kRec] = -acc;  // (else the first blocks')
     }
     float* z = dq_acc + (size_t)(row0 + r) * D + lane * EPL;
     if constexpr (EPL == 2) *reinterpret_cast<float2*>(z) = make_float2(0.0f, 0.0f);
@@ -1051,16 +1101,17 @@ cudaError_t launch_bwd_window_finish(const BwdParams& prm, void* dq, long long e
 }
 
 cudaError_t launch_bwd_prep(const void* o, const void* dout, const float* lse, float* vecs, float* dq_acc,
-                            long long bhq, int nq, int nrec, int d, bool f16, cudaStream_t stream) {
+                            long long bhq, int nq, int nrec, int d, bool f16, const BwdEarly& early,
+                            cudaStream_t stream) {
   const long long prows = bhq * nrec * kRec;
   const long long per_block = 8LL * (d == 64 ? PREP_ROWS<64> : PREP_ROWS<128>);
-  const unsigned blocks = (unsigned)((prows + per_block - 1) / per_block);
+  const unsigned blocks = (unsigned)((prows + per_block - 1) / per_block) + (unsigned)early.blocks;
   if (d == 64) {
-    if (f16) bwd_prep_kernel<64, true><<<blocks, 256, 0, stream>>>(o, dout, lse, vecs, dq_acc, prows, nq, nrec);
-    else bwd_prep_kernel<64, false><<<blocks, 256, 0, stream>>>(o, dout, lse, vecs, dq_acc, prows, nq, nrec);
+    if (f16) bwd_prep_kernel<64, true><<<blocks, 256, 0, stream>>>(o, dout, lse, vecs, dq_acc, prows, nq, nrec, early);
+    else bwd_prep_kernel<64, false><<<blocks, 256, 0, stream>>>(o, dout, lse, vecs, dq_acc, prows, nq, nrec, early);
   } else if (d == 128) {
-    if (f16) bwd_prep_kernel<128, true><<<blocks, 256, 0, stream>>>(o, dout, lse, vecs, dq_acc, prows, nq, nrec);
-    else bwd_prep_kernel<128, false><<<blocks, 256, 0, stream>>>(o, dout, lse, vecs, dq_acc, prows, nq, nrec);
+    if (f16) bwd_prep_kernel<128, true><<<blocks, 256, 0, stream>>>(o, dout, lse, vecs, dq_acc, prows, nq, nrec, early);
+    else bwd_prep_kernel<128, false><<<blocks, 256, 0, stream>>>(o, dout, lse, vecs, dq_acc, prows, nq, nrec, early);
   } else {
     return cudaErrorInvalidValue;
   }

@@ -64,10 +64,27 @@ cudaError_t launch_attn_bwd(const BwdLaunch& L);
 cudaError_t launch_bwd_window_finish(const BwdParams& prm, void* dq, long long elems, int d, bool f16,
                                      cudaStream_t stream);
 
-// Records of -LSE_i * log2(e) and -D_i (D_i = dO_i . O_i) for every query
-// row, padded to nrec 64-row records per head, and dq_acc := 0.
+// The first positions' D.  dO . O carries O's rounding, which dS = P (dP - D)
+// hands on to a row of few keys (with one key dS must vanish) and which
+// averages out over many.  So rows at positions below 32 take D = sum_j P_j
+// dP_j over their keys, a warp each, in blocks of their own (1025 tokens, 8
+// heads, window 200, 130 sinks: dQ's error against 64 bits 2.48e-3 -> 2.36e-3 in
+// bf16, one rounding being 1.65e-3; 1.6 us, 8 heads of 1025 rows).
+// blocks 0: dO . O everywhere (fa_bwd, and a window over everything, which
+// equals it bit for bit).
+struct BwdEarly {
+  int blocks;  // 4 per query head
+  const void *q, *k, *v, *dout;
+  int Hq, Hkv, Nk;
+  int window, sinks;
+  float scale_log2;
+};
+
+// Records of -LSE_i * log2(e) and -D_i (D_i = dO_i . O_i, see BwdEarly) for
+// every query row, padded to nrec 64-row records per head, and dq_acc := 0.
 cudaError_t launch_bwd_prep(const void* o, const void* dout, const float* lse, float* vecs, float* dq_acc,
-                            long long bhq, int nq, int nrec, int d, bool f16, cudaStream_t stream);
+                            long long bhq, int nq, int nrec, int d, bool f16, const BwdEarly& early,
+                            cudaStream_t stream);
 
 // Query rows per kernel step for head dimension d, and the records per
 // query head the kernel reads (whole steps).
