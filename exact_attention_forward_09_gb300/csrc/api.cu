@@ -826,7 +826,7 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, c
   if (!q || !o || !lse || !dout || !dq) return FA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(o) || !aligned16(lse) || !aligned16(dout) || !aligned16(dq))
     return FA_ERR_INVALID_ARG;
-  // the preprocessing kernel runs one block per 8 padded query rows
+  // the preprocessing kernel's blocks (at least 32 padded query rows each, and those of BwdFewKeys)
   if ((B * Hq * fa::bwd_records_per_head(Nq, (int)d) * 64 + 7) / 8 > 0x7fffffffLL) return FA_ERR_UNSUPPORTED;
   size_t need = 0;
   if ((st = window > 0 ? fa_bwd_window_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, window, sinks, &need)
@@ -841,12 +841,19 @@ fa_status bwd_impl(const void* q, const void* k, const void* v, const void* o, c
   float* vecs = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + (rows * d * 4 + 255) / 256 * 256);
   const bool f16 = dtype == FA_DTYPE_FP16;
   const long long nrec = fa::bwd_records_per_head(Nq, (int)d);
-  fa::BwdEarly early = {};
-  if (window > 0 && window < Nk && Nk - Nq < 32 && B * Hq <= (1 << 24)) {
-    early = {(int)(B * Hq * 4), q, k, v, dout, (int)Hq, (int)Hkv, (int)Nk, (int)window, (int)(sinks < Nk ? sinks : Nk),
-             (float)((double)scale * 1.4426950408889634)};
+  fa::BwdFewKeys few = {};
+  if (window > 0) {
+    few = fa::bwd_few_keys(B * Hq, Nq, Nk, window, sinks);
+    few.q = q;
+    few.k = k;
+    few.v = v;
+    few.dout = dout;
+    few.Hq = (int)Hq;
+    few.Hkv = (int)Hkv;
+    few.Nk = (int)Nk;
+    few.scale_log2 = (float)((double)scale * 1.4426950408889634);
   }
-  if (fa::launch_bwd_prep(o, dout, lse, vecs, dq_acc, (long long)(B * Hq), (int)Nq, (int)nrec, (int)d, f16, early,
+  if (fa::launch_bwd_prep(o, dout, lse, vecs, dq_acc, (long long)(B * Hq), (int)Nq, (int)nrec, (int)d, f16, few,
                           stream) != cudaSuccess)
     return FA_ERR_CUDA;
 

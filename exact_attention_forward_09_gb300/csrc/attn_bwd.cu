@@ -738,67 +738,142 @@ __global__ void __launch_bounds__(BwdCfg<ELEM, D, CAUSAL>::THREADS, 1)
 template <int D>
 constexpr int PREP_ROWS = D == 64 ? 8 : 4;
 
-// two 16-bit elements in fp32
+// c += A B over 16 columns of 16 keys (A) and 8 query rows (B), products exact,
+// sums in fp32: lane = 4 g + t holds keys g and g + 8 at rows 2 t and 2 t + 1.
 template <bool F16>
-__device__ __forceinline__ float2 unpack2(uint32_t x) {
-  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&x));
-  else return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&x));
+__device__ __forceinline__ void mma_16x8(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
-// D of a row at position p < 32 as sum_j P_j dP_j over its keys (lane = key).
-template <int D, bool F16>
-__device__ __forceinline__ float exact_d(const BwdEarly& e, long long row, long long bhkv, int p, float nlse) {
-  const int j = threadIdx.x & 31;
-  float s = 0.0f, dp = 0.0f;
-  const bool sees = j <= p && (j > p - e.window || j < e.sinks);
-  if (sees) {
-    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(e.q) + row * D);
-    const uint4* g = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(e.dout) + row * D);
-    const size_t key = ((size_t)bhkv * e.Nk + j) * D;
-    const uint4* k = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(e.k) + key);
-    const uint4* v = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(e.v) + key);
-#pragma unroll 4
-    for (int c = 0; c < D / 8; ++c) {
-      const uint4 a = q[c], b = k[c], x = g[c], y = v[c];
-      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-      const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
+// D = sum_j P_j dP_j of 8 NB rows of head bhq from row qp0 on (those below
+// `end`), a warp's: 16 keys at a time, over the sink keys and those from the first
+// row's window to the last row's position.  A lane's 16 bytes of a row are four
+// pairs of columns, which two MMAs take as their columns 2 t, 2 t + 1 and 2 t + 8,
+// 2 t + 9: the order of columns in a product is free.
+template <int D, bool F16, int NB>
+__device__ __forceinline__ void few_key_d(const BwdFewKeys& f, const float* __restrict__ lse, float* __restrict__ vecs,
+                                          long long bhq, int qp0, int end, int nq, int nrec) {
+  constexpr int CH = D / 32;
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const long long bhkv = bhq / f.Hq * f.Hkv + bhq % f.Hq / (f.Hq / f.Hkv);
+  const int off = f.Nk - nq;
+  uint4 q[NB][CH], x[NB][CH];
+  float nlse[NB][2], sum[NB][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 a2 = unpack2<F16>(aw[i]), b2 = unpack2<F16>(bw[i]), x2 = unpack2<F16>(xw[i]), y2 = unpack2<F16>(yw[i]);
-        s = fmaf(a2.x, b2.x, fmaf(a2.y, b2.y, s));
-        dp = fmaf(x2.x, y2.x, fmaf(x2.y, y2.y, dp));
-      }
+  for (int n = 0; n < NB; ++n) {
+    const size_t at = (size_t)(bhq * nq + min(qp0 + 8 * n + g, end - 1)) * D + 8 * t;
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      q[n][c] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(f.q) + at + 32 * c);
+      x[n][c] = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(f.dout) + at + 32 * c);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float l = lse[bhq * nq + min(qp0 + 8 * n + 2 * t + i, end - 1)];
+      nlse[n][i] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;  // (P = 0, as in the gradient kernel)
+      sum[n][i] = 0.0f;
     }
   }
-  float sum = sees ? exp2f(fmaf(s, e.scale_log2, nlse)) * dp : 0.0f;
+  const int last = min(qp0 + 8 * NB, end) - 1 + off;  // position of the last row
+  const int lo = max(0, qp0 + off - f.window + 1);
+  const int sink_tiles = (min(f.sinks, last + 1) + 15) / 16;
+  for (int kt = sink_tiles > 0 ? 0 : lo / 16; 16 * kt <= last; ++kt) {
+    if (kt >= sink_tiles && kt < lo / 16) kt = lo / 16;
+    size_t at[2];  // of the lane's two keys (one behind the last is seen by no row)
 #pragma unroll
-  for (int m = 16; m > 0; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-  return sum;
+    for (int i = 0; i < 2; ++i) at[i] = ((size_t)bhkv * f.Nk + min(16 * kt + g + 8 * i, f.Nk - 1)) * D + 8 * t;
+    float s[NB][4] = {}, dp[NB][4] = {};
+#pragma unroll
+    for (int c = 0; c < CH; ++c) {
+      uint4 a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(f.k) + at[0] + 32 * c);
+      uint4 b = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(f.k) + at[1] + 32 * c);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        mma_16x8<F16>(s[n], a.x, b.x, a.y, b.y, q[n][c].x, q[n][c].y);
+        mma_16x8<F16>(s[n], a.z, b.z, a.w, b.w, q[n][c].z, q[n][c].w);
+      }
+      a = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(f.v) + at[0] + 32 * c);
+      b = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(f.v) + at[1] + 32 * c);
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        mma_16x8<F16>(dp[n], a.x, b.x, a.y, b.y, x[n][c].x, x[n][c].y);
+        mma_16x8<F16>(dp[n], a.z, b.z, a.w, b.w, x[n][c].z, x[n][c].w);
+      }
+    }
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = 16 * kt + g + 8 * (i >> 1), p = qp0 + 8 * n + 2 * t + (i & 1) + off;
+        if (j <= p && (j > p - f.window || j < f.sinks))
+          sum[n][i & 1] = fmaf(exp2f(fmaf(s[n][i], f.scale_log2, nlse[n][i & 1])), dp[n][i], sum[n][i & 1]);
+      }
+  }
+#pragma unroll
+  for (int n = 0; n < NB; ++n)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+#pragma unroll
+      for (int m = 4; m < 32; m <<= 1) sum[n][i] += __shfl_xor_sync(0xffffffffu, sum[n][i], m);
+      const int r = qp0 + 8 * n + 2 * t + i;
+      if (g == 0 && r < end) vecs[(bhq * nrec + r / kRec) * (2 * kRec) + kRec + r % kRec] = -sum[n][i];
+    }
 }
 
+// The preparation where every row sees few keys: a warp takes 16 rows.
 template <int D, bool F16>
-__global__ void __launch_bounds__(256) bwd_prep_kernel(const void* __restrict__ o, const void* __restrict__ dout,
+__global__ void __launch_bounds__(256, 2) bwd_prep_few_kernel(const float* __restrict__ lse, float* __restrict__ vecs,
+                                                           float* __restrict__ dq_acc, long long prow_total, int nq, int nrec,
+                                                           const BwdFewKeys few) {
+  const long long prow = ((long long)blockIdx.x * 8 + (threadIdx.x >> 5)) * 16;
+  if (prow >= prow_total) return;
+  const int lane = threadIdx.x & 31;
+  const long long bhq = prow / ((long long)nrec * kRec);
+  const int qp0 = (int)(prow % ((long long)nrec * kRec));  // (records are whole 64-row blocks: rows of one head)
+  const int rows = min(16, nq - qp0);
+  if (lane < 16) {
+    float* rec = vecs + (bhq * nrec + qp0 / kRec) * (2 * kRec) + qp0 % kRec + lane;
+    const float l = lane < rows ? lse[bhq * nq + qp0 + lane] : -INFINITY;
+    rec[0] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
+    if (lane >= rows) rec[kRec] = 0.0f;
+  }
+  if (rows <= 0) return;
+  float4* z = reinterpret_cast<float4*>(dq_acc + (size_t)(bhq * nq + qp0) * D);
+  for (int i = lane; i < rows * (D / 4); i += 32) z[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  few_key_d<D, F16, 2>(few, lse, vecs, bhq, qp0, nq, nq, nrec);
+}
+
+template <int D, bool F16, bool FEW>  // FEW: the rows of few keys among them
+__global__ void __launch_bounds__(256, 4) bwd_prep_kernel(const void* __restrict__ o, const void* __restrict__ dout,
                                                        const float* __restrict__ lse, float* __restrict__ vecs,
                                                        float* __restrict__ dq_acc, long long prow_total, int nq,
-                                                       int nrec, const BwdEarly early) {
+                                                       int nrec, const BwdFewKeys few) {
   constexpr int R = PREP_ROWS<D>;
   constexpr int EPL = D / 32;  // elements per lane
   using Vec = std::conditional_t<EPL == 4, uint2, uint32_t>;
   static_assert(sizeof(Vec) == 2 * EPL, "a lane's elements of a row");
   const int lane = threadIdx.x & 31;
-  if (blockIdx.x < early.blocks) {
-    // the first blocks: a warp for each row at a position below 32
-    const long long x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const long long bhq = x / 32;
-    const int p = (int)(x % 32), qp = p - (early.Nk - nq);
-    if (qp < 0 || qp >= nq) return;
-    const long long bhkv = bhq / early.Hq * early.Hkv + bhq % early.Hq / (early.Hq / early.Hkv);
-    const float dsum = exact_d<D, F16>(early, bhq * nq + qp, bhkv, p, -lse[bhq * nq + qp] * 1.4426950408889634f);
-    if (lane == 0) vecs[(bhq * nrec + qp / kRec) * (2 * kRec) + kRec + qp % kRec] = -dsum;
-    return;
+  if constexpr (FEW) {
+    if (blockIdx.x < few.blocks) {
+      // the first blocks: a warp for every 8 rows of few keys of a head
+      const int tiles = (few.rows + 7) / 8;
+      const long long x = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+      const long long bhq = x / tiles;
+      if (bhq < prow_total / ((long long)nrec * kRec))
+        few_key_d<D, F16, 1>(few, lse, vecs, bhq, few.first + (int)(x % tiles) * 8, few.first + few.rows, nq, nrec);
+      return;
+    }
   }
   // (records are whole 64-row blocks, so a warp's rows are of one head)
-  const long long prow = ((long long)(blockIdx.x - early.blocks) * 8 + (threadIdx.x >> 5)) * R;
+  const long long prow = ((long long)(blockIdx.x - (FEW ? few.blocks : 0)) * 8 + (threadIdx.x >> 5)) * R;
   if (prow >= prow_total) return;
   const long long bhq = prow / ((long long)nrec * kRec);
   const int qp0 = (int)(prow % ((long long)nrec * kRec));  // first row within the head, padded
@@ -843,8 +918,7 @@ __global__ void __launch_bounds__(256) bwd_prep_kernel(const void* __restrict__ 
     for (int m = 16; m > 0; m >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, m);
     if (lane == 0) {
       rec[0] = (l[r] == -INFINITY) ? -INFINITY : -l[r] * 1.4426950408889634f;  // a row with no key: P = 0
-      const int p = qp + early.Nk - nq;
-      if (early.blocks == 0 || p < 0 || p >= 32) rec[kRec] = -acc;  // (else the first blocks')
+      if (!FEW || qp < few.first || qp >= few.first + few.rows) rec[kRec] = -acc;  // (else the first blocks')
     }
     float* z = dq_acc + (size_t)(row0 + r) * D + lane * EPL;
     if constexpr (EPL == 2) *reinterpret_cast<float2*>(z) = make_float2(0.0f, 0.0f);
@@ -1031,7 +1105,7 @@ BwdWindow bwd_window_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_
   // share and shared: 4096 tokens, 16/1 heads, d = 128, window 1024 455 and 173
   // us; 1023 tokens, 32/4 heads, window 977 206 and 84; the last 48 of 200 tiles
   // (2 x 3100 tokens, 16/4 heads, window 700) 216 and 187.  (A window over
-  // everything stays fa_bwd bit for bit, and so unshared.)
+  // everything sums as fa_bwd does, bit for bit, and so unshared.)
   const int64_t sms = 152, most_parts = 1024, bhkv = B * Hkv;
   const double whole = (double)usual + 3.0;
   auto time_of = [&](int64_t u, int64_t n) {  // u whole tiles, the others in n shares
@@ -1075,6 +1149,20 @@ BwdWindow bwd_window_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_
   return w;
 }
 
+BwdFewKeys bwd_few_keys(int64_t BHq, int64_t Nq, int64_t Nk, int64_t window, int64_t sinks) {
+  constexpr int64_t kFew = 32;
+  BwdFewKeys f = {};
+  f.window = (int)(window < Nk ? window : Nk);
+  f.sinks = (int)(sinks < Nk ? sinks : Nk);
+  f.all = window <= kFew && sinks <= kFew - window;
+  const int64_t first = Nq > Nk ? Nq - Nk : 0, at = first + Nk - Nq;  // the first such row and its position
+  if (f.all || at >= kFew || first >= Nq) return f;
+  f.first = (int)first;
+  f.rows = (int)(Nq - first < kFew - at ? Nq - first : kFew - at);
+  f.blocks = (int)((BHq * ((f.rows + 7) / 8) + 7) / 8);
+  return f;
+}
+
 cudaError_t launch_bwd_window_finish(const BwdParams& prm, void* dq, long long elems, int d, bool f16,
                                      cudaStream_t stream) {
   const long long n8 = elems / 8;
@@ -1101,21 +1189,30 @@ cudaError_t launch_bwd_window_finish(const BwdParams& prm, void* dq, long long e
 }
 
 cudaError_t launch_bwd_prep(const void* o, const void* dout, const float* lse, float* vecs, float* dq_acc,
-                            long long bhq, int nq, int nrec, int d, bool f16, const BwdEarly& early,
+                            long long bhq, int nq, int nrec, int d, bool f16, const BwdFewKeys& few,
                             cudaStream_t stream) {
   const long long prows = bhq * nrec * kRec;
-  const long long per_block = 8LL * (d == 64 ? PREP_ROWS<64> : PREP_ROWS<128>);
-  const unsigned blocks = (unsigned)((prows + per_block - 1) / per_block) + (unsigned)early.blocks;
-  if (d == 64) {
-    if (f16) bwd_prep_kernel<64, true><<<blocks, 256, 0, stream>>>(o, dout, lse, vecs, dq_acc, prows, nq, nrec, early);
-    else bwd_prep_kernel<64, false><<<blocks, 256, 0, stream>>>(o, dout, lse, vecs, dq_acc, prows, nq, nrec, early);
-  } else if (d == 128) {
-    if (f16) bwd_prep_kernel<128, true><<<blocks, 256, 0, stream>>>(o, dout, lse, vecs, dq_acc, prows, nq, nrec, early);
-    else bwd_prep_kernel<128, false><<<blocks, 256, 0, stream>>>(o, dout, lse, vecs, dq_acc, prows, nq, nrec, early);
-  } else {
-    return cudaErrorInvalidValue;
+  if (d != 64 && d != 128) return cudaErrorInvalidValue;
+  if (few.all) {
+    auto go = [&](auto kern) {
+      kern<<<(unsigned)((prows + 127) / 128), 256, 0, stream>>>(lse, vecs, dq_acc, prows, nq, nrec, few);
+      return cudaGetLastError();
+    };
+    if (d == 64) return f16 ? go(bwd_prep_few_kernel<64, true>) : go(bwd_prep_few_kernel<64, false>);
+    return f16 ? go(bwd_prep_few_kernel<128, true>) : go(bwd_prep_few_kernel<128, false>);
   }
-  return cudaGetLastError();
+  const long long per_block = 8LL * (d == 64 ? PREP_ROWS<64> : PREP_ROWS<128>);
+  const unsigned blocks = (unsigned)((prows + per_block - 1) / per_block) + (unsigned)few.blocks;
+  auto go = [&](auto kern) {
+    kern<<<blocks, 256, 0, stream>>>(o, dout, lse, vecs, dq_acc, prows, nq, nrec, few);
+    return cudaGetLastError();
+  };
+  if (few.blocks == 0) {
+    if (d == 64) return f16 ? go(bwd_prep_kernel<64, true, false>) : go(bwd_prep_kernel<64, false, false>);
+    return f16 ? go(bwd_prep_kernel<128, true, false>) : go(bwd_prep_kernel<128, false, false>);
+  }
+  if (d == 64) return f16 ? go(bwd_prep_kernel<64, true, true>) : go(bwd_prep_kernel<64, false, true>);
+  return f16 ? go(bwd_prep_kernel<128, true, true>) : go(bwd_prep_kernel<128, false, true>);
 }
 
 cudaError_t launch_bwd_dq_convert(const float* dq_acc, void* dq, float scale, long long elems, bool f16,

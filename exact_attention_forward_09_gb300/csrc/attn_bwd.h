@@ -64,26 +64,34 @@ cudaError_t launch_attn_bwd(const BwdLaunch& L);
 cudaError_t launch_bwd_window_finish(const BwdParams& prm, void* dq, long long elems, int d, bool f16,
                                      cudaStream_t stream);
 
-// The first positions' D.  dO . O carries O's rounding, which dS = P (dP - D)
-// hands on to a row of few keys (with one key dS must vanish) and which
-// averages out over many.  So rows at positions below 32 take D = sum_j P_j
-// dP_j over their keys, a warp each, in blocks of their own (1025 tokens, 8
-// heads, window 200, 130 sinks: dQ's error against 64 bits 2.48e-3 -> 2.36e-3 in
-// bf16, one rounding being 1.65e-3; 1.6 us, 8 heads of 1025 rows).
-// blocks 0: dO . O everywhere (fa_bwd, and a window over everything, which
-// equals it bit for bit).
-struct BwdEarly {
-  int blocks;  // 4 per query head
+// The rows of few keys.  D = dO . O carries O's rounding, which dS = P (dP - D)
+// hands on to every key of a row, and which averages out over many keys only.  So
+// under a window the rows that see at most 32 keys take D = sum_j P_j dP_j over
+// them, in fp32: every row where window + sinks <= 32, in a preparation kernel of
+// its own, else those at positions below 32, in blocks of their own.
+// Relative error of dQ against 64 bits, bf16, 1000 tokens, d = 128, with dO . O and
+// so (rounding dQ alone gives 1.66e-3): two keys to a row 3.74e-3 and 2.33e-3, 30
+// and 2 sinks 2.47e-3 and 2.35e-3.  Cost: 0 within 0.5 us where only the first
+// positions are such rows; where all are, 16/4 heads x 8192 rows, window 30, 2
+// sinks, the backward takes 149 us instead of 119 (d = 64 92 instead of 81).
+// blocks 0, not all: dO . O everywhere (fa_bwd).
+struct BwdFewKeys {
+  int blocks;
+  int first, rows;  // rows first .. first + rows - 1 of every head
+  bool all;         // every row
   const void *q, *k, *v, *dout;
   int Hq, Hkv, Nk;
   int window, sinks;
   float scale_log2;
 };
+// Which rows they are (a row before position 0 sees no key, and O = 0 gives it
+// D = 0); the pointers, heads and scale are the caller's to fill in.
+BwdFewKeys bwd_few_keys(int64_t BHq, int64_t Nq, int64_t Nk, int64_t window, int64_t sinks);
 
-// Records of -LSE_i * log2(e) and -D_i (D_i = dO_i . O_i, see BwdEarly) for
+// Records of -LSE_i * log2(e) and -D_i (D_i = dO_i . O_i, see BwdFewKeys) for
 // every query row, padded to nrec 64-row records per head, and dq_acc := 0.
 cudaError_t launch_bwd_prep(const void* o, const void* dout, const float* lse, float* vecs, float* dq_acc,
-                            long long bhq, int nq, int nrec, int d, bool f16, const BwdEarly& early,
+                            long long bhq, int nq, int nrec, int d, bool f16, const BwdFewKeys& few,
                             cudaStream_t stream);
 
 // Query rows per kernel step for head dimension d, and the records per
