@@ -764,8 +764,9 @@ def quant_fp8_per_tensor_noalloc(x: torch.Tensor, signs=None, x8: torch.Tensor |
 
 
 def check_device_error(device=None):
-    """Synchronise the current stream and raise FaError if a kernel reported
-    a pipeline timeout since the last check."""
+    """Synchronise the current stream and raise FaError if a kernel reported a
+    pipeline timeout (FA_ERR_TIMEOUT), or an index out of range in device memory
+    (FA_ERR_INDEX), that no check has reported yet."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     with torch.cuda.device(dev):
         st = _lib().fa_check_device_error(torch.cuda.current_stream(dev).cuda_stream)

@@ -45,6 +45,8 @@ namespace {
 
 __device__ int g_fa_device_error;
 
+__global__ void clear_error_kernel(int* word, int bit) { atomicAnd(word, ~bit); }
+
 constexpr int kMaxDevices = 64;
 
 struct DeviceState {
@@ -971,12 +973,13 @@ fa_status fa_check_device_error(cudaStream_t stream) {
   if (st != FA_OK) return st;
   int h = 0;
   if (cudaMemcpyFromSymbol(&h, g_fa_device_error, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
-  if (h != 0) {
-    const int zero = 0;
-    if (cudaMemcpyToSymbol(g_fa_device_error, &zero, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
-    return h == fa::FA_DEVERR_INDEX ? FA_ERR_INDEX : FA_ERR_TIMEOUT;
-  }
-  return FA_OK;
+  if (h == 0) return FA_OK;
+  // one error is reported and its bit cleared; the others, and what kernels of
+  // other streams add meanwhile, stay
+  const int bit = (h & fa::FA_DEVERR_TIMEOUT) ? fa::FA_DEVERR_TIMEOUT : fa::FA_DEVERR_INDEX;
+  clear_error_kernel<<<1, 1, 0, stream>>>(err, bit);
+  if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(stream) != cudaSuccess) return FA_ERR_CUDA;
+  return bit == fa::FA_DEVERR_INDEX ? FA_ERR_INDEX : FA_ERR_TIMEOUT;
 }
 
 fa_status fa_debug_inject(int flags) {

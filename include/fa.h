@@ -573,10 +573,11 @@ const char* fa_status_string(fa_status status);
 /*
  * fa_check_device_error -- synchronises `stream`, then reports and clears the
  * library's device error word on the current device: FA_ERR_TIMEOUT if a
- * kernel gave up on a pipeline wait since the last check, FA_ERR_INDEX if a
- * kernel met an index out of range in device memory (fa_fwd_paged,
- * fa_cache_append), FA_ERR_CUDA if the synchronisation itself failed, else
- * FA_OK.
+ * kernel gave up on a pipeline wait since that was last reported, else
+ * FA_ERR_INDEX if a kernel met an index out of range in device memory
+ * (fa_fwd_paged, fa_cache_append) since that was, FA_ERR_CUDA if the
+ * synchronisation itself failed, else FA_OK.  One error is reported per call:
+ * after both kinds the next call reports the second.
  */
 fa_status fa_check_device_error(cudaStream_t stream);
 
