@@ -213,10 +213,10 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(
 
 // -------------------------------------------------------------- append --
 // All bytes: each new q, k and v row is read once and written once.  One
-// block per token: its threads are D/16 column chunks (16 columns each: the
-// two 8-column halves of 8 rotary pairs) times 128/(D/16) heads, so a thread
-// loads the 8 angles of its chunk once and uses them for every head it
-// takes.  The pair (a, b) becomes (a c - b s, a s + b c) in fp32, each
+// block per token (and one that looks the token ranges over): its threads are
+// D/16 column chunks (16 columns each: the two 8-column halves of 8 rotary
+// pairs) times 128/(D/16) heads, so a thread loads the 8 angles of its chunk
+// once and uses them for every head it takes.  The pair (a, b) becomes (a c - b s, a s + b c) in fp32, each
 // product rounded before the sum, rounded once to the element type.
 //   9125 tokens, 32 + 2 x 8 heads, d = 128, read out of one projection: 229 MB
 //   in 37.5 us, 6.1 TB/s (0.90 of the measured copy rate; 39.6 us with four
@@ -256,6 +256,17 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams pr
   constexpr int MORE = 2;           // rows in flight per thread (4 take 72 registers and leave fewer blocks: see above)
   const int t = blockIdx.x;
   const int lane = threadIdx.x & 31;
+  if (t == prm.T) {
+    // the last block: token ranges that do not fit T, or go back (those that no
+    // token lies in are nobody else's to find)
+    bool bad = false;
+    for (int b = threadIdx.x; b < prm.B; b += 128) {
+      const int a = prm.cu_q[b], e = prm.cu_q[b + 1];
+      bad |= a < 0 || e < a || e > prm.T;
+    }
+    if (bad) atomicOr(prm.err, FA_DEVERR_INDEX);
+    return;
+  }
   const int c = threadIdx.x % CL, h0 = threadIdx.x / CL;
   // columns of the two 8-element pieces of this chunk
   const int x0 = LAYOUT == FA_ROPE_HALF ? 8 * c : 16 * c;
@@ -282,7 +293,8 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams pr
   // the three dependent look-ups (sequence, lengths, page) pass together
   load(h0);
   const int b = find_sequence(prm.cu_q, prm.B, t, lane);
-  const int q0 = prm.cu_q[b], q1 = prm.cu_q[b + 1];
+  // (a range is cut to the T tokens there are, as fa_fwd_paged does)
+  const int q0 = max(0, prm.cu_q[b]), q1 = min(prm.T, prm.cu_q[b + 1]);
   if (t < q0 || t >= q1) return;  // a row that belongs to no sequence
   const long long pos = (long long)prm.seq_k[b] - (q1 - q0) + (t - q0);
   // device data that leads out of range: nothing is written for the token
@@ -353,7 +365,7 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams pr
 
 template <int D, bool F16>
 cudaError_t append_layout(const AppendParams& prm, int layout, cudaStream_t stream) {
-  const unsigned grid = (unsigned)prm.T;
+  const unsigned grid = (unsigned)prm.T + 1;  // (the last block looks the token ranges over)
   if (layout == 0) cache_append_kernel<D, F16, 0><<<grid, 128, 0, stream>>>(prm);
   else if (layout == FA_ROPE_HALF) cache_append_kernel<D, F16, FA_ROPE_HALF><<<grid, 128, 0, stream>>>(prm);
   else cache_append_kernel<D, F16, FA_ROPE_INTERLEAVED><<<grid, 128, 0, stream>>>(prm);

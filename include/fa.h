@@ -488,10 +488,11 @@ typedef struct {
  *   seq_k        [B] int32 (device)
  * All three are device data, read by the kernels when they run, so a captured
  * graph follows their contents.  The host cannot refuse what they hold; the
- * kernels do: a length is cut to the arrays it would overrun, a page number
- * out of range reads as zeros (fa_fwd_paged) or drops the token
- * (fa_cache_append), nothing out of bounds is touched, and
- * fa_check_device_error then returns FA_ERR_INDEX.
+ * kernels do: a token range is cut to the T rows there are (by both calls
+ * alike), a number of keys to the table (fa_fwd_paged), a page number out of
+ * range reads as zeros (fa_fwd_paged) or drops the token (fa_cache_append),
+ * nothing out of bounds is touched, and fa_check_device_error then returns
+ * FA_ERR_INDEX.
  */
 
 /*
