@@ -195,7 +195,7 @@ struct WinParams {
   int num_pages, page_shift;
   int g;              // query heads per key/value head
   int tpt;            // tokens per query tile (tpt * g <= 128)
-  int min_places;     // a CTA's run of the line is at least this long
+  uint32_t max_places;  // the longest line of work of token ranges that do not overlap, below 2^31
   float* o_part;      // [2 * grid][slot rows][D] partial results of cut units
   float* lse_part;    // [2 * grid][slot rows], NQT * 128 of them
   int4* desc;         // [grid] cut units: {parts, first token, kv head, rows}
@@ -509,10 +509,10 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
     seq_e = prm.cu_q[seq_b0 + 1];
     seq_n = prm.seq_k[seq_b0];
   }
-  // paged: this CTA's run [line0, line0 + line_n) of the line of work.  (The
-  // host refuses batches whose line could pass 2^31 places; token ranges that
-  // overlap, against the contract, may wrap it: the results are then wrong,
-  // but every index below is checked where it is used.)
+  // paged: this CTA's run [line0, line0 + line_n) of the line of work.  The
+  // host refuses batches whose line could pass 2^31 places.  Token ranges that
+  // overlap, against the contract, can make it longer than that: the sums stop
+  // one behind the most that others can have, and nothing of such a line is run.
   uint32_t line_per = 0, line0 = 0, line_n = 0;
   if constexpr (PAGED) {
     pdl_launch();  // the join can be launched; it waits for this kernel's end
@@ -535,18 +535,19 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
     auto group_places = [&](const WinSeq& q, int i) -> uint32_t {
       return win_places<C::NQT>(win_group_len(prm, q, tpg, i), min(tpg, q.nq - i * tpg), tpt) * (uint32_t)prm.Hkv;
     };
+    auto add = [&](uint32_t a, uint32_t b) -> uint32_t { return min(a + b, prm.max_places + 1); };  // (both at most that)
     auto seq_places = [&](const WinSeq& q) -> uint32_t {
       uint32_t n = 0;
-      for (int i = 0; i * tpg < q.nq; ++i) n += group_places(q, i);
+      for (int i = 0; i * tpg < q.nq && n <= prm.max_places; ++i) n = add(n, group_places(q, i));
       return n;
     };
     uint32_t mine = 0;
-    for (int b = seq_b0; b < b1; ++b) mine += seq_places(seq_of(b));
+    for (int b = seq_b0; b < b1 && mine <= prm.max_places; ++b) mine = add(mine, seq_places(seq_of(b)));
     uint32_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
       const uint32_t x = __shfl_up_sync(0xffffffffu, incl, d);
-      if (lane >= d) incl += x;
+      if (lane >= d) incl = add(incl, x);
     }
     if (lane == 31) bars->warp_sum[warp] = incl;
     __syncthreads();
@@ -554,11 +555,14 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
 #pragma unroll
     for (int w = 0; w < C::THREADS / 32; ++w) {
       const uint32_t x = bars->warp_sum[w];
-      if (w < warp) before += x;
-      total += x;
+      if (w < warp) before = add(before, x);
+      total = add(total, x);
     }
-    line_per = (total + gridDim.x - 1) / gridDim.x;
-    if (line_per < (uint32_t)prm.min_places) line_per = prm.min_places;
+    if (total > prm.max_places) {
+      total = 0;
+      bad = true;
+    }
+    line_per = max((total + gridDim.x - 1) / gridDim.x, 1u);
     if (C::NQT == 2) line_per = (line_per + 1) & ~1u;
     line0 = line_per * blockIdx.x;
     line_n = line0 >= total ? 0u : min(line_per, total - line0);

@@ -129,13 +129,12 @@ fa_status check_cache(const fa_kv_cache* c) {
 }
 
 // What a ragged batch over a cache needs of its index arrays.
-fa_status check_batch(const fa_kv_cache* c, const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+fa_status check_batch(const int32_t* block_table, int64_t table_stride, int64_t max_pages,
                       const int32_t* cu_q, const int32_t* seq_k, int64_t B, int64_t T) {
   if (max_pages < 1 || (B > 1 && table_stride < max_pages)) return FA_ERR_INVALID_ARG;
   if (!block_table || !cu_q || !seq_k) return FA_ERR_INVALID_ARG;
   if (!aligned4(block_table) || !aligned4(cu_q) || !aligned4(seq_k)) return FA_ERR_INVALID_ARG;
   if (B > (1 << 24) || T > kMaxLen || max_pages > kMaxLen) return FA_ERR_UNSUPPORTED;
-  (void)c;
   return FA_OK;
 }
 
@@ -218,7 +217,7 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   if (Hq % Hkv != 0) return FA_ERR_INVALID_ARG;
   if (Hq / Hkv > fa::kBM) return FA_ERR_UNSUPPORTED;  // a token's heads share one query tile
   if (B == 0 || T == 0 || Hq == 0) return FA_OK;
-  if ((st = check_batch(cache, block_table, table_stride, max_pages, cu_q, seq_k, B, T)) != FA_OK) return st;
+  if ((st = check_batch(block_table, table_stride, max_pages, cu_q, seq_k, B, T)) != FA_OK) return st;
   if (!q || !o || !lse || !aligned16(q) || !aligned16(o) || !aligned4(lse)) return FA_ERR_INVALID_ARG;
   if (T > 1 && (q_stride < Hq * d || q_stride % 8 != 0)) return FA_ERR_INVALID_ARG;
   if (q_stride >= (int64_t)1 << 38 || Hq > (1 << 20)) return FA_ERR_UNSUPPORTED;
@@ -298,7 +297,6 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   p.page_shift = shift_of(cache->page_size);
   p.g = (int)g;
   p.tpt = (int)tpt;
-  p.min_places = 1;
   // the line of work: at most this many units, each of at most this many
   // key tiles, two places to a tile
   const int64_t unit_tok = (pair ? 2 : 1) * tpt;
@@ -307,6 +305,7 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   if (p.window + (int64_t)p.sinks + unit_tok < keys) tiles = (p.window + (int64_t)p.sinks + unit_tok) / fa::kBN + 4;
   const int64_t units = (T / unit_tok + B) * Hkv;
   if (units >= (int64_t)0x7fffffff / (2 * (tiles + 1))) return FA_ERR_UNSUPPORTED;
+  p.max_places = (uint32_t)(units * 2 * (tiles + 1));
   uint8_t* w = static_cast<uint8_t*>(workspace);
   p.o_part = reinterpret_cast<float*>(w);
   p.lse_part = reinterpret_cast<float*>(w + ws.lse_at);
@@ -332,7 +331,7 @@ fa_status fa_cache_append(const fa_kv_cache* cache, const void* q, const void* k
   fa_status st = check_cache(cache);
   if (st != FA_OK) return st;
   if (B == 0 || T == 0) return FA_OK;
-  if ((st = check_batch(cache, block_table, table_stride, max_pages, cu_q, seq_k, B, T)) != FA_OK) return st;
+  if ((st = check_batch(block_table, table_stride, max_pages, cu_q, seq_k, B, T)) != FA_OK) return st;
   const int64_t d = cache->d, Hkv = cache->heads;
   if (rope_layout != 0 && (!rope_cos || !rope_sin || !aligned16(rope_cos) || !aligned16(rope_sin)))
     return FA_ERR_INVALID_ARG;

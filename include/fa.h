@@ -492,7 +492,9 @@ typedef struct {
  * alike), a number of keys to the table (fa_fwd_paged), a page number out of
  * range reads as zeros (fa_fwd_paged) or drops the token (fa_cache_append),
  * nothing out of bounds is touched, and fa_check_device_error then returns
- * FA_ERR_INDEX.
+ * FA_ERR_INDEX.  (Ranges that go back overlap others: which of them a shared
+ * row follows is not defined, and fa_fwd_paged writes nothing at all where
+ * their work passes the most that T, B and max_pages allow without.)
  */
 
 /*

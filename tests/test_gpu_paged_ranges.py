@@ -1,6 +1,8 @@
 """Token ranges (cu_q) that do not fit the packed arrays, which only the kernels
 can see: they are cut to what exists, the same by fa_cache_append and
 fa_fwd_paged, and reported."""
+import math
+
 import pytest
 import torch
 
@@ -79,3 +81,26 @@ def test_append_of_good_ranges_reports_nothing(fa):
     at = table[39:39 + n, 0].long()
     assert torch.equal(kp[at, 0, 0], k[3:3 + n, 0]) and torch.equal(vp[at, 0, 0], v[3:3 + n, 0])
     assert int((kp != 0).any(-1).sum()) == n
+
+
+@pytest.mark.parametrize("B,T,Hkv,page,pages", [(64, 8192, 1, 16, 64), (20000, 65536, 8, 1024, 64)])
+def test_more_work_than_ranges_without_overlap_can_have_is_not_run(fa, B, T, Hkv, page, pages):
+    # every other sequence claims all tokens; the second batch's key tiles, 1.05e10, do not fit 32 bits
+    d = 64
+    q = torch.zeros((T, Hkv, d), dtype=torch.bfloat16, device="cuda")
+    kp = torch.zeros((pages, Hkv, page, d), dtype=torch.bfloat16, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").expand(B, pages).contiguous()
+    sk = torch.full((B,), page * pages, dtype=torch.int32, device="cuda")
+    cu = ints([0, T] * (B // 2) + [0])
+    o = torch.full((T, Hkv, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((T, Hkv), 7.0, device="cuda")
+    fa.check_device_error()
+    fa.fwd_paged(q, kp, kp, table, cu, sk, out=o, lse=lse)
+    _index_error(fa)
+    assert bool((o == 7.0).all()) and bool((lse == 7.0).all())
+    # the same arrays with ranges that fit: every row sees its window's 100 keys, of score 0
+    cu = ints([i * T // B for i in range(B + 1)])
+    fa.fwd_paged(q, kp, kp, table, cu, sk, window=100, out=o, lse=lse)
+    fa.check_device_error()
+    # (ln 100 in fp32, by a hardware logarithm within 2^-21 of it, as in window_util)
+    assert bool((o == 0.0).all()) and float((lse.double() - math.log(100)).abs().max()) <= 2.0 ** -20 + 2.0 ** -21 * math.log(100)
