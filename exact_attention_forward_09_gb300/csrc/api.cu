@@ -43,9 +43,7 @@ FA_EXTERN_ATTN(kE4M3, 256, true, false)
 
 namespace {
 
-__device__ int g_fa_device_error;
-
-__global__ void clear_error_kernel(int* word, int bit) { atomicAnd(word, ~bit); }
+__device__ int g_fa_device_error[2];  // FA_DEVERR_TIMEOUT; behind it, FA_DEVERR_INDEX (see ptx_window.cuh)
 
 constexpr int kMaxDevices = 64;
 
@@ -971,15 +969,16 @@ fa_status fa_check_device_error(cudaStream_t stream) {
   int* err = nullptr;
   fa_status st = device_setup(&dev, &err);
   if (st != FA_OK) return st;
-  int h = 0;
-  if (cudaMemcpyFromSymbol(&h, g_fa_device_error, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
-  if (h == 0) return FA_OK;
-  // one error is reported and its bit cleared; the others, and what kernels of
-  // other streams add meanwhile, stay
-  const int bit = (h & fa::FA_DEVERR_TIMEOUT) ? fa::FA_DEVERR_TIMEOUT : fa::FA_DEVERR_INDEX;
-  clear_error_kernel<<<1, 1, 0, stream>>>(err, bit);
-  if (cudaGetLastError() != cudaSuccess || cudaStreamSynchronize(stream) != cudaSuccess) return FA_ERR_CUDA;
-  return bit == fa::FA_DEVERR_INDEX ? FA_ERR_INDEX : FA_ERR_TIMEOUT;
+  // one error is reported, and its word alone cleared
+  for (int word = 0; word < 2; ++word) {
+    int h = 0;
+    const int zero = 0;
+    if (cudaMemcpyFromSymbol(&h, g_fa_device_error, sizeof(int), word * sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
+    if (h == 0) continue;
+    if (cudaMemcpyToSymbol(g_fa_device_error, &zero, sizeof(int), word * sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
+    return word == 0 ? FA_ERR_TIMEOUT : FA_ERR_INDEX;
+  }
+  return FA_OK;
 }
 
 fa_status fa_debug_inject(int flags) {

@@ -592,7 +592,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
       bars->start_len = win_group_len(prm, q, tpg, i);
       bars->start_off = line0 - at;
     }
-    if (bad && blockIdx.x == 0) atomicOr(prm.err, FA_DEVERR_INDEX);
+    if (bad && blockIdx.x == 0) report_index(prm.err);
   }
   tc_fence_before();
   __syncthreads();
@@ -611,7 +611,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
       if (key < w.nk && (key < prm.sinks || key + box_rows > w.lo)) {
         id = prm.table[(long long)w.seq * prm.table_stride + (key >> prm.page_shift)];
         if ((unsigned)id >= (unsigned)prm.num_pages) {
-          atomicOr(prm.err, FA_DEVERR_INDEX);
+          report_index(prm.err);
           id = -1;
         }
       }

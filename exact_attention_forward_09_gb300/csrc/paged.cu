@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams pr
       const int a = prm.cu_q[b], e = prm.cu_q[b + 1];
       bad |= a < 0 || e < a || e > prm.T;
     }
-    if (bad) atomicOr(prm.err, FA_DEVERR_INDEX);
+    if (bad) report_index(prm.err);
     return;
   }
   const int c = threadIdx.x % CL, h0 = threadIdx.x / CL;
@@ -302,7 +302,7 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams pr
   if (pos >= 0 && (pos >> prm.page_shift) < prm.max_pages && (LAYOUT == 0 || pos < prm.rope_len))
     page = prm.table[b * prm.table_stride + (pos >> prm.page_shift)];
   if ((unsigned)page >= (unsigned)prm.num_pages) {
-    if (threadIdx.x == 0) atomicOr(prm.err, FA_DEVERR_INDEX);
+    if (threadIdx.x == 0) report_index(prm.err);
     return;
   }
   float cs[8], sn[8];

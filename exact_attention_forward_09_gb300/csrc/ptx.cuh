@@ -72,7 +72,7 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volati
     if (*abort_flag) return false;
     if (globaltimer() - t0 > FA_WAIT_LIMIT_NS) {
       *abort_flag = 1;
-      atomicOr(err_word, FA_DEVERR_TIMEOUT);
+      atomicExch(err_word, FA_DEVERR_TIMEOUT);
       return false;
     }
   }
