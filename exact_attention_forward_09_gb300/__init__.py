@@ -350,6 +350,13 @@ def _guard(index: int):
 _TYPES = {torch.bfloat16: FA_DTYPE_BF16, torch.float16: FA_DTYPE_FP16}
 
 
+def _count(x) -> int:
+    """x as a whole number that 64 bits hold (one beyond them would reach the
+    library as what is left of it): the nearest one."""
+    x = int(x)
+    return x if -1 << 63 <= x < 1 << 63 else ((1 << 63) - 1 if x > 0 else -1 << 63)
+
+
 def _scale(scale, d):
     return 1.0 / math.sqrt(d) if scale is None else float(scale)
 
@@ -399,7 +406,7 @@ def fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, s
         _check_out("lse", lse, (B, Hq, Nq), torch.float32, index)
     with _guard(index):
         st = _lib().fa_fwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
-                                  B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks), _scale(scale, d), _TYPES[q.dtype],
+                                  B, Hq, Hkv, Nq, Nk, d, _count(window), _count(sinks), _scale(scale, d), _TYPES[q.dtype],
                                   _current_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_fwd_window")
@@ -407,12 +414,15 @@ def fwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, window: int, s
 
 
 @functools.lru_cache(maxsize=256)
-def bwd_window_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int, window: int, sinks: int = 0) -> int:
-    """Bytes of device workspace ``bwd_window`` needs for this shape."""
+def _bwd_window_bytes(*sizes: int) -> int:
     n = ctypes.c_size_t(0)
-    _check(_lib().fa_bwd_window_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, int(window), int(sinks), ctypes.byref(n)),
-           "fa_bwd_window_workspace_bytes")
+    _check(_lib().fa_bwd_window_workspace_bytes(*sizes, ctypes.byref(n)), "fa_bwd_window_workspace_bytes")
     return n.value
+
+
+def bwd_window_workspace_bytes(B: int, Hq: int, Hkv: int, Nq: int, Nk: int, d: int, window: int, sinks: int = 0) -> int:
+    """Bytes of device workspace ``bwd_window`` needs for this shape, on any device."""
+    return _bwd_window_bytes(B, Hq, Hkv, Nq, Nk, d, _count(window), _count(sinks))
 
 
 def bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor, lse: torch.Tensor,
@@ -424,6 +434,7 @@ def bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
     the forward with the same window, sinks and scale; d 64 or 128.  Returns
     (dq, dk, dv)."""
     B, Hq, Nq, d, Hkv, Nk, index = _dense(q, k, v)
+    window, sinks = _count(window), _count(sinks)
     dt = q.dtype
     _check_out("out", out, q.shape, dt, index)
     _check_out("dout", dout, q.shape, dt, index)
@@ -442,11 +453,11 @@ def bwd_window(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Ten
         _check_out("dv", dv, v.shape, dt, index)
     with _guard(index):
         if workspace is None:
-            need = bwd_window_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, window, sinks)
+            need = _bwd_window_bytes(B, Hq, Hkv, Nq, Nk, d, window, sinks)
             workspace = torch.empty((need or 1,), dtype=torch.uint8, device=q.device)
         st = _lib().fa_bwd_window(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(),
                                   dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv, Nq, Nk, d,
-                                  int(window), int(sinks), _scale(scale, d), _TYPES[dt],
+                                  window, sinks, _scale(scale, d), _TYPES[dt],
                                   *_workspace(workspace, index), _current_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_bwd_window")
@@ -539,7 +550,7 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, blo
             workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
         st = _lib().fa_fwd_paged(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
                                  table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), B, T, Hq, q_stride,
-                                 int(max_q), 1 << 30 if window is None else int(window), int(sinks), _scale(scale, d),
+                                 _count(max_q), 1 << 30 if window is None else _count(window), _count(sinks), _scale(scale, d),
                                  *_workspace(workspace, index), _current_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_fwd_paged")
