@@ -41,6 +41,11 @@
 // (BwdWindow), which a small kernel sums in a fixed order.  The walks of the
 // other tiles, or of the last of them, over all query heads of a group, are
 // shared out likewise where whole ones would leave much of the GPU idle.
+//
+// Roundings: P and dS to the element type, as operands of 16-bit MMAs (which
+// take one type; dS in two pieces would double two of the five products), each
+// gradient once at its end; LSE, D, dP - D and all sums are fp32.  Relative error
+// against 64 bits: 2.3 to 2.4e-3 in bf16, where rounding a gradient alone gives 1.7e-3.
 #include <cmath>
 #include <cstdint>
 #include <type_traits>
@@ -1106,6 +1111,8 @@ BwdWindow bwd_window_plan(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_
   // us; 1023 tokens, 32/4 heads, window 977 206 and 84; the last 48 of 200 tiles
   // (2 x 3100 tokens, 16/4 heads, window 700) 216 and 187.  (A window over
   // everything sums as fa_bwd does, bit for bit, and so unshared.)
+  // (152 SMs whatever the device: the workspace's size, which callers ask for
+  // without one, and the bits of dK and dV follow from the shares.)
   const int64_t sms = 152, most_parts = 1024, bhkv = B * Hkv;
   const double whole = (double)usual + 3.0;
   auto time_of = [&](int64_t u, int64_t n) {  // u whole tiles, the others in n shares

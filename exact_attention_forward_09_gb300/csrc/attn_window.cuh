@@ -34,6 +34,13 @@
 //     the sequence's end in its last page, pages that left the window) may be
 //     anything, NaN included: its scores are replaced, and its V rows are
 //     zeroed in shared memory before P V.
+//
+// Roundings.  Scores, maxima, sums, O and the parts that are joined are fp32.  P
+// is rounded to the element type: both operands of a 16-bit MMA have one type, and
+// P in two 16-bit pieces would double P V.  It is rounded before its division by
+// the row's sum, which is taken of the unrounded P.  With O's own rounding that
+// makes a relative error against 64 bits of 2.0 to 2.4e-3 in bf16 and 2.5 to 2.9e-4
+// in fp16, where rounding O alone gives 1.6e-3 and 2.1e-4.
 #pragma once
 
 #include <cstdint>
@@ -67,8 +74,9 @@ namespace fa {
 // ends.  (One token each, 32/8 heads, against WIN_ONE: 256 sequences under a
 // window of 1024 at d = 64, 128, 256: 149 -> 107, 224 -> 186, 430 -> 367 us; of
 // 50 to 600 keys 78 -> 62, 125 -> 115, 190 -> 168; 64 of 2000 to 16000 at d = 64
-// 224 -> 195, 6.5 TB/s.)  An infinite value in a row of V that is seen can give
-// NaN, as the copies that do not take its key weigh it with 0.
+// 224 -> 195, 6.5 TB/s.)  An infinite value in a row of V that is seen gives
+// NaN, as the copies that do not take its key weigh it with 0; the other forms
+// give infinity unless a row of the tile weighs it with 0.
 // WIN_FEW2 (d <= 128): the same with two CTAs per SM, where a unit's start and
 // end pass while the other CTA works.  At d = 128 it takes units of up to 8 rows
 // and half the tiles in flight, and pays where units are many (256 of 50 to 600
@@ -323,7 +331,9 @@ __device__ __forceinline__ int win_group_len(const WinParams& prm, const WinSeq&
 // Places on the line of a unit of `len` key tiles: two to a tile when both
 // query tiles are in use (such a step takes 1.8 times a single one's time),
 // one otherwise, rounded up to even, so that CTAs, which start at even
-// places, start at whole tiles.  (One query tile per CTA, d = 256: one each.)
+// places, start at whole tiles.  (Forms with one query tile per CTA: one each.)
+// A unit's start and end are not counted, so runs that hold many short units
+// take longer than others.
 template <int NQT>
 __device__ __forceinline__ uint32_t win_places(int len, int ntok, int tpt) {
   if (NQT == 1) return (uint32_t)len;

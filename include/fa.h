@@ -448,7 +448,8 @@ fa_status fa_bwd_window(const void* q, const void* k, const void* v, const void*
 /*
  * fa_bwd_window_workspace_bytes -- bytes of device workspace fa_bwd_window
  * needs: fa_bwd's, and fp32 dK and dV parts of the key tiles whose queries are
- * shared out (at most 256 MiB at d = 128).  Same checks as fa_bwd_window.
+ * shared out (at most 256 MiB at d = 128).  Same checks as fa_bwd_window.  The
+ * size depends on the arguments alone, not on a device (none is needed to ask).
  */
 fa_status fa_bwd_window_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d,
                                         int64_t window, int64_t sinks, size_t* bytes);
@@ -507,14 +508,18 @@ typedef struct {
  *   Hq         a multiple of cache->heads, at most 128 query heads to each
  *   max_q      the most new tokens any sequence brings, 0 if not known.  A
  *              hint: it sizes the query tiles; results are right for any value
+ *              (of finite inputs: see below)
  *   window, sinks, scale  as fa_fwd_window (pages that left every query's
  *              window, sinks apart, may be freed: they are not read)
  *   workspace  DEVICE pointer, 256-byte aligned, owned by the caller, at least
  *              fa_paged_workspace_bytes(d) bytes; overwritten; calls sharing
  *              it must not overlap on the GPU (two captured graphs included)
  * Rows of the cache behind a sequence's end, and pages it does not see, may
- * hold anything (NaN included); an infinity in a value row that is seen may
- * reach its column of O as NaN.  Two kernels on `stream`, no allocation.  The
+ * hold anything (NaN included).  A NaN or infinity in a value row that a new
+ * token of the sequence sees may also reach its column of O, as NaN, in those
+ * of its tokens that do not see it, and an infinity as NaN in those that do:
+ * which of them depends on the rest of the batch and on max_q, as these pick
+ * the form of the kernel.  Two kernels on `stream`, no allocation.  The
  * result of one sequence may differ in its last bits with the rest of the
  * batch (the work is cut evenly over the GPU and the pieces are joined), but
  * is the same from run to run.
