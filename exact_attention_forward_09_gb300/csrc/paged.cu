@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(
 //   9125 tokens, 32 + 2 x 8 heads, d = 128, read out of one projection: 229 MB
 //   in 37.5 us, 6.1 TB/s (0.90 of the measured copy rate; 39.6 us with four
 //   rows in flight per thread, which cost registers and so blocks; 43.8 with
-//   256 threads per token, whose second round is half empty).  64 tokens: 3.4
+//   256 threads per token, whose second round is half empty).  64 tokens: 2.9
 //   us, three dependent look-ups (sequence, lengths, page) behind the launch.
 
 // the last b with cu[b] <= t, by 32-way search over cu[0 .. B-1]

@@ -429,8 +429,10 @@ fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, fl
  * layouts (d 64 or 128) with P restricted to the visible keys.  Rows that see
  * at most 32 keys take D = sum_j P_j dP_j over them in fp32 in place of
  * dO . O, whose rounded O few keys do not average out (with one key dS must
- * vanish); with that a window of at least Nk gives fa_bwd's causal gradients
- * but for those rows' share, and their bits where Nk - Nq >= 32.
+ * vanish).  But for these rows a window of at least Nk without sinks runs as
+ * fa_bwd's causal kernel, with the same bits of dK and dV (so with its key
+ * tiles whole: with few key/value heads a shorter window, whose tiles are shared
+ * out over the GPU, can take less time).
  *   lse        [B, Hq, Nq] fp32 as fa_fwd_window wrote it
  *   workspace  at least fa_bwd_window_workspace_bytes(...) bytes, 256-byte
  *              aligned; overwritten; calls sharing it must not overlap
