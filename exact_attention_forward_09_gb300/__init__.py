@@ -21,10 +21,11 @@ import torch
 from .build import LIB as _LIB_PATH
 
 __all__ = ["fwd_host", "fwd_host_workspace_bytes", "bwd", "bwd_workspace_bytes", "fwd_splitkv", "splitkv_workspace_bytes", "fwd", "fwd_gqa", "fwd_window", "bwd_window", "bwd_window_workspace_bytes",
-           "fwd_paged", "paged_workspace_bytes", "cache_append", "fwd_fp8", "fwd_fp8_gqa", "quant_fp8", "quant_fp8_per_tensor_noalloc", "check_device_error", "lib",
+           "fwd_paged", "paged_workspace_bytes", "cache_append", "rope", "rope_table", "fwd_fp8", "fwd_fp8_gqa", "quant_fp8", "quant_fp8_per_tensor_noalloc", "check_device_error", "lib",
            "FaError", "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
            "FA_ERR_SCRATCH_LIMIT", "FA_ERR_INDEX", "FA_DTYPE_BF16", "FA_DTYPE_FP16", "FP8_BLOCK_ROWS",
-           "FA_ROPE_INTERLEAVED", "FA_ROPE_HALF",
+           "FA_ROPE_INTERLEAVED", "FA_ROPE_HALF", "FA_ROPE_SCALE_NONE", "FA_ROPE_SCALE_LINEAR", "FA_ROPE_SCALE_BASE",
+           "FA_ROPE_SCALE_TURNS", "FA_ROPE_SCALE_INDEX",
            "QUANT_NOALLOC_MAX_BLOCKS"]
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT = 0, 1, 2, 3, 4
@@ -33,6 +34,7 @@ FA_ERR_INDEX = 6
 QUANT_NOALLOC_MAX_BLOCKS = 65536
 FA_DTYPE_BF16, FA_DTYPE_FP16 = 0, 1
 FA_ROPE_INTERLEAVED, FA_ROPE_HALF = 1, 2
+FA_ROPE_SCALE_NONE, FA_ROPE_SCALE_LINEAR, FA_ROPE_SCALE_BASE, FA_ROPE_SCALE_TURNS, FA_ROPE_SCALE_INDEX = 0, 1, 2, 3, 4
 FP8_BLOCK_ROWS = 128
 
 
@@ -53,6 +55,8 @@ class _KvCache(ctypes.Structure):
 
 
 _KV_PACK = struct.Struct("@PPqqqqqqqi4x").pack
+_ROPE_PACK = struct.Struct("@PPqqqqqqq").pack      # fa_rope_array
+_SCALING_PACK = struct.Struct("@i4xddddd").pack    # fa_rope_scaling
 
 
 _LIB = None
@@ -112,6 +116,14 @@ def _lib():
         lib.fa_cache_append.argtypes = [cache, vp, vp, vp, vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, i64, i64, vp,
                                         vp, i64, i32, vp]
         lib.fa_cache_append.restype = i32
+        lib.fa_cache_append_at.argtypes = [cache, vp, vp, vp, vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, i64, i64, vp,
+                                           vp, i64, i64, i32, vp, vp]
+        lib.fa_cache_append_at.restype = i32
+        packed = ctypes.c_char_p  # the bytes of fa_rope_array, fa_rope_scaling structures
+        lib.fa_rope_table.argtypes = [vp, vp, i64, i64, ctypes.c_double, i64, packed, vp]
+        lib.fa_rope_table.restype = i32
+        lib.fa_rope.argtypes = [packed, i64, i64, i64, i64, vp, i64, i64, vp, vp, i64, i64, i32, i32, i32, vp]
+        lib.fa_rope.restype = i32
         lib.fa_status_string.argtypes = [i32]
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_check_device_error.argtypes = [vp]
@@ -557,16 +569,30 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, blo
     return out, lse
 
 
+def _check_rope(rope, index):
+    """(cos, sin, positions, rotated columns, layout) of a rope = (cos, sin, layout)."""
+    cos, sin, layout = rope
+    if layout not in (FA_ROPE_INTERLEAVED, FA_ROPE_HALF):
+        raise ValueError("rope layout must be FA_ROPE_INTERLEAVED or FA_ROPE_HALF")
+    if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
+        raise ValueError("rope cos must be a [positions, rope_dim/2] tensor")
+    shape = cos.shape
+    _check_out("rope cos", cos, shape, torch.float32, index)
+    _check_out("rope sin", sin, shape, torch.float32, index)
+    return cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], int(layout)
+
+
 def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
                  block_table: torch.Tensor, cu_q: torch.Tensor, seq_k: torch.Tensor, q: torch.Tensor | None = None,
-                 rope=None, q_out: torch.Tensor | None = None):
+                 rope=None, q_out: torch.Tensor | None = None, positions: torch.Tensor | None = None):
     """Writes the new tokens' keys and values, [T, heads, d], into their pages
-    (``fa_cache_append``; the batch as in ``fwd_paged``).  ``rope``: None, or
-    (cos, sin, layout) with cos / sin contiguous fp32 [positions, d/2] and
-    layout FA_ROPE_INTERLEAVED or FA_ROPE_HALF: keys, and the queries q [T,
-    Hq, d] if given, are rotated by their positions first.  k, v and q may be
-    slices of one projection.  Returns the rotated queries (``q_out``), or
-    None without q."""
+    (``fa_cache_append_at``; the batch as in ``fwd_paged``).  ``rope``: None, or
+    (cos, sin, layout) with cos / sin contiguous fp32 [length, rope_dim/2] and
+    layout FA_ROPE_INTERLEAVED or FA_ROPE_HALF: the first rope_dim columns of
+    keys, and of the queries q [T, Hq, d] if given, are rotated first, by the
+    tokens' positions in their sequences or by ``positions`` (int32 [T], as
+    ``tree_plan`` gives them).  k, v and q may be slices of one projection.
+    Returns the rotated queries (``q_out``), or None without q."""
     cache, heads, d, dt, index = _cache(k_pages, v_pages)
     if not isinstance(k, torch.Tensor) or k.dim() != 3:
         raise ValueError("k must be a [T, heads, d] CUDA tensor")
@@ -585,24 +611,123 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
         qp, op = q.data_ptr(), q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out needs q")
-    cp, sp, n, layout = None, None, 0, 0
+    cp, sp, n, r, layout, pp = None, None, 0, 0, 0, None
     if rope is not None:
-        cos, sin, layout = rope
-        if layout not in (FA_ROPE_INTERLEAVED, FA_ROPE_HALF):
-            raise ValueError("rope layout must be FA_ROPE_INTERLEAVED or FA_ROPE_HALF")
-        if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
-            raise ValueError("rope cos must be a [positions, d/2] tensor")
-        n = cos.shape[0]
-        _check_out("rope cos", cos, (n, d // 2), torch.float32, index)
-        _check_out("rope sin", sin, (n, d // 2), torch.float32, index)
-        cp, sp = cos.data_ptr(), sin.data_ptr()
+        cp, sp, n, r, layout = _check_rope(rope, index)
+        if positions is not None:
+            _check_out("positions", positions, (T,), torch.int32, index)
+            pp = positions.data_ptr()
+    elif positions is not None:
+        raise ValueError("positions need rope")
     with _guard(index):
-        st = _lib().fa_cache_append(cache, qp, k.data_ptr(), v.data_ptr(), op, qs, ks, vs, block_table.data_ptr(),
-                                    table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), B, T, Hq, cp, sp, n,
-                                    int(layout), _current_stream(index))
+        st = _lib().fa_cache_append_at(cache, qp, k.data_ptr(), v.data_ptr(), op, qs, ks, vs, block_table.data_ptr(),
+                                       table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), B, T, Hq, cp, sp, n,
+                                       r, layout, pp, _current_stream(index))
     if st != FA_OK:
-        raise FaError(st, "fa_cache_append")
+        raise FaError(st, "fa_cache_append_at")
     return q_out
+
+
+_SCALE_KINDS = {"none": FA_ROPE_SCALE_NONE, "linear": FA_ROPE_SCALE_LINEAR, "base": FA_ROPE_SCALE_BASE,
+                "turns": FA_ROPE_SCALE_TURNS, "index": FA_ROPE_SCALE_INDEX}
+
+
+def rope_table(length: int, rope_dim: int, theta: float = 10000.0, scaling=None, start: int = 0, device=None, out=None):
+    """Angle tables of the positions start .. start + length - 1
+    (``fa_rope_table``): (cos, sin), fp32 [length, rope_dim/2] on ``device``
+    (default: the current CUDA device), or written to ``out`` = (cos, sin).
+    ``scaling``: None, or a dict with ``kind`` ("none", "linear", "base",
+    "turns" or "index"), ``factor``, for the last two ``original``, ``low`` and
+    ``high``, and ``amplitude`` (1 unless given)."""
+    sc = None
+    if scaling is not None:
+        more = set(scaling) - {"kind", "factor", "original", "low", "high", "amplitude"}
+        if scaling.get("kind") not in _SCALE_KINDS or more:
+            raise ValueError(f"scaling kind must be one of {sorted(_SCALE_KINDS)}" if not more else f"scaling has no {sorted(more)}")
+        sc = _SCALING_PACK(_SCALE_KINDS[scaling["kind"]], float(scaling.get("factor", 1.0)), float(scaling.get("original", 0.0)),
+                           float(scaling.get("low", 0.0)), float(scaling.get("high", 0.0)), float(scaling.get("amplitude", 1.0)))
+    length, rope_dim = _count(length), _count(rope_dim)
+    if out is None:
+        dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if length < 0 or rope_dim < 0:
+            raise ValueError("length and rope_dim must not be negative")
+        cos = torch.empty((length, rope_dim // 2), dtype=torch.float32, device=dev)
+        sin = torch.empty((length, rope_dim // 2), dtype=torch.float32, device=dev)
+        index = cos.get_device()
+    else:
+        cos, sin = out
+        index = cos.get_device() if isinstance(cos, torch.Tensor) else -1
+        _check_out("cos", cos, (length, rope_dim // 2), torch.float32, index)
+        _check_out("sin", sin, (length, rope_dim // 2), torch.float32, index)
+    if index < 0:
+        raise ValueError("rope tables are CUDA tensors")
+    with _guard(index):
+        st = _lib().fa_rope_table(cos.data_ptr(), sin.data_ptr(), length, rope_dim, float(theta), _count(start), sc,
+                                  _current_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_rope_table")
+    return cos, sin
+
+
+def _rope_strides(name, t, lead, d, dt, index):
+    """(heads, batch, head and token strides) of [B, heads, N, d] or [N, heads, d]."""
+    shape = t.shape if isinstance(t, torch.Tensor) else ()
+    four = len(lead) == 2
+    if len(shape) != (4 if four else 3) or t.dtype is not dt or t.get_device() != index or shape[-1] != d \
+            or shape[0] != lead[0] or (four and shape[2] != lead[1]):
+        raise ValueError(f"{name} must be a {dt} {'[B, heads, N, d]' if four else '[N, heads, d]'} tensor on cuda:{index}, as q is")
+    st = t.stride()
+    if t.numel() and st[-1] != 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return (shape[1], st[0], st[1], st[2]) if four else (shape[1], 0, st[1], st[0])
+
+
+def rope(q: torch.Tensor, k: torch.Tensor | None, rope, positions: torch.Tensor | None = None, offset: int = 0,
+         inverse: bool = False, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None):
+    """Rotary positions of q and k (None: q alone) in one launch
+    (``fa_rope``): both [B, heads, N, d], or both [N, heads, d], bf16 or fp16,
+    with any strides but of d.  ``rope`` = (cos, sin, layout) as in
+    ``cache_append``: the first rope_dim columns of a row are rotated, the others
+    copied.  Token n is at ``offset`` + n, or at ``positions`` (int32 [N], or
+    [B, N]).  ``inverse`` turns back, which takes gradients of the results to
+    those of q and k.  Returns (q_out, k_out), contiguous unless given; q_out = q
+    works in place."""
+    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4) or q.dtype not in _TYPES or q.get_device() < 0:
+        raise ValueError("q must be a bf16 or fp16 [B, heads, N, d] or [N, heads, d] CUDA tensor")
+    index, dt, shape = q.get_device(), q.dtype, q.shape
+    d, N = shape[-1], shape[2] if len(shape) == 4 else shape[0]
+    B = shape[0] if len(shape) == 4 else 1
+    lead = (shape[0], N) if len(shape) == 4 else (N,)
+    cp, sp, length, r, layout = _check_rope(rope, index)
+    arrays = b""
+    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            if y is not None:
+                raise ValueError("k_out needs k")
+            continue
+        heads, xb, xh, xn = _rope_strides(name, x, lead, d, dt, index)
+        if y is None:
+            y = torch.empty(x.shape, dtype=dt, device=x.device)
+        elif not isinstance(y, torch.Tensor) or y.shape != x.shape:
+            raise ValueError(f"{name}_out must have {name}'s shape")
+        _, yb, yh, yn = _rope_strides(name + "_out", y, lead, d, dt, index)
+        arrays += _ROPE_PACK(x.data_ptr(), y.data_ptr(), heads, xb, xh, xn, yb, yh, yn)
+        if name == "q":
+            q_out = y
+        else:
+            k_out = y
+    pp, ps = None, 0
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 or positions.get_device() != index \
+                or positions.shape not in ((N,), (B, N)) or not positions.is_contiguous():
+            raise ValueError(f"positions must be a contiguous int32 [{N}] or [{B}, {N}] tensor on cuda:{index}")
+        pp, ps = positions.data_ptr(), N if positions.dim() == 2 else 0
+    with _guard(index):
+        st = _lib().fa_rope(arrays, 1 if k is None else 2, B, N, d, pp, ps, _count(offset), cp, sp, length, r, layout,
+                            int(bool(inverse)), _TYPES[dt], _current_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_rope")
+    return q_out, k_out
 
 
 def fwd_fp8_gqa(q8, k8, v8, q_descale, k_descale, v_descale, causal: bool = False,

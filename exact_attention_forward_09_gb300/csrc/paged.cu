@@ -268,9 +268,10 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams pr
     return;
   }
   const int c = threadIdx.x % CL, h0 = threadIdx.x / CL;
+  const bool turn = LAYOUT != 0 && c < prm.rope_dim / 16;
   // columns of the two 8-element pieces of this chunk
-  const int x0 = LAYOUT == FA_ROPE_HALF ? 8 * c : 16 * c;
-  const int x1 = LAYOUT == FA_ROPE_HALF ? D / 2 + 8 * c : 16 * c + 8;
+  const int x0 = LAYOUT == FA_ROPE_HALF && turn ? 8 * c : 16 * c;
+  const int x1 = LAYOUT == FA_ROPE_HALF && turn ? prm.rope_dim / 2 + 8 * c : 16 * c + 8;
   const int rows = prm.Hq + 2 * prm.Hkv;
   auto source = [&](int r) -> const uint16_t* {
     if (r < prm.Hq) return prm.q + t * prm.q_stride + (long long)r * D;
@@ -292,23 +293,25 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams pr
   // the first rows do not depend on where they go: their latency and that of
   // the three dependent look-ups (sequence, lengths, page) pass together
   load(h0);
+  const int given = LAYOUT != 0 && prm.positions ? prm.positions[t] : 0;
   const int b = find_sequence(prm.cu_q, prm.B, t, lane);
   // (a range is cut to the T tokens there are, as fa_fwd_paged does)
   const int q0 = max(0, prm.cu_q[b]), q1 = min(prm.T, prm.cu_q[b + 1]);
   if (t < q0 || t >= q1) return;  // a row that belongs to no sequence
   const long long pos = (long long)prm.seq_k[b] - (q1 - q0) + (t - q0);
+  const long long angle = LAYOUT != 0 && prm.positions ? given : pos;  // the row of the tables
   // device data that leads out of range: nothing is written for the token
   int page = -1;
-  if (pos >= 0 && (pos >> prm.page_shift) < prm.max_pages && (LAYOUT == 0 || pos < prm.rope_len))
+  if (pos >= 0 && (pos >> prm.page_shift) < prm.max_pages && (LAYOUT == 0 || (angle >= 0 && angle < prm.rope_len)))
     page = prm.table[b * prm.table_stride + (pos >> prm.page_shift)];
   if ((unsigned)page >= (unsigned)prm.num_pages) {
     if (threadIdx.x == 0) report_index(prm.err);
     return;
   }
   float cs[8], sn[8];
-  if constexpr (LAYOUT != 0) {
-    const float4* pc = reinterpret_cast<const float4*>(prm.cos + pos * (D / 2) + 8 * c);
-    const float4* ps = reinterpret_cast<const float4*>(prm.sin + pos * (D / 2) + 8 * c);
+  if (LAYOUT != 0 && turn) {
+    const float4* pc = reinterpret_cast<const float4*>(prm.cos + angle * (prm.rope_dim / 2) + 8 * c);
+    const float4* ps = reinterpret_cast<const float4*>(prm.sin + angle * (prm.rope_dim / 2) + 8 * c);
     *reinterpret_cast<float4*>(cs) = pc[0];
     *reinterpret_cast<float4*>(cs + 4) = pc[1];
     *reinterpret_cast<float4*>(sn) = ps[0];
@@ -325,7 +328,7 @@ __global__ void __launch_bounds__(128) cache_append_kernel(const AppendParams pr
       if (r < prm.Hq) dst = prm.q_out + ((long long)t * prm.Hq + r) * D;
       else if (r < prm.Hq + prm.Hkv) dst = prm.k_pages + slot + (r - prm.Hq) * prm.head_stride;
       else dst = prm.v_pages + slot + (r - prm.Hq - prm.Hkv) * prm.head_stride;
-      if (LAYOUT != 0 && r < prm.Hq + prm.Hkv) {
+      if (LAYOUT != 0 && turn && r < prm.Hq + prm.Hkv) {
         uint32_t uu[4] = {u[j].x, u[j].y, u[j].z, u[j].w}, ww[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
         float a[8], z[8];  // the pairs' first and second elements
 #pragma unroll

@@ -27,8 +27,9 @@ struct AppendParams {
   long long table_stride;
   int max_pages, num_pages, page_shift;
   int B, T, Hq, Hkv;           // Hq = 0: no queries
-  const float *cos, *sin;      // [rope_len, d / 2]; null: no rotation
-  int rope_len;
+  const float *cos, *sin;      // [rope_len, rope_dim / 2]; null: no rotation
+  int rope_len, rope_dim;      // rope_dim: rotated columns, a multiple of 16
+  const int* positions;        // [T] positions of the rotation; null: where the token is written
   int* err;
 };
 cudaError_t launch_cache_append(const AppendParams& prm, int d, bool f16, int rope_layout, cudaStream_t stream);

@@ -326,12 +326,24 @@ fa_status fa_cache_append(const fa_kv_cache* cache, const void* q, const void* k
                           int64_t table_stride, int64_t max_pages, const int32_t* cu_q, const int32_t* seq_k,
                           int64_t B, int64_t T, int64_t Hq, const float* rope_cos, const float* rope_sin,
                           int64_t rope_len, int rope_layout, cudaStream_t stream) {
+  return fa_cache_append_at(cache, q, k, v, q_out, q_stride, k_stride, v_stride, block_table, table_stride, max_pages, cu_q,
+                            seq_k, B, T, Hq, rope_cos, rope_sin, rope_len, cache ? cache->d : 0, rope_layout, nullptr, stream);
+}
+
+fa_status fa_cache_append_at(const fa_kv_cache* cache, const void* q, const void* k, const void* v, void* q_out,
+                             int64_t q_stride, int64_t k_stride, int64_t v_stride, const int32_t* block_table,
+                             int64_t table_stride, int64_t max_pages, const int32_t* cu_q, const int32_t* seq_k,
+                             int64_t B, int64_t T, int64_t Hq, const float* rope_cos, const float* rope_sin,
+                             int64_t rope_len, int64_t rope_dim, int rope_layout, const int32_t* positions,
+                             cudaStream_t stream) {
   if (B < 0 || T < 0 || Hq < 0 || rope_len < 0) return FA_ERR_INVALID_ARG;
   if (rope_layout != 0 && rope_layout != FA_ROPE_INTERLEAVED && rope_layout != FA_ROPE_HALF) return FA_ERR_INVALID_ARG;
   fa_status st = check_cache(cache);
   if (st != FA_OK) return st;
+  if (rope_layout != 0 && (rope_dim < 16 || rope_dim > cache->d || rope_dim % 16 != 0)) return FA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return FA_OK;
   if ((st = check_batch(block_table, table_stride, max_pages, cu_q, seq_k, B, T)) != FA_OK) return st;
+  if (rope_layout != 0 && positions && !aligned4(positions)) return FA_ERR_INVALID_ARG;
   const int64_t d = cache->d, Hkv = cache->heads;
   if (rope_layout != 0 && (!rope_cos || !rope_sin || !aligned16(rope_cos) || !aligned16(rope_sin)))
     return FA_ERR_INVALID_ARG;
@@ -373,6 +385,8 @@ fa_status fa_cache_append(const fa_kv_cache* cache, const void* q, const void* k
   p.cos = rope_cos;
   p.sin = rope_sin;
   p.rope_len = (int)(rope_len < kMaxLen ? rope_len : kMaxLen);
+  p.rope_dim = (int)(rope_layout != 0 ? rope_dim : 0);
+  p.positions = positions;
   p.err = err;
   return fa::launch_cache_append(p, (int)d, cache->dtype == FA_DTYPE_FP16, rope_layout, stream) == cudaSuccess
              ? FA_OK

@@ -577,6 +577,127 @@ fa_status fa_cache_append(const fa_kv_cache* cache, const void* q, const void* k
                           const float* rope_cos, const float* rope_sin, int64_t rope_len, int rope_layout,
                           cudaStream_t stream);
 
+/*
+ * fa_cache_append_at -- fa_cache_append with the rotation's positions given, and
+ * of part of the head:
+ *   positions  [T] int32 (device): token t is turned by the angles of
+ *              positions[t]; where its key and value are written follows from cu_q
+ *              and seq_k all the same.  (The nodes of a tree of drafted tokens
+ *              lie one behind the other in the cache, but at positions by their
+ *              depth: see fa_tree_plan.)  NULL: by where it is written
+ *   rope_dim   the rotated columns, a multiple of 16 up to d; the tables are
+ *              [rope_len, rope_dim/2].  The columns behind them are copied
+ * fa_cache_append is this call with positions = NULL and rope_dim = d.  A token
+ * whose position lies outside the tables is dropped and reported.
+ * Errors: as fa_cache_append, FA_ERR_UNSUPPORTED also for another rope_dim
+ * (which is not looked at with rope_layout 0, nor are the positions).
+ */
+fa_status fa_cache_append_at(const fa_kv_cache* cache, const void* q, const void* k, const void* v, void* q_out,
+                             int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                             const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                             const int32_t* cu_q, const int32_t* seq_k, int64_t B, int64_t T, int64_t Hq,
+                             const float* rope_cos, const float* rope_sin, int64_t rope_len, int64_t rope_dim,
+                             int rope_layout, const int32_t* positions, cudaStream_t stream);
+
+/*
+ * ---- rotary positions ----
+ *
+ * Pair (a, b) of a row at position p becomes (a*c - b*s, a*s + b*c) with c =
+ * rope_cos[p][i], s = rope_sin[p][i], each product rounded to fp32 before the
+ * sum, the sum once to the element type.  The first rope_dim columns of a row
+ * are rotated -- pairs (2i, 2i+1) (FA_ROPE_INTERLEAVED) or (i, i + rope_dim/2)
+ * (FA_ROPE_HALF), i < rope_dim/2 -- and the columns behind them are copied.
+ */
+
+/*
+ * How a table's frequencies are scaled for contexts longer than a model was
+ * trained on.  With f_i = theta^(-2i/rope_dim) the unscaled angle per position
+ * of pair i, s = factor, and keep clamped to 0..1:
+ *   FA_ROPE_SCALE_NONE    f_i
+ *   FA_ROPE_SCALE_LINEAR  f_i / s
+ *   FA_ROPE_SCALE_BASE    f_i of theta * s^(rope_dim / (rope_dim - 2))
+ *   FA_ROPE_SCALE_TURNS   (1 - keep) f_i / s + keep f_i, with keep = (w_i - low)
+ *                         / (high - low) of the turns w_i = original f_i / 2 pi
+ *                         that the pair makes over the original length
+ *   FA_ROPE_SCALE_INDEX   the same with keep = 1 - (i - a) / max(b - a, 0.001)
+ *                         between the pairs a = max(0, floor(i(high))) and b =
+ *                         min(rope_dim - 1, ceil(i(low))), i(w) = rope_dim ln(original
+ *                         / (2 pi w)) / (2 ln theta) the (fractional) pair of w turns
+ * amplitude multiplies cosines and sines (with every kind; usually 1).
+ */
+enum {
+    FA_ROPE_SCALE_NONE = 0,
+    FA_ROPE_SCALE_LINEAR = 1,
+    FA_ROPE_SCALE_BASE = 2,
+    FA_ROPE_SCALE_TURNS = 3,
+    FA_ROPE_SCALE_INDEX = 4
+};
+typedef struct {
+    int kind;
+    double factor;      /* at least 1 */
+    double original;    /* TURNS, INDEX: the original length, at least 1 */
+    double low, high;   /* TURNS, INDEX: 0 <= low < high (INDEX: 0 < low) */
+    double amplitude;   /* finite */
+} fa_rope_scaling;
+
+/*
+ * fa_rope_table -- cosines and sines of the positions start .. start + n - 1,
+ * the tables that fa_rope, fa_cache_append, fa_cache_append_at and
+ * fa_quant_fp8_rope take.
+ *   rope_cos, rope_sin  [n, rope_dim/2] fp32 (device, written, 16-byte aligned)
+ *   rope_dim            a multiple of 16, at most 256
+ *   theta               above 1
+ *   scaling             as above (HOST pointer, read during the call), or NULL
+ * Angles are reduced exactly at every position: a value is within about two
+ * units of fp32's last place of the exact one.
+ * Errors: FA_ERR_INVALID_ARG for negative sizes, bad pointers, theta or scaling;
+ * FA_ERR_UNSUPPORTED for another rope_dim, n or start above 2^30, or a device
+ * other than sm_103.  n = 0 is a no-op.
+ */
+fa_status fa_rope_table(float* rope_cos, float* rope_sin, int64_t n, int64_t rope_dim, double theta, int64_t start,
+                        const fa_rope_scaling* scaling, cudaStream_t stream);
+
+/*
+ * One array that fa_rope turns: element (b, h, n, c) lies at x + b * x_batch +
+ * h * x_head + n * x_token + c, of the result at y + b * y_batch + ... (strides
+ * in elements, multiples of 8, of y at least d; one whose size is 1 is not
+ * looked at).  [B, heads, N, d], [N, heads, d] with B = 1, and slices of a fused
+ * projection are such arrays.  y = x with the same strides turns in place (and
+ * leaves the columns behind rope_dim alone); no other overlap is allowed.
+ */
+typedef struct {
+    const void* x;      /* device, 16-byte aligned */
+    void* y;            /* device, 16-byte aligned */
+    int64_t heads;
+    int64_t x_batch, x_head, x_token;
+    int64_t y_batch, y_head, y_token;
+} fa_rope_array;
+
+/*
+ * fa_rope -- rotates one or two arrays (a layer's queries and keys) by their
+ * positions, or back by them.
+ *   arrays, count  HOST array of 1 or 2 (read during the call); both have B
+ *                  batch entries of N tokens, and their own numbers of heads
+ *   positions      int32 (device): token n of entry b is at positions[b *
+ *                  pos_stride + n] (pos_stride 0: the same in every entry); or
+ *                  NULL: at offset + n
+ *   rope_cos, rope_sin  [rope_len, rope_dim/2] fp32 (device, 16-byte aligned)
+ *   rope_dim       a multiple of 16, at most d (64, 128 or 256)
+ *   inverse        1: sines negated, the transposed matrix.  It undoes the
+ *                  rotation, and it is its gradient: of sum(dy * rope(x)) by x
+ *   dtype          FA_DTYPE_BF16 or FA_DTYPE_FP16
+ * A row whose position from device memory lies outside the tables is not
+ * written, and reported by fa_check_device_error as FA_ERR_INDEX.
+ * Errors: FA_ERR_INVALID_ARG for bad pointers, alignment, sizes, strides,
+ * layout, flags, or offset + N above rope_len without positions;
+ * FA_ERR_UNSUPPORTED for d, rope_dim or sizes outside the above (N, B, rope_len
+ * and offset at most 2^30, heads 2^20) or a device other than sm_103.
+ * B * N * heads = 0 is a no-op.
+ */
+fa_status fa_rope(const fa_rope_array* arrays, int64_t count, int64_t B, int64_t N, int64_t d, const int32_t* positions,
+                  int64_t pos_stride, int64_t offset, const float* rope_cos, const float* rope_sin, int64_t rope_len,
+                  int64_t rope_dim, int rope_layout, int inverse, int dtype, cudaStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fa_status_string(fa_status status);
 
