@@ -21,7 +21,8 @@ import torch
 from .build import LIB as _LIB_PATH
 
 __all__ = ["fwd_host", "fwd_host_workspace_bytes", "bwd", "bwd_workspace_bytes", "fwd_splitkv", "splitkv_workspace_bytes", "fwd", "fwd_gqa", "fwd_window", "bwd_window", "bwd_window_workspace_bytes",
-           "fwd_paged", "paged_workspace_bytes", "cache_append", "rope", "rope_table", "fwd_fp8", "fwd_fp8_gqa", "quant_fp8", "quant_fp8_per_tensor_noalloc", "check_device_error", "lib",
+           "fwd_paged", "paged_workspace_bytes", "cache_append", "rope", "rope_table", "pages_resize", "pages_fork",
+           "cache_copy", "cache_compact", "fwd_fp8", "fwd_fp8_gqa", "quant_fp8", "quant_fp8_per_tensor_noalloc", "check_device_error", "lib",
            "FaError", "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
            "FA_ERR_SCRATCH_LIMIT", "FA_ERR_INDEX", "FA_DTYPE_BF16", "FA_DTYPE_FP16", "FP8_BLOCK_ROWS",
            "FA_ROPE_INTERLEAVED", "FA_ROPE_HALF", "FA_ROPE_SCALE_NONE", "FA_ROPE_SCALE_LINEAR", "FA_ROPE_SCALE_BASE",
@@ -124,6 +125,14 @@ def _lib():
         lib.fa_rope_table.restype = i32
         lib.fa_rope.argtypes = [packed, i64, i64, i64, i64, vp, i64, i64, vp, vp, i64, i64, i32, i32, i32, vp]
         lib.fa_rope.restype = i32
+        lib.fa_pages_resize.argtypes = [vp, i64, i64, vp, i64, i64, vp, vp, i64, vp]
+        lib.fa_pages_resize.restype = i32
+        lib.fa_pages_fork.argtypes = [cache, i64, i64, vp, vp, i64, i64, vp, i64, vp, vp, vp, i64, vp]
+        lib.fa_pages_fork.restype = i32
+        lib.fa_cache_copy.argtypes = [cache, i64, i64, vp, vp, i64, vp]
+        lib.fa_cache_copy.restype = i32
+        lib.fa_cache_compact.argtypes = [cache, i64, i64, vp, i64, i64, vp, vp, i64, i64, vp, vp, i64, vp]
+        lib.fa_cache_compact.restype = i32
         lib.fa_status_string.argtypes = [i32]
         lib.fa_status_string.restype = ctypes.c_char_p
         lib.fa_check_device_error.argtypes = [vp]
@@ -728,6 +737,125 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, rope, positions: torch.Tensor 
     if st != FA_OK:
         raise FaError(st, "fa_rope")
     return q_out, k_out
+
+
+def _layers(k_pages, v_pages):
+    """The ``fa_kv_cache`` of the first layer, the number of layers, the
+    elements between them and the device index, of pages [num_pages, heads,
+    page_size, d] or [layers, num_pages, heads, page_size, d]."""
+    if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 5 and isinstance(v_pages, torch.Tensor) and v_pages.dim() == 5:
+        n = k_pages.shape[0]
+        if n == 0 or v_pages.shape[0] != n or v_pages.stride(0) != k_pages.stride(0):
+            raise ValueError("k_pages and v_pages must have the same layers, at least one, and the same strides")
+        cache, _, _, _, index = _cache(k_pages[0], v_pages[0])
+        return cache, n, k_pages.stride(0), index
+    cache, _, _, _, index = _cache(k_pages, v_pages)
+    return cache, 1, 0, index
+
+
+def _check_ints(index, **tensors):
+    for name, t in tensors.items():
+        if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 1 or t.get_device() != index \
+                or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous 1-D int32 tensor on cuda:{index}")
+
+
+def _check_table(block_table, rows, index):
+    """(table stride, table width) of a block table with a row for each of ``rows``."""
+    if isinstance(block_table, torch.Tensor) and block_table.dtype is torch.int32 and block_table.dim() == 2 \
+            and block_table.get_device() == index and block_table.shape[0] == rows \
+            and (block_table.shape[1] < 2 or block_table.stride(1) == 1):
+        return block_table.stride(0), block_table.shape[1]
+    raise ValueError(f"block_table must be an int32 [{rows}, max_pages] tensor on cuda:{index}, each row contiguous")
+
+
+def pages_resize(refs: torch.Tensor, block_table: torch.Tensor, seq_k: torch.Tensor, want: torch.Tensor, page_size: int):
+    """Rows of a block table give back pages or get free ones
+    (``fa_pages_resize``), in place: refs [num_pages] (0: a free page),
+    block_table [B, max_pages], seq_k [B] the tokens that a row holds pages for,
+    want [B] those that it shall, all int32.  Afterwards seq_k is want, or less
+    where the pages ran out."""
+    index = refs.get_device() if isinstance(refs, torch.Tensor) else -1
+    if index < 0:
+        raise ValueError("refs must be a CUDA tensor")
+    _check_ints(index, refs=refs, seq_k=seq_k, want=want)
+    B = seq_k.shape[0]
+    if want.shape[0] != B:
+        raise ValueError("want must have seq_k's length")
+    stride, width = _check_table(block_table, B, index)
+    with _guard(index):
+        st = _lib().fa_pages_resize(refs.data_ptr(), refs.shape[0], _count(page_size), block_table.data_ptr(), stride, width,
+                                    seq_k.data_ptr(), want.data_ptr(), B, _current_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_pages_resize")
+
+
+def pages_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, refs: torch.Tensor, block_table: torch.Tensor,
+               seq_k: torch.Tensor, src: torch.Tensor, dst: torch.Tensor):
+    """Row dst[i] becomes a second copy of the sequence in row src[i]
+    (``fa_pages_fork``), in place: it shares the full pages and gets a copy of the
+    last, partly filled one.  Pages as in ``fwd_paged``, or of all layers [layers,
+    num_pages, heads, page_size, d]; refs [num_pages], block_table [rows,
+    max_pages], seq_k [rows], src and dst [n], int32.  Rows dst are empty before
+    (seq_k 0), not among src and given once.  Returns fresh [n]: the page that a
+    fork got, -1: none was needed, -2: refused, -3: no page was left."""
+    cache, layers, layer_stride, index = _layers(k_pages, v_pages)
+    _check_ints(index, refs=refs, seq_k=seq_k, src=src, dst=dst)
+    if refs.shape[0] != k_pages.shape[-4]:
+        raise ValueError("refs must have an entry for each page")
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have the same length")
+    rows, n = seq_k.shape[0], src.shape[0]
+    stride, width = _check_table(block_table, rows, index)
+    fresh = torch.empty_like(src)
+    with _guard(index):
+        st = _lib().fa_pages_fork(cache, layers, layer_stride, refs.data_ptr(), block_table.data_ptr(), stride, width,
+                                  seq_k.data_ptr(), rows, src.data_ptr(), dst.data_ptr(), fresh.data_ptr(), n,
+                                  _current_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_pages_fork")
+    return fresh
+
+
+def cache_copy(k_pages: torch.Tensor, v_pages: torch.Tensor, src: torch.Tensor, dst: torch.Tensor):
+    """Copies page src[i] to page dst[i] (``fa_cache_copy``), keys and values of
+    all layers (pages as in ``pages_fork``); src and dst int32 [n], no page twice
+    in dst or in both."""
+    cache, layers, layer_stride, index = _layers(k_pages, v_pages)
+    _check_ints(index, src=src, dst=dst)
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have the same length")
+    with _guard(index):
+        st = _lib().fa_cache_copy(cache, layers, layer_stride, src.data_ptr(), dst.data_ptr(), src.shape[0],
+                                  _current_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_copy")
+
+
+def cache_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor, first: torch.Tensor,
+                  keep: torch.Tensor, keep_n: torch.Tensor):
+    """Moves the kept tokens of each sequence together (``fa_cache_compact``), in
+    place: for i < keep_n[b], position keep[b, i] goes to position first[b] + i,
+    in all layers (pages as in ``pages_fork``).  block_table [B, max_pages], first
+    [B], keep [B, max_keep] with keep[b, i] >= first[b] + i (any ascending list
+    from first[b] on), keep_n [B], int32.  Returns the new lengths first + keep_n."""
+    cache, layers, layer_stride, index = _layers(k_pages, v_pages)
+    _check_ints(index, first=first, keep_n=keep_n)
+    B = first.shape[0]
+    if keep_n.shape[0] != B:
+        raise ValueError("keep_n must have first's length")
+    if not isinstance(keep, torch.Tensor) or keep.dtype is not torch.int32 or keep.dim() != 2 or keep.shape[0] != B \
+            or keep.get_device() != index or (keep.shape[1] > 1 and keep.stride(1) != 1):
+        raise ValueError(f"keep must be an int32 [{B}, max_keep] tensor on cuda:{index}, each row contiguous")
+    stride, width = _check_table(block_table, B, index)
+    seq_k = torch.empty_like(first)
+    with _guard(index):
+        st = _lib().fa_cache_compact(cache, layers, layer_stride, block_table.data_ptr(), stride, width, first.data_ptr(),
+                                     keep.data_ptr(), keep.stride(0), keep.shape[1], keep_n.data_ptr(), seq_k.data_ptr(), B,
+                                     _current_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_cache_compact")
+    return seq_k
 
 
 def fwd_fp8_gqa(q8, k8, v8, q_descale, k_descale, v_descale, causal: bool = False,

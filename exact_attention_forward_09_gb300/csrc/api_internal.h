@@ -27,6 +27,11 @@ fa_status internal_encode_map(CUtensorMap* map, const void* base, CUtensorMapDat
 fa_status internal_encode_map_nd(CUtensorMap* map, const void* base, CUtensorMapDataType dt, int rank,
                                  const uint64_t* dims, const uint64_t* strides, const uint32_t* box);
 
+// The layout of a cache (window_api.cu): sizes, strides that a TMA map can
+// describe, a page size that boxes of whole 8-row swizzle groups cover.
+fa_status internal_check_cache(const fa_kv_cache* cache);
+int internal_shift_of(int64_t page_size);
+
 // The failure injection asked for by fa_debug_inject (bit 0), consumed.
 bool internal_take_inject();
 

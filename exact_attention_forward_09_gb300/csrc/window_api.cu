@@ -146,6 +146,11 @@ int shift_of(int64_t page_size) {
 
 }  // namespace
 
+namespace fa {
+fa_status internal_check_cache(const fa_kv_cache* cache) { return check_cache(cache); }
+int internal_shift_of(int64_t page_size) { return shift_of(page_size); }
+}  // namespace fa
+
 extern "C" {
 
 fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int64_t B, int64_t Hq,

@@ -698,6 +698,112 @@ fa_status fa_rope(const fa_rope_array* arrays, int64_t count, int64_t B, int64_t
                   int64_t pos_stride, int64_t offset, const float* rope_cos, const float* rope_sin, int64_t rope_len,
                   int64_t rope_dim, int rope_layout, int inverse, int dtype, cudaStream_t stream);
 
+/*
+ * ---- the pages of a cache ----
+ *
+ * A pool of pages is its reference counts: refs[p], int32 (device, 16-byte
+ * aligned), is how many rows of the block table hold page p, 0 for a free page.
+ * Row r of the table holds the pages of its first seq_k[r] tokens, one entry for
+ * each page begun; entries behind them are -1 or not looked at.  The calls below
+ * keep the three in step, on the device and in stream order, so a captured graph
+ * can hold them; a free page is always handed out lowest number first, so that
+ * results do not depend on timing.  Calls that change one pool must not overlap
+ * on the GPU.
+ *
+ * fa_pages_fork, fa_cache_copy and fa_cache_compact move keys and values in all
+ * layers of a cache at once: `cache` describes the first, and layer l lies l *
+ * layer_stride elements behind it (a multiple of 8; not looked at for one layer),
+ * at most 32767.
+ */
+
+/*
+ * fa_pages_resize -- rows of a block table shrink or grow.  Rows with want[r] <
+ * seq_k[r] give back the pages that want[r] tokens do not need (want 0: all);
+ * then rows with want[r] > seq_k[r] get pages, the lowest-numbered free ones, in
+ * the order of rows.  Entries given back become -1.
+ *   refs         [num_pages] int32 (device, read and written)
+ *   page_size    a power of two, 16 to 1024
+ *   block_table  [B, max_pages] int32 (device, read and written), rows
+ *                table_stride apart
+ *   seq_k        [B] int32 (device, read and written): afterwards want[r], or if
+ *                the pages ran out as many tokens as the row has pages for
+ *                (its entries that got none are -1)
+ *   want         [B] int32 (device, read only)
+ * Pages are not written: new ones hold what they held.  A page that several rows
+ * share is free once the last of them has given it back.
+ * Lengths below 0 or above max_pages * page_size are cut, page numbers outside
+ * the pool and pages that nobody held are passed over, and both are reported by
+ * fa_check_device_error as FA_ERR_INDEX.
+ * Errors: FA_ERR_INVALID_ARG for bad pointers, alignment or sizes;
+ * FA_ERR_UNSUPPORTED for page_size outside the above, B above 49152, max_pages
+ * above 2^30 or a device other than sm_103.  B = 0 is a no-op.
+ */
+fa_status fa_pages_resize(int32_t* refs, int64_t num_pages, int64_t page_size, int32_t* block_table, int64_t table_stride,
+                          int64_t max_pages, int32_t* seq_k, const int32_t* want, int64_t B, cudaStream_t stream);
+
+/*
+ * fa_pages_fork -- row dst[i] becomes a second copy of the sequence in row
+ * src[i]: it shares the source's full pages, and gets the lowest-numbered free
+ * page for a last page that is partly filled, whose rows are copied.  (So pages
+ * that are shared are full, and both sequences go on without writing into them.)
+ *   refs         [cache->num_pages] int32 (device, read and written)
+ *   block_table  [rows, max_pages] int32 (device, read and written)
+ *   seq_k        [rows] int32 (device, read and written)
+ *   src, dst     [n] int32 (device, read only).  A source may be given several
+ *                times.  A row dst[i] holds no tokens (seq_k 0: give its pages back
+ *                first), and is neither given twice nor a source
+ *   fresh        [n] int32 (device, written): the page that the fork got, -1 if
+ *                it needed none, -2 if it was refused, -3 if no page was left
+ * Forks take their pages in the order of i.  One that breaks the above, or whose
+ * source has a bad length or last page, is refused as a whole and reported by
+ * fa_check_device_error as FA_ERR_INDEX; one without a page is not done, and not
+ * reported.
+ * Errors: FA_ERR_INVALID_ARG for bad pointers, alignment, sizes or strides;
+ * FA_ERR_UNSUPPORTED for a cache outside fa_kv_cache's limits, rows above 2^18, n
+ * above 16384, a page of one layer's keys above 32 GiB, or a device other than
+ * sm_103.  n = 0 is a no-op.
+ */
+fa_status fa_pages_fork(const fa_kv_cache* cache, int64_t layers, int64_t layer_stride, int32_t* refs, int32_t* block_table,
+                        int64_t table_stride, int64_t max_pages, int32_t* seq_k, int64_t rows, const int32_t* src,
+                        const int32_t* dst, int32_t* fresh, int64_t n, cudaStream_t stream);
+
+/*
+ * fa_cache_copy -- copies page src[i] to page dst[i], keys and values of all
+ * layers, i < n (both [n] int32, device).  No page may be given twice in dst, or
+ * in both (their contents are then not defined).  A pair with a page number
+ * outside the cache is passed over and reported by fa_check_device_error as
+ * FA_ERR_INDEX.  Errors: as fa_pages_fork.  n * layers = 0 is a no-op.
+ */
+fa_status fa_cache_copy(const fa_kv_cache* cache, int64_t layers, int64_t layer_stride, const int32_t* src, const int32_t* dst,
+                        int64_t n, cudaStream_t stream);
+
+/*
+ * fa_cache_compact -- moves the tokens of each sequence that are kept together:
+ * for i < keep_n[b], the keys and values at position keep[b][i] of sequence b go
+ * to position first[b] + i, as if all were read before one is written.  With
+ * first = the cached tokens before a step it keeps the accepted ones of the
+ * step's drafted tokens; with first = 0 it evicts tokens from a cache.
+ *   block_table  [B, max_pages] int32 (device, read only)
+ *   first        [B] int32 (device, read only)
+ *   keep         [B, max_keep] int32 (device, read only), rows keep_stride apart;
+ *                keep[b][i] >= first[b] + i, as in any ascending list of positions
+ *                from first[b] on
+ *   keep_n       [B] int32 (device, read only)
+ *   seq_k_out    [B] int32 (device, written): first[b] + keep_n[b].  Not one of
+ *                the inputs
+ * The table is not changed: fa_pages_resize gives back the pages behind the new
+ * lengths.  Pages that are written to must not be shared with another sequence.
+ * Counts are cut to max_keep, and positions that are out of range, lead to no
+ * page or break the above are passed over; both are reported by
+ * fa_check_device_error as FA_ERR_INDEX.
+ * Errors: as fa_pages_fork, FA_ERR_UNSUPPORTED for B above 2^24 or B * heads
+ * above 2^29.  B = 0 is a no-op.
+ */
+fa_status fa_cache_compact(const fa_kv_cache* cache, int64_t layers, int64_t layer_stride, const int32_t* block_table,
+                           int64_t table_stride, int64_t max_pages, const int32_t* first, const int32_t* keep,
+                           int64_t keep_stride, int64_t max_keep, const int32_t* keep_n, int32_t* seq_k_out, int64_t B,
+                           cudaStream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char* fa_status_string(fa_status status);
 
