@@ -21,7 +21,7 @@ import torch
 from .build import LIB as _LIB_PATH
 
 __all__ = ["fwd_host", "fwd_host_workspace_bytes", "bwd", "bwd_workspace_bytes", "fwd_splitkv", "splitkv_workspace_bytes", "fwd", "fwd_gqa", "fwd_window", "bwd_window", "bwd_window_workspace_bytes",
-           "fwd_paged", "paged_workspace_bytes", "cache_append", "rope", "rope_table", "pages_resize", "pages_fork",
+           "fwd_paged", "paged_workspace_bytes", "tree_plan", "fwd_tree", "cache_append", "rope", "rope_table", "pages_resize", "pages_fork",
            "cache_copy", "cache_compact", "fwd_fp8", "fwd_fp8_gqa", "quant_fp8", "quant_fp8_per_tensor_noalloc", "check_device_error", "lib",
            "FaError", "FA_OK", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED", "FA_ERR_CUDA", "FA_ERR_TIMEOUT",
            "FA_ERR_SCRATCH_LIMIT", "FA_ERR_INDEX", "FA_DTYPE_BF16", "FA_DTYPE_FP16", "FP8_BLOCK_ROWS",
@@ -114,6 +114,10 @@ def _lib():
         lib.fa_paged_workspace_bytes.restype = i32
         lib.fa_fwd_paged.argtypes = [vp, cache, vp, vp, vp, i64, i64, vp, vp] + [i64] * 7 + [f32, vp, ctypes.c_size_t, vp]
         lib.fa_fwd_paged.restype = i32
+        lib.fa_tree_plan.argtypes = [vp, vp, vp, i64, i64, vp, i64, vp, vp]
+        lib.fa_tree_plan.restype = i32
+        lib.fa_fwd_tree.argtypes = [vp, cache, vp, vp, vp, i64, i64, vp, vp, vp, i64, vp] + [i64] * 7 + [f32, vp, ctypes.c_size_t, vp]
+        lib.fa_fwd_tree.restype = i32
         lib.fa_cache_append.argtypes = [cache, vp, vp, vp, vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, i64, i64, vp,
                                         vp, i64, i32, vp]
         lib.fa_cache_append.restype = i32
@@ -546,6 +550,10 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, blo
     ``window`` None: every key up to a query's own.  ``max_q``: the most new
     tokens of any sequence, if known.  Returns (O [T, Hq, d], LSE [T, Hq]);
     rows outside every sequence are left as they were."""
+    return _fwd_paged(q, k_pages, v_pages, block_table, cu_q, seq_k, None, None, window, sinks, scale, max_q, out, lse, workspace)
+
+
+def _fwd_paged(q, k_pages, v_pages, block_table, cu_q, seq_k, mask, positions, window, sinks, scale, max_q, out, lse, workspace):
     cache, heads, d, dt, index = _cache(k_pages, v_pages)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a [T, Hq, d] CUDA tensor")
@@ -563,19 +571,77 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, blo
         lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
     else:
         _check_out("lse", lse, (T, Hq), torch.float32, index)
+    if mask is not None:
+        if not isinstance(mask, torch.Tensor) or mask.dim() != 2:
+            raise ValueError("mask must be an int32 [T, words] tensor")
+        _check_out("mask", mask, (T, mask.shape[1]), torch.int32, index)
+        if positions is not None:
+            _check_out("positions", positions, (T,), torch.int32, index)
     with _guard(index):
         if workspace is None:
             need = _PAGED_BYTES.get((index, d))
             if need is None:
                 need = _PAGED_BYTES[index, d] = paged_workspace_bytes(d)
             workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-        st = _lib().fa_fwd_paged(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
-                                 table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), B, T, Hq, q_stride,
-                                 _count(max_q), 1 << 30 if window is None else _count(window), _count(sinks), _scale(scale, d),
-                                 *_workspace(workspace, index), _current_stream(index))
+        sizes = (B, T, Hq, q_stride, _count(max_q), 1 << 30 if window is None else _count(window), _count(sinks), _scale(scale, d),
+                 *_workspace(workspace, index), _current_stream(index))
+        if mask is None:
+            st = _lib().fa_fwd_paged(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
+                                     table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), *sizes)
+        else:
+            st = _lib().fa_fwd_tree(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
+                                    table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), mask.data_ptr(), mask.shape[1],
+                                    None if positions is None else positions.data_ptr(), *sizes)
     if st != FA_OK:
-        raise FaError(st, "fa_fwd_paged")
+        raise FaError(st, "fa_fwd_paged" if mask is None else "fa_fwd_tree")
     return out, lse
+
+
+def tree_plan(parents: torch.Tensor, cu_q: torch.Tensor, seq_k: torch.Tensor, max_tree: int,
+              mask: torch.Tensor | None = None, positions: torch.Tensor | None = None):
+    """Lays out trees of drafted tokens (``fa_tree_plan``): parents int32 [T],
+    each a node's parent by its number within its sequence, or -1; cu_q and
+    seq_k as in ``fwd_paged``; ``max_tree``: the most nodes of a tree, up to 1024
+    (sequences of more tokens than its next multiple of 32 are chunks of a
+    prompt).  Returns (mask int32 [T, ceil(max_tree / 32)], positions int32 [T])
+    for ``fwd_tree`` and ``cache_append``."""
+    index = parents.get_device() if isinstance(parents, torch.Tensor) else -1
+    if index < 0:
+        raise ValueError("parents must be a CUDA tensor")
+    _check_ints(index, parents=parents, cu_q=cu_q, seq_k=seq_k)
+    T, B, words = parents.shape[0], seq_k.shape[0], (_count(max_tree) + 31) // 32
+    if cu_q.shape[0] != B + 1:
+        raise ValueError("cu_q must have one entry more than seq_k")
+    if not 1 <= words <= 32:
+        raise ValueError("max_tree must be 1 to 1024")
+    if mask is None:
+        mask = torch.empty((T, words), dtype=torch.int32, device=parents.device)
+    else:
+        _check_out("mask", mask, (T, words), torch.int32, index)
+    if positions is None:
+        positions = torch.empty((T,), dtype=torch.int32, device=parents.device)
+    else:
+        _check_out("positions", positions, (T,), torch.int32, index)
+    with _guard(index):
+        st = _lib().fa_tree_plan(parents.data_ptr(), cu_q.data_ptr(), seq_k.data_ptr(), B, T, mask.data_ptr(), words,
+                                 positions.data_ptr(), _current_stream(index))
+    if st != FA_OK:
+        raise FaError(st, "fa_tree_plan")
+    return mask, positions
+
+
+def fwd_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: torch.Tensor,
+             cu_q: torch.Tensor, seq_k: torch.Tensor, mask: torch.Tensor, positions: torch.Tensor | None = None,
+             window: int | None = None, sinks: int = 0, scale: float | None = None, max_q: int = 0,
+             out: torch.Tensor | None = None, lse: torch.Tensor | None = None, workspace: torch.Tensor | None = None):
+    """``fwd_paged`` where the new tokens of a sequence are the nodes of a tree
+    (``fa_fwd_tree``): each sees the cached keys (under a window by its own
+    position, from ``positions`` int32 [T]) and the new tokens up to itself that
+    its row of ``mask`` (int32 [T, words], 32 tokens of its sequence to a word)
+    has a bit for.  Sequences of more than 32 * words new tokens are plain chunks."""
+    if mask is None:
+        raise ValueError("mask must be an int32 [T, words] tensor")
+    return _fwd_paged(q, k_pages, v_pages, block_table, cu_q, seq_k, mask, positions, window, sinks, scale, max_q, out, lse, workspace)
 
 
 def _check_rope(rope, index):

@@ -22,10 +22,12 @@ LIB = os.path.join(HERE, "libfa.so")
 LIB_ABLATE = os.path.join(HERE, "libfa_ablate.so")
 UNITS = ["api.cu", "attn_bf16.cu", "attn_fp16.cu", "attn_fp8.cu", "quant_fp8.cu", "quant_fp8_noalloc.cu",
          "splitkv.cu", "attn_split_bf16.cu", "attn_split_fp16.cu", "attn_bwd.cu", "window_api.cu", "attn_window_bf16.cu",
-         "attn_window_fp16.cu", "attn_paged_bf16.cu", "attn_paged_fp16.cu", "paged.cu", "rope.cu", "rope_api.cu", "pages.cu", "pages_api.cu"]
+         "attn_window_fp16.cu", "attn_paged_bf16.cu", "attn_paged_fp16.cu", "paged.cu", "rope.cu", "rope_api.cu", "pages.cu", "pages_api.cu",
+         "attn_tree_bf16.cu", "attn_tree_fp16.cu", "tree.cu"]
 ABLATE_UNITS = ["ablate_api.cu", "ablate_bf16.cu", "ablate_bf16_causal.cu", "ablate_fp8.cu", "ablate_d64.cu"]
 HEADERS = ["ptx.cuh", "attn_fwd.cuh", "quant_fp8.h", "attn_bwd.h", "splitkv.h", "ablate_inst.h", "api_internal.h",
-           "attn_window.cuh", "paged.h", "ptx_window.cuh", "rope.h", "pages.h"]
+           "attn_window.cuh", "paged.h", "ptx_window.cuh", "rope.h", "pages.h",
+           "tree.h", "paged_search.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -34,6 +34,15 @@
 //     the sequence's end in its last page, pages that left the window) may be
 //     anything, NaN included: its scores are replaced, and its V rows are
 //     zeroed in shared memory before P V.
+// and for TREE (of PAGED), where a sequence's new tokens are the nodes of a tree:
+//   * a node's row sees the cached keys by its own position (the window's start)
+//     and the new keys by the bits of its mask row.  Only the tiles that hold a new
+//     key are masked so (one or two at the end of a context), and the words of such
+//     a tile are on their way before its scores are waited for;
+//   * every unit of a sequence starts its window at the first position that a
+//     node can have, the cached tokens' end, as a node's position is known to its own
+//     row alone; nodes lie one behind the other up to their own slot, as tokens do;
+//   * sequences of more tokens than a mask row has bits are plain chunks.
 //
 // Roundings.  Scores, maxima, sums, O and the parts that are joined are fp32.  P
 // is rounded to the element type: both operands of a 16-bit MMA have one type, and
@@ -207,6 +216,10 @@ struct WinParams {
   float* o_part;      // [2 * grid][slot rows][D] partial results of cut units
   float* lse_part;    // [2 * grid][slot rows], NQT * 128 of them
   int4* desc;         // [grid] cut units: {parts, first token, kv head, rows}
+  // trees
+  const uint32_t* mask;  // [T, words] which new tokens of its sequence a token sees
+  const int* positions;  // [T] positions of the tokens in their sequence; null: where they lie
+  int words;             // 32 words is at most 2^30
 };
 
 // The key tiles that a unit of up to two query tiles visits.
@@ -228,14 +241,17 @@ __host__ __device__ __forceinline__ void win_range(int first, int last, int wind
   if (sk > w1) sk = w1;
 }
 
-// p0: position of the unit's first token; ntok: its valid tokens, tpt to a query tile.
-__host__ __device__ __forceinline__ WinTiles win_tiles(int p0, int ntok, int tpt, int nqt, int window, int sinks) {
+// p0: position of the unit's first token; ntok: its valid tokens, tpt to a query tile;
+// base: a position at which any of them may sit (trees).
+__host__ __device__ __forceinline__ WinTiles win_tiles(int p0, int ntok, int tpt, int nqt, int window, int sinks,
+                                                       int base = 0x7fffffff) {
   WinTiles u;
   int w0[2] = {0, 0}, w1[2] = {0, 0}, sk[2] = {0, 0};
   const int n0 = ntok < tpt ? ntok : tpt;
-  win_range(p0, p0 + n0 - 1, window, sinks, w0[0], w1[0], sk[0]);
+  auto from = [&](int first) { return first < base ? first : base; };
+  win_range(from(p0), p0 + n0 - 1, window, sinks, w0[0], w1[0], sk[0]);
   const bool two = nqt == 2 && ntok > tpt;
-  if (two) win_range(p0 + tpt, p0 + ntok - 1, window, sinks, w0[1], w1[1], sk[1]);
+  if (two) win_range(from(p0 + tpt), p0 + ntok - 1, window, sinks, w0[1], w1[1], sk[1]);
   const int top = two ? w1[1] : w1[0];
   u.ns = two ? sk[1] : sk[0];
   u.skip = w0[0] > u.ns ? w0[0] - u.ns : 0;
@@ -318,13 +334,16 @@ __device__ __forceinline__ WinSeq win_seq(const WinParams& prm, int a, int e, in
   if (s.tok0 != a || end != e || s.nk != n) *bad = true;
   return s;
 }
+// Whether a sequence's nq new tokens are a tree's nodes (else a plain chunk).
+__device__ __forceinline__ bool win_is_tree(const WinParams& prm, int nq) { return nq <= 32 * prm.words; }
 // Key tiles of query group i (at least 1, so that a group without visible
 // keys still has its place on the line and gets its zero rows written).
+template <bool TREE>
 __device__ __forceinline__ int win_group_len(const WinParams& prm, const WinSeq& s, int tpg, int i) {
   const int first = s.nk - s.nq + i * tpg;
   const int last = min(first + tpg, s.nk) - 1;
   int w0, w1, sk;
-  win_range(first, last, prm.window, prm.sinks, w0, w1, sk);
+  win_range(TREE && win_is_tree(prm, s.nq) ? s.nk - s.nq : first, last, prm.window, prm.sinks, w0, w1, sk);
   const int len = w1 - max(0, w0 - sk);
   return len > 0 ? len : 1;
 }
@@ -349,6 +368,20 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
 // its own, and from its window's first on or below `sinks`.
 __device__ __forceinline__ uint32_t win_visible(int p, int window, int sinks, int c0) {
   return low_bits(p + 1 - c0) & (~low_bits(p - window + 1 - c0) | low_bits(sinks - c0));
+}
+
+// Which of the 32 keys from c0 on a tree's node sees that sits at position p and
+// lies at `slot`: the cached keys (below ctx) as above, and the new ones up to
+// its own that its mask row has a bit for.
+__device__ __forceinline__ uint32_t tree_visible(const uint32_t* row, int words, int ctx, int slot, int p, int window, int sinks, int c0) {
+  const uint32_t cached = low_bits(ctx - c0);
+  uint32_t see = cached & (~low_bits(p - window + 1 - c0) | low_bits(sinks - c0));
+  const int rel = c0 - ctx, w = rel >> 5;  // (may be negative: the words begin inside these keys)
+  if (row != nullptr && w >= -1 && w < words) {
+    const uint32_t lo = w >= 0 ? __ldg(row + w) : 0u, hi = w + 1 < words ? __ldg(row + w + 1) : 0u;
+    see |= __funnelshift_r(lo, hi, rel & 31) & low_bits(slot + 1 - c0) & ~cached;
+  }
+  return see;
 }
 
 // The softmax of a narrow tile, the first one of its rows: 32 columns of S at
@@ -382,6 +415,36 @@ __device__ __noinline__ float2 narrow_softmax(uint32_t s_addr, uint32_t see, flo
   tmem_wait_st();
   return make_float2(m, l);
 }
+
+// What a row of a unit needs to know which keys it sees, where its sequence's
+// new tokens are a tree.  tok: its token in the unit, -1: the row does not exist
+// (it sees what any would).
+template <bool TREE>
+struct WinTreeRow {
+  bool tree;
+  int ctx, slot, pos;
+  const uint32_t* row;
+  __device__ __forceinline__ WinTreeRow(const WinParams& prm, const WinUnit& w, int tok, int at) {
+    tree = false;
+    if constexpr (TREE) {
+      ctx = w.p0 - w.q_row;
+      tree = win_is_tree(prm, w.nk - ctx);
+      if (!tree) return;
+      pos = slot = w.p0 + at;
+      row = nullptr;
+      if (tok < 0) return;
+      row = prm.mask + (long long)(w.qz + tok) * prm.words;
+      if (prm.positions) {
+        const int p = prm.positions[w.qz + tok];
+        pos = min(max(p, ctx), slot);  // (a node has as many nodes above it as lie before it at most)
+        if (p != pos) report_index(prm.err);
+      }
+    }
+  }
+  __device__ __forceinline__ uint32_t see(const WinParams& prm, int c0) const {
+    return tree_visible(row, prm.words, ctx, slot, pos, prm.window, prm.sinks, c0);
+  }
+};
 
 // Waits for the V tile at ring position pv and, where `dead`, zeroes this
 // thread's row of it (row: its shared-memory address in slot 0); made visible
@@ -456,14 +519,16 @@ __device__ __forceinline__ void cluster_join(uint8_t* smem, const WinUnit& w, co
   }
 }
 
-template <int ELEM, int D, bool PAGED, int FORM>
+template <int ELEM, int D, bool PAGED, int FORM, bool TREE>
 __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<ELEM, D, PAGED, FORM>::OCC)
     attn_window_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o,
                        const WinParams prm) {
   using C = WinCfg<ELEM, D, PAGED, FORM>;
   using Bars = WinBars<C::NS>;
+  using TreeRow = WinTreeRow<TREE>;
   static_assert(sizeof(Bars) <= 1024, "barrier area");
+  static_assert(!TREE || PAGED, "trees lie in a paged cache");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars* bars = reinterpret_cast<Bars*>(smem + C::OFF_BAR);
@@ -543,7 +608,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
       return win_seq(prm, prm.cu_q[b], prm.cu_q[b + 1], prm.seq_k[b], &bad);
     };
     auto group_places = [&](const WinSeq& q, int i) -> uint32_t {
-      return win_places<C::NQT>(win_group_len(prm, q, tpg, i), min(tpg, q.nq - i * tpg), tpt) * (uint32_t)prm.Hkv;
+      return win_places<C::NQT>(win_group_len<TREE>(prm, q, tpg, i), min(tpg, q.nq - i * tpg), tpt) * (uint32_t)prm.Hkv;
     };
     auto add = [&](uint32_t a, uint32_t b) -> uint32_t { return min(a + b, prm.max_places + 1); };  // (both at most that)
     auto seq_places = [&](const WinSeq& q) -> uint32_t {
@@ -599,7 +664,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
       bars->start_nq = q.nq;
       bars->start_nk = q.nk;
       bars->start_group = i;
-      bars->start_len = win_group_len(prm, q, tpg, i);
+      bars->start_len = win_group_len<TREE>(prm, q, tpg, i);
       bars->start_off = line0 - at;
     }
     if (bad && blockIdx.x == 0) report_index(prm.err);
@@ -808,8 +873,11 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
             w.p0 = s.nk - s.nq + w.q_row;
             w.ntok = ntok;
             w.nk = s.nk;
-            w.lo = max(0, w.p0 - prm.window + 1);
-            const WinTiles u = win_tiles(w.p0, w.ntok, tpt, C::NQT, prm.window, prm.sinks);
+            const int base = TREE && win_is_tree(prm, s.nq) ? s.nk - s.nq : w.p0;
+            w.lo = max(0, base - prm.window + 1);
+            const WinTiles u = TREE ? win_tiles(w.p0, w.ntok, tpt, C::NQT, prm.window, prm.sinks,
+                                                win_is_tree(prm, s.nq) ? base : 0x7fffffff)
+                                    : win_tiles(w.p0, w.ntok, tpt, C::NQT, prm.window, prm.sinks);
             take_tiles(u);
             w.r0 = min(u.len, (int)off / per_tile);
             w.r1 = ends ? u.len : min(u.len, (int)(off + run) / per_tile);
@@ -835,7 +903,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
                 } while (s.nq == 0);
                 if (b >= prm.B) break;
               }
-              len = win_group_len(prm, s, tpg, i);
+              len = win_group_len<TREE>(prm, s, tpg, i);
               ntok = min(tpg, s.nq - i * tpg);
               places = win_places<C::NQT>(len, ntok, tpt);
             }
@@ -1234,7 +1302,9 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
         // this row's last visible key, its own position (a valid row's lies in
         // the sequence); the tile's strictest last and first (window) ones
         const int last = w.p0 + tok;
-        const int tile_last = w.p0 + t * tpt;                              // of its first row
+        const TreeRow node(prm, w, !C::FEW && valid ? tok : -1, tok);
+        // the last key that all of the tile's rows see (but for their windows): its first row's
+        const int tile_last = TREE && node.tree ? node.ctx - 1 : w.p0 + t * tpt;
         const int tile_lo = w.p0 + min(w.ntok, (t + 1) * tpt) - prm.window;    // of its last row
         float m_run = -INFINITY;  // reference maximum, log2 units
         float l_run = 0.0f;
@@ -1253,9 +1323,15 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
           // lane = row, this warp's columns 32 wq .. 32 wq + 31
           const int nr = w.ntok * g;
           const int lo = w.p0 + w.ntok - prm.window;  // first key of the last row's window
+          const TreeRow node(prm, w, lane < nr ? row_tok : -1, row_tok);
           for (int j = 0; j < n && ok; ++j) {
             const int x = it + j, l = r0 + j;
             const int buf = C::ALT ? 0 : (x & 1);
+            uint32_t seen = 0;  // TREE: asked for ahead of the scores
+            if constexpr (TREE) {
+              const int c0 = (l < w.ns ? l : l + w.skip) * kBN + 32 * wq;
+              if (node.tree && (c0 + 32 > node.ctx || (c0 < lo && c0 + 32 > prm.sinks))) seen = node.see(prm, c0);
+            }
             ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], (uint32_t)((C::ALT ? sc : x >> 1) & 1),
                                                    abort_flag, prm.err));
             ++sc;
@@ -1288,8 +1364,9 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
               tmem_ld32(s_addr + 32 * wq, u);
               tmem_wait_ld();
               const int c0 = col0 + 32 * wq;
-              if (c0 + 31 > w.p0 || (c0 < lo && c0 + 32 > prm.sinks)) {
-                const uint32_t see = win_visible(w.p0 + row_tok, prm.window, prm.sinks, c0);
+              const int masked_from = TREE && node.tree ? node.ctx : w.p0 + 1;  // keys that not every row sees
+              if (c0 + 32 > masked_from || (c0 < lo && c0 + 32 > prm.sinks)) {
+                const uint32_t see = TREE && node.tree ? seen : win_visible(w.p0 + row_tok, prm.window, prm.sinks, c0);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) u[i] = (see & (1u << i)) ? u[i] : __float_as_uint(mask_val);
               }
@@ -1492,7 +1569,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
             if (!ok) break;
           }
           const float2 ml = narrow_softmax<ELEM>(tmem + lane_addr + buf * kBN,
-                                                 win_visible(last, prm.window, prm.sinks, 0), cj);
+                                                 win_visible(TREE && node.tree ? node.pos : last, prm.window, prm.sinks, 0), cj);
           m_run = ml.x;
           l_run = ml.y;
           tc_fence_before();
@@ -1505,6 +1582,15 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
           const int x = it + j;
           const int buf = C::ALT ? t : (x & 1);
           const uint32_t ph = C::ALT ? (uint32_t)(sc & 1) : (uint32_t)((x >> 1) & 1);
+          uint32_t seen[4];
+          if constexpr (TREE) {
+            // (asked for ahead of the scores)
+            const int c0 = (l < w.ns ? l : l + w.skip) * kBN;
+            if (node.tree && (c0 + kBN - 1 > tile_last || (c0 < tile_lo && c0 + kBN > prm.sinks))) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) seen[q] = node.see(prm, c0 + 32 * q);
+            }
+          }
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], ph, abort_flag, prm.err));
           ++sc;
           if (!ok) break;
@@ -1557,7 +1643,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
             // visible columns of this row as four words
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const uint32_t see = win_visible(last, prm.window, prm.sinks, col0 + 32 * q);
+              const uint32_t see = TREE && node.tree ? seen[q] : win_visible(last, prm.window, prm.sinks, col0 + 32 * q);
 #pragma unroll
               for (int i = 0; i < 32; ++i) s[32 * q + i] = (see & (1u << i)) ? s[32 * q + i] : mask_val;
             }
@@ -1778,10 +1864,10 @@ struct WinLaunch {
   cudaStream_t stream;
 };
 
-template <int ELEM, int D, bool PAGED, int FORM = (D <= 128 ? WIN_PAIR : WIN_ONE)>
+template <int ELEM, int D, bool PAGED, int FORM = (D <= 128 ? WIN_PAIR : WIN_ONE), bool TREE = false>
 cudaError_t launch_attn_window(const WinLaunch& L) {
   using C = WinCfg<ELEM, D, PAGED, FORM>;
-  auto kern = attn_window_kernel<ELEM, D, PAGED, FORM>;
+  auto kern = attn_window_kernel<ELEM, D, PAGED, FORM, TREE>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;

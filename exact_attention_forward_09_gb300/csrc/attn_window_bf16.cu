@@ -17,7 +17,7 @@ int window_clusters(int dev, int n) {
   const int k = n == 8 ? 3 : n == 4 ? 2 : 1;
   if (dev < 0 || dev >= 64) return 0;
   if (known[dev][k] == 0) {
-    auto kern = attn_window_kernel<kBF16, 128, false, WIN_SPLIT>;
+    auto kern = attn_window_kernel<kBF16, 128, false, WIN_SPLIT, false>;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)n, 1, 1);
     cfg.blockDim = dim3(C::THREADS, 1, 1);

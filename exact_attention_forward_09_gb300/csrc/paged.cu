@@ -7,6 +7,7 @@
 
 #include "fa.h"
 #include "paged.h"
+#include "paged_search.cuh"
 #include "ptx_window.cuh"
 
 namespace fa {
@@ -223,20 +224,6 @@ __global__ void __launch_bounds__(kThreads) paged_combine_kernel(
 //   rows in flight per thread, which cost registers and so blocks; 43.8 with
 //   256 threads per token, whose second round is half empty).  64 tokens: 2.9
 //   us, three dependent look-ups (sequence, lengths, page) behind the launch.
-
-// the last b with cu[b] <= t, by 32-way search over cu[0 .. B-1]
-__device__ __forceinline__ int find_sequence(const int* __restrict__ cu, int B, int t, int lane) {
-  int lo = 0, n = B;
-  while (n > 1) {
-    const int step = (n + 31) / 32;
-    const int i = lane * step;
-    const uint32_t yes = __ballot_sync(0xffffffffu, i < n && cu[lo + i] <= t);
-    const int last = yes == 0u ? 0 : 31 - __clz(yes);
-    lo += last * step;
-    n = min(step, n - last * step);
-  }
-  return lo;
-}
 
 template <bool F16>
 __device__ __forceinline__ float2 unpack2(uint32_t x) {

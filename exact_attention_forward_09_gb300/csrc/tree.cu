@@ -1,0 +1,71 @@
+// tree.cu -- the layout of trees of drafted tokens: which nodes a node descends
+// from, and the position that its depth gives it.
+#include <cstdint>
+
+#include "paged_search.cuh"
+#include "ptx_window.cuh"
+#include "tree.h"
+
+namespace fa {
+namespace {
+
+// One warp per node climbs from it to its root; lane l keeps word l of the mask
+// row.  All latency: a step would be a dependent load, so the warp loads the 32
+// parents around the node it has come to at once and climbs by shuffles until it
+// leaves them (parents lie before their nodes, so a tree of n nodes takes at most
+// n / 32 + 1 loads, whatever its depth).
+constexpr int kPlanThreads = 128;
+
+__global__ void __launch_bounds__(kPlanThreads) tree_plan_kernel(const int* __restrict__ parents, const int* __restrict__ cu_q,
+                                                                 const int* __restrict__ seq_k, int B, int T,
+                                                                 uint32_t* __restrict__ mask, int words,
+                                                                 int* __restrict__ positions, int* err) {
+  const int lane = threadIdx.x & 31;
+  const int t = blockIdx.x * (kPlanThreads / 32) + (threadIdx.x >> 5);
+  if (t >= T) return;
+  const int b = find_sequence(cu_q, B, t, lane);
+  const int q0 = max(0, cu_q[b]), q1 = min(T, cu_q[b + 1]);  // (cut as the other calls cut them)
+  if (t < q0 || t >= q1) return;  // a row that belongs to no sequence
+  const int n = q1 - q0, self = t - q0, first = seq_k[b] - n;
+  uint32_t word = 0;
+  int depth = 0;
+  bool bad = false;
+  if (n > 32 * words) {
+    // a chunk of a prompt: each token follows the one before
+    const int left = self + 1 - 32 * lane;
+    word = left <= 0 ? 0u : left >= 32 ? 0xffffffffu : (1u << left) - 1;
+    depth = self;
+    bad = parents[t] != self - 1;
+  } else {
+    int at = self, have = -1, mine = -1;
+    for (;;) {
+      if (lane == at >> 5) word |= 1u << (at & 31);
+      if (at >> 5 != have) {
+        have = at >> 5;
+        mine = 32 * have + lane < n ? parents[q0 + 32 * have + lane] : -1;
+      }
+      const int up = __shfl_sync(0xffffffffu, mine, at & 31);
+      bad |= up < -1 || up >= at;  // (such a node counts as a root, so the climb ends)
+      if (up < 0 || up >= at) break;
+      at = up;
+      ++depth;
+    }
+  }
+  if (lane < words) mask[(long long)t * words + lane] = word;
+  if (lane == 0) {
+    positions[t] = first + depth;
+    if (bad) report_index(err);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_tree_plan(const int* parents, const int* cu_q, const int* seq_k, int B, int T, uint32_t* mask, int words,
+                             int* positions, int* err, cudaStream_t stream) {
+  const int per = kPlanThreads / 32;
+  tree_plan_kernel<<<(unsigned)((T + (long long)per - 1) / per), kPlanThreads, 0, stream>>>(parents, cu_q, seq_k, B, T, mask, words,
+                                                                                        positions, err);
+  return cudaGetLastError();
+}
+
+}  // namespace fa

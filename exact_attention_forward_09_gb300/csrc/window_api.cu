@@ -13,9 +13,13 @@
 #include "api_internal.h"
 #include "attn_window.cuh"
 #include "paged.h"
+#include "tree.h"
 
 namespace fa {
 #define FA_EXTERN_WINDOW(E, D, P, F) extern template cudaError_t launch_attn_window<E, D, P, F>(const WinLaunch&);
+#define FA_EXTERN_PAGED(E, D, F)     \
+  FA_EXTERN_WINDOW(E, D, true, F)      \
+  extern template cudaError_t launch_attn_window<E, D, true, F, true>(const WinLaunch&);
 #define FA_EXTERN_ELEM(E)                 \
   FA_EXTERN_WINDOW(E, 64, false, WIN_PAIR)  \
   FA_EXTERN_WINDOW(E, 128, false, WIN_PAIR) \
@@ -24,23 +28,25 @@ namespace fa {
   FA_EXTERN_WINDOW(E, 64, false, WIN_SPLIT)  \
   FA_EXTERN_WINDOW(E, 128, false, WIN_SPLIT) \
   FA_EXTERN_WINDOW(E, 256, false, WIN_SPLIT) \
-  FA_EXTERN_WINDOW(E, 64, true, WIN_FEW2)   \
-  FA_EXTERN_WINDOW(E, 64, true, WIN_ONE)    \
-  FA_EXTERN_WINDOW(E, 64, true, WIN_PAIR)   \
-  FA_EXTERN_WINDOW(E, 128, true, WIN_FEW)   \
-  FA_EXTERN_WINDOW(E, 128, true, WIN_FEW2)  \
-  FA_EXTERN_WINDOW(E, 128, true, WIN_ONE)   \
-  FA_EXTERN_WINDOW(E, 128, true, WIN_PAIR)  \
-  FA_EXTERN_WINDOW(E, 256, true, WIN_FEW)   \
-  FA_EXTERN_WINDOW(E, 256, true, WIN_ONE)
+  FA_EXTERN_PAGED(E, 64, WIN_FEW2)      \
+  FA_EXTERN_PAGED(E, 64, WIN_ONE)      \
+  FA_EXTERN_PAGED(E, 64, WIN_PAIR)      \
+  FA_EXTERN_PAGED(E, 128, WIN_FEW)      \
+  FA_EXTERN_PAGED(E, 128, WIN_FEW2)      \
+  FA_EXTERN_PAGED(E, 128, WIN_ONE)      \
+  FA_EXTERN_PAGED(E, 128, WIN_PAIR)      \
+  FA_EXTERN_PAGED(E, 256, WIN_FEW)      \
+  FA_EXTERN_PAGED(E, 256, WIN_ONE)
 FA_EXTERN_ELEM(kBF16)
 FA_EXTERN_ELEM(kFP16)
 #undef FA_EXTERN_ELEM
+#undef FA_EXTERN_PAGED
 #undef FA_EXTERN_WINDOW
 }  // namespace fa
 
 namespace {
 
+constexpr int64_t kMaxWords = 32;              // of a mask row: a lane has one
 constexpr int64_t kMaxLen = (int64_t)1 << 30;  // positions, windows and token counts fit int arithmetic
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -71,21 +77,21 @@ fa_status launch_dense(const fa::WinLaunch& L, int64_t d, int form) {
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
-template <int ELEM>
+template <int ELEM, bool TREE>
 fa_status launch_paged(const fa::WinLaunch& L, int64_t d, int form) {
   cudaError_t e = cudaErrorInvalidValue;
   if (d == 64) {
-    if (form == fa::WIN_FEW2) e = fa::launch_attn_window<ELEM, 64, true, fa::WIN_FEW2>(L);
-    if (form == fa::WIN_ONE) e = fa::launch_attn_window<ELEM, 64, true, fa::WIN_ONE>(L);
-    if (form == fa::WIN_PAIR) e = fa::launch_attn_window<ELEM, 64, true, fa::WIN_PAIR>(L);
+    if (form == fa::WIN_FEW2) e = fa::launch_attn_window<ELEM, 64, true, fa::WIN_FEW2, TREE>(L);
+    if (form == fa::WIN_ONE) e = fa::launch_attn_window<ELEM, 64, true, fa::WIN_ONE, TREE>(L);
+    if (form == fa::WIN_PAIR) e = fa::launch_attn_window<ELEM, 64, true, fa::WIN_PAIR, TREE>(L);
   } else if (d == 128) {
-    if (form == fa::WIN_FEW) e = fa::launch_attn_window<ELEM, 128, true, fa::WIN_FEW>(L);
-    if (form == fa::WIN_FEW2) e = fa::launch_attn_window<ELEM, 128, true, fa::WIN_FEW2>(L);
-    if (form == fa::WIN_ONE) e = fa::launch_attn_window<ELEM, 128, true, fa::WIN_ONE>(L);
-    if (form == fa::WIN_PAIR) e = fa::launch_attn_window<ELEM, 128, true, fa::WIN_PAIR>(L);
+    if (form == fa::WIN_FEW) e = fa::launch_attn_window<ELEM, 128, true, fa::WIN_FEW, TREE>(L);
+    if (form == fa::WIN_FEW2) e = fa::launch_attn_window<ELEM, 128, true, fa::WIN_FEW2, TREE>(L);
+    if (form == fa::WIN_ONE) e = fa::launch_attn_window<ELEM, 128, true, fa::WIN_ONE, TREE>(L);
+    if (form == fa::WIN_PAIR) e = fa::launch_attn_window<ELEM, 128, true, fa::WIN_PAIR, TREE>(L);
   } else {
-    if (form == fa::WIN_FEW) e = fa::launch_attn_window<ELEM, 256, true, fa::WIN_FEW>(L);
-    if (form == fa::WIN_ONE) e = fa::launch_attn_window<ELEM, 256, true, fa::WIN_ONE>(L);
+    if (form == fa::WIN_FEW) e = fa::launch_attn_window<ELEM, 256, true, fa::WIN_FEW, TREE>(L);
+    if (form == fa::WIN_ONE) e = fa::launch_attn_window<ELEM, 256, true, fa::WIN_ONE, TREE>(L);
   }
   return e == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
@@ -144,76 +150,11 @@ int shift_of(int64_t page_size) {
   return s;
 }
 
-}  // namespace
-
-namespace fa {
-fa_status internal_check_cache(const fa_kv_cache* cache) { return check_cache(cache); }
-int internal_shift_of(int64_t page_size) { return shift_of(page_size); }
-}  // namespace fa
-
-extern "C" {
-
-fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int64_t B, int64_t Hq,
-                        int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d, int64_t window, int64_t sinks, float scale,
-                        int dtype, cudaStream_t stream) {
-  if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_FP16) return FA_ERR_INVALID_ARG;
-  if (window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
-  bool empty = false;
-  fa_status st = fa::internal_check_common(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, &empty);
-  if (st != FA_OK || empty) return st;
-  if (Nq > kMaxLen || Nk > kMaxLen) return FA_ERR_UNSUPPORTED;
-  int dev = 0;
-  int* err = nullptr;
-  if ((st = fa::internal_device_setup(&dev, &err)) != FA_OK) return st;
-  fa::WinLaunch L;
-  std::memset(&L, 0, sizeof(L));
-  const CUtensorMapDataType dt = map_type(dtype);
-  if ((st = fa::internal_encode_map(&L.q, q, dt, 2, B * Hq, Nq, d, 128)) != FA_OK) return st;
-  if ((st = fa::internal_encode_map(&L.k, k, dt, 2, B * Hkv, Nk, d, 128)) != FA_OK) return st;
-  if ((st = fa::internal_encode_map(&L.v, v, dt, 2, B * Hkv, Nk, d, 128)) != FA_OK) return st;
-  if ((st = fa::internal_encode_map(&L.o, o, dt, 2, B * Hq, Nq, d, 32)) != FA_OK) return st;
-  L.prm.o = o;
-  L.prm.lse = lse;
-  L.prm.err = err;
-  L.prm.window = (int)(window < kMaxLen ? window : kMaxLen);
-  L.prm.sinks = (int)(sinks < kMaxLen ? sinks : kMaxLen);
-  L.prm.scale_log2 = log2_scale(scale);
-  L.prm.Hq = (int)Hq;
-  L.prm.Hkv = (int)Hkv;
-  L.prm.o_vec32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
-  L.prm.drop_pos = fa::internal_take_inject() ? 1 : -1;  // (a slot that any unit with a key uses)
-  L.prm.N = (int)Nq;
-  L.prm.Nk = (int)Nk;
-  L.prm.BH = (int)(B * Hq);
-  L.stream = stream;
-  // few query tiles over some key tiles: a cluster for each, as large as all run
-  // at once, a key tile and more per CTA (see WinForm; below 512 keys the join
-  // takes what the split gives)
-  const int64_t tiles = B * Hq * ((Nq + fa::kBM - 1) / fa::kBM);
-  int64_t reach = L.prm.window + (int64_t)L.prm.sinks + fa::kBM;  // keys a query tile sees, and what its edges add
-  if (reach > Nk) reach = Nk;
-  for (int c = 8; c > 1 && L.cluster == 0; c /= 2)
-    if (reach >= 512 && reach >= c * fa::kBN && tiles <= fa::window_clusters(dev, c)) L.cluster = c;
-  int form = d == 256 ? fa::WIN_ONE : fa::WIN_PAIR;
-  if (d == 64 && reach <= 6 * fa::kBN && tiles > fa::internal_sm_count(dev)) form = fa::WIN_TWO;
-  if (L.cluster > 0) form = fa::WIN_SPLIT;
-  return dtype == FA_DTYPE_BF16 ? launch_dense<fa::kBF16>(L, d, form) : launch_dense<fa::kFP16>(L, d, form);
-}
-
-fa_status fa_paged_workspace_bytes(int64_t d, size_t* bytes) {
-  if (!bytes) return FA_ERR_INVALID_ARG;
-  *bytes = 0;
-  if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
-  *bytes = paged_workspace(fa::internal_sm_count(dev), d).bytes;
-  return FA_OK;
-}
-
-fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, const int32_t* block_table,
-                       int64_t table_stride, int64_t max_pages, const int32_t* cu_q, const int32_t* seq_k, int64_t B,
-                       int64_t T, int64_t Hq, int64_t q_stride, int64_t max_q, int64_t window, int64_t sinks,
-                       float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+// fa_fwd_paged, and with a mask fa_fwd_tree.
+fa_status fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, const int32_t* block_table,
+                    int64_t table_stride, int64_t max_pages, const int32_t* cu_q, const int32_t* seq_k, const uint32_t* mask,
+                    int64_t words, const int32_t* positions, int64_t B, int64_t T, int64_t Hq, int64_t q_stride, int64_t max_q,
+                    int64_t window, int64_t sinks, float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   if (B < 0 || T < 0 || Hq < 0 || max_q < 0) return FA_ERR_INVALID_ARG;
   if (window < 1 || sinks < 0 || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
   fa_status st = check_cache(cache);
@@ -300,6 +241,9 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   p.table_stride = table_stride;
   p.num_pages = (int)cache->num_pages;
   p.page_shift = shift_of(cache->page_size);
+  p.mask = mask;
+  p.words = (int)words;
+  p.positions = positions;
   p.g = (int)g;
   p.tpt = (int)tpt;
   // the line of work: at most this many units, each of at most this many
@@ -307,7 +251,8 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   const int64_t unit_tok = (pair ? 2 : 1) * tpt;
   const int64_t keys = max_pages * cache->page_size < kMaxLen ? max_pages * cache->page_size : kMaxLen;
   int64_t tiles = keys / fa::kBN + 1;
-  if (p.window + (int64_t)p.sinks + unit_tok < keys) tiles = (p.window + (int64_t)p.sinks + unit_tok) / fa::kBN + 4;
+  const int64_t reach = p.window + (int64_t)p.sinks + unit_tok + 32 * words;  // (a tree's units start their windows at its root's)
+  if (reach < keys) tiles = reach / fa::kBN + 4;
   const int64_t units = (T / unit_tok + B) * Hkv;
   if (units >= (int64_t)0x7fffffff / (2 * (tiles + 1))) return FA_ERR_UNSUPPORTED;
   p.max_places = (uint32_t)(units * 2 * (tiles + 1));
@@ -317,11 +262,116 @@ fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* 
   p.desc = reinterpret_cast<int4*>(w + ws.desc_at);
   L.grid = ctas;
   L.stream = stream;
-  st = cache->dtype == FA_DTYPE_BF16 ? launch_paged<fa::kBF16>(L, d, form) : launch_paged<fa::kFP16>(L, d, form);
+  if (mask)
+    st = cache->dtype == FA_DTYPE_BF16 ? launch_paged<fa::kBF16, true>(L, d, form) : launch_paged<fa::kFP16, true>(L, d, form);
+  else
+    st = cache->dtype == FA_DTYPE_BF16 ? launch_paged<fa::kBF16, false>(L, d, form) : launch_paged<fa::kFP16, false>(L, d, form);
   if (st != FA_OK) return st;
   const int64_t most = (max_q > 0 && max_q < unit_tok ? max_q : unit_tok) * g;
   return fa::launch_paged_combine(p.o_part, p.lse_part, p.desc, o, lse, sms, ctas, (int)units, slot_rows, (int)most,
                                   (int)g, (int)Hq, (int)d, cache->dtype == FA_DTYPE_FP16, stream) == cudaSuccess
+             ? FA_OK
+             : FA_ERR_CUDA;
+}
+
+}  // namespace
+
+namespace fa {
+fa_status internal_check_cache(const fa_kv_cache* cache) { return check_cache(cache); }
+int internal_shift_of(int64_t page_size) { return shift_of(page_size); }
+}  // namespace fa
+
+extern "C" {
+
+fa_status fa_fwd_window(const void* q, const void* k, const void* v, void* o, float* lse, int64_t B, int64_t Hq,
+                        int64_t Hkv, int64_t Nq, int64_t Nk, int64_t d, int64_t window, int64_t sinks, float scale,
+                        int dtype, cudaStream_t stream) {
+  if (dtype != FA_DTYPE_BF16 && dtype != FA_DTYPE_FP16) return FA_ERR_INVALID_ARG;
+  if (window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
+  bool empty = false;
+  fa_status st = fa::internal_check_common(q, k, v, o, lse, B, Hq, Hkv, Nq, Nk, d, scale, &empty);
+  if (st != FA_OK || empty) return st;
+  if (Nq > kMaxLen || Nk > kMaxLen) return FA_ERR_UNSUPPORTED;
+  int dev = 0;
+  int* err = nullptr;
+  if ((st = fa::internal_device_setup(&dev, &err)) != FA_OK) return st;
+  fa::WinLaunch L;
+  std::memset(&L, 0, sizeof(L));
+  const CUtensorMapDataType dt = map_type(dtype);
+  if ((st = fa::internal_encode_map(&L.q, q, dt, 2, B * Hq, Nq, d, 128)) != FA_OK) return st;
+  if ((st = fa::internal_encode_map(&L.k, k, dt, 2, B * Hkv, Nk, d, 128)) != FA_OK) return st;
+  if ((st = fa::internal_encode_map(&L.v, v, dt, 2, B * Hkv, Nk, d, 128)) != FA_OK) return st;
+  if ((st = fa::internal_encode_map(&L.o, o, dt, 2, B * Hq, Nq, d, 32)) != FA_OK) return st;
+  L.prm.o = o;
+  L.prm.lse = lse;
+  L.prm.err = err;
+  L.prm.window = (int)(window < kMaxLen ? window : kMaxLen);
+  L.prm.sinks = (int)(sinks < kMaxLen ? sinks : kMaxLen);
+  L.prm.scale_log2 = log2_scale(scale);
+  L.prm.Hq = (int)Hq;
+  L.prm.Hkv = (int)Hkv;
+  L.prm.o_vec32 = (reinterpret_cast<uintptr_t>(o) & 31u) == 0;
+  L.prm.drop_pos = fa::internal_take_inject() ? 1 : -1;  // (a slot that any unit with a key uses)
+  L.prm.N = (int)Nq;
+  L.prm.Nk = (int)Nk;
+  L.prm.BH = (int)(B * Hq);
+  L.stream = stream;
+  // few query tiles over some key tiles: a cluster for each, as large as all run
+  // at once, a key tile and more per CTA (see WinForm; below 512 keys the join
+  // takes what the split gives)
+  const int64_t tiles = B * Hq * ((Nq + fa::kBM - 1) / fa::kBM);
+  int64_t reach = L.prm.window + (int64_t)L.prm.sinks + fa::kBM;  // keys a query tile sees, and what its edges add
+  if (reach > Nk) reach = Nk;
+  for (int c = 8; c > 1 && L.cluster == 0; c /= 2)
+    if (reach >= 512 && reach >= c * fa::kBN && tiles <= fa::window_clusters(dev, c)) L.cluster = c;
+  int form = d == 256 ? fa::WIN_ONE : fa::WIN_PAIR;
+  if (d == 64 && reach <= 6 * fa::kBN && tiles > fa::internal_sm_count(dev)) form = fa::WIN_TWO;
+  if (L.cluster > 0) form = fa::WIN_SPLIT;
+  return dtype == FA_DTYPE_BF16 ? launch_dense<fa::kBF16>(L, d, form) : launch_dense<fa::kFP16>(L, d, form);
+}
+
+fa_status fa_paged_workspace_bytes(int64_t d, size_t* bytes) {
+  if (!bytes) return FA_ERR_INVALID_ARG;
+  *bytes = 0;
+  if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  *bytes = paged_workspace(fa::internal_sm_count(dev), d).bytes;
+  return FA_OK;
+}
+
+fa_status fa_fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse, const int32_t* block_table,
+                       int64_t table_stride, int64_t max_pages, const int32_t* cu_q, const int32_t* seq_k, int64_t B,
+                       int64_t T, int64_t Hq, int64_t q_stride, int64_t max_q, int64_t window, int64_t sinks,
+                       float scale, void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  return fwd_paged(q, cache, o, lse, block_table, table_stride, max_pages, cu_q, seq_k, nullptr, 0, nullptr, B, T, Hq, q_stride,
+                   max_q, window, sinks, scale, workspace, workspace_bytes, stream);
+}
+
+fa_status fa_fwd_tree(const void* q, const fa_kv_cache* cache, void* o, float* lse, const int32_t* block_table,
+                      int64_t table_stride, int64_t max_pages, const int32_t* cu_q, const int32_t* seq_k,
+                      const uint32_t* mask, int64_t words, const int32_t* positions, int64_t B, int64_t T, int64_t Hq,
+                      int64_t q_stride, int64_t max_q, int64_t window, int64_t sinks, float scale, void* workspace,
+                      size_t workspace_bytes, cudaStream_t stream) {
+  if (words < 1) return FA_ERR_INVALID_ARG;
+  if (words > kMaxWords) return FA_ERR_UNSUPPORTED;
+  if (B > 0 && T > 0 && Hq > 0 && (!mask || !aligned4(mask) || (positions && !aligned4(positions)))) return FA_ERR_INVALID_ARG;
+  return fwd_paged(q, cache, o, lse, block_table, table_stride, max_pages, cu_q, seq_k, mask, words, positions, B, T, Hq, q_stride,
+                   max_q, window, sinks, scale, workspace, workspace_bytes, stream);
+}
+
+fa_status fa_tree_plan(const int32_t* parents, const int32_t* cu_q, const int32_t* seq_k, int64_t B, int64_t T,
+                       uint32_t* mask, int64_t words, int32_t* positions, cudaStream_t stream) {
+  if (B < 0 || T < 0 || words < 1) return FA_ERR_INVALID_ARG;
+  if (words > kMaxWords || B > (1 << 24) || T > kMaxLen) return FA_ERR_UNSUPPORTED;
+  if (B == 0 || T == 0) return FA_OK;
+  if (!parents || !cu_q || !seq_k || !mask || !positions) return FA_ERR_INVALID_ARG;
+  if (!aligned4(parents) || !aligned4(cu_q) || !aligned4(seq_k) || !aligned4(mask) || !aligned4(positions)) return FA_ERR_INVALID_ARG;
+  int dev = 0;
+  int* err = nullptr;
+  const fa_status st = fa::internal_device_setup(&dev, &err);
+  if (st != FA_OK) return st;
+  return fa::launch_tree_plan(parents, cu_q, seq_k, (int)B, (int)T, mask, (int)words, positions, err, stream) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
 }

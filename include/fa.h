@@ -600,6 +600,65 @@ fa_status fa_cache_append_at(const fa_kv_cache* cache, const void* q, const void
                              int rope_layout, const int32_t* positions, cudaStream_t stream);
 
 /*
+ * ---- trees of drafted tokens ----
+ *
+ * A sequence of the ragged batch brings the nodes of a tree (or several) in
+ * place of consecutive tokens: continuations that are tried at once, of which one
+ * path will be kept.  Node i's parent is an earlier node of its sequence, or none:
+ * then it follows the cached tokens.  Nodes lie in the cache one behind the other,
+ * node i at position seq_k[b] - n + i as any new token, but sit in their sequence
+ * at the position that their depth gives them: seq_k[b] - n + (nodes above it).
+ * The steps of one round: fa_tree_plan once; in each layer fa_cache_append_at with
+ * its positions, and fa_fwd_tree; then fa_cache_compact keeps the accepted path.
+ */
+
+/*
+ * fa_tree_plan -- mask rows and positions of the nodes.
+ *   parents    [T] int32 (device): the parent's number within its sequence, below
+ *              the node's own, or -1
+ *   cu_q, seq_k, B, T  the batch, as in fa_fwd_paged
+ *   mask       [T, words] uint32 (device, written): bit k of word w of a node's
+ *              row says that node 32 w + k of its sequence is the node itself or
+ *              above it
+ *   words      1 to 32.  A sequence of more than 32 * words tokens is a plain chunk
+ *              (of a prompt): the parent of its token i has to be i - 1, and the rows
+ *              get what words bits there are
+ *   positions  [T] int32 (device, written)
+ * Rows outside every sequence are not written.  A parent that is out of range
+ * counts as -1, and it or a chunk that is not one is reported by
+ * fa_check_device_error as FA_ERR_INDEX.
+ * Errors: FA_ERR_INVALID_ARG for bad pointers, alignment or sizes;
+ * FA_ERR_UNSUPPORTED for words above 32, B above 2^24, T above 2^30, or a device
+ * other than sm_103.  B * T = 0 is a no-op.
+ */
+fa_status fa_tree_plan(const int32_t* parents, const int32_t* cu_q, const int32_t* seq_k, int64_t B, int64_t T,
+                       uint32_t* mask, int64_t words, int32_t* positions, cudaStream_t stream);
+
+/*
+ * fa_fwd_tree -- fa_fwd_paged where the new tokens of a sequence are a tree's
+ * nodes.  Node i, at position p, sees
+ *   the cached keys j < seq_k[b] - n with j > p - window or j < sinks, and
+ *   new token k <= i iff bit k of its mask row is set (the window does not apply;
+ *   a row without any bit and any cached key gets O = 0 and LSE = -inf).
+ *   mask       [T, words] uint32 (device), as fa_tree_plan writes it, or any other
+ *              (bits behind a token's own are not looked at)
+ *   words      1 to 32.  Sequences of more than 32 * words new tokens attend as in
+ *              fa_fwd_paged, whatever their mask rows hold
+ *   positions  [T] int32 (device), as fa_tree_plan writes them: between seq_k[b] -
+ *              n and where the token lies (others are cut to that, and reported by
+ *              fa_check_device_error as FA_ERR_INDEX).  NULL: where the tokens lie.
+ *              They matter under a window alone
+ * Everything else as in fa_fwd_paged, its workspace included.  Pages that hold
+ * no key from position seq_k[b] - n - window + 1 on, nor a sink, are not read.
+ */
+fa_status fa_fwd_tree(const void* q, const fa_kv_cache* cache, void* o, float* lse,
+                      const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                      const int32_t* cu_q, const int32_t* seq_k, const uint32_t* mask, int64_t words,
+                      const int32_t* positions, int64_t B, int64_t T, int64_t Hq, int64_t q_stride, int64_t max_q,
+                      int64_t window, int64_t sinks, float scale, void* workspace, size_t workspace_bytes,
+                      cudaStream_t stream);
+
+/*
  * ---- rotary positions ----
  *
  * Pair (a, b) of a row at position p becomes (a*c - b*s, a*s + b*c) with c =
