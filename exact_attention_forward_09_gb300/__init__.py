@@ -361,6 +361,7 @@ def fwd_gqa(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = Fa
 # The calls below are often small, and then the time on the host counts: they
 # ask for the current stream and switch devices only as far as needed.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device  # (asked with CUDA tensors in hand)
 _NO_GUARD = contextlib.nullcontext()
 
 
@@ -369,7 +370,7 @@ def _current_stream(index: int) -> int:
 
 
 def _guard(index: int):
-    return _NO_GUARD if torch.cuda.current_device() == index else torch.cuda.device(index)
+    return _NO_GUARD if _raw_device() == index else torch.cuda.device(index)
 
 
 _TYPES = {torch.bfloat16: FA_DTYPE_BF16, torch.float16: FA_DTYPE_FP16}
@@ -572,11 +573,11 @@ def _fwd_paged(q, k_pages, v_pages, block_table, cu_q, seq_k, mask, positions, w
     else:
         _check_out("lse", lse, (T, Hq), torch.float32, index)
     if mask is not None:
-        if not isinstance(mask, torch.Tensor) or mask.dim() != 2:
+        if not isinstance(mask, torch.Tensor) or len(mask.shape) != 2:
             raise ValueError("mask must be an int32 [T, words] tensor")
-        _check_out("mask", mask, (T, mask.shape[1]), torch.int32, index)
-        if positions is not None:
-            _check_out("positions", positions, (T,), torch.int32, index)
+        words = mask.shape[1]
+        _check_out("mask", mask, (T, words), torch.int32, index)
+        pp = None if positions is None else _check_ints("positions", positions, T, index)
     with _guard(index):
         if workspace is None:
             need = _PAGED_BYTES.get((index, d))
@@ -590,8 +591,7 @@ def _fwd_paged(q, k_pages, v_pages, block_table, cu_q, seq_k, mask, positions, w
                                      table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), *sizes)
         else:
             st = _lib().fa_fwd_tree(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
-                                    table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), mask.data_ptr(), mask.shape[1],
-                                    None if positions is None else positions.data_ptr(), *sizes)
+                                    table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), mask.data_ptr(), words, pp, *sizes)
     if st != FA_OK:
         raise FaError(st, "fa_fwd_paged" if mask is None else "fa_fwd_tree")
     return out, lse
@@ -605,13 +605,9 @@ def tree_plan(parents: torch.Tensor, cu_q: torch.Tensor, seq_k: torch.Tensor, ma
     (sequences of more tokens than its next multiple of 32 are chunks of a
     prompt).  Returns (mask int32 [T, ceil(max_tree / 32)], positions int32 [T])
     for ``fwd_tree`` and ``cache_append``."""
-    index = parents.get_device() if isinstance(parents, torch.Tensor) else -1
-    if index < 0:
-        raise ValueError("parents must be a CUDA tensor")
-    _check_ints(index, parents=parents, cu_q=cu_q, seq_k=seq_k)
-    T, B, words = parents.shape[0], seq_k.shape[0], (_count(max_tree) + 31) // 32
-    if cu_q.shape[0] != B + 1:
-        raise ValueError("cu_q must have one entry more than seq_k")
+    T, index = _ints("parents", parents)
+    B, words = _ints("seq_k", seq_k)[0], (_count(max_tree) + 31) // 32
+    cp, sp = _check_ints("cu_q", cu_q, B + 1, index), _check_ints("seq_k", seq_k, B, index)
     if not 1 <= words <= 32:
         raise ValueError("max_tree must be 1 to 1024")
     if mask is None:
@@ -619,12 +615,12 @@ def tree_plan(parents: torch.Tensor, cu_q: torch.Tensor, seq_k: torch.Tensor, ma
     else:
         _check_out("mask", mask, (T, words), torch.int32, index)
     if positions is None:
-        positions = torch.empty((T,), dtype=torch.int32, device=parents.device)
+        positions = torch.empty_like(parents)
     else:
         _check_out("positions", positions, (T,), torch.int32, index)
     with _guard(index):
-        st = _lib().fa_tree_plan(parents.data_ptr(), cu_q.data_ptr(), seq_k.data_ptr(), B, T, mask.data_ptr(), words,
-                                 positions.data_ptr(), _current_stream(index))
+        st = _lib().fa_tree_plan(parents.data_ptr(), cp, sp, B, T, mask.data_ptr(), words, positions.data_ptr(),
+                                 _current_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_tree_plan")
     return mask, positions
@@ -649,12 +645,13 @@ def _check_rope(rope, index):
     cos, sin, layout = rope
     if layout not in (FA_ROPE_INTERLEAVED, FA_ROPE_HALF):
         raise ValueError("rope layout must be FA_ROPE_INTERLEAVED or FA_ROPE_HALF")
-    if not isinstance(cos, torch.Tensor) or cos.dim() != 2:
-        raise ValueError("rope cos must be a [positions, rope_dim/2] tensor")
-    shape = cos.shape
-    _check_out("rope cos", cos, shape, torch.float32, index)
-    _check_out("rope sin", sin, shape, torch.float32, index)
-    return cos.data_ptr(), sin.data_ptr(), shape[0], 2 * shape[1], int(layout)
+    if isinstance(cos, torch.Tensor) and isinstance(sin, torch.Tensor):
+        shape, f32 = cos.shape, torch.float32
+        if len(shape) == 2 and sin.shape == shape and cos.dtype is f32 and sin.dtype is f32 and cos.get_device() == index \
+                and sin.get_device() == index and cos.is_contiguous() and sin.is_contiguous():
+            n, half = shape
+            return cos.data_ptr(), sin.data_ptr(), n, 2 * half, int(layout)
+    raise ValueError(f"rope cos and sin must be contiguous fp32 [positions, rope_dim/2] tensors on cuda:{index}")
 
 
 def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -744,17 +741,31 @@ def rope_table(length: int, rope_dim: int, theta: float = 10000.0, scaling=None,
     return cos, sin
 
 
-def _rope_strides(name, t, lead, d, dt, index):
-    """(heads, batch, head and token strides) of [B, heads, N, d] or [N, heads, d]."""
-    shape = t.shape if isinstance(t, torch.Tensor) else ()
-    four = len(lead) == 2
-    if len(shape) != (4 if four else 3) or t.dtype is not dt or t.get_device() != index or shape[-1] != d \
-            or shape[0] != lead[0] or (four and shape[2] != lead[1]):
-        raise ValueError(f"{name} must be a {dt} {'[B, heads, N, d]' if four else '[N, heads, d]'} tensor on cuda:{index}, as q is")
-    st = t.stride()
-    if t.numel() and st[-1] != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return (shape[1], st[0], st[1], st[2]) if four else (shape[1], 0, st[1], st[0])
+def _rope_array(name, x, y, four, B, N, d, dt, index):
+    """(the result, the bytes of an ``fa_rope_array``) of one array and its
+    result, where one is given."""
+    if isinstance(x, torch.Tensor):
+        shape, st = x.shape, x.stride()
+        if x.dtype is dt and x.get_device() == index and len(shape) == 3 + four:
+            if four:
+                b, heads, n, c = shape
+                xb, xh, xn, xc = st
+            else:
+                n, heads, c = shape
+                xn, xh, xc = st
+                b, xb = 1, 0
+            if b == B and n == N and c == d and (xc == 1 or x.numel() == 0):
+                if y is None:
+                    y = torch.empty(shape, dtype=dt, device=x.device)
+                    yb, yh, yn = (heads * N * d, N * d, d) if four else (0, d, heads * d)
+                elif isinstance(y, torch.Tensor) and y.shape == shape and y.dtype is dt and y.get_device() == index \
+                        and (y.stride(-1) == 1 or y.numel() == 0):
+                    yb, yh, yn = y.stride()[:3] if four else (0, y.stride(1), y.stride(0))
+                else:
+                    raise ValueError(f"{name}_out must be a {dt} {list(shape)} tensor on cuda:{index}, its last dimension contiguous")
+                return y, _ROPE_PACK(x.data_ptr(), y.data_ptr(), heads, xb, xh, xn, yb, yh, yn)
+    raise ValueError(f"{name} must be a {dt} {'[B, heads, N, d]' if four else '[N, heads, d]'} tensor on cuda:{index} with "
+                     "q's B, N and d, its last dimension contiguous")
 
 
 def rope(q: torch.Tensor, k: torch.Tensor | None, rope, positions: torch.Tensor | None = None, offset: int = 0,
@@ -767,39 +778,32 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, rope, positions: torch.Tensor 
     [B, N]).  ``inverse`` turns back, which takes gradients of the results to
     those of q and k.  Returns (q_out, k_out), contiguous unless given; q_out = q
     works in place."""
-    if not isinstance(q, torch.Tensor) or q.dim() not in (3, 4) or q.dtype not in _TYPES or q.get_device() < 0:
+    shape = q.shape if isinstance(q, torch.Tensor) else ()
+    four = len(shape) == 4
+    if not (four or len(shape) == 3) or q.dtype not in _TYPES or q.get_device() < 0:
         raise ValueError("q must be a bf16 or fp16 [B, heads, N, d] or [N, heads, d] CUDA tensor")
-    index, dt, shape = q.get_device(), q.dtype, q.shape
-    d, N = shape[-1], shape[2] if len(shape) == 4 else shape[0]
-    B = shape[0] if len(shape) == 4 else 1
-    lead = (shape[0], N) if len(shape) == 4 else (N,)
+    index, dt = q.get_device(), q.dtype
+    if four:
+        B, _, N, d = shape
+    else:
+        N, _, d = shape
+        B = 1
     cp, sp, length, r, layout = _check_rope(rope, index)
-    arrays = b""
-    for name, x, y in (("q", q, q_out), ("k", k, k_out)):
-        if x is None:
-            if y is not None:
-                raise ValueError("k_out needs k")
-            continue
-        heads, xb, xh, xn = _rope_strides(name, x, lead, d, dt, index)
-        if y is None:
-            y = torch.empty(x.shape, dtype=dt, device=x.device)
-        elif not isinstance(y, torch.Tensor) or y.shape != x.shape:
-            raise ValueError(f"{name}_out must have {name}'s shape")
-        _, yb, yh, yn = _rope_strides(name + "_out", y, lead, d, dt, index)
-        arrays += _ROPE_PACK(x.data_ptr(), y.data_ptr(), heads, xb, xh, xn, yb, yh, yn)
-        if name == "q":
-            q_out = y
-        else:
-            k_out = y
+    q_out, arrays = _rope_array("q", q, q_out, four, B, N, d, dt, index)
+    if k is not None:
+        k_out, more = _rope_array("k", k, k_out, four, B, N, d, dt, index)
+        arrays += more
+    elif k_out is not None:
+        raise ValueError("k_out needs k")
     pp, ps = None, 0
     if positions is not None:
         if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 or positions.get_device() != index \
                 or positions.shape not in ((N,), (B, N)) or not positions.is_contiguous():
             raise ValueError(f"positions must be a contiguous int32 [{N}] or [{B}, {N}] tensor on cuda:{index}")
-        pp, ps = positions.data_ptr(), N if positions.dim() == 2 else 0
+        pp, ps = positions.data_ptr(), N if len(positions.shape) == 2 else 0
     with _guard(index):
         st = _lib().fa_rope(arrays, 1 if k is None else 2, B, N, d, pp, ps, _count(offset), cp, sp, length, r, layout,
-                            int(bool(inverse)), _TYPES[dt], _current_stream(index))
+                            1 if inverse else 0, _TYPES[dt], _current_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_rope")
     return q_out, k_out
@@ -809,29 +813,40 @@ def _layers(k_pages, v_pages):
     """The ``fa_kv_cache`` of the first layer, the number of layers, the
     elements between them and the device index, of pages [num_pages, heads,
     page_size, d] or [layers, num_pages, heads, page_size, d]."""
-    if isinstance(k_pages, torch.Tensor) and k_pages.dim() == 5 and isinstance(v_pages, torch.Tensor) and v_pages.dim() == 5:
-        n = k_pages.shape[0]
-        if n == 0 or v_pages.shape[0] != n or v_pages.stride(0) != k_pages.stride(0):
-            raise ValueError("k_pages and v_pages must have the same layers, at least one, and the same strides")
-        cache, _, _, _, index = _cache(k_pages[0], v_pages[0])
-        return cache, n, k_pages.stride(0), index
+    if isinstance(k_pages, torch.Tensor) and isinstance(v_pages, torch.Tensor) and len(k_pages.shape) == 5:
+        shape, stride, dt, index = k_pages.shape, k_pages.stride(), k_pages.dtype, k_pages.get_device()
+        if index >= 0 and dt in _TYPES and stride[4] == 1 and shape[0] > 0 and v_pages.shape == shape and v_pages.stride() == stride \
+                and v_pages.dtype is dt and v_pages.get_device() == index:
+            layers, n, h, ps, d = shape
+            return _KV_PACK(k_pages.data_ptr(), v_pages.data_ptr(), n, ps, h, d, stride[1], stride[2], stride[3],
+                            _TYPES[dt]), layers, stride[0], index
+        raise ValueError("k_pages and v_pages must be bf16 or fp16 [layers, num_pages, heads, page_size, d] CUDA tensors of one "
+                         "shape, dtype, device and strides, their last dimension contiguous")
     cache, _, _, _, index = _cache(k_pages, v_pages)
     return cache, 1, 0, index
 
 
-def _check_ints(index, **tensors):
-    for name, t in tensors.items():
-        if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.dim() != 1 or t.get_device() != index \
-                or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous 1-D int32 tensor on cuda:{index}")
+def _check_ints(name, t, n, index):
+    """The address of a contiguous int32 [n] tensor."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.shape != (n,) or t.get_device() != index \
+            or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on cuda:{index}")
+    return t.data_ptr()
+
+
+def _ints(name, t):
+    """(entries, device index) of the 1-D int32 CUDA tensor that others are checked against."""
+    if isinstance(t, torch.Tensor) and len(t.shape) == 1 and t.dtype is torch.int32 and t.get_device() >= 0 and t.is_contiguous():
+        return t.shape[0], t.get_device()
+    raise ValueError(f"{name} must be a contiguous 1-D int32 CUDA tensor")
 
 
 def _check_table(block_table, rows, index):
-    """(table stride, table width) of a block table with a row for each of ``rows``."""
-    if isinstance(block_table, torch.Tensor) and block_table.dtype is torch.int32 and block_table.dim() == 2 \
-            and block_table.get_device() == index and block_table.shape[0] == rows \
-            and (block_table.shape[1] < 2 or block_table.stride(1) == 1):
-        return block_table.stride(0), block_table.shape[1]
+    """(address, row stride, width) of a block table with ``rows`` rows."""
+    if isinstance(block_table, torch.Tensor) and block_table.dtype is torch.int32 and block_table.get_device() == index:
+        shape, st = block_table.shape, block_table.stride()
+        if len(shape) == 2 and shape[0] == rows and (st[1] == 1 or shape[1] < 2):
+            return block_table.data_ptr(), st[0], shape[1]
     raise ValueError(f"block_table must be an int32 [{rows}, max_pages] tensor on cuda:{index}, each row contiguous")
 
 
@@ -841,17 +856,12 @@ def pages_resize(refs: torch.Tensor, block_table: torch.Tensor, seq_k: torch.Ten
     block_table [B, max_pages], seq_k [B] the tokens that a row holds pages for,
     want [B] those that it shall, all int32.  Afterwards seq_k is want, or less
     where the pages ran out."""
-    index = refs.get_device() if isinstance(refs, torch.Tensor) else -1
-    if index < 0:
-        raise ValueError("refs must be a CUDA tensor")
-    _check_ints(index, refs=refs, seq_k=seq_k, want=want)
-    B = seq_k.shape[0]
-    if want.shape[0] != B:
-        raise ValueError("want must have seq_k's length")
-    stride, width = _check_table(block_table, B, index)
+    pages, index = _ints("refs", refs)
+    B, _ = _ints("seq_k", seq_k)
+    sp, wp = _check_ints("seq_k", seq_k, B, index), _check_ints("want", want, B, index)
+    tp, stride, width = _check_table(block_table, B, index)
     with _guard(index):
-        st = _lib().fa_pages_resize(refs.data_ptr(), refs.shape[0], _count(page_size), block_table.data_ptr(), stride, width,
-                                    seq_k.data_ptr(), want.data_ptr(), B, _current_stream(index))
+        st = _lib().fa_pages_resize(refs.data_ptr(), pages, _count(page_size), tp, stride, width, sp, wp, B, _current_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_pages_resize")
 
@@ -866,17 +876,13 @@ def pages_fork(k_pages: torch.Tensor, v_pages: torch.Tensor, refs: torch.Tensor,
     (seq_k 0), not among src and given once.  Returns fresh [n]: the page that a
     fork got, -1: none was needed, -2: refused, -3: no page was left."""
     cache, layers, layer_stride, index = _layers(k_pages, v_pages)
-    _check_ints(index, refs=refs, seq_k=seq_k, src=src, dst=dst)
-    if refs.shape[0] != k_pages.shape[-4]:
-        raise ValueError("refs must have an entry for each page")
-    if src.shape != dst.shape:
-        raise ValueError("src and dst must have the same length")
-    rows, n = seq_k.shape[0], src.shape[0]
-    stride, width = _check_table(block_table, rows, index)
+    n, rows = _ints("src", src)[0], _ints("seq_k", seq_k)[0]
+    rp = _check_ints("refs", refs, k_pages.shape[-4], index)
+    kp, ap, bp = _check_ints("seq_k", seq_k, rows, index), _check_ints("src", src, n, index), _check_ints("dst", dst, n, index)
+    tp, stride, width = _check_table(block_table, rows, index)
     fresh = torch.empty_like(src)
     with _guard(index):
-        st = _lib().fa_pages_fork(cache, layers, layer_stride, refs.data_ptr(), block_table.data_ptr(), stride, width,
-                                  seq_k.data_ptr(), rows, src.data_ptr(), dst.data_ptr(), fresh.data_ptr(), n,
+        st = _lib().fa_pages_fork(cache, layers, layer_stride, rp, tp, stride, width, kp, rows, ap, bp, fresh.data_ptr(), n,
                                   _current_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_pages_fork")
@@ -888,12 +894,10 @@ def cache_copy(k_pages: torch.Tensor, v_pages: torch.Tensor, src: torch.Tensor, 
     all layers (pages as in ``pages_fork``); src and dst int32 [n], no page twice
     in dst or in both."""
     cache, layers, layer_stride, index = _layers(k_pages, v_pages)
-    _check_ints(index, src=src, dst=dst)
-    if src.shape != dst.shape:
-        raise ValueError("src and dst must have the same length")
+    n, _ = _ints("src", src)
+    ap, bp = _check_ints("src", src, n, index), _check_ints("dst", dst, n, index)
     with _guard(index):
-        st = _lib().fa_cache_copy(cache, layers, layer_stride, src.data_ptr(), dst.data_ptr(), src.shape[0],
-                                  _current_stream(index))
+        st = _lib().fa_cache_copy(cache, layers, layer_stride, ap, bp, n, _current_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_cache_copy")
 
@@ -906,18 +910,16 @@ def cache_compact(k_pages: torch.Tensor, v_pages: torch.Tensor, block_table: tor
     [B], keep [B, max_keep] with keep[b, i] >= first[b] + i (any ascending list
     from first[b] on), keep_n [B], int32.  Returns the new lengths first + keep_n."""
     cache, layers, layer_stride, index = _layers(k_pages, v_pages)
-    _check_ints(index, first=first, keep_n=keep_n)
-    B = first.shape[0]
-    if keep_n.shape[0] != B:
-        raise ValueError("keep_n must have first's length")
-    if not isinstance(keep, torch.Tensor) or keep.dtype is not torch.int32 or keep.dim() != 2 or keep.shape[0] != B \
-            or keep.get_device() != index or (keep.shape[1] > 1 and keep.stride(1) != 1):
-        raise ValueError(f"keep must be an int32 [{B}, max_keep] tensor on cuda:{index}, each row contiguous")
-    stride, width = _check_table(block_table, B, index)
+    B, _ = _ints("first", first)
+    fp, np = _check_ints("first", first, B, index), _check_ints("keep_n", keep_n, B, index)
+    tp, stride, width = _check_table(block_table, B, index)
+    try:
+        kp, kept, most = _check_table(keep, B, index)
+    except ValueError:
+        raise ValueError(f"keep must be an int32 [{B}, max_keep] tensor on cuda:{index}, each row contiguous") from None
     seq_k = torch.empty_like(first)
     with _guard(index):
-        st = _lib().fa_cache_compact(cache, layers, layer_stride, block_table.data_ptr(), stride, width, first.data_ptr(),
-                                     keep.data_ptr(), keep.stride(0), keep.shape[1], keep_n.data_ptr(), seq_k.data_ptr(), B,
+        st = _lib().fa_cache_compact(cache, layers, layer_stride, tp, stride, width, fp, kp, kept, most, np, seq_k.data_ptr(), B,
                                      _current_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_cache_compact")
