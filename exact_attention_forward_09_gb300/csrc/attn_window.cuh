@@ -37,8 +37,7 @@
 // and for TREE (of PAGED), where a sequence's new tokens are the nodes of a tree:
 //   * a node's row sees the cached keys by its own position (the window's start)
 //     and the new keys by the bits of its mask row.  Only the tiles that hold a new
-//     key are masked so (one or two at the end of a context), and the words of such
-//     a tile are on their way before its scores are waited for;
+//     key are masked so (one or two at the end of a context), out of line;
 //   * every unit of a sequence starts its window at the first position that a
 //     node can have, the cached tokens' end, as a node's position is known to its own
 //     row alone; nodes lie one behind the other up to their own slot, as tokens do;
@@ -372,16 +371,10 @@ __device__ __forceinline__ uint32_t win_visible(int p, int window, int sinks, in
 
 // Which of the 32 keys from c0 on a tree's node sees that sits at position p and
 // lies at `slot`: the cached keys (below ctx) as above, and the new ones up to
-// its own that its mask row has a bit for.
-__device__ __forceinline__ uint32_t tree_visible(const uint32_t* row, int words, int ctx, int slot, int p, int window, int sinks, int c0) {
+// its own that `bits`, the part of its mask row, has.
+__device__ __forceinline__ uint32_t tree_visible(uint32_t bits, int ctx, int slot, int p, int window, int sinks, int c0) {
   const uint32_t cached = low_bits(ctx - c0);
-  uint32_t see = cached & (~low_bits(p - window + 1 - c0) | low_bits(sinks - c0));
-  const int rel = c0 - ctx, w = rel >> 5;  // (may be negative: the words begin inside these keys)
-  if (row != nullptr && w >= -1 && w < words) {
-    const uint32_t lo = w >= 0 ? __ldg(row + w) : 0u, hi = w + 1 < words ? __ldg(row + w + 1) : 0u;
-    see |= __funnelshift_r(lo, hi, rel & 31) & low_bits(slot + 1 - c0) & ~cached;
-  }
-  return see;
+  return (cached & (~low_bits(p - window + 1 - c0) | low_bits(sinks - c0))) | (bits & low_bits(slot + 1 - c0) & ~cached);
 }
 
 // The softmax of a narrow tile, the first one of its rows: 32 columns of S at
@@ -416,35 +409,69 @@ __device__ __noinline__ float2 narrow_softmax(uint32_t s_addr, uint32_t see, flo
   return make_float2(m, l);
 }
 
-// What a row of a unit needs to know which keys it sees, where its sequence's
-// new tokens are a tree.  tok: its token in the unit, -1: the row does not exist
-// (it sees what any would).
+// What a row of a unit needs to know which keys it sees, in a batch of trees.
+// tok: its token in the unit; real: whether the row exists (others see the cached
+// keys).  A plain chunk's token takes all keys up to its own as cached ones.
 template <bool TREE>
 struct WinTreeRow {
-  bool tree;
   int ctx, slot, pos;
   const uint32_t* row;
-  __device__ __forceinline__ WinTreeRow(const WinParams& prm, const WinUnit& w, int tok, int at) {
-    tree = false;
+  __device__ __forceinline__ WinTreeRow(const WinParams& prm, const WinUnit& w, int tok, bool real) {
     if constexpr (TREE) {
       ctx = w.p0 - w.q_row;
-      tree = win_is_tree(prm, w.nk - ctx);
-      if (!tree) return;
-      pos = slot = w.p0 + at;
+      pos = slot = w.p0 + tok;
       row = nullptr;
-      if (tok < 0) return;
-      row = prm.mask + (long long)(w.qz + tok) * prm.words;
-      if (prm.positions) {
-        const int p = prm.positions[w.qz + tok];
-        pos = min(max(p, ctx), slot);  // (a node has as many nodes above it as lie before it at most)
-        if (p != pos) report_index(prm.err);
+      if (!win_is_tree(prm, w.nk - ctx)) {
+        ctx = slot + 1;
+      } else if (real) {
+        row = prm.mask + (long long)(w.qz + tok) * prm.words;
+        if (prm.positions && w.lo > 0) {  // (else the window reaches over the whole sequence)
+          const int p = prm.positions[w.qz + tok];
+          pos = min(max(p, ctx), slot);  // (a node has as many nodes above it as lie before it at most)
+          if (p != pos) report_index(prm.err);
+        }
       }
     }
   }
   __device__ __forceinline__ uint32_t see(const WinParams& prm, int c0) const {
-    return tree_visible(row, prm.words, ctx, slot, pos, prm.window, prm.sinks, c0);
+    const int at = (c0 - ctx) >> 5;  // (the word of the first key; below 0: the nodes begin behind it)
+    const uint32_t lo = row && (unsigned)at < (unsigned)prm.words ? __ldg(row + at) : 0u;
+    const uint32_t hi = row && (unsigned)(at + 1) < (unsigned)prm.words ? __ldg(row + at + 1) : 0u;
+    return tree_visible(__funnelshift_r(lo, hi, (c0 - ctx) & 31), ctx, slot, pos, prm.window, prm.sinks, c0);
   }
 };
+
+// Replaces the scores that a row does not see, in a batch of trees: 128 of them at
+// s_addr, of the keys from c0 on.  Out of line, and a loop: it runs once or twice
+// per unit, and straight code would be fetched from memory line by line (unrolled
+// in the tile loop it took 4 us of a call's last tile, and 2 us of each short
+// unit; looked up ahead of the scores, with more code, 1 us).
+static __device__ __noinline__ void tree_mask_scores(uint32_t s_addr, int c0, const uint32_t* row, int words, int ctx, int slot,
+                                                     int pos, int window, int sinks, float mask_val) {
+  int at = (c0 - ctx) >> 5;  // the word that holds the first key's bit (below 0: the nodes begin behind it)
+  const int shift = (c0 - ctx) & 31;
+  auto word = [&](int i) { return (unsigned)i < (unsigned)words ? __ldg(row + i) : 0u; };
+  if (row == nullptr) words = 0;
+  uint32_t lo = word(at);
+#pragma unroll 1
+  for (int q = 0; q < 4; ++q, c0 += 32, s_addr += 32) {
+    const uint32_t hi = word(++at);
+    const uint32_t see = tree_visible(__funnelshift_r(lo, hi, shift), ctx, slot, pos, window, sinks, c0);
+    lo = hi;
+    if (__all_sync(0xffffffffu, see == 0xffffffffu)) continue;
+    uint32_t u[32];
+    tmem_ld32(s_addr, u);
+    tmem_wait_ld();
+#pragma unroll
+    for (int h = 0; h < 32; h += 16) {
+      uint32_t x[16];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) x[i] = (see & (1u << (h + i))) ? u[h + i] : __float_as_uint(mask_val);
+      tmem_st16(s_addr + h, x);
+    }
+  }
+  tmem_wait_st();
+}
 
 // Waits for the V tile at ring position pv and, where `dead`, zeroes this
 // thread's row of it (row: its shared-memory address in slot 0); made visible
@@ -837,6 +864,15 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
         pos += 2 * n * C::SPT;
         ++k;
       };
+      // Trees: the softmax warps' first look at their mask rows and positions
+      // would be a trip to memory for each unit; this warp, which is ahead of them,
+      // has the lines brought into the SM's cache (nothing waits for them here).
+      auto warm_rows = [&](const WinUnit& w) {
+        const char* rows = reinterpret_cast<const char*>(prm.mask + (long long)w.qz * prm.words);
+        const int bytes = w.ntok * prm.words * 4;
+        for (int i = lane * 128; i < bytes; i += 32 * 128) prefetch_l1(rows + i);
+        if (prm.positions && w.lo > 0 && lane * 32 < w.ntok) prefetch_l1(prm.positions + w.qz + lane * 32);
+      };
       WinUnit w;
       auto take_tiles = [&](const WinTiles& u) {
         w.ns = u.ns;
@@ -888,6 +924,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
               prm.desc[blockIdx.x] = make_int4((int)(last - blockIdx.x) + 1, w.qz, head, w.ntok * g);
             }
             ok = publish(r++, w);
+            if constexpr (TREE) warm_rows(w);
             if (ok) load_unit(w);
             rem -= run;
             at += run;
@@ -1302,9 +1339,10 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
         // this row's last visible key, its own position (a valid row's lies in
         // the sequence); the tile's strictest last and first (window) ones
         const int last = w.p0 + tok;
-        const TreeRow node(prm, w, !C::FEW && valid ? tok : -1, tok);
-        // the last key that all of the tile's rows see (but for their windows): its first row's
-        const int tile_last = TREE && node.tree ? node.ctx - 1 : w.p0 + t * tpt;
+        // the last key that all of the tile's rows see (but for their windows): its
+        // first row's, or where the rows are a tree's nodes the last cached one
+        int tile_last = w.p0 + t * tpt;
+        if (TREE && win_is_tree(prm, w.nk - (w.p0 - w.q_row))) tile_last = w.p0 - w.q_row - 1;
         const int tile_lo = w.p0 + min(w.ntok, (t + 1) * tpt) - prm.window;    // of its last row
         float m_run = -INFINITY;  // reference maximum, log2 units
         float l_run = 0.0f;
@@ -1323,14 +1361,15 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
           // lane = row, this warp's columns 32 wq .. 32 wq + 31
           const int nr = w.ntok * g;
           const int lo = w.p0 + w.ntok - prm.window;  // first key of the last row's window
-          const TreeRow node(prm, w, lane < nr ? row_tok : -1, row_tok);
+          const TreeRow node(prm, w, row_tok, lane < nr);
+          const int masked_from = TREE && tile_last < w.p0 ? tile_last + 1 : w.p0 + 1;  // keys that not every row sees
           for (int j = 0; j < n && ok; ++j) {
             const int x = it + j, l = r0 + j;
             const int buf = C::ALT ? 0 : (x & 1);
             uint32_t seen = 0;  // TREE: asked for ahead of the scores
             if constexpr (TREE) {
               const int c0 = (l < w.ns ? l : l + w.skip) * kBN + 32 * wq;
-              if (node.tree && (c0 + 32 > node.ctx || (c0 < lo && c0 + 32 > prm.sinks))) seen = node.see(prm, c0);
+              if (c0 + 32 > masked_from || (c0 < lo && c0 + 32 > prm.sinks)) seen = node.see(prm, c0);
             }
             ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], (uint32_t)((C::ALT ? sc : x >> 1) & 1),
                                                    abort_flag, prm.err));
@@ -1364,9 +1403,8 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
               tmem_ld32(s_addr + 32 * wq, u);
               tmem_wait_ld();
               const int c0 = col0 + 32 * wq;
-              const int masked_from = TREE && node.tree ? node.ctx : w.p0 + 1;  // keys that not every row sees
               if (c0 + 32 > masked_from || (c0 < lo && c0 + 32 > prm.sinks)) {
-                const uint32_t see = TREE && node.tree ? seen : win_visible(w.p0 + row_tok, prm.window, prm.sinks, c0);
+                const uint32_t see = TREE ? seen : win_visible(w.p0 + row_tok, prm.window, prm.sinks, c0);
 #pragma unroll
                 for (int i = 0; i < 32; ++i) u[i] = (see & (1u << i)) ? u[i] : __float_as_uint(mask_val);
               }
@@ -1569,7 +1607,8 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
             if (!ok) break;
           }
           const float2 ml = narrow_softmax<ELEM>(tmem + lane_addr + buf * kBN,
-                                                 win_visible(TREE && node.tree ? node.pos : last, prm.window, prm.sinks, 0), cj);
+                                                 TREE ? TreeRow(prm, w, tok, valid).see(prm, 0)
+                                                      : win_visible(last, prm.window, prm.sinks, 0), cj);
           m_run = ml.x;
           l_run = ml.y;
           tc_fence_before();
@@ -1582,15 +1621,6 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
           const int x = it + j;
           const int buf = C::ALT ? t : (x & 1);
           const uint32_t ph = C::ALT ? (uint32_t)(sc & 1) : (uint32_t)((x >> 1) & 1);
-          uint32_t seen[4];
-          if constexpr (TREE) {
-            // (asked for ahead of the scores)
-            const int c0 = (l < w.ns ? l : l + w.skip) * kBN;
-            if (node.tree && (c0 + kBN - 1 > tile_last || (c0 < tile_lo && c0 + kBN > prm.sinks))) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) seen[q] = node.see(prm, c0 + 32 * q);
-            }
-          }
           ok = __all_sync(0xffffffffu, mbar_wait(&bars->s_full[buf], ph, abort_flag, prm.err));
           ++sc;
           if (!ok) break;
@@ -1628,6 +1658,12 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
               if (!ok) break;
             }
           }
+          if constexpr (TREE) {
+            if (need_mask) {
+              const TreeRow node(prm, w, tok, valid);
+              tree_mask_scores(s_addr, col0, node.row, prm.words, node.ctx, node.slot, node.pos, prm.window, prm.sinks, mask_val);
+            }
+          }
           float s[kBN];
           {
             uint32_t u[32];
@@ -1639,11 +1675,11 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
             }
             tmem_wait_ld();
           }
-          if (need_mask) {
+          if (!TREE && need_mask) {
             // visible columns of this row as four words
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const uint32_t see = TREE && node.tree ? seen[q] : win_visible(last, prm.window, prm.sinks, col0 + 32 * q);
+              const uint32_t see = win_visible(last, prm.window, prm.sinks, col0 + 32 * q);
 #pragma unroll
               for (int i = 0; i < 32; ++i) s[32 * q + i] = (see & (1u << i)) ? s[32 * q + i] : mask_val;
             }

@@ -24,6 +24,9 @@ __device__ __forceinline__ void tma_load_4d_hint(void* smem_dst, const CUtensorM
       : "memory");
 }
 
+// Asks for a global address's line in the SM's first-level cache.
+__device__ __forceinline__ void prefetch_l1(const void* p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
+
 // In a kernel launched with programmatic stream serialisation: waits until
 // the kernel before it in the stream has ended and its writes are visible
 // (returns at once otherwise).
