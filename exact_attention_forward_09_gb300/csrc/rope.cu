@@ -37,8 +37,12 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // once per block and not once per head; a block is 256/(d/16) tokens in a row,
 // which lie together in either order of heads and tokens.  The first rows' loads
 // go out before the position and its angles are known.
+//   2 x 8192 tokens, 16 + 4 heads, d = 128: 168 MB in 27.5 us, 6.1 TB/s (0.90 of the
+//   measured copy rate; 29.2 with four rows in flight); 8 x 4096 of 32 + 8 heads
+//   103 us, 6.5 TB/s; 64 columns of d = 256 in place 15.6 us where copying the others
+//   takes 22.8; 65 tokens 2.3 us.
 constexpr int kRopeThreads = 256;
-constexpr int kRopeRows = 4;  // rows in flight per thread
+constexpr int kRopeRows = 2;  // rows in flight per thread (four take 80 registers and leave three blocks to an SM)
 
 template <int D, bool F16, int LAYOUT>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams prm, const float sign) {
@@ -143,23 +147,35 @@ cudaError_t rope_layout(const RopeParams& prm, dim3 grid, int layout, float sign
 // product would be off by p 2^-24 radians.  The nearest quarter turn is split off as
 // two bits, and what remains (at most an eighth of a turn, exact in 62 bits) is
 // rounded to fp32 relative to itself, so that values near zero keep their digits.
-// A thread keeps four pairs and steps through positions by adding.
-constexpr int kTableThreads = 256;
+// A thread keeps four pairs and steps through positions by adding; two blocks to
+// an SM, as a thread's start (four 64-bit products, frequencies at addresses that
+// differ within the warp) costs as much as some positions (eight blocks: +1.3 us).
+//   Instructions bound it: 131072 positions of 64 pairs in 12.4 us, 5.4 TB/s (a
+//   fill of as many bytes takes 9.6); 16.5 with a conversion from 64 bits, which has
+//   a small part of the rate of one from 32, and 17.9 with the library's sincospif.
+constexpr int kTableThreads = 256, kTableBlocks = 2;
 
 __device__ __forceinline__ void turn_of(uint64_t t, float& c, float& s) {
-  const uint32_t quarter = (uint32_t)((t + (1ull << 61)) >> 62);
-  const long long rest = (long long)(t - ((uint64_t)quarter << 62));
-  float a, b;  // of the rest: sine and cosine
-  sincospif((float)rest * 0x1p-63f, &a, &b);
-  const bool odd = quarter & 1;
-  c = odd ? -a : b;
-  s = odd ? b : a;
-  if (quarter & 2) {
-    c = -c;
-    s = -s;
-  }
+  const uint32_t h = (uint32_t)(t >> 32) + 0x20000000u;  // bits 31, 30: the nearest quarter turn
+  const int top = (int)(h & 0x3fffffffu) - 0x20000000;   // the rest's upper word
+  // The rest in half turns, at most a quarter, rounded once: its upper 24 bits are
+  // exact in fp32, and the 32 behind them add to them.
+  const float x = fmaf((float)(top >> 6), 0x1p-25f, (float)__funnelshift_r((uint32_t)t, (uint32_t)top, 6) * 0x1p-57f);
+  // sin(pi x) and cos(pi x): polynomials in x^2 that are nearest to them over this
+  // range (fitted by weighted least squares, the weights moved toward the largest
+  // errors as Lawson's method does), to 1.8e-11 and 2e-10; pi in two parts
+  const float u = x * x;
+  const float ps = fmaf(u, fmaf(u, fmaf(u, fmaf(u, 0.0812298f, -0.59922882f), 2.5501636f), -5.1677128f), -8.7422777e-8f);
+  const float pc = fmaf(u, fmaf(u, fmaf(u, 0.23212635f, -1.3351379f), 4.0587106f), -4.9348022f);
+  const float a = fmaf(x, 3.14159274f, x * ps), b = fmaf(u, pc, 1.0f);
+  // an odd quarter swaps the two; the sine's sign is the quarter's upper bit, the
+  // cosine's that and the lower one
+  const bool odd = h & 0x40000000u;
+  c = __uint_as_float(__float_as_uint(odd ? a : b) ^ ((h ^ (h << 1)) & 0x80000000u));
+  s = __uint_as_float(__float_as_uint(odd ? b : a) ^ (h & 0x80000000u));
 }
 
+template <bool AMP>  // whether there is an amplitude other than 1
 __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_constant__ RopeTableParams prm) {
   const int groups = prm.half / 4;                 // threads of a position
   const int per = kTableThreads / groups;          // positions of a block at a time
@@ -180,9 +196,11 @@ __global__ void __launch_bounds__(kTableThreads) rope_table_kernel(const __grid_
     for (int i = 0; i < 4; ++i) {
       turn_of(t[i], c[i], s[i]);
       t[i] += dt[i];
-      // times the amplitude, rounded once
-      c[i] = fmaf(c[i], prm.amp_hi, c[i] * prm.amp_lo);
-      s[i] = fmaf(s[i], prm.amp_hi, s[i] * prm.amp_lo);
+      if constexpr (AMP) {
+        // rounded once
+        c[i] = fmaf(c[i], prm.amp_hi, c[i] * prm.amp_lo);
+        s[i] = fmaf(s[i], prm.amp_hi, s[i] * prm.amp_lo);
+      }
     }
     const long long at = p * prm.half + 4 * g;
     *reinterpret_cast<float4*>(prm.cos + at) = make_float4(c[0], c[1], c[2], c[3]);
@@ -197,9 +215,9 @@ cudaError_t launch_rope(RopeParams prm, int64_t B, int d, bool f16, int layout, 
   prm.tiles = (prm.N + tb - 1) / tb;
   const int64_t blocks = B * prm.tiles;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  // As many heads to a block as leave eight blocks per SM, so that a small call
+  // As many heads to a block as leave 16 blocks per SM, so that a small call
   // spreads over the GPU and a large one reads its angles seldom.
-  int64_t groups = (8LL * sms + blocks - 1) / blocks;
+  int64_t groups = (16LL * sms + blocks - 1) / blocks;
   if (groups > prm.heads) groups = prm.heads;
   if (groups < 1) groups = 1;
   prm.heads_per_block = (int)((prm.heads + groups - 1) / groups);
@@ -217,8 +235,9 @@ cudaError_t launch_rope(RopeParams prm, int64_t B, int d, bool f16, int layout, 
 cudaError_t launch_rope_table(const RopeTableParams& prm, int sms, cudaStream_t stream) {
   const int per = kTableThreads / (prm.half / 4);
   int64_t blocks = ((int64_t)prm.n + per - 1) / per;
-  if (blocks > 8LL * sms) blocks = 8LL * sms;  // (all the threads that an SM holds; then each steps on)
-  rope_table_kernel<<<(unsigned)blocks, kTableThreads, 0, stream>>>(prm);
+  if (blocks > kTableBlocks * (int64_t)sms) blocks = kTableBlocks * (int64_t)sms;  // (then each steps on)
+  if (prm.amp_hi == 1.0f && prm.amp_lo == 0.0f) rope_table_kernel<false><<<(unsigned)blocks, kTableThreads, 0, stream>>>(prm);
+  else rope_table_kernel<true><<<(unsigned)blocks, kTableThreads, 0, stream>>>(prm);
   return cudaGetLastError();
 }
 
