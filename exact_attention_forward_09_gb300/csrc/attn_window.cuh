@@ -425,7 +425,7 @@ struct WinTreeRow {
         ctx = slot + 1;
       } else if (real) {
         row = prm.mask + (long long)(w.qz + tok) * prm.words;
-        if (prm.positions && w.lo > 0) {  // (else the window reaches over the whole sequence)
+        if (prm.positions && prm.window < w.nk) {  // (else the window reaches over the whole sequence)
           const int p = prm.positions[w.qz + tok];
           pos = min(max(p, ctx), slot);  // (a node has as many nodes above it as lie before it at most)
           if (p != pos) report_index(prm.err);
@@ -871,7 +871,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
         const char* rows = reinterpret_cast<const char*>(prm.mask + (long long)w.qz * prm.words);
         const int bytes = w.ntok * prm.words * 4;
         for (int i = lane * 128; i < bytes; i += 32 * 128) prefetch_l1(rows + i);
-        if (prm.positions && w.lo > 0 && lane * 32 < w.ntok) prefetch_l1(prm.positions + w.qz + lane * 32);
+        if (prm.positions && prm.window < w.nk && lane * 32 < w.ntok) prefetch_l1(prm.positions + w.qz + lane * 32);
       };
       WinUnit w;
       auto take_tiles = [&](const WinTiles& u) {

@@ -175,6 +175,14 @@ def test_window_and_sinks(fa, window, sinks, d):
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
+def test_windows_that_end_among_the_nodes(fa, d):
+    # longer than what is cached, shorter than where the last node lies: by its depth a node may see all of it
+    for window in (30, 33, 34, 60, 69, 70):
+        _run(fa, [(37, 70), (37, 70), (4, 36), (60, 61)], 4, 1, d, torch.float16, 32, window=window, sinks=1)
+        _run(fa, [(4, 30), (3, 33), (4, 34)], 4, 1, d, torch.bfloat16, 16, words=1, window=min(window, 31), max_q=4)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("window", [ALL, 300])
 def test_few_nodes_under_a_window(fa, d, window):
     _run(fa, FEW + [(4, 3000)] * 3, 4, 1, d, torch.float16, 16, words=1, window=window, sinks=4, max_q=4)
