@@ -351,12 +351,18 @@ __device__ __forceinline__ int win_group_len(const WinParams& prm, const WinSeq&
 // one otherwise, rounded up to even, so that CTAs, which start at even
 // places, start at whole tiles.  (Forms with one query tile per CTA: one each.)
 // A unit's start and end are not counted, so runs that hold many short units
-// take longer than others.
+// take longer than others; but for trees, whose units are all of a batch's, and
+// take two tiles' places behind their own (32 x 60 nodes over 1000 to 8000 keys
+// 152.7 -> 142.2 us, 200 x 20 to 60 over 100 to 600 182 -> 156; with one tile's places
+// 146.8 and 165; with three 141.6 and 158, but 32 x 16 nodes 111.5 -> 113.6).  A run
+// that begins within them has none of the unit.
 template <int NQT>
 __device__ __forceinline__ uint32_t win_places(int len, int ntok, int tpt) {
   if (NQT == 1) return (uint32_t)len;
   return ntok > tpt ? 2u * (uint32_t)len : ((uint32_t)len + 1u) & ~1u;
 }
+template <int NQT, bool TREE>
+constexpr uint32_t end_places() { return TREE ? 2u * NQT : 0u; }
 
 // bits [0, n) of a 32-bit word, n clamped to 0..32
 __device__ __forceinline__ uint32_t low_bits(int n) {
@@ -554,6 +560,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
   using C = WinCfg<ELEM, D, PAGED, FORM>;
   using Bars = WinBars<C::NS>;
   using TreeRow = WinTreeRow<TREE>;
+  constexpr uint32_t END = end_places<C::NQT, TREE>();  // of a unit's places, those behind its tiles'
   static_assert(sizeof(Bars) <= 1024, "barrier area");
   static_assert(!TREE || PAGED, "trees lie in a paged cache");
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -635,7 +642,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
       return win_seq(prm, prm.cu_q[b], prm.cu_q[b + 1], prm.seq_k[b], &bad);
     };
     auto group_places = [&](const WinSeq& q, int i) -> uint32_t {
-      return win_places<C::NQT>(win_group_len<TREE>(prm, q, tpg, i), min(tpg, q.nq - i * tpg), tpt) * (uint32_t)prm.Hkv;
+      return (win_places<C::NQT>(win_group_len<TREE>(prm, q, tpg, i), min(tpg, q.nq - i * tpg), tpt) + END) * (uint32_t)prm.Hkv;
     };
     auto add = [&](uint32_t a, uint32_t b) -> uint32_t { return min(a + b, prm.max_places + 1); };  // (both at most that)
     auto seq_places = [&](const WinSeq& q) -> uint32_t {
@@ -893,7 +900,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
           int b = bars->start_b, i = bars->start_group, len = bars->start_len;
           WinSeq s = {bars->start_tok0, bars->start_nq, bars->start_nk};
           int ntok = min(tpg, s.nq - i * tpg);
-          uint32_t places = win_places<C::NQT>(len, ntok, tpt);
+          uint32_t places = win_places<C::NQT>(len, ntok, tpt) + END;
           int head = (int)(bars->start_off / places);
           uint32_t off = bars->start_off % places;
           bool bad = false;
@@ -901,7 +908,8 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
             // [off, off + run) of the unit's places are this CTA's
             const uint32_t run = min(rem, places - off);
             const int per_tile = C::NQT == 2 && ntok > tpt ? 2 : 1;
-            const bool begins = off == 0, ends = off + run == places;
+            const bool begins = off == 0, ends = off + run >= places - END;
+            const bool none = TREE && off >= places - END;  // of its tiles
             w.kz = head;
             w.seq = b;
             w.q_row = i * tpg;
@@ -919,13 +927,15 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
             w.r1 = ends ? u.len : min(u.len, (int)(off + run) / per_tile);
             w.part = begins && ends ? -1 : 2 * (int)blockIdx.x + (begins ? 1 : 0);
             if (begins && !ends && lane == 0) {
-              // parts: up to the CTA that holds the unit's last place
-              const uint32_t last = min((at + places - 1) / line_per, gridDim.x - 1);
+              // parts: up to the CTA that holds the last place of the unit's tiles
+              const uint32_t last = min((at + places - END - 1) / line_per, gridDim.x - 1);
               prm.desc[blockIdx.x] = make_int4((int)(last - blockIdx.x) + 1, w.qz, head, w.ntok * g);
             }
-            ok = publish(r++, w);
-            if constexpr (TREE) warm_rows(w);
-            if (ok) load_unit(w);
+            if (!none) {
+              ok = publish(r++, w);
+              if constexpr (TREE) warm_rows(w);
+              if (ok) load_unit(w);
+            }
             rem -= run;
             at += run;
             if (rem == 0) break;
@@ -942,7 +952,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
               }
               len = win_group_len<TREE>(prm, s, tpg, i);
               ntok = min(tpg, s.nq - i * tpg);
-              places = win_places<C::NQT>(len, ntok, tpt);
+              places = win_places<C::NQT>(len, ntok, tpt) + END;
             }
           }
         }

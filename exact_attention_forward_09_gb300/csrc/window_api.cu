@@ -254,6 +254,7 @@ fa_status fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse
   const int64_t reach = p.window + (int64_t)p.sinks + unit_tok + 32 * words;  // (a tree's units start their windows at its root's)
   if (reach < keys) tiles = reach / fa::kBN + 4;
   const int64_t units = (T / unit_tok + B) * Hkv;
+  if (mask) tiles += 2;  // (the places behind a tree unit's: end_places)
   if (units >= (int64_t)0x7fffffff / (2 * (tiles + 1))) return FA_ERR_UNSUPPORTED;
   p.max_places = (uint32_t)(units * 2 * (tiles + 1));
   uint8_t* w = static_cast<uint8_t*>(workspace);
