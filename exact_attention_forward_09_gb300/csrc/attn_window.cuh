@@ -441,8 +441,8 @@ struct WinTreeRow {
   }
   __device__ __forceinline__ uint32_t see(const WinParams& prm, int c0) const {
     const int at = (c0 - ctx) >> 5;  // (the word of the first key; below 0: the nodes begin behind it)
-    const uint32_t lo = row && (unsigned)at < (unsigned)prm.words ? __ldg(row + at) : 0u;
-    const uint32_t hi = row && (unsigned)(at + 1) < (unsigned)prm.words ? __ldg(row + at + 1) : 0u;
+    const uint32_t lo = row && (unsigned)at < (unsigned)prm.words ? row[at] : 0u;
+    const uint32_t hi = row && (unsigned)(at + 1) < (unsigned)prm.words ? row[at + 1] : 0u;
     return tree_visible(__funnelshift_r(lo, hi, (c0 - ctx) & 31), ctx, slot, pos, prm.window, prm.sinks, c0);
   }
 };
@@ -456,7 +456,7 @@ static __device__ __noinline__ void tree_mask_scores(uint32_t s_addr, int c0, co
                                                      int pos, int window, int sinks, float mask_val) {
   int at = (c0 - ctx) >> 5;  // the word that holds the first key's bit (below 0: the nodes begin behind it)
   const int shift = (c0 - ctx) & 31;
-  auto word = [&](int i) { return (unsigned)i < (unsigned)words ? __ldg(row + i) : 0u; };
+  auto word = [&](int i) { return (unsigned)i < (unsigned)words ? row[i] : 0u; };
   if (row == nullptr) words = 0;
   uint32_t lo = word(at);
 #pragma unroll 1

@@ -48,10 +48,11 @@ __device__ __forceinline__ void load_cols(float (&x)[E], const float* src) {
 // of a NaN row has weight NaN, and the row stays NaN
 __device__ __forceinline__ float part_weight(float l, float m) { return l == -INFINITY ? 0.0f : expf(l - m); }
 
+// (No pointer is __restrict__: what is read through a const one that is may be read
+// ahead of pdl_wait, by the compiler's choice.)
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads) paged_combine_kernel(
-    const float* __restrict__ o_part, const float* __restrict__ lse_part, const int4* __restrict__ desc,
-    void* __restrict__ o, float* __restrict__ lse, int ctas, int slot_rows, int g, int Hq) {
+    const float* o_part, const float* lse_part, const int4* desc, void* o, float* lse, int ctas, int slot_rows, int g, int Hq) {
   constexpr int E = D / 32;
   __shared__ float red[8][D];
   __shared__ float red_w[8];

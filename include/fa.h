@@ -645,9 +645,10 @@ fa_status fa_tree_plan(const int32_t* parents, const int32_t* cu_q, const int32_
  *   words      1 to 32.  Sequences of more than 32 * words new tokens attend as in
  *              fa_fwd_paged, whatever their mask rows hold
  *   positions  [T] int32 (device), as fa_tree_plan writes them: between seq_k[b] -
- *              n and where the token lies (others are cut to that, and reported by
- *              fa_check_device_error as FA_ERR_INDEX).  NULL: where the tokens lie.
- *              They matter under a window alone
+ *              n and where the token lies.  NULL: where the tokens lie.  They are
+ *              looked at under a window shorter than the sequence alone; others are
+ *              then cut to the above and reported by fa_check_device_error as
+ *              FA_ERR_INDEX
  * Everything else as in fa_fwd_paged, its workspace included.  Pages that hold
  * no key from position seq_k[b] - n - window + 1 on, nor a sink, are not read.
  */
@@ -871,7 +872,8 @@ const char* fa_status_string(fa_status status);
  * library's device error word on the current device: FA_ERR_TIMEOUT if a
  * kernel gave up on a pipeline wait since that was last reported, else
  * FA_ERR_INDEX if a kernel met an index out of range in device memory
- * (fa_fwd_paged, fa_cache_append) since that was, FA_ERR_CUDA if the
+ * (fa_fwd_paged and the calls on trees, positions and pages) since that was,
+ * FA_ERR_CUDA if the
  * synchronisation itself failed, else FA_OK.  One error is reported per call:
  * after both kinds the next call reports the second.
  */
@@ -879,8 +881,8 @@ fa_status fa_check_device_error(cudaStream_t stream);
 
 /*
  * fa_debug_inject -- TEST HOOK for the failure path; not for production use.
- * flags bit 0: the next fa_fwd / fa_fwd_fp8 / fa_fwd_window / fa_fwd_paged
- * launch has its first CTA leave one K/V ring slot unfilled (the next fa_bwd
+ * flags bit 0: the next fa_fwd / fa_fwd_fp8 / fa_fwd_window / fa_fwd_paged /
+ * fa_fwd_tree launch has its first CTA leave one K/V ring slot unfilled (the next fa_bwd
  * or fa_bwd_window launch: one Q/dO stage of its first CTA's second step), so the bounded waits on it run out (about 2 s):
  * the kernel then stops every role, frees its tensor memory and ends, and
  * fa_check_device_error() returns FA_ERR_TIMEOUT.  The output of that
