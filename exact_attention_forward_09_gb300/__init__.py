@@ -640,8 +640,8 @@ def fwd_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, bloc
     return _fwd_paged(q, k_pages, v_pages, block_table, cu_q, seq_k, mask, positions, window, sinks, scale, max_q, out, lse, workspace)
 
 
-def _check_rope(rope, index):
-    """(cos, sin, positions, rotated columns, layout) of a rope = (cos, sin, layout)."""
+def _check_rope(rope, d, index):
+    """(cos, sin, positions, rotated columns, layout) of a rope = (cos, sin, layout) for rows of d."""
     cos, sin, layout = rope
     if layout not in (FA_ROPE_INTERLEAVED, FA_ROPE_HALF):
         raise ValueError("rope layout must be FA_ROPE_INTERLEAVED or FA_ROPE_HALF")
@@ -650,8 +650,10 @@ def _check_rope(rope, index):
         if len(shape) == 2 and sin.shape == shape and cos.dtype is f32 and sin.dtype is f32 and cos.get_device() == index \
                 and sin.get_device() == index and cos.is_contiguous() and sin.is_contiguous():
             n, half = shape
-            return cos.data_ptr(), sin.data_ptr(), n, 2 * half, int(layout)
-    raise ValueError(f"rope cos and sin must be contiguous fp32 [positions, rope_dim/2] tensors on cuda:{index}")
+            if 8 <= half <= d // 2 and half % 8 == 0:
+                return cos.data_ptr(), sin.data_ptr(), n, 2 * half, int(layout)
+    raise ValueError(f"rope cos and sin must be contiguous fp32 [positions, rope_dim/2] tensors on cuda:{index}, rope_dim a "
+                     f"multiple of 16 up to d = {d}")
 
 
 def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -685,7 +687,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
         raise ValueError("q_out needs q")
     cp, sp, n, r, layout, pp = None, None, 0, 0, 0, None
     if rope is not None:
-        cp, sp, n, r, layout = _check_rope(rope, index)
+        cp, sp, n, r, layout = _check_rope(rope, d, index)
         if positions is not None:
             _check_out("positions", positions, (T,), torch.int32, index)
             pp = positions.data_ptr()
@@ -788,7 +790,7 @@ def rope(q: torch.Tensor, k: torch.Tensor | None, rope, positions: torch.Tensor 
     else:
         N, _, d = shape
         B = 1
-    cp, sp, length, r, layout = _check_rope(rope, index)
+    cp, sp, length, r, layout = _check_rope(rope, d, index)
     q_out, arrays = _rope_array("q", q, q_out, four, B, N, d, dt, index)
     if k is not None:
         k_out, more = _rope_array("k", k, k_out, four, B, N, d, dt, index)

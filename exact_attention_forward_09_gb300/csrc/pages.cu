@@ -10,8 +10,6 @@
 namespace fa {
 namespace {
 
-constexpr int kPoolThreads = 1024;
-
 // Tokens as a row of the table can hold them; *bad where they had to be cut.
 __device__ __forceinline__ int cut_tokens(int n, const PoolParams& prm, bool& bad) {
   const long long cap = (long long)prm.max_pages << prm.page_shift;
@@ -23,7 +21,8 @@ __device__ __forceinline__ int pages_of(int tokens, int shift) {
   return (int)(((long long)tokens + (1 << shift) - 1) >> shift);
 }
 
-// Exclusive sum over the block's threads, and the total.
+// Exclusive sum over the block's THREADS threads, and the total.
+template <int THREADS>
 __device__ __forceinline__ long long block_scan(long long x, long long& total, long long* sums) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long incl = x;
@@ -35,13 +34,13 @@ __device__ __forceinline__ long long block_scan(long long x, long long& total, l
   __syncthreads();  // (the sums of the call before have been read)
   if (lane == 31) sums[warp] = incl;
   __syncthreads();
-  long long w = sums[lane];
+  long long w = lane < THREADS / 32 ? sums[lane] : 0;
 #pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
+  for (int d = 1; d < THREADS / 32; d <<= 1) {
     const long long y = __shfl_up_sync(0xffffffffu, w, d);
     if (lane >= d) w += y;
   }
-  total = __shfl_sync(0xffffffffu, w, 31);
+  total = __shfl_sync(0xffffffffu, w, THREADS / 32 - 1);
   const long long before = __shfl_sync(0xffffffffu, w, warp == 0 ? 0 : warp - 1);
   return incl - x + (warp == 0 ? 0 : before);
 }
@@ -49,9 +48,9 @@ __device__ __forceinline__ long long block_scan(long long x, long long& total, l
 // The lowest-numbered free pages: give(rank, page) for the first `need` of
 // them in ascending order.  Returns how many there are (at least `need` where
 // there are more).  The reference counts are read 16 to a thread and block-wide
-// round, the next round's on their way while this one's are counted: 16384 pages
-// a round, and no list of free pages has to be kept.
-template <typename Give>
+// round, the next round's on their way while this one's are counted, and no list of
+// free pages has to be kept.
+template <int THREADS, typename Give>
 __device__ __forceinline__ long long take_free(const int* refs, int num_pages, long long need, long long* sums, Give give) {
   constexpr int PER = 16;
   int4 next[PER / 4];
@@ -72,14 +71,14 @@ __device__ __forceinline__ long long take_free(const int* refs, int num_pages, l
   };
   long long found = 0;
   if (need > 0) load(0);
-  for (long long base = 0; base < num_pages && found < need; base += kPoolThreads * PER) {
+  for (long long base = 0; base < num_pages && found < need; base += THREADS * PER) {
     uint32_t free = 0;
 #pragma unroll
     for (int i = 0; i < PER / 4; ++i)
       free |= ((next[i].x == 0 ? 1u : 0u) | (next[i].y == 0 ? 2u : 0u) | (next[i].z == 0 ? 4u : 0u) | (next[i].w == 0 ? 8u : 0u)) << (4 * i);
-    load(base + kPoolThreads * PER);
+    load(base + THREADS * PER);
     long long total;
-    long long rank = found + block_scan(__popc(free), total, sums);
+    long long rank = found + block_scan<THREADS>(__popc(free), total, sums);
     for (; free != 0 && rank < need; ++rank, free &= free - 1)
       give(rank, (int)(base + threadIdx.x * PER + (__ffs(free) - 1)));
     found += total;
@@ -99,71 +98,77 @@ __device__ __forceinline__ int owner_of(const int* start, int n, long long rank)
 }
 
 // -------------------------------------------------------------- resize --
-// All latency: a few words per row and page.  One block, so that the rows that
-// shrink have given their pages back before the free ones are counted, in one
-// launch; where the table is large a kernel with a warp per row does the giving
-// back (SPLIT).
-__device__ __forceinline__ void release_row(const PoolParams& prm, const int* want, int row) {
-  const int lane = threadIdx.x & 31;
+// All latency: a few words per row and page.  A block per row gives back, then one
+// block hands out, launched ahead and waiting: of 256 threads, whose barriers take
+// less, or of 1024 where many counts or rows are looked over.
+//   64 rows that grow by a page each 9.0 us, 10.4 with 1024 threads; with the free
+//   ones behind 64000 pages 18.1 and 16.5; 4096 rows 30.7 and 26.4.  256 rows of 1024
+//   pages all given back: 6.9 us, and 163 by one block that does both; 16 rows of
+//   64: 2.9 and 4.2 (0.7 less where nothing is given back).
+constexpr int kReleaseThreads = 128;
+
+__global__ void __launch_bounds__(kReleaseThreads) release_kernel(const PoolParams prm, const int* __restrict__ want) {
+  constexpr int AHEAD = 4;  // entries in flight per thread
+  pdl_launch();
+  const int row = blockIdx.x;
   bool bad = false;
   const int hold = pages_of(cut_tokens(prm.seq_k[row], prm, bad), prm.page_shift);
   const int goal = pages_of(cut_tokens(want[row], prm, bad), prm.page_shift);
   int* entries = prm.table + row * prm.table_stride;
-  for (int j = goal + lane; j < hold; j += 32) {
-    const int page = entries[j];
-    entries[j] = -1;
-    if ((unsigned)page >= (unsigned)prm.num_pages) {
+  for (long long j0 = goal + threadIdx.x; j0 < hold; j0 += kReleaseThreads * AHEAD) {
+    int page[AHEAD], held[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) page[i] = j0 + i * kReleaseThreads < hold ? entries[j0 + i * kReleaseThreads] : 0;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      held[i] = 1;
+      if (j0 + i * kReleaseThreads >= hold) continue;
+      entries[j0 + i * kReleaseThreads] = -1;
+      held[i] = (unsigned)page[i] < (unsigned)prm.num_pages ? atomicSub(prm.refs + page[i], 1) : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      if (held[i] > 0) continue;
       bad = true;
-    } else if (atomicSub(prm.refs + page, 1) <= 0) {
-      atomicAdd(prm.refs + page, 1);  // nobody held it
-      bad = true;
+      if ((unsigned)page[i] < (unsigned)prm.num_pages) atomicAdd(prm.refs + page[i], 1);  // nobody held it
     }
   }
   if (bad) report_index(prm.err);
 }
 
-__global__ void __launch_bounds__(256) release_kernel(const PoolParams prm, const int* __restrict__ want) {
-  pdl_launch();
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
-  if (row < prm.rows) release_row(prm, want, row);
-}
-
-template <bool SPLIT>
-__global__ void __launch_bounds__(kPoolThreads) resize_kernel(const PoolParams prm, const int* want) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) resize_kernel(const PoolParams prm, const int* want) {
   extern __shared__ int start[];  // [rows] the rank of a row's first new page
   __shared__ long long sums[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if constexpr (SPLIT) {
-    pdl_wait();
-  } else {
-    for (int row = warp; row < prm.rows; row += kPoolThreads / 32) release_row(prm, want, row);
-    __syncthreads();
-  }
-  bool bad = false;  // (cut lengths have been reported by release_row)
+  pdl_wait();
+  bool bad = false;  // (cut lengths have been reported by release_kernel)
   auto hold_of = [&](int row) { return pages_of(cut_tokens(prm.seq_k[row], prm, bad), prm.page_shift); };
   auto goal_of = [&](int row) { return pages_of(cut_tokens(want[row], prm, bad), prm.page_shift); };
-  // each thread a contiguous share of the rows
-  const int share = (prm.rows + kPoolThreads - 1) / kPoolThreads;
-  const int row0 = min(prm.rows, (int)threadIdx.x * share), row1 = min(prm.rows, row0 + share);
-  long long mine = 0, need;
-  for (int row = row0; row < row1; ++row) mine += max(0, goal_of(row) - hold_of(row));
-  long long at = block_scan(mine, need, sums);
-  for (int row = row0; row < row1; ++row) {
-    start[row] = (int)min(at, (long long)INT_MAX);  // (no page has so high a rank)
-    at += max(0, goal_of(row) - hold_of(row));
+  long long need = 0;
+  for (int base = 0; base < prm.rows; base += THREADS) {
+    const int row = base + threadIdx.x;
+    long long total;
+    const long long before = block_scan<THREADS>(row < prm.rows ? max(0, goal_of(row) - hold_of(row)) : 0, total, sums);
+    if (row < prm.rows) start[row] = (int)min(need + before, (long long)INT_MAX);  // (no page has so high a rank)
+    need += total;
   }
   __syncthreads();
-  const long long found = take_free(prm.refs, prm.num_pages, need, sums, [&](long long rank, int page) {
+  const long long found = take_free<THREADS>(prm.refs, prm.num_pages, need, sums, [&](long long rank, int page) {
     const int row = owner_of(start, prm.rows, rank);
     prm.table[row * prm.table_stride + hold_of(row) + (rank - start[row])] = page;
     prm.refs[page] = 1;
   });
   __syncthreads();  // the rows' old lengths have been read
-  for (int row = warp; row < prm.rows; row += kPoolThreads / 32) {
+  if (found >= need) {
+    for (int row = threadIdx.x; row < prm.rows; row += THREADS) prm.seq_k[row] = cut_tokens(want[row], prm, bad);
+    return;
+  }
+  // the pages ran out: the entries that got none are marked
+  for (int row = warp; row < prm.rows; row += THREADS / 32) {
     const int hold = hold_of(row), goal = goal_of(row), tokens = cut_tokens(want[row], prm, bad);
     int room = goal;
-    if (goal > hold && found < need) {
-      // the pages ran out: the entries that got none are marked
+    if (goal > hold) {
       room = hold + (int)max(0LL, min((long long)(goal - hold), found - start[row]));
       for (int j = room + lane; j < goal; j += 32) prm.table[row * prm.table_stride + j] = -1;
     }
@@ -234,7 +239,8 @@ __global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const PageRows
 // (there was none left).
 constexpr int kWhole = -1, kRefused = -2, kNoPage = -3;
 
-__global__ void __launch_bounds__(kPoolThreads) fork_plan_kernel(const PoolParams prm, const int* src, const int* dst, int* fresh, int n) {
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) fork_plan_kernel(const PoolParams prm, const int* src, const int* dst, int* fresh, int n) {
   extern __shared__ int smem[];
   __shared__ long long sums[32];
   pdl_launch();
@@ -242,9 +248,9 @@ __global__ void __launch_bounds__(kPoolThreads) fork_plan_kernel(const PoolParam
   const int words = (prm.rows + 31) / 32;
   uint32_t* is_src = reinterpret_cast<uint32_t*>(smem + n);
   uint32_t *is_dst = is_src + words, *twice = is_dst + words;
-  for (int i = threadIdx.x; i < 3 * words; i += kPoolThreads) is_src[i] = 0;
+  for (int i = threadIdx.x; i < 3 * words; i += THREADS) is_src[i] = 0;
   __syncthreads();
-  for (int f = threadIdx.x; f < n; f += kPoolThreads) {
+  for (int f = threadIdx.x; f < n; f += THREADS) {
     const int a = src[f], b = dst[f];
     if ((unsigned)a < (unsigned)prm.rows) atomicOr(is_src + (a >> 5), 1u << (a & 31));
     if ((unsigned)b < (unsigned)prm.rows && (atomicOr(is_dst + (b >> 5), 1u << (b & 31)) >> (b & 31) & 1))
@@ -263,7 +269,7 @@ __global__ void __launch_bounds__(kPoolThreads) fork_plan_kernel(const PoolParam
     if ((tokens & ((1 << prm.page_shift) - 1)) == 0) return kWhole;
     return (unsigned)prm.table[a * prm.table_stride + (tokens >> prm.page_shift)] < (unsigned)prm.num_pages ? 0 : kRefused;
   };
-  const int share = (n + kPoolThreads - 1) / kPoolThreads;
+  const int share = (n + THREADS - 1) / THREADS;
   const int f0 = min(n, (int)threadIdx.x * share), f1 = min(n, f0 + share);
   long long mine = 0, need;
   for (int f = f0; f < f1; ++f) {
@@ -273,14 +279,14 @@ __global__ void __launch_bounds__(kPoolThreads) fork_plan_kernel(const PoolParam
     mine += what == 0;
     start[f] = what == 0;
   }
-  long long at = block_scan(mine, need, sums);
+  long long at = block_scan<THREADS>(mine, need, sums);
   for (int f = f0; f < f1; ++f) {
     const int one = start[f];
     start[f] = (int)at;
     at += one;
   }
   __syncthreads();
-  take_free(prm.refs, prm.num_pages, need, sums, [&](long long rank, int page) {
+  take_free<THREADS>(prm.refs, prm.num_pages, need, sums, [&](long long rank, int page) {
     fresh[owner_of(start, n, rank)] = page;
     prm.refs[page] = 1;
   });
@@ -414,38 +420,44 @@ void dependent_launch(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, dim3 g
   cfg.numAttrs = 1;
 }
 
-// Lets a kernel take the shared memory that `bytes` ask for.
+// Lets a kernel take `bytes` of dynamic shared memory.  (48 KB, its static part
+// included, need no asking.)
 template <typename K>
 cudaError_t allow_smem(K kern, size_t bytes) {
-  return bytes <= 48 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  return bytes <= 40 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
 }
 
 }  // namespace
 
+// Whether a pool's block has 1024 threads: see release_kernel.
+static bool large_pool(int num_pages, int rows) { return num_pages > 16384 || rows > 1024; }
+
 cudaError_t launch_pages_resize(const PoolParams& prm, const int* want, cudaStream_t stream) {
   const size_t smem = (size_t)prm.rows * sizeof(int);
-  const bool split = (int64_t)prm.rows * prm.max_pages > 65536;
-  cudaError_t e = split ? allow_smem(resize_kernel<true>, smem) : allow_smem(resize_kernel<false>, smem);
-  if (e != cudaSuccess) return e;
-  if (!split) {
-    resize_kernel<false><<<1, kPoolThreads, smem, stream>>>(prm, want);
-    return cudaGetLastError();
-  }
-  release_kernel<<<(unsigned)((prm.rows + 7) / 8), 256, 0, stream>>>(prm, want);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg;
-  cudaLaunchAttribute attr[1];
-  dependent_launch(cfg, attr, dim3(1, 1, 1), kPoolThreads, smem, stream);
-  return cudaLaunchKernelEx(&cfg, resize_kernel<true>, prm, want);
+  auto go = [&](auto kern, unsigned threads) {
+    cudaError_t e = allow_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    release_kernel<<<(unsigned)prm.rows, kReleaseThreads, 0, stream>>>(prm, want);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    dependent_launch(cfg, attr, dim3(1, 1, 1), threads, smem, stream);
+    return cudaLaunchKernelEx(&cfg, kern, prm, want);
+  };
+  return large_pool(prm.num_pages, prm.rows) ? go(resize_kernel<1024>, 1024) : go(resize_kernel<256>, 256);
 }
 
 cudaError_t launch_pages_fork(const PoolParams& prm, const PageRows& rows, int d, const int* src, const int* dst, int* fresh, int n,
                               cudaStream_t stream) {
   const size_t smem = ((size_t)n + 3 * ((prm.rows + 31) / 32)) * sizeof(int);
-  cudaError_t e = allow_smem(fork_plan_kernel, smem);
+  auto plan = [&](auto kern, int threads) {
+    const cudaError_t e = allow_smem(kern, smem);
+    if (e != cudaSuccess) return e;
+    kern<<<1, threads, smem, stream>>>(prm, src, dst, fresh, n);
+    return cudaGetLastError();
+  };
+  const cudaError_t e = large_pool(prm.num_pages, n) ? plan(fork_plan_kernel<1024>, 1024) : plan(fork_plan_kernel<256>, 256);
   if (e != cudaSuccess) return e;
-  fork_plan_kernel<<<1, kPoolThreads, smem, stream>>>(prm, src, dst, fresh, n);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   cudaLaunchConfig_t cfg;
   cudaLaunchAttribute attr[1];
   auto go = [&](auto kern, unsigned blocks) {

@@ -265,9 +265,9 @@ class Pool:
 
 
 @pytest.mark.parametrize("num_pages,rows,max_pages,page", [(40, 9, 12, 16), (7, 3, 5, 64), (300, 33, 40, 16), (1, 1, 1, 16), (17001, 5, 6000, 16),
-                                                           (40000, 70, 1200, 32), (1003, 1500, 3, 16)])
+                                                           (40000, 70, 1200, 32), (1003, 1500, 3, 16), (2000, 12288, 1, 16)])
 def test_resize_follows_the_model(fa, num_pages, rows, max_pages, page):
-    # (the last three: several rounds over the counts; a table that takes a launch of its own; more rows than threads)
+    # (the last four: several rounds over the counts, long rows, more rows than threads, and as many as 48 KB hold ranks of)
     rng = random.Random(num_pages)
     pool = Pool(num_pages, rows, max_pages, page)
     refs, table, seq = ints(pool.refs), ints(pool.table), ints(pool.seq)

@@ -276,3 +276,11 @@ def test_a_captured_graph_follows_the_positions(fa):
     g.replay()
     fa.check_device_error()
     check_turned(out, q, cos[pos.long()][:, None], sin[pos.long()][:, None], HALF, "replayed")
+
+
+def test_tables_of_another_width_are_refused(fa):
+    q = _normal((3, 2, 64), 17, torch.bfloat16)
+    for half in (4, 12, 40, 0):
+        cos = torch.zeros(8, half, device="cuda")
+        with pytest.raises(ValueError):
+            fa.rope(q, None, (cos, cos, HALF))
