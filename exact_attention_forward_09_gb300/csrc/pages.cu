@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const PoolParams prm
 // Row i of the kept ones moves from slot keep[i] to slot first + i, keep[i] >=
 // first + i.  All bytes; what has to be right is the order, since slots are both
 // read and written: slot first + i is read by rows up to i alone.  So a block
-// takes the rows in rounds, in order, and has read a round (RS * kMoves rows, in
+// takes the rows in rounds, in order, and has read a round (RS * MOVES rows, in
 // registers) before it writes it: no row behind the round reads what the round
 // writes.  Between blocks there is nothing to order, as each has planes, heads and
 // columns of its own.  A block's threads are PV pieces of a row (a part of the head),
@@ -338,10 +338,15 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const PoolParams prm
 // kTile rows at once, into shared memory.
 //   8 sequences of 12000 to 16000 tokens, 2 layers of 8 heads, 4000 of each kept:
 //   344 MB in 65 us, 5.3 TB/s (a row's columns shared by two blocks; whole 74, by
-//   four 71).  8 of the last 60 tokens of 32 sequences, 8 layers: 8.4 us, four
+//   four 71).  8 of the last 60 tokens of 32 sequences, 8 layers: 6.3 us, four
 //   dependent look-ups and a round.
-constexpr int kCompactThreads = 256, kMoves = 8, kTile = 1024;
+// Rows in flight per thread: two where there are at most four to a thread in all (up
+// to 8, 24, 64 tokens kept of 32 sequences, 8 layers: 6.3, 10.5, 16.4 us; with eight,
+// which leave fewer blocks to an SM, 8.5, 14.7, 19.5), else eight (300 tokens 68.6,
+// with two 70.7; the 4000 above 60.8 and 73.8, on one box).
+constexpr int kCompactThreads = 256, kTile = 1024;
 
+template <int MOVES>
 __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const __grid_constant__ CompactParams prm, int lg_pv, int parts,
                                                                         int lg_rs, int head_groups) {
   __shared__ long long from[kTile], to[kTile];
@@ -389,16 +394,16 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const __
       to[i] = q;
     }
     __syncthreads();
-    for (int i0 = 0; i0 < rows; i0 += kMoves << lg_rs) {
-      uint4 u[kMoves];
+    for (int i0 = 0; i0 < rows; i0 += MOVES << lg_rs) {
+      uint4 u[MOVES];
 #pragma unroll
-      for (int k = 0; k < kMoves; ++k) {
+      for (int k = 0; k < MOVES; ++k) {
         const int i = i0 + (k << lg_rs) + rs;
         if (mine && i < rows && from[i] >= 0) u[k] = *reinterpret_cast<const uint4*>(base + from[i]);
       }
       __syncthreads();  // the round has been read
 #pragma unroll
-      for (int k = 0; k < kMoves; ++k) {
+      for (int k = 0; k < MOVES; ++k) {
         const int i = i0 + (k << lg_rs) + rs;
         if (mine && i < rows && from[i] >= 0) *reinterpret_cast<uint4*>(base + to[i]) = u[k];
       }
@@ -508,8 +513,11 @@ cudaError_t launch_cache_compact(const CompactParams& prm, int d, int sms, cudaS
   }
   const int64_t x = (int64_t)prm.B * groups * parts;
   if (x > 0x7fffffffLL) return cudaErrorInvalidValue;
-  cache_compact_kernel<<<dim3((unsigned)x, 2u * prm.rows.layers, 1), kCompactThreads, 0, stream>>>(prm, lg_pv, parts, lg_rs, groups);
-  return cudaGetLastError();
+  auto go = [&](auto kern) {
+    kern<<<dim3((unsigned)x, 2u * prm.rows.layers, 1), kCompactThreads, 0, stream>>>(prm, lg_pv, parts, lg_rs, groups);
+    return cudaGetLastError();
+  };
+  return prm.max_keep <= 4 << lg_rs ? go(cache_compact_kernel<2>) : go(cache_compact_kernel<8>);
 }
 
 }  // namespace fa
