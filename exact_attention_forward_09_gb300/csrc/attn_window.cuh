@@ -351,14 +351,19 @@ __device__ __forceinline__ int win_group_len(const WinParams& prm, const WinSeq&
 // one otherwise, rounded up to even, so that CTAs, which start at even
 // places, start at whole tiles.  (Forms with one query tile per CTA: one each.)
 // A unit's start and end are not counted, so runs that hold many short units
-// take longer than others; but for trees, whose units are all of a batch's, and
-// take two tiles' places behind their own (32 x 60 nodes over 1000 to 8000 keys
-// 152.7 -> 142.2 us, 200 x 20 to 60 over 100 to 600 182 -> 156; with one tile's places
-// 146.8 and 165; with three 141.6 and 158, but 32 x 16 nodes 111.5 -> 113.6).  A run
-// that begins within them has none of the unit.
-template <int NQT>
+// take longer than others.
+// Trees, whose sequences seldom fill their query tiles evenly, are counted closer to
+// what they take: two tiles' places more for each unit, behind its tiles' own
+// (32 x 60 nodes over 1000 to 8000 keys 152.7 -> 142.2 us, 200 x 20 to 60 over 100 to 600
+// 182 -> 156; with one tile's places 146.8 and 165; with three 141.6 and 158, but 32 x
+// 16 nodes 111.5 -> 113.6), and as much for a step of one query tile as for one of two,
+// since its chain takes nearly as long (8 chunks of 1000 tokens beside 25 trees of 1 to
+// 40 nodes, over 5000 to 8000 keys 504 -> 349 us, 8 x 200 nodes 105 -> 80; 30 trees of 1
+// to 40 under a window of 1000 26.3 -> 29.8, which now take the form with one query
+// tile, 25.1).  A run that begins behind a unit's tiles has none of it.
+template <int NQT, bool TREE>
 __device__ __forceinline__ uint32_t win_places(int len, int ntok, int tpt) {
-  if (NQT == 1) return (uint32_t)len;
+  if (NQT == 1 || TREE) return (uint32_t)(NQT * len);
   return ntok > tpt ? 2u * (uint32_t)len : ((uint32_t)len + 1u) & ~1u;
 }
 template <int NQT, bool TREE>
@@ -642,7 +647,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
       return win_seq(prm, prm.cu_q[b], prm.cu_q[b + 1], prm.seq_k[b], &bad);
     };
     auto group_places = [&](const WinSeq& q, int i) -> uint32_t {
-      return (win_places<C::NQT>(win_group_len<TREE>(prm, q, tpg, i), min(tpg, q.nq - i * tpg), tpt) + END) * (uint32_t)prm.Hkv;
+      return (win_places<C::NQT, TREE>(win_group_len<TREE>(prm, q, tpg, i), min(tpg, q.nq - i * tpg), tpt) + END) * (uint32_t)prm.Hkv;
     };
     auto add = [&](uint32_t a, uint32_t b) -> uint32_t { return min(a + b, prm.max_places + 1); };  // (both at most that)
     auto seq_places = [&](const WinSeq& q) -> uint32_t {
@@ -900,14 +905,14 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
           int b = bars->start_b, i = bars->start_group, len = bars->start_len;
           WinSeq s = {bars->start_tok0, bars->start_nq, bars->start_nk};
           int ntok = min(tpg, s.nq - i * tpg);
-          uint32_t places = win_places<C::NQT>(len, ntok, tpt) + END;
+          uint32_t places = win_places<C::NQT, TREE>(len, ntok, tpt) + END;
           int head = (int)(bars->start_off / places);
           uint32_t off = bars->start_off % places;
           bool bad = false;
           while (ok) {
             // [off, off + run) of the unit's places are this CTA's
             const uint32_t run = min(rem, places - off);
-            const int per_tile = C::NQT == 2 && ntok > tpt ? 2 : 1;
+            const int per_tile = C::NQT == 2 && (TREE || ntok > tpt) ? 2 : 1;
             const bool begins = off == 0, ends = off + run >= places - END;
             const bool none = TREE && off >= places - END;  // of its tiles
             w.kz = head;
@@ -952,7 +957,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
               }
               len = win_group_len<TREE>(prm, s, tpg, i);
               ntok = min(tpg, s.nq - i * tpg);
-              places = win_places<C::NQT>(len, ntok, tpt) + END;
+              places = win_places<C::NQT, TREE>(len, ntok, tpt) + END;
             }
           }
         }

@@ -196,8 +196,13 @@ fa_status fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse
   // longest is far above the average, so that most are short.
   // (One tile against a pair at d = 64, 16/4 heads: 32 x 1 token over 3000 keys
   // 32 and 37 us; 33 sequences, 30 of them one token, 31 and 36; but 32 x 24
-  // tokens over 1100 keys, cut into twice as many parts, 24 and 19.)
-  const bool pair = few == 0 && d <= 128 && (T * g > fa::kBM * B || (T * g > 32 * B && B * Hkv < 2 * sms &&
+  // tokens over 1100 keys, cut into twice as many parts, 24 and 19.)  Trees, whose
+  // line counts a step of one query tile as one of a pair: one where they bring up
+  // to a tile's rows on average (one against a pair, 32/8 heads: 32 x 16 nodes over
+  // 1000 to 8000 keys 72.6 and 87.4 us at d = 64, 110.4 and 110.9 at d = 128, under a
+  // window of 1000 34.5 and 42.0, 43.5 and 49.3; 32 nodes 84.5 and 90.6, 117.3 and 117.6;
+  // above, 33 to 40 nodes 137 and 109, 200 and 131).
+  const bool pair = few == 0 && d <= 128 && (T * g > fa::kBM * B || (!mask && T * g > 32 * B && B * Hkv < 2 * sms &&
                                                                     (max_q < T ? max_q : T) * B <= 4 * T));
   const int form = few2 ? fa::WIN_FEW2 : few > 0 ? fa::WIN_FEW : pair ? fa::WIN_PAIR : fa::WIN_ONE;
   const int ctas = few2 || (form == fa::WIN_ONE && d == 64) ? 2 * sms : sms;

@@ -240,15 +240,18 @@ def test_any_mask(fa, d, words):
 
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("n", [3, 20, 60])
-def test_a_line_of_nodes_is_a_chunk(fa, d, n):
-    # the same bits as fwd_paged, window included (one unit per sequence: equal tiles)
+def test_a_line_of_nodes_sees_what_a_chunk_sees(fa, d, n):
+    # fwd_paged on the same batch has the same reference, window included (no
+    # window here ends among the nodes).  Not the same bits: the two cut the work at
+    # other places and may take other forms, so the parts of a row are summed in
+    # another order; each is held to the bound of its own arithmetic.
     x = Batch([(n, n), (n, 500), (n, 128 + n)], 2, 1, d, torch.bfloat16, 32, 2, trees=[list(range(-1, n - 1))] * 3)
     c = x.cache
     for window, sinks in ((ALL, 0), (70, 3)):
-        a = x.run(fa, window=window, sinks=sinks, max_q=n)
-        b = fa.fwd_paged(x.q, c.k, c.v, c.table, x.cu, x.sk, window=window, sinks=sinks, max_q=n)
-        fa.check_device_error()
-        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        for o, lse in (x.run(fa, window=window, sinks=sinks, max_q=n),
+                       fa.fwd_paged(x.q, c.k, c.v, c.table, x.cu, x.sk, window=window, sinks=sinks, max_q=n)):
+            fa.check_device_error()
+            x.check(o, lse, f"a line of {n}", window, sinks)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
