@@ -651,6 +651,8 @@ fa_status fa_tree_plan(const int32_t* parents, const int32_t* cu_q, const int32_
  *              FA_ERR_INDEX
  * Everything else as in fa_fwd_paged, its workspace included.  Pages that hold
  * no key from position seq_k[b] - n - window + 1 on, nor a sink, are not read.
+ * For what a NaN or an infinity in a value row reaches, the new tokens' rows and
+ * the cached ones from that position on count as seen.
  */
 fa_status fa_fwd_tree(const void* q, const fa_kv_cache* cache, void* o, float* lse,
                       const int32_t* block_table, int64_t table_stride, int64_t max_pages,
@@ -790,7 +792,9 @@ fa_status fa_rope(const fa_rope_array* arrays, int64_t count, int64_t B, int64_t
  *                (its entries that got none are -1)
  *   want         [B] int32 (device, read only)
  * Pages are not written: new ones hold what they held.  A page that several rows
- * share is free once the last of them has given it back.
+ * share is free once the last of them has given it back.  A row that is cut to a
+ * length within a page it shares must not be written to from there on, as the
+ * others hold those tokens (a fork of it may: fa_pages_fork copies such a page).
  * Lengths below 0 or above max_pages * page_size are cut, page numbers outside
  * the pool and pages that nobody held are passed over, and both are reported by
  * fa_check_device_error as FA_ERR_INDEX.
