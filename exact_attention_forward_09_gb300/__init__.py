@@ -374,6 +374,7 @@ def _guard(index: int):
 
 
 _TYPES = {torch.bfloat16: FA_DTYPE_BF16, torch.float16: FA_DTYPE_FP16}
+_I32, _F32, _U8, _empty = torch.int32, torch.float32, torch.uint8, torch.empty
 
 
 def _count(x) -> int:
@@ -555,43 +556,71 @@ def fwd_paged(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, blo
 
 
 def _fwd_paged(q, k_pages, v_pages, block_table, cu_q, seq_k, mask, positions, window, sinks, scale, max_q, out, lse, workspace):
-    cache, heads, d, dt, index = _cache(k_pages, v_pages)
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a [T, Hq, d] CUDA tensor")
-    T, Hq, _ = q.shape
-    q_stride = _check_tokens("q", q, T, Hq, d, dt, index)
-    B, table_stride, max_pages = _check_batch(block_table, cu_q, seq_k, index)
+    # The checks of _cache, _check_tokens and _check_batch in one place, as a
+    # call's time on the host counts; what fails goes to them, which say what is wrong.
+    try:
+        pages, heads, page_size, d = shape = k_pages.shape
+        s0, s1, s2, s3 = strides = k_pages.stride()
+        dt, index = k_pages.dtype, k_pages.get_device()
+        T, Hq, c = q.shape
+        q_stride, qh, qc = q.stride()
+        B, max_pages = block_table.shape
+        table_stride, tc = block_table.stride()
+        good = s3 == 1 and index >= 0 and dt in _TYPES and v_pages.shape == shape and v_pages.stride() == strides \
+            and v_pages.dtype is dt and v_pages.get_device() == index and c == d and q.dtype is dt and q.get_device() == index \
+            and qc == 1 and (qh == d or Hq == 1) and block_table.dtype is _I32 and cu_q.dtype is _I32 and seq_k.dtype is _I32 \
+            and block_table.get_device() == index and cu_q.get_device() == index and seq_k.get_device() == index \
+            and cu_q.shape == (B + 1,) and seq_k.shape == (B,) and cu_q.is_contiguous() and seq_k.is_contiguous() \
+            and (tc == 1 or max_pages < 2) and isinstance(q, torch.Tensor)
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if good:
+        cache = _KV_PACK(k_pages.data_ptr(), v_pages.data_ptr(), pages, page_size, heads, d, s0, s1, s2, _TYPES[dt])
+    else:
+        cache, heads, d, dt, index = _cache(k_pages, v_pages)
+        if not isinstance(q, torch.Tensor) or q.dim() != 3:
+            raise ValueError("q must be a [T, Hq, d] CUDA tensor")
+        T, Hq, _ = q.shape
+        q_stride = _check_tokens("q", q, T, Hq, d, dt, index)
+        B, table_stride, max_pages = _check_batch(block_table, cu_q, seq_k, index)
     if heads == 0 or Hq % heads != 0:
         raise ValueError("the number of query heads must be a multiple of the number of key/value heads")
     dev = k_pages.device
     if out is None:
-        out = torch.empty((T, Hq, d), dtype=dt, device=dev)
+        out = _empty((T, Hq, d), dtype=dt, device=dev)
     else:
         _check_out("out", out, (T, Hq, d), dt, index)
     if lse is None:
-        lse = torch.empty((T, Hq), dtype=torch.float32, device=dev)
+        lse = _empty((T, Hq), dtype=_F32, device=dev)
     else:
-        _check_out("lse", lse, (T, Hq), torch.float32, index)
+        _check_out("lse", lse, (T, Hq), _F32, index)
     if mask is not None:
         if not isinstance(mask, torch.Tensor) or len(mask.shape) != 2:
             raise ValueError("mask must be an int32 [T, words] tensor")
         words = mask.shape[1]
-        _check_out("mask", mask, (T, words), torch.int32, index)
+        _check_out("mask", mask, (T, words), _I32, index)
         pp = None if positions is None else _check_ints("positions", positions, T, index)
-    with _guard(index):
-        if workspace is None:
-            need = _PAGED_BYTES.get((index, d))
-            if need is None:
+    if workspace is None:
+        need = _PAGED_BYTES.get((index, d))
+        if need is None:
+            with torch.cuda.device(index):
                 need = _PAGED_BYTES[index, d] = paged_workspace_bytes(d)
-            workspace = torch.empty((need,), dtype=torch.uint8, device=dev)
-        sizes = (B, T, Hq, q_stride, _count(max_q), 1 << 30 if window is None else _count(window), _count(sinks), _scale(scale, d),
-                 *_workspace(workspace, index), _current_stream(index))
+        workspace = _empty((need,), dtype=_U8, device=dev)
+        wp = workspace.data_ptr()
+    else:
+        wp, need = _workspace(workspace, index)
+    lib = _LIB or _lib()
+    with _guard(index):
         if mask is None:
-            st = _lib().fa_fwd_paged(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
-                                     table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), *sizes)
+            st = lib.fa_fwd_paged(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr(), block_table.data_ptr(), table_stride,
+                                  max_pages, cu_q.data_ptr(), seq_k.data_ptr(), B, T, Hq, q_stride, _count(max_q),
+                                  1 << 30 if window is None else _count(window), _count(sinks), _scale(scale, d), wp, need,
+                                  _current_stream(index))
         else:
-            st = _lib().fa_fwd_tree(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr(), block_table.data_ptr(),
-                                    table_stride, max_pages, cu_q.data_ptr(), seq_k.data_ptr(), mask.data_ptr(), words, pp, *sizes)
+            st = lib.fa_fwd_tree(q.data_ptr(), cache, out.data_ptr(), lse.data_ptr(), block_table.data_ptr(), table_stride,
+                                 max_pages, cu_q.data_ptr(), seq_k.data_ptr(), mask.data_ptr(), words, pp, B, T, Hq, q_stride,
+                                 _count(max_q), 1 << 30 if window is None else _count(window), _count(sinks), _scale(scale, d),
+                                 wp, need, _current_stream(index))
     if st != FA_OK:
         raise FaError(st, "fa_fwd_paged" if mask is None else "fa_fwd_tree")
     return out, lse
@@ -667,19 +696,46 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     tokens' positions in their sequences or by ``positions`` (int32 [T], as
     ``tree_plan`` gives them).  k, v and q may be slices of one projection.
     Returns the rotated queries (``q_out``), or None without q."""
-    cache, heads, d, dt, index = _cache(k_pages, v_pages)
-    if not isinstance(k, torch.Tensor) or k.dim() != 3:
-        raise ValueError("k must be a [T, heads, d] CUDA tensor")
-    T = k.shape[0]
-    ks = _check_tokens("k", k, T, heads, d, dt, index)
-    vs = _check_tokens("v", v, T, heads, d, dt, index)
-    B, table_stride, max_pages = _check_batch(block_table, cu_q, seq_k, index)
+    # (checked in one place, as in _fwd_paged)
     Hq, qs, qp, op = 0, 0, None, None
+    try:
+        pages, heads, page_size, d = shape = k_pages.shape
+        s0, s1, s2, s3 = strides = k_pages.stride()
+        dt, index = k_pages.dtype, k_pages.get_device()
+        T = k.shape[0]
+        ks, kh, kc = k.stride()
+        vs, vh, vc = v.stride()
+        B, max_pages = block_table.shape
+        table_stride, tc = block_table.stride()
+        good = s3 == 1 and index >= 0 and dt in _TYPES and v_pages.shape == shape and v_pages.stride() == strides \
+            and v_pages.dtype is dt and v_pages.get_device() == index and k.shape == (T, heads, d) and v.shape == (T, heads, d) \
+            and k.dtype is dt and v.dtype is dt and k.get_device() == index and v.get_device() == index and kc == 1 and vc == 1 \
+            and (heads == 1 or (kh == d and vh == d)) and block_table.dtype is _I32 and cu_q.dtype is _I32 and seq_k.dtype is _I32 \
+            and block_table.get_device() == index and cu_q.get_device() == index and seq_k.get_device() == index \
+            and cu_q.shape == (B + 1,) and seq_k.shape == (B,) and cu_q.is_contiguous() and seq_k.is_contiguous() \
+            and (tc == 1 or max_pages < 2)
+        if good and q is not None:
+            t, Hq, c = q.shape
+            qs, qh, qc = q.stride()
+            good = t == T and c == d and q.dtype is dt and q.get_device() == index and qc == 1 and (qh == d or Hq == 1)
+    except (AttributeError, TypeError, ValueError):
+        good = False
+    if good:
+        cache = _KV_PACK(k_pages.data_ptr(), v_pages.data_ptr(), pages, page_size, heads, d, s0, s1, s2, _TYPES[dt])
+    else:
+        cache, heads, d, dt, index = _cache(k_pages, v_pages)
+        if not isinstance(k, torch.Tensor) or k.dim() != 3:
+            raise ValueError("k must be a [T, heads, d] CUDA tensor")
+        T = k.shape[0]
+        ks = _check_tokens("k", k, T, heads, d, dt, index)
+        vs = _check_tokens("v", v, T, heads, d, dt, index)
+        B, table_stride, max_pages = _check_batch(block_table, cu_q, seq_k, index)
+        if q is not None:
+            Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
+            qs = _check_tokens("q", q, T, Hq, d, dt, index)
     if q is not None:
-        Hq = q.shape[1] if isinstance(q, torch.Tensor) and q.dim() == 3 else -1
-        qs = _check_tokens("q", q, T, Hq, d, dt, index)
         if q_out is None:
-            q_out = torch.empty((T, Hq, d), dtype=dt, device=q.device)
+            q_out = _empty((T, Hq, d), dtype=dt, device=q.device)
         else:
             _check_out("q_out", q_out, (T, Hq, d), dt, index)
         qp, op = q.data_ptr(), q_out.data_ptr()
@@ -689,8 +745,7 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_page
     if rope is not None:
         cp, sp, n, r, layout = _check_rope(rope, d, index)
         if positions is not None:
-            _check_out("positions", positions, (T,), torch.int32, index)
-            pp = positions.data_ptr()
+            pp = _check_ints("positions", positions, T, index)
     elif positions is not None:
         raise ValueError("positions need rope")
     with _guard(index):
@@ -830,7 +885,7 @@ def _layers(k_pages, v_pages):
 
 def _check_ints(name, t, n, index):
     """The address of a contiguous int32 [n] tensor."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.shape != (n,) or t.get_device() != index \
+    if not isinstance(t, torch.Tensor) or t.dtype is not _I32 or t.shape != (n,) or t.get_device() != index \
             or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous int32 [{n}] tensor on cuda:{index}")
     return t.data_ptr()
