@@ -396,6 +396,37 @@ def test_many_forks_of_one(fa):
     assert bool((seq == 60).all())
 
 
+def test_the_most_rows_and_forks(fa):
+    # as many rows of a resize as it takes, and as many rows and forks of a fork
+    rows, pages = 49152, 50000
+    refs, table, seq = (torch.zeros(x, dtype=torch.int32, device="cuda") for x in ((pages,), (rows, 1), (rows,)))
+    table -= 1
+    want = torch.full_like(seq, 16)
+    fa.pages_resize(refs, table, seq, want, 16)
+    assert not _reported(fa)
+    number = torch.arange(rows, dtype=torch.int32, device="cuda")
+    assert torch.equal(table[:, 0], number) and torch.equal(seq, want) and int(refs.sum()) == rows
+    want[1::2] = 0
+    fa.pages_resize(refs, table, seq, want, 16)
+    assert torch.equal(table[:, 0], torch.where(number % 2 == 1, torch.full_like(number, -1), number)) and torch.equal(seq, want)
+    assert int(refs.sum()) == rows // 2 and int(refs[1:rows:2].sum()) == 0
+    with pytest.raises(fa.FaError):
+        fa.pages_resize(refs, torch.zeros(rows + 1, 1, dtype=torch.int32, device="cuda"), *(torch.zeros(rows + 1, dtype=torch.int32, device="cuda"),) * 2, 16)
+    rows, n, pages = 1 << 18, 16384, 20000
+    k, v = _pages(1, pages, 1, 16, 64)
+    refs, table, seq = (torch.zeros(x, dtype=torch.int32, device="cuda") for x in ((pages,), (rows, 2), (rows,)))
+    table[5], refs[[7, 9]], seq[5] = ints([7, 9]), 1, 21
+    src, dst = ints([5]).repeat(n), torch.arange(rows - n, rows, dtype=torch.int32, device="cuda")
+    fresh = fa.pages_fork(k, v, refs, table, seq, src, dst)
+    assert not _reported(fa)
+    free = torch.tensor([p for p in range(n + 2) if p not in (7, 9)], dtype=torch.int32, device="cuda")
+    assert torch.equal(fresh, free) and bool((seq[rows - n:] == 21).all()) and int(refs[7]) == n + 1
+    assert torch.equal(table[rows - n:, 1], free) and bool((table[rows - n:, 0] == 7).all())
+    assert torch.equal(_raw(k[0, free.long(), :, :5]), _raw(k[0, 9:10, :, :5]).expand(n, -1, -1, -1))
+    with pytest.raises(fa.FaError):
+        fa.pages_fork(k, v, refs, table, seq, ints([5]).repeat(n + 1), ints([6]).repeat(n + 1))
+
+
 # -------------------------------------------------------------- together --
 
 def test_a_captured_graph_follows_the_arrays(fa):
