@@ -209,17 +209,21 @@ class Pool:
     def __init__(self, num_pages, rows, max_pages, page):
         self.refs, self.page, self.max = [0] * num_pages, page, max_pages
         self.table, self.seq = [[-1] * max_pages for _ in range(rows)], [0] * rows
+        self.low = 0  # no page below is free
 
     def count(self, n):
         return -(-n // self.page)
 
     def free(self):
-        return next((p for p, r in enumerate(self.refs) if r == 0), None)
+        while self.low < len(self.refs) and self.refs[self.low] > 0:
+            self.low += 1
+        return self.low if self.low < len(self.refs) else None
 
     def resize(self, want):
         for r, w in enumerate(want):
             for j in range(self.count(w), self.count(self.seq[r])):
                 self.refs[self.table[r][j]] -= 1
+                self.low = min(self.low, self.table[r][j])
                 self.table[r][j] = -1
         for r, w in enumerate(want):
             room = min(self.count(w), self.count(self.seq[r]))

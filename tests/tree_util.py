@@ -25,11 +25,11 @@ def layout(parents, words):
 
 def mask_of(rows, words):
     """Sets of seen nodes -> int32 [n, words]."""
-    out = torch.zeros(len(rows), words, dtype=torch.int64)
-    for i, row in enumerate(rows):
-        for k in row:
-            if k < 32 * words:
-                out[i, k // 32] |= 1 << (k % 32)
+    out = []
+    for row in rows:
+        bits = sum(1 << k for k in row if k < 32 * words)
+        out.append([(bits >> (32 * w)) & 0xffffffff for w in range(words)])
+    out = torch.tensor(out, dtype=torch.int64).view(len(rows), words)
     return torch.where(out >= 1 << 31, out - (1 << 32), out).to(torch.int32)
 
 
