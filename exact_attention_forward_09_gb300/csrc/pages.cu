@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(THREADS) fork_plan_kernel(const PoolParams prm
   __syncthreads();
   bool bad = false;
   // what fork f needs: kWhole nothing, 0 a page, kRefused it cannot be done
-  auto judge = [&](int f) -> int {
+  auto need_of = [&](int f) -> int {
     const int a = src[f], b = dst[f];
     if ((unsigned)a >= (unsigned)prm.rows || (unsigned)b >= (unsigned)prm.rows) return kRefused;
     if ((is_src[b >> 5] | twice[b >> 5]) >> (b & 31) & 1) return kRefused;
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(THREADS) fork_plan_kernel(const PoolParams prm
   const int f0 = min(n, (int)threadIdx.x * share), f1 = min(n, f0 + share);
   long long mine = 0, need;
   for (int f = f0; f < f1; ++f) {
-    const int what = judge(f);
+    const int what = need_of(f);
     bad |= what == kRefused;
     fresh[f] = what == 0 ? kNoPage : what;
     mine += what == 0;
