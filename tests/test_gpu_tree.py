@@ -323,6 +323,23 @@ def test_rows_outside_the_sequences_are_left(fa):
     assert bool((o[:3] == 7).all()) and bool((o[17:] == 7).all()) and bool((lse[:3] == 5).all()) and bool((lse[17:] == 5).all())
 
 
+def test_queries_out_of_a_projection_and_given_outputs(fa):
+    x = Batch([(20, 60), (1, 300), (7, 7)], 4, 2, 128, torch.bfloat16, 16, 1)
+    wide = torch.full((x.T, 9, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+    wide[:, 2:6] = x.q
+    c, ws = x.cache, torch.empty(fa.paged_workspace_bytes(128), dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(x.q), torch.empty(x.T, 4, device="cuda")
+    got = fa.fwd_tree(wide[:, 2:6], c.k, c.v, c.table, x.cu, x.sk, x.mask, x.positions, out=o, lse=lse, workspace=ws)
+    fa.check_device_error()
+    assert got[0] is o and got[1] is lse
+    x.check(o, lse, "strided queries")
+    for bad in (dict(out=o[:, :2]), dict(lse=lse[1:]), dict(mask=x.mask[1:]), dict(positions=x.positions[1:]), dict(positions=x.positions.long())):
+        with pytest.raises(ValueError):
+            x.run(fa, **bad)
+    with pytest.raises(fa.FaError):
+        x.run(fa, workspace=ws[:1000])
+
+
 def test_nonfinite_values_of_masked_nodes(fa):
     # the scores of keys that a row does not see are replaced, NaN or not; LSE shows it alone
     x = Batch([(30, 200), (4, 50)], 4, 2, 128, torch.bfloat16, 32, 1, trees=[[-1] + [0] * 29, [-1, 0, 0, 0]])
