@@ -219,6 +219,7 @@ struct WinParams {
   const uint32_t* mask;  // [T, words] which new tokens of its sequence a token sees
   const int* positions;  // [T] positions of the tokens in their sequence; null: where they lie
   int words;             // 32 words is at most 2^30
+  int kv_few;            // keys and values are read by few units each: the first to leave L2
 };
 
 // The key tiles that a unit of up to two query tiles visits.
@@ -784,7 +785,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
     if constexpr (C::REALLOC) regs_dec<C::CTRL_REGS>();
     if (C::V_WARP && warp == C::LOADV_WARP) {
       // -------------------------------------------------------- load V --
-      const uint64_t pol_kv = policy_evict_last();
+      const uint64_t pol_kv = TREE && prm.kv_few ? policy_evict_first() : policy_evict_last();
       int pos = 0;
       bool ok = true;
       for (int r = 0; ok; ++r) {
@@ -811,7 +812,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
       // ---------------------------------------------------------- load --
       // The whole warp runs the loop; lane 0 waits, arms barriers and
       // publishes units; paged boxes are issued one per lane.
-      const uint64_t pol_kv = policy_evict_last();
+      const uint64_t pol_kv = TREE && prm.kv_few ? policy_evict_first() : policy_evict_last();
       const uint64_t pol_q = policy_evict_first();
       int pos = 0;    // ring position (continues across units)
       int k = 0;      // units with keys loaded by this CTA
