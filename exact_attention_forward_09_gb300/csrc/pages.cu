@@ -182,7 +182,8 @@ __global__ void __launch_bounds__(THREADS) resize_kernel(const PoolParams prm, c
 // values) with `tokens` rows per head, a block's share of them.  All bytes,
 // each read once and written once; a thread has eight pieces on their way.
 //   160 pages of 64 tokens, 8 layers of 8 heads, d = 128: 671 MB moved in 99.8 us,
-//   6.7 TB/s (0.99 of the measured copy rate).
+//   6.7 TB/s (0.99 of the measured copy rate); call after call 99.5, and 102 where
+//   each is launched at the end of the one before.
 constexpr int kCopyThreads = 256, kCopyPieces = 8;
 
 template <int D>
@@ -220,8 +221,9 @@ unsigned page_blocks(const PageRows& r) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const PageRows r, const int* __restrict__ src,
-                                                                  const int* __restrict__ dst, int blocks, int* err) {
+__global__ void __launch_bounds__(kCopyThreads) cache_copy_kernel(const PageRows r, const int* src, const int* dst, int blocks, int* err) {
+  pdl_launch();
+  pdl_wait();
   const int pair = blockIdx.x / blocks, block = blockIdx.x - pair * blocks;
   const int a = src[pair], b = dst[pair];
   if ((unsigned)a >= (unsigned)r.num_pages || (unsigned)b >= (unsigned)r.num_pages) {
@@ -412,7 +414,8 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const __
   if (bad && teller) report_index(prm.err);
 }
 
-// A launch that may begin while the kernel before it in the stream still runs.
+// A launch that may begin while the kernel before it in the stream still runs
+// (what that one is: its blocks then wait for its end, and the next launch need not).
 void dependent_launch(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, dim3 grid, unsigned threads, size_t smem, cudaStream_t stream) {
   cfg = {};
   cfg.gridDim = grid;
@@ -480,8 +483,10 @@ cudaError_t launch_pages_fork(const PoolParams& prm, const PageRows& rows, int d
 cudaError_t launch_cache_copy(const PageRows& rows, int d, const int* src, const int* dst, int n, int* err, cudaStream_t stream) {
   auto go = [&](auto kern, unsigned blocks) {
     if ((int64_t)blocks * n > 0x7fffffffLL) return cudaErrorInvalidValue;
-    kern<<<dim3(blocks * (unsigned)n, 2u * rows.layers, 1), kCopyThreads, 0, stream>>>(rows, src, dst, (int)blocks, err);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg;
+    cudaLaunchAttribute attr[1];
+    dependent_launch(cfg, attr, dim3(blocks * (unsigned)n, 2u * rows.layers, 1), kCopyThreads, 0, stream);
+    return cudaLaunchKernelEx(&cfg, kern, rows, src, dst, (int)blocks, err);
   };
   switch (d) {
     case 64: return go(cache_copy_kernel<64>, page_blocks<64>(rows));

@@ -37,8 +37,9 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
 // once per block and not once per head; a block is 256/(d/16) tokens in a row,
 // which lie together in either order of heads and tokens.  The first rows' loads
 // go out before the position and its angles are known.
-//   2 x 8192 tokens, 16 + 4 heads, d = 128: 168 MB in 27.5 us, 6.1 TB/s (0.90 of the
-//   measured copy rate; 29.2 with four rows in flight); 8 x 4096 of 32 + 8 heads
+//   2 x 8192 tokens, 16 + 4 heads, d = 128: 168 MB in 27.4 us, 6.1 TB/s (0.90 of the
+//   measured copy rate; 29.2 with four rows in flight; forward and back in a stream
+//   56.2 us, 60.5 where each is launched at the end of the one before); 8 x 4096 of 32 + 8 heads
 //   103 us, 6.5 TB/s; 64 columns of d = 256 in place 15.6 us where copying the others
 //   takes 22.8; 65 tokens 2.3 us.
 constexpr int kRopeThreads = 256;
@@ -48,6 +49,8 @@ template <int D, bool F16, int LAYOUT>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeParams prm, const float sign) {
   constexpr int CL = D / 16;  // column chunks of a row
   constexpr int TB = kRopeThreads / CL;
+  pdl_launch();  // (the gradients' rotation, say, may be launched; it waits for this kernel's end)
+  pdl_wait();
   const int c = threadIdx.x % CL;
   const int batch = blockIdx.x / prm.tiles;
   const int n = (blockIdx.x - batch * prm.tiles) * TB + threadIdx.x / CL;
@@ -134,9 +137,17 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
 
 template <int D, bool F16>
 cudaError_t rope_layout(const RopeParams& prm, dim3 grid, int layout, float sign, cudaStream_t stream) {
-  if (layout == FA_ROPE_HALF) rope_kernel<D, F16, FA_ROPE_HALF><<<grid, kRopeThreads, 0, stream>>>(prm, sign);
-  else rope_kernel<D, F16, FA_ROPE_INTERLEAVED><<<grid, kRopeThreads, 0, stream>>>(prm, sign);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(kRopeThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return layout == FA_ROPE_HALF ? cudaLaunchKernelEx(&cfg, rope_kernel<D, F16, FA_ROPE_HALF>, prm, sign)
+                                : cudaLaunchKernelEx(&cfg, rope_kernel<D, F16, FA_ROPE_INTERLEAVED>, prm, sign);
 }
 
 // --------------------------------------------------------------- table --
