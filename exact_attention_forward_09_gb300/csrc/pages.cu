@@ -428,12 +428,18 @@ void dependent_launch(cudaLaunchConfig_t& cfg, cudaLaunchAttribute* attr, dim3 g
   cfg.numAttrs = 1;
 }
 
-// Lets a kernel take `bytes` of dynamic shared memory.  (48 KB, its static part
-// included, need no asking.)
+// Lets a kernel take `bytes` of dynamic shared memory, at most `most` in any call.
+// (48 KB, its static part included, need no asking.)  The limit belongs to the kernel,
+// not to a launch: what is asked for is always the most, so that no call lowers the
+// limit between another thread's asking and its launch.
 template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes) {
-  return bytes <= 40 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+cudaError_t allow_smem(K kern, size_t bytes, size_t most) {
+  return bytes <= 40 * 1024 ? cudaSuccess : cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
 }
+constexpr size_t resize_smem(size_t rows) { return rows * sizeof(int); }
+constexpr size_t fork_smem(size_t n, size_t rows) { return (n + 3 * ((rows + 31) / 32)) * sizeof(int); }
+static_assert(resize_smem(kMaxResizeRows) <= 226 * 1024 && fork_smem(kMaxForks, kMaxForkRows) <= 226 * 1024,
+              "a block's dynamic shared memory, beside the static");
 
 }  // namespace
 
@@ -441,9 +447,9 @@ cudaError_t allow_smem(K kern, size_t bytes) {
 static bool large_pool(int num_pages, int rows) { return num_pages > 16384 || rows > 1024; }
 
 cudaError_t launch_pages_resize(const PoolParams& prm, const int* want, cudaStream_t stream) {
-  const size_t smem = (size_t)prm.rows * sizeof(int);
+  const size_t smem = resize_smem(prm.rows);
   auto go = [&](auto kern, unsigned threads) {
-    cudaError_t e = allow_smem(kern, smem);
+    cudaError_t e = allow_smem(kern, smem, resize_smem(kMaxResizeRows));
     if (e != cudaSuccess) return e;
     release_kernel<<<(unsigned)prm.rows, kReleaseThreads, 0, stream>>>(prm, want);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -457,9 +463,9 @@ cudaError_t launch_pages_resize(const PoolParams& prm, const int* want, cudaStre
 
 cudaError_t launch_pages_fork(const PoolParams& prm, const PageRows& rows, int d, const int* src, const int* dst, int* fresh, int n,
                               cudaStream_t stream) {
-  const size_t smem = ((size_t)n + 3 * ((prm.rows + 31) / 32)) * sizeof(int);
+  const size_t smem = fork_smem(n, prm.rows);
   auto plan = [&](auto kern, int threads) {
-    const cudaError_t e = allow_smem(kern, smem);
+    const cudaError_t e = allow_smem(kern, smem, fork_smem(kMaxForks, kMaxForkRows));
     if (e != cudaSuccess) return e;
     kern<<<1, threads, smem, stream>>>(prm, src, dst, fresh, n);
     return cudaGetLastError();

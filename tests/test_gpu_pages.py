@@ -3,6 +3,7 @@ fa_cache_copy, fa_cache_compact) against a plain model on the host.  Everything
 here is whole numbers and copies: results have to be equal, the bytes that are
 not to be written included."""
 import random
+import threading
 
 import pytest
 import torch
@@ -462,3 +463,74 @@ def test_a_captured_graph_follows_the_arrays(fa):
         assert not _reported(fa)
         pool.check(refs, table, seq)
         assert torch.equal(_raw(k), _raw(mk)) and torch.equal(_raw(v), _raw(mv))
+
+
+def _at_once(*loops):
+    """Runs the loops at once, each in a thread and on a stream of its own; what one raised is raised here."""
+    failed = []
+
+    def go(loop):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                loop()
+                torch.cuda.current_stream().synchronize()
+        except BaseException as e:  # noqa: B902 (raised again below)
+            failed.append(e)
+
+    torch.cuda.synchronize()  # what the loops use has been made
+    threads = [threading.Thread(target=go, args=(loop,)) for loop in loops]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    if failed:
+        raise failed[0]
+
+
+def test_pools_of_several_threads(fa):
+    # Calls of one kernel that take different amounts of shared memory, above what a launch may have unasked: what one
+    # thread asks for must not be lost to another's call in between.  (Threads of a pool of their own each.)
+    def pool(rows, steps):
+        refs, table, seq = (torch.zeros(x, dtype=torch.int32, device="cuda") for x in ((rows + 5,), (rows, 1), (rows,)))
+        some, none = torch.full_like(seq, 16), torch.zeros_like(seq)
+
+        def loop():
+            for _ in range(steps):
+                fa.pages_resize(refs, table, seq, some, 16)
+                fa.pages_resize(refs, table, seq, none, 16)
+            fa.pages_resize(refs, table, seq, some, 16)
+
+        return loop, refs, table, seq
+
+    pools = [pool(49152, 200), pool(12288, 600), pool(20000, 400)]
+    _at_once(*(p[0] for p in pools))
+    assert not _reported(fa)
+    for _, refs, table, seq in pools:
+        rows = len(seq)
+        assert torch.equal(table[:, 0], torch.arange(rows, dtype=torch.int32, device="cuda")) and bool((seq == 16).all())
+        assert bool((refs[:rows] == 1).all()) and bool((refs[rows:] == 0).all())
+
+
+def test_forks_of_several_threads(fa):
+    def forks(rows, n, steps):
+        k, v = _pages(1, n + 3, 1, 16, 64)
+        refs, table, seq = (torch.zeros(x, dtype=torch.int32, device="cuda") for x in ((n + 3,), (rows, 2), (rows,)))
+        table[5], refs[[0, 1]], seq[5] = ints([0, 1]), 1, 21
+        src, dst = ints([5]).repeat(n), torch.arange(rows - n, rows, dtype=torch.int32, device="cuda")
+        back = seq.clone()
+        fresh = []
+
+        def loop():
+            for i in range(steps):
+                if i:
+                    fa.pages_resize(refs, table[rows - n:], seq[rows - n:], back[rows - n:], 16)
+                fresh.append(fa.pages_fork(k, v, refs, table, seq, src, dst))
+
+        return loop, fresh, n
+
+    both = [forks(1 << 18, 16384, 60), forks(20000, 12000, 80)]
+    _at_once(*(f[0] for f in both))
+    assert not _reported(fa)
+    for _, fresh, n in both:
+        for got in (fresh[0], fresh[-1]):
+            assert torch.equal(got, torch.arange(2, n + 2, dtype=torch.int32, device="cuda"))
