@@ -39,7 +39,8 @@ def nvcc() -> str:
 
 
 def _flags(extra=()):
-    return ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", CSRC, "-I", INCLUDE,
+    # (host code rounds every product, as it is written: what sums pairs of doubles relies on it)
+    return ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC,-ffp-contract=off", "-I", CSRC, "-I", INCLUDE,
                    "--expt-relaxed-constexpr"] + list(extra)
 
 

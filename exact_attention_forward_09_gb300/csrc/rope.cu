@@ -154,8 +154,8 @@ cudaError_t rope_layout(const RopeParams& prm, dim3 grid, int layout, float sign
 // The angle of pair i at position p is p f_i turns.  With f_i as a 64-bit
 // fraction of a turn the product's whole turns fall off the top of a 64-bit
 // integer, so its reduction is exact at any position: what is left of the angle
-// carries the frequency's own error (2^-65 turns, times p) alone, where an fp32
-// product would be off by p 2^-24 radians.  The nearest quarter turn is split off as
+// carries the frequency's own error (the host rounds it to the nearest, 2^-65 turns,
+// times p) alone, where an fp32 product would be off by p 2^-24 radians.  The nearest quarter turn is split off as
 // two bits, and what remains (at most an eighth of a turn, exact in 62 bits) is
 // rounded to fp32 relative to itself, so that values near zero keep their digits.
 // A thread keeps four pairs and steps through positions by adding; two blocks to

@@ -20,9 +20,46 @@ bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0
 
 bool rope_dim_ok(int64_t r, int64_t most) { return r >= 16 && r <= most && r % 16 == 0; }
 
+// A number as the sum of two doubles, about 104 bits.  An angle far out is a
+// frequency times its position, and so is its error: a double's, 2^-53 of it, would
+// be some hundred units of a small sine's last place by position 2^26.
+struct Two {
+  double hi, lo;
+};
+Two sum(double a, double b) {  // exact
+  const double s = a + b, t = s - a;
+  return {s, (a - (s - t)) + (b - t)};
+}
+Two operator+(Two a, Two b) {
+  const Two s = sum(a.hi, b.hi);
+  return sum(s.hi, s.lo + (a.lo + b.lo));
+}
+Two operator-(Two a, Two b) { return a + Two{-b.hi, -b.lo}; }
+Two operator*(Two a, Two b) {
+  const double p = a.hi * b.hi;
+  return sum(p, std::fma(a.hi, b.hi, -p) + (a.hi * b.lo + a.lo * b.hi));
+}
+Two operator/(Two a, Two b) {
+  const double q = a.hi / b.hi;
+  return Two{q, 0.0} + Two{(a - b * Two{q, 0.0}).hi / b.hi, 0.0};
+}
+Two one(double x) { return {x, 0.0}; }
+
+// x^(-1/n), x >= 1: a double, and one step of Newton's method for y^n x = 1, whose
+// error is the square of the double's.
+Two root(double x, int n) {
+  const Two y = one(std::pow(x, -1.0 / n));
+  Two p = one(x), square = y;
+  for (int k = n; k > 0; k >>= 1, square = square * square)
+    if (k & 1) p = p * square;
+  return y - y * (p - one(1.0)) / one(n);
+}
+
+const Two kTurns = {0x1.45f306dc9c883p-3, -0x1.6b01ec5417056p-57};  // 1 / 2 pi
+
 // The angle per position of pair i of r/2.
-bool scaled_frequencies(int64_t r, double theta, const fa_rope_scaling* sc, double* f) {
-  const int64_t half = r / 2;
+bool scaled_frequencies(int64_t r, double theta, const fa_rope_scaling* sc, Two* f) {
+  const int half = (int)(r / 2);
   const int kind = sc ? sc->kind : FA_ROPE_SCALE_NONE;
   const double s = sc ? sc->factor : 1.0;
   if (!std::isfinite(theta) || theta <= 1.0) return false;
@@ -35,24 +72,48 @@ bool scaled_frequencies(int64_t r, double theta, const fa_rope_scaling* sc, doub
     if (sc->original < 1.0 || sc->low < 0.0 || sc->high <= sc->low) return false;
     if (kind == FA_ROPE_SCALE_INDEX && sc->low <= 0.0) return false;
   }
-  if (kind == FA_ROPE_SCALE_BASE) theta = theta * std::pow(s, (double)r / (double)(r - 2));
-  if (!std::isfinite(theta)) return false;
-  double lo = 0.0, hi = 0.0;
+  // from one pair to the next: theta^(-1/half), and where the base is scaled, by
+  // factor^(half/(half - 1)), that of it
+  Two step = root(theta, half);
+  if (kind == FA_ROPE_SCALE_BASE) {
+    if (!std::isfinite(theta * std::pow(s, (double)r / (double)(r - 2)))) return false;
+    step = step * root(s, half - 1);
+  }
+  // keep = start + (a pair's frequency, or its number) * rise, clamped
+  Two start = one(1.0), rise = one(0.0);
+  if (kind == FA_ROPE_SCALE_LINEAR) start = one(0.0);
+  if (kind == FA_ROPE_SCALE_TURNS) {
+    const Two width = sum(sc->high, -sc->low);
+    start = one(0.0) - one(sc->low) / width;
+    rise = one(sc->original) * kTurns / width;
+  }
   if (kind == FA_ROPE_SCALE_INDEX) {
     auto at = [&](double turns) { return (double)r * std::log(sc->original / (turns * kTurn)) / (2.0 * std::log(theta)); };
-    lo = std::fmax(0.0, std::floor(at(sc->high)));
-    hi = std::fmin((double)(r - 1), std::ceil(at(sc->low)));
+    const double lo = std::fmax(0.0, std::floor(at(sc->high)));
+    const double hi = std::fmin((double)(r - 1), std::ceil(at(sc->low)));
+    rise = one(-1.0) / one(std::fmax(hi - lo, 0.001));
+    start = one(1.0) - one(lo) * rise;
   }
-  for (int64_t i = 0; i < half; ++i) {
-    const double base = std::pow(theta, -2.0 * (double)i / (double)r);
-    double keep = 1.0;  // the share of the unscaled frequency
-    if (kind == FA_ROPE_SCALE_LINEAR) keep = 0.0;
-    if (kind == FA_ROPE_SCALE_TURNS) keep = (sc->original * base / kTurn - sc->low) / (sc->high - sc->low);
-    if (kind == FA_ROPE_SCALE_INDEX) keep = 1.0 - std::fmin(1.0, std::fmax(0.0, ((double)i - lo) / std::fmax(hi - lo, 0.001)));
-    keep = std::fmin(1.0, std::fmax(0.0, keep));
-    f[i] = parts || kind == FA_ROPE_SCALE_LINEAR ? (1.0 - keep) * base / s + keep * base : base;
+  const bool scaled = parts || kind == FA_ROPE_SCALE_LINEAR;
+  const Two inverse = one(1.0) / one(scaled ? s : 1.0), rest = one(1.0) - inverse;
+  Two base = one(1.0);
+  for (int i = 0; i < half; ++i, base = base * step) {
+    f[i] = base;
+    if (!scaled) continue;
+    Two keep = parts ? start + (kind == FA_ROPE_SCALE_TURNS ? base : one(i)) * rise : start;
+    if (!std::isfinite(keep.hi)) keep = one((sc->original * base.hi / kTurn - sc->low) / (sc->high - sc->low));  // (past 1e308)
+    if (!(keep.hi > 0.0)) f[i] = base * inverse;
+    else if ((keep - one(1.0)).hi < 0.0) f[i] = base * (inverse + keep * rest);
   }
   return true;
+}
+
+// 2^64 times the turns that f radians are, to the nearest.  (f is at most one
+// radian, so this stays below 2^62, and what a double's 53 bits leave is an integer.)
+uint64_t turns_of(Two f) {
+  const Two t = f * kTurns;
+  const double hi = std::ldexp(t.hi, 64), whole = std::floor(hi);
+  return (uint64_t)whole + (uint64_t)(int64_t)std::floor((hi - whole) + std::ldexp(t.lo, 64) + 0.5);
 }
 
 }  // namespace
@@ -63,7 +124,7 @@ fa_status fa_rope_table(float* rope_cos, float* rope_sin, int64_t n, int64_t rop
                         const fa_rope_scaling* scaling, cudaStream_t stream) {
   if (n < 0 || start < 0) return FA_ERR_INVALID_ARG;
   if (!rope_dim_ok(rope_dim, 256)) return FA_ERR_UNSUPPORTED;
-  double f[128];
+  Two f[128];
   if (!scaled_frequencies(rope_dim, theta, scaling, f)) return FA_ERR_INVALID_ARG;
   if (n > kMaxLen || start > kMaxLen) return FA_ERR_UNSUPPORTED;
   if (n == 0) return FA_OK;
@@ -82,8 +143,7 @@ fa_status fa_rope_table(float* rope_cos, float* rope_sin, int64_t n, int64_t rop
   const double amp = scaling ? scaling->amplitude : 1.0;
   p.amp_hi = (float)amp;
   p.amp_lo = (float)(amp - (double)p.amp_hi);
-  // (f is at most one radian, so this stays below 2^62)
-  for (int i = 0; i < p.half; ++i) p.turns[i] = (uint64_t)std::floor(std::ldexp(f[i] / kTurn, 64) + 0.5);
+  for (int i = 0; i < p.half; ++i) p.turns[i] = turns_of(f[i]);
   return fa::launch_rope_table(p, fa::internal_sm_count(dev), stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 

@@ -710,8 +710,11 @@ typedef struct {
  *   rope_dim            a multiple of 16, at most 256
  *   theta               above 1
  *   scaling             as above (HOST pointer, read during the call), or NULL
- * Angles are reduced exactly at every position: a value is within about two
- * units of fp32's last place of the exact one.
+ * A frequency is kept to 2^-65 of a turn, and its product with the position is
+ * reduced exactly: a value at position p is within two units of its own last fp32
+ * place, and amplitude * (p + 128) * 2^-62 beside them, of the exact one.  (The
+ * latter is less than a unit for every value above 2^-18 up to position 2^20, and
+ * above 2^-7 at any.)
  * Errors: FA_ERR_INVALID_ARG for negative sizes, bad pointers, theta or scaling;
  * FA_ERR_UNSUPPORTED for another rope_dim, n or start above 2^30, or a device
  * other than sm_103.  n = 0 is a no-op.
