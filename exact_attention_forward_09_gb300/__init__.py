@@ -116,6 +116,8 @@ def _lib():
         lib.fa_fwd_paged.restype = i32
         lib.fa_tree_plan.argtypes = [vp, vp, vp, i64, i64, vp, i64, vp, vp]
         lib.fa_tree_plan.restype = i32
+        lib.fa_tree_plan_window.argtypes = [vp, vp, vp, i64, i64, vp, i64, vp, i64, i64, vp]
+        lib.fa_tree_plan_window.restype = i32
         lib.fa_fwd_tree.argtypes = [vp, cache, vp, vp, vp, i64, i64, vp, vp, vp, i64, vp] + [i64] * 7 + [f32, vp, ctypes.c_size_t, vp]
         lib.fa_fwd_tree.restype = i32
         lib.fa_cache_append.argtypes = [cache, vp, vp, vp, vp, i64, i64, i64, vp, i64, i64, vp, vp, i64, i64, i64, vp,
@@ -627,13 +629,14 @@ def _fwd_paged(q, k_pages, v_pages, block_table, cu_q, seq_k, mask, positions, w
 
 
 def tree_plan(parents: torch.Tensor, cu_q: torch.Tensor, seq_k: torch.Tensor, max_tree: int,
-              mask: torch.Tensor | None = None, positions: torch.Tensor | None = None):
-    """Lays out trees of drafted tokens (``fa_tree_plan``): parents int32 [T],
-    each a node's parent by its number within its sequence, or -1; cu_q and
+              mask: torch.Tensor | None = None, positions: torch.Tensor | None = None, window: int | None = None, sinks: int = 0):
+    """Lays out trees of drafted tokens (``fa_tree_plan_window``): parents int32
+    [T], each a node's parent by its number within its sequence, or -1; cu_q and
     seq_k as in ``fwd_paged``; ``max_tree``: the most nodes of a tree, up to 1024
     (sequences of more tokens than its next multiple of 32 are chunks of a
-    prompt).  Returns (mask int32 [T, ceil(max_tree / 32)], positions int32 [T])
-    for ``fwd_tree`` and ``cache_append``."""
+    prompt); ``window`` and ``sinks`` those of ``fwd_tree``, so that nodes do not see
+    the nodes above them that have left the window.  Returns (mask int32 [T,
+    ceil(max_tree / 32)], positions int32 [T]) for ``fwd_tree`` and ``cache_append``."""
     T, index = _ints("parents", parents)
     B, words = _ints("seq_k", seq_k)[0], (_count(max_tree) + 31) // 32
     cp, sp = _check_ints("cu_q", cu_q, B + 1, index), _check_ints("seq_k", seq_k, B, index)
@@ -648,10 +651,10 @@ def tree_plan(parents: torch.Tensor, cu_q: torch.Tensor, seq_k: torch.Tensor, ma
     else:
         _check_out("positions", positions, (T,), torch.int32, index)
     with _guard(index):
-        st = _lib().fa_tree_plan(parents.data_ptr(), cp, sp, B, T, mask.data_ptr(), words, positions.data_ptr(),
-                                 _current_stream(index))
+        st = _lib().fa_tree_plan_window(parents.data_ptr(), cp, sp, B, T, mask.data_ptr(), words, positions.data_ptr(),
+                                        1 << 30 if window is None else _count(window), _count(sinks), _current_stream(index))
     if st != FA_OK:
-        raise FaError(st, "fa_tree_plan")
+        raise FaError(st, "fa_tree_plan_window")
     return mask, positions
 
 
@@ -663,7 +666,8 @@ def fwd_tree(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, bloc
     (``fa_fwd_tree``): each sees the cached keys (under a window by its own
     position, from ``positions`` int32 [T]) and the new tokens up to itself that
     its row of ``mask`` (int32 [T, words], 32 tokens of its sequence to a word)
-    has a bit for.  Sequences of more than 32 * words new tokens are plain chunks."""
+    has a bit for, whatever the window: give ``tree_plan`` the same window and
+    sinks.  Sequences of more than 32 * words new tokens are plain chunks."""
     if mask is None:
         raise ValueError("mask must be an int32 [T, words] tensor")
     return _fwd_paged(q, k_pages, v_pages, block_table, cu_q, seq_k, mask, positions, window, sinks, scale, max_q, out, lse, workspace)

@@ -373,7 +373,13 @@ fa_status fa_fwd_tree(const void* q, const fa_kv_cache* cache, void* o, float* l
 
 fa_status fa_tree_plan(const int32_t* parents, const int32_t* cu_q, const int32_t* seq_k, int64_t B, int64_t T,
                        uint32_t* mask, int64_t words, int32_t* positions, cudaStream_t stream) {
-  if (B < 0 || T < 0 || words < 1) return FA_ERR_INVALID_ARG;
+  return fa_tree_plan_window(parents, cu_q, seq_k, B, T, mask, words, positions, kMaxLen, 0, stream);
+}
+
+fa_status fa_tree_plan_window(const int32_t* parents, const int32_t* cu_q, const int32_t* seq_k, int64_t B, int64_t T,
+                              uint32_t* mask, int64_t words, int32_t* positions, int64_t window, int64_t sinks,
+                              cudaStream_t stream) {
+  if (B < 0 || T < 0 || words < 1 || window < 1 || sinks < 0) return FA_ERR_INVALID_ARG;
   if (words > kMaxWords || B > (1 << 24) || T > kMaxLen) return FA_ERR_UNSUPPORTED;
   if (B == 0 || T == 0) return FA_OK;
   if (!parents || !cu_q || !seq_k || !mask || !positions) return FA_ERR_INVALID_ARG;
@@ -382,7 +388,9 @@ fa_status fa_tree_plan(const int32_t* parents, const int32_t* cu_q, const int32_
   int* err = nullptr;
   const fa_status st = fa::internal_device_setup(&dev, &err);
   if (st != FA_OK) return st;
-  return fa::launch_tree_plan(parents, cu_q, seq_k, (int)B, (int)T, mask, (int)words, positions, err, stream) == cudaSuccess
+  return fa::launch_tree_plan(parents, cu_q, seq_k, (int)B, (int)T, mask, (int)words, positions,
+                              (int)(window < kMaxLen ? window : kMaxLen), (int)(sinks < kMaxLen ? sinks : kMaxLen), err,
+                              stream) == cudaSuccess
              ? FA_OK
              : FA_ERR_CUDA;
 }

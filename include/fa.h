@@ -608,7 +608,8 @@ fa_status fa_cache_append_at(const fa_kv_cache* cache, const void* q, const void
  * then it follows the cached tokens.  Nodes lie in the cache one behind the other,
  * node i at position seq_k[b] - n + i as any new token, but sit in their sequence
  * at the position that their depth gives them: seq_k[b] - n + (nodes above it).
- * The steps of one round: fa_tree_plan once; in each layer fa_cache_append_at with
+ * The steps of one round: fa_tree_plan (under a window fa_tree_plan_window, with the
+ * layers' own) once; in each layer fa_cache_append_at with
  * its positions, and fa_fwd_tree; then fa_cache_compact keeps the accepted path.
  */
 
@@ -635,12 +636,28 @@ fa_status fa_tree_plan(const int32_t* parents, const int32_t* cu_q, const int32_
                        uint32_t* mask, int64_t words, int32_t* positions, cudaStream_t stream);
 
 /*
+ * fa_tree_plan_window -- fa_tree_plan under a sliding window with sinks: a node
+ * at position p keeps the bits of those nodes above it that sit at a position j >
+ * p - window or j < sinks, as it would see them if its path were decoded token by
+ * token with fa_fwd_paged.  (The rows of a chunk are fa_tree_plan's: fa_fwd_tree
+ * does not look at them.)
+ * A round under a window takes its plan from this call, with the window and sinks
+ * that fa_fwd_tree gets.  fa_tree_plan is this call without a window.
+ * Errors: as fa_tree_plan, FA_ERR_INVALID_ARG also for window < 1 or sinks < 0.
+ */
+fa_status fa_tree_plan_window(const int32_t* parents, const int32_t* cu_q, const int32_t* seq_k, int64_t B, int64_t T,
+                              uint32_t* mask, int64_t words, int32_t* positions, int64_t window, int64_t sinks,
+                              cudaStream_t stream);
+
+/*
  * fa_fwd_tree -- fa_fwd_paged where the new tokens of a sequence are a tree's
  * nodes.  Node i, at position p, sees
  *   the cached keys j < seq_k[b] - n with j > p - window or j < sinks, and
- *   new token k <= i iff bit k of its mask row is set (the window does not apply;
- *   a row without any bit and any cached key gets O = 0 and LSE = -inf).
- *   mask       [T, words] uint32 (device), as fa_tree_plan writes it, or any other
+ *   new token k <= i iff bit k of its mask row is set (the window does not apply
+ *   to these: fa_tree_plan_window leaves out the bits of nodes that have left it; a
+ *   row without any bit and any cached key gets O = 0 and LSE = -inf).
+ *   mask       [T, words] uint32 (device), as fa_tree_plan and fa_tree_plan_window
+ *              write it, or any other
  *              (bits behind a token's own are not looked at)
  *   words      1 to 32.  Sequences of more than 32 * words new tokens attend as in
  *              fa_fwd_paged, whatever their mask rows hold

@@ -416,3 +416,72 @@ def test_a_wait_that_runs_out_is_reported(fa):
     o, lse = x.run(fa)
     fa.check_device_error()
     x.check(o, lse, "after it")
+
+
+# ------------------------------------------- windows among the nodes --
+
+def _kept(rows, pos, n, window, sinks):
+    """Of what a node sees of its own path, what its window and the sinks leave."""
+    return [frozenset(k for k in row if k < n and (pos[k] > pos[i] - window or pos[k] < sinks)) for i, row in enumerate(rows)]
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (2, 3), (5, 0), (7, 40), (33, 1), (64, 70), (1000, 0), (ALL, 9), (1, 1 << 40)])
+@pytest.mark.parametrize("words", [1, 3, 32])
+def test_plan_under_a_window(fa, words, window, sinks):
+    # trees, lines and chunks, behind no cached token, a few (within the sinks) and many
+    rng = random.Random(words)
+    lens, trees = [], []
+    for ctx in (0, 1, 2, 30, 39, 70, 500):
+        for n in (1, 7, 32 * words, 32 * words - 1, 32 * words + 1 + 5 * ctx):
+            lens.append((n, ctx + n))
+            trees.append(list(range(-1, n - 1)) if n > 32 * words or n % 2 else random_tree(n, rng))
+    cu = [0]
+    for n, _ in lens:
+        cu.append(cu[-1] + n)
+    args = ints([p for t in trees for p in t]), ints(cu), ints([nk for _, nk in lens]), 32 * words
+    mask, pos = fa.tree_plan(*args, window=window, sinks=sinks)
+    assert not _reported(fa)
+    want = []
+    for (n, nk), parents in zip(lens, trees):
+        rows, depth = layout(parents, words)
+        want.append(mask_of(rows if n > 32 * words else _kept(rows, [nk - n + x for x in depth], n, window, sinks), words))
+    assert torch.equal(mask.cpu(), torch.cat(want))
+    plain = fa.tree_plan(*args)
+    assert torch.equal(pos, plain[1])
+    if window == ALL:
+        assert torch.equal(mask, plain[0])
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("n", [3, 20, 60])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (2, 1), (5, 0), (16, 4), (40, 25)])
+def test_a_line_of_nodes_under_a_window_is_a_chunk(fa, d, n, window, sinks):
+    # windows that end among the nodes: laid out under it, a line sees what the same tokens of a chunk see
+    x = Batch([(n, n), (n, n + 2), (n, 128 + n), (n, 500)], 2, 1, d, torch.bfloat16, 32, 2, trees=[list(range(-1, n - 1))] * 4)
+    mask, pos = fa.tree_plan(ints([p for t in x.parents for p in t]), x.cu, x.sk, 64, window=window, sinks=sinks)
+    x.chunk = [True] * 4
+    for max_q in (0, n):
+        o, lse = x.run(fa, mask=mask, positions=pos, window=window, sinks=sinks, max_q=max_q)
+        fa.check_device_error()
+        x.check(o, lse, f"a line of {n}", window, sinks)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("window,sinks", [(3, 0), (9, 2), (20, 50)])
+def test_a_tree_under_a_window_sees_what_its_paths_see(fa, d, window, sinks):
+    # each path of a tree decoded token by token: the cached tokens, then the nodes from the root on
+    n, ctx = 40, 45
+    parents = random_tree(n, random.Random(5), 4)
+    x = Batch([(n, ctx + n)], 4, 2, d, torch.bfloat16, 32, 2, trees=[parents])
+    mask, pos = fa.tree_plan(ints(parents), x.cu, x.sk, 64, window=window, sinks=sinks)
+    o, lse = x.run(fa, mask=mask, positions=pos, window=window, sinks=sinks)
+    fa.check_device_error()
+    k, v = x.seqs[0]
+    for i in range(n):
+        path = [i]
+        while parents[path[0]] >= 0:
+            path.insert(0, parents[path[0]])
+        at = list(range(ctx)) + [ctx + j for j in path]
+        see = sees(1, len(at) - 1, None, None, window, sinks, chunk=True)
+        ref = reference(x.q[i:i + 1], k[:, at], v[:, at], see, d ** -0.5)
+        check_forward(o[i:i + 1].transpose(0, 1), lse[i:i + 1].transpose(0, 1), ref, x.q.dtype, d, len(at), f"node {i}")

@@ -80,3 +80,16 @@ def test_models_agree():
             a = sees(n, 9, line, [9 + d for d in depth], window, 2)
             b = sees(n, 9, None, None, window, 2, chunk=True)
             assert torch.equal(a[:, :9], b[:, :9])
+
+
+def test_plan_under_a_window_refusals(fa):
+    def call(**kw):
+        a = dict(parents=P, cu=P, sk=P, B=2, T=9, mask=P, words=1, pos=P, window=4, sinks=0)
+        a.update(kw)
+        return fa.lib().fa_tree_plan_window(*a.values(), None)
+
+    for kw in (dict(parents=None), dict(mask=P + 1), dict(words=0), dict(pos=None), dict(window=0), dict(window=-1), dict(sinks=-1)):
+        assert call(**kw) == fa.FA_ERR_INVALID_ARG, kw
+    for kw in (dict(words=33), dict(B=(1 << 24) + 1), dict(T=(1 << 30) + 1)):
+        assert call(**kw) == fa.FA_ERR_UNSUPPORTED, kw
+    assert call(T=0, mask=None, window=1 << 62, sinks=1 << 62) == fa.FA_OK
