@@ -219,7 +219,6 @@ struct WinParams {
   const uint32_t* mask;  // [T, words] which new tokens of its sequence a token sees
   const int* positions;  // [T] positions of the tokens in their sequence; null: where they lie
   int words;             // 32 words is at most 2^30
-  int kv_few;            // keys and values are read by few units each: the first to leave L2
 };
 
 // The key tiles that a unit of up to two query tiles visits.
@@ -783,9 +782,31 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
 
   if (warp >= C::SOFTMAX_WARPS) {
     if constexpr (C::REALLOC) regs_dec<C::CTRL_REGS>();
+    // How long a unit's keys and values stay in L2.  Trees bring few units to a sequence
+    // as a rule: up to four, its keys and values leave L2 first, for the partial results
+    // that the join reads back (32 x 60 nodes over 1000 to 8000 keys 141 -> 138 us, 26 over
+    // 131000 44 -> 41).  A longer chunk's stay, read by many units (2 x 1500 tokens over
+    // 30000 keys beside 60 single ones 1150, and 1240 where they leave), and those that
+    // other rows hold as well, as rows do that fa_pages_fork made (4 x 8 rows over 8000
+    // shared keys each, d = 128: one token a row 124 and 146, 16 nodes 131 and 139, 60
+    // nodes of 32 rows over 16000 370 and 419; at d = 64 16 nodes 95 and 91).  Looked at
+    // are the rows before and behind, at the page where the unit begins: lane 1's row and
+    // lane 2's, and the others ask for its own.
+    auto near_row = [&](const WinUnit& w) -> int { return min(max(w.seq + (lane == 1) - (lane == 2), 0), prm.B - 1); };
+    auto near_page = [&](const WinUnit& w) -> int {
+      if (!TREE) return 0;
+      const int key = (w.r0 < w.ns ? w.r0 : w.r0 + w.skip) * kBN;
+      return prm.table[near_row(w) * prm.table_stride + (key >> prm.page_shift)];
+    };
+    const uint64_t pol_last = policy_evict_last(), pol_first = policy_evict_first();
+    auto kv_policy = [&](const WinUnit& w, int near) -> uint64_t {
+      if (!TREE) return pol_last;
+      const int own = __shfl_sync(0xffffffffu, near, 0);
+      const bool shared = __any_sync(0xffffffffu, near == own && near_row(w) != w.seq);
+      return shared || w.nk - w.p0 + w.q_row > 4 * tpg ? pol_last : pol_first;
+    };
     if (C::V_WARP && warp == C::LOADV_WARP) {
       // -------------------------------------------------------- load V --
-      const uint64_t pol_kv = TREE && prm.kv_few ? policy_evict_first() : policy_evict_last();
       int pos = 0;
       bool ok = true;
       for (int r = 0; ok; ++r) {
@@ -797,7 +818,9 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
         if (w.kz < 0) break;
         const int n = w.r1 - w.r0;
         if (n <= 0) continue;
+        const int near = near_page(w);
         int ids = pages_of(w, w.r0), ids1 = pages_of(w, w.r0 + 1);
+        const uint64_t pol_kv = kv_policy(w, near);
         for (int j = 0; j < n && ok; ++j) {
           const int ids2 = pages_of(w, w.r0 + j + 2);  // two tiles ahead: its latency hides behind the loads
           ok = load_tile(w, &tm_v, pos + v_at(j, n), w.r0 + j, ids, pol_kv);
@@ -812,8 +835,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
       // ---------------------------------------------------------- load --
       // The whole warp runs the loop; lane 0 waits, arms barriers and
       // publishes units; paged boxes are issued one per lane.
-      const uint64_t pol_kv = TREE && prm.kv_few ? policy_evict_first() : policy_evict_last();
-      const uint64_t pol_q = policy_evict_first();
+      const uint64_t pol_q = pol_first;
       int pos = 0;    // ring position (continues across units)
       int k = 0;      // units with keys loaded by this CTA
       bool ok = true;
@@ -834,6 +856,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
       auto load_unit = [&](const WinUnit& w) {
         const int n = w.r1 - w.r0;
         if (n <= 0) return;  // no visible key: nothing to load
+        const int near = near_page(w);
         int ids = pages_of(w, w.r0), ids1 = pages_of(w, w.r0 + 1);
         const int n0 = win_count(w, 0), n1 = C::NQT == 2 ? win_count(w, 1) : 0;
         // the Q buffer is free once the previous unit's last Q K^T finished
@@ -862,6 +885,7 @@ __global__ void __launch_bounds__(WinCfg<ELEM, D, PAGED, FORM>::THREADS, WinCfg<
           }
         }
         __syncwarp();
+        const uint64_t pol_kv = kv_policy(w, near);
         for (int j = 0; j < n && ok; ++j) {
           const int ids2 = pages_of(w, w.r0 + j + 2);
           ok = load_tile(w, &tm_k, pos + k_at(j), w.r0 + j, ids, pol_kv);

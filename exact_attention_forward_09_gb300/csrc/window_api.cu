@@ -258,11 +258,6 @@ fa_status fwd_paged(const void* q, const fa_kv_cache* cache, void* o, float* lse
   int64_t tiles = keys / fa::kBN + 1;
   const int64_t reach = p.window + (int64_t)p.sinks + unit_tok + 32 * words;  // (a tree's units start their windows at its root's)
   if (reach < keys) tiles = reach / fa::kBN + 4;
-  // Trees bring few units to a sequence as a rule.  Up to four on average, its keys
-  // and values leave L2 to the partial results that the join reads back (32 x 60 nodes
-  // over 1000 to 8000 keys 141 -> 137 us, 26 over 131000 44.6 -> 41.0, 8 x 256 over 8000 to
-  // 30000, four units each, 578 -> 566; but chunks of 2048 tokens, 32 units each, 307 -> 334).
-  p.kv_few = mask && T <= 4 * unit_tok * B;
   const int64_t units = (T / unit_tok + B) * Hkv;
   if (mask) tiles += 2;  // (the places behind a tree unit's: end_places)
   if (units >= (int64_t)0x7fffffff / (2 * (tiles + 1))) return FA_ERR_UNSUPPORTED;
