@@ -64,7 +64,7 @@ bool scaled_frequencies(int64_t r, double theta, const fa_rope_scaling* sc, Two*
   const double s = sc ? sc->factor : 1.0;
   if (!std::isfinite(theta) || theta <= 1.0) return false;
   if (kind < FA_ROPE_SCALE_NONE || kind > FA_ROPE_SCALE_INDEX) return false;
-  if (sc && (!std::isfinite(sc->amplitude))) return false;
+  if (sc && !std::isfinite((float)sc->amplitude)) return false;  // (the tables are fp32)
   if (kind != FA_ROPE_SCALE_NONE && (!std::isfinite(s) || s < 1.0)) return false;
   const bool parts = kind == FA_ROPE_SCALE_TURNS || kind == FA_ROPE_SCALE_INDEX;
   if (parts) {

@@ -716,7 +716,7 @@ typedef struct {
     double factor;      /* at least 1 */
     double original;    /* TURNS, INDEX: the original length, at least 1 */
     double low, high;   /* TURNS, INDEX: 0 <= low < high (INDEX: 0 < low) */
-    double amplitude;   /* finite */
+    double amplitude;   /* within fp32's range */
 } fa_rope_scaling;
 
 /*

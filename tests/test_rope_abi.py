@@ -125,3 +125,11 @@ def test_reference_frequencies():
         turns = 4096.0 * x / (2 * math.pi)
         assert y == pytest.approx(x if turns >= 4 else x / 8 if turns <= 1 else y)
         assert x / 8 <= y <= x
+
+
+def test_an_amplitude_beyond_fp32_is_refused(fa):
+    # (the tables would hold infinities and NaN)
+    for a in (3.5e38, -1e39, 1e308):
+        assert _table(fa, _scaling(fa, amplitude=a)) == fa.FA_ERR_INVALID_ARG
+    for a in (3.4e38, -3.4e38, 1e-45, 0.0):
+        assert _table(fa, _scaling(fa, amplitude=a)) == fa.FA_OK
