@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(kCompactThreads) cache_compact_kernel(const __
   const long long cap = (long long)prm.max_pages << r.page_shift;
   const bool teller = part == 0 && group == 0 && blockIdx.y == 0;  // speaks for the sequence
   bool bad = asked != n || first < 0 || (long long)first + n > cap;
-  if (teller && threadIdx.x == 0 && prm.seq_k_out) prm.seq_k_out[b] = (int)min(max((long long)first + n, 0LL), cap);
+  if (teller && threadIdx.x == 0) prm.seq_k_out[b] = (int)min(max((long long)first + n, 0LL), cap);
   const int head = group * heads_at_once + hs;
   const bool mine = head < r.heads;
   uint16_t* base = (blockIdx.y & 1 ? r.v : r.k) + (blockIdx.y >> 1) * r.layer_stride + head * r.head_stride +

@@ -40,7 +40,7 @@ struct CompactParams {
   const int *table, *first, *keep, *keep_n;
   long long table_stride, keep_stride;
   int max_pages, max_keep, B;
-  int* seq_k_out;           // [B] first + keep_n, or null
+  int* seq_k_out;           // [B] first + keep_n
   int* err;
 };
 cudaError_t launch_cache_compact(const CompactParams& prm, int d, int sms, cudaStream_t stream);
