@@ -668,6 +668,8 @@ fa_status fa_tree_plan_window(const int32_t* parents, const int32_t* cu_q, const
  *              FA_ERR_INDEX
  * Everything else as in fa_fwd_paged, its workspace included.  Pages that hold
  * no key from position seq_k[b] - n - window + 1 on, nor a sink, are not read.
+ * (Any entry of block_table's [B, max_pages] may be, to see which rows share pages;
+ * it then changes what stays in the GPU's cache, and no result.)
  * For what a NaN or an infinity in a value row reaches, the new tokens' rows and
  * the cached ones from that position on count as seen.
  */

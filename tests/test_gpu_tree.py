@@ -485,3 +485,28 @@ def test_a_tree_under_a_window_sees_what_its_paths_see(fa, d, window, sinks):
         see = sees(1, len(at) - 1, None, None, window, sinks, chunk=True)
         ref = reference(x.q[i:i + 1], k[:, at], v[:, at], see, d ** -0.5)
         check_forward(o[i:i + 1].transpose(0, 1), lse[i:i + 1].transpose(0, 1), ref, x.q.dtype, d, len(at), f"node {i}")
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_rows_that_share_pages(fa, d):
+    # beams: rows with the same full pages (neighbours or not), and the same batch with copies of them: the same bits
+    page, full, n = 32, 9, [5, 1, 20, 7, 3, 60]
+    group = [0, 0, 1, 1, 0, 1]
+    lens = [(x, page * full + 3 + x) for x in n]
+    x = Batch(lens, 4, 2, d, torch.bfloat16, page, 2)
+    c = x.cache
+    at = {0: 0, 1: 2}
+    shared = c.table.clone()
+    for b, g in enumerate(group):
+        own, first = c.table[b, :full].long(), c.table[at[g], :full].long()
+        c.k[own], c.v[own] = c.k[first], c.v[first]
+        shared[b, :full] = shared[at[g], :full]
+        x.seqs[b][0][:, :page * full], x.seqs[b][1][:, :page * full] = (t[:, :page * full] for t in x.seqs[at[g]])
+    for window, sinks, max_q in ((ALL, 0, 0), (100, 40, 60), (ALL, 0, 3)):
+        c.table, copies = shared, c.table
+        o, lse = x.run(fa, window=window, sinks=sinks, max_q=max_q)
+        c.table = copies
+        p, mse = x.run(fa, window=window, sinks=sinks, max_q=max_q)
+        fa.check_device_error()
+        assert torch.equal(o, p) and torch.equal(lse, mse)
+        x.check(o, lse, "shared pages", window, sinks)
