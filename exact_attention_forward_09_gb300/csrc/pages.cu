@@ -341,7 +341,9 @@ __global__ void __launch_bounds__(kCopyThreads) fork_kernel(const PoolParams prm
 //   8 sequences of 12000 to 16000 tokens, 2 layers of 8 heads, 4000 of each kept:
 //   344 MB in 65 us, 5.3 TB/s (a row's columns shared by two blocks; whole 74, by
 //   four 71).  8 of the last 60 tokens of 32 sequences, 8 layers: 6.3 us, four
-//   dependent look-ups and a round.
+//   dependent look-ups and a round.  One sequence makes few blocks, each of which
+//   waits for its own reads round after round: 4000 of 16000 tokens of 8 heads, one
+//   layer 28.6 us (floor 4.8), 8 layers in one call 58 (39), 32 layers 179 (154).
 // Rows in flight per thread: two where there are at most four to a thread in all (up
 // to 8, 24, 64 tokens kept of 32 sequences, 8 layers: 6.3, 10.5, 16.4 us; with eight,
 // which leave fewer blocks to an SM, 8.5, 14.7, 19.5), else eight (300 tokens 68.6,

@@ -174,7 +174,8 @@ __device__ __forceinline__ void turn_of(uint64_t t, float& c, float& s) {
   const float x = fmaf((float)(top >> 6), 0x1p-25f, (float)__funnelshift_r((uint32_t)t, (uint32_t)top, 6) * 0x1p-57f);
   // sin(pi x) and cos(pi x): polynomials in x^2 that are nearest to them over this
   // range (fitted by weighted least squares, the weights moved toward the largest
-  // errors as Lawson's method does), to 1.8e-11 and 2e-10; pi in two parts
+  // errors as Lawson's method does), with these coefficients to 1.3e-9 and 9.1e-9 (a
+  // unit of fp32 just below 1 is 6e-8); pi in two parts
   const float u = x * x;
   const float ps = fmaf(u, fmaf(u, fmaf(u, fmaf(u, 0.0812298f, -0.59922882f), 2.5501636f), -5.1677128f), -8.7422777e-8f);
   const float pc = fmaf(u, fmaf(u, fmaf(u, 0.23212635f, -1.3351379f), 4.0587106f), -4.9348022f);
